@@ -24,8 +24,34 @@ BMOE_E_EXPERT = 5
 STATUS = {
     0: "BMOE_OK", 1: "BMOE_E_NULL", 2: "BMOE_E_SHAPE", 3: "BMOE_E_DTYPE",
     4: "BMOE_E_TERNARY", 5: "BMOE_E_EXPERT", 6: "BMOE_E_WORKSPACE", 7: "BMOE_E_HIP",
-    8: "BMOE_E_ALIGN",
+    8: "BMOE_E_ALIGN", 9: "BMOE_E_VALUE",
 }
+
+BMOE_SCORE_SOFTMAX = 0
+BMOE_SCORE_SIGMOID = 1
+BMOE_GROUP_MAX = 0
+BMOE_GROUP_TOP2 = 1
+_SCORES = {"softmax": BMOE_SCORE_SOFTMAX, "sigmoid": BMOE_SCORE_SIGMOID}
+_GROUP_SCORES = {"max": BMOE_GROUP_MAX, "top2": BMOE_GROUP_TOP2}
+
+
+class RouteSpec(ctypes.Structure):
+    """bmoe_route_spec: how scores, groups and gates are formed."""
+    _fields_ = [("score", ctypes.c_int), ("renorm", ctypes.c_int), ("scale", ctypes.c_float),
+                ("n_groups", ctypes.c_int), ("topk_groups", ctypes.c_int),
+                ("group_score", ctypes.c_int)]
+
+    def __init__(self, score: str = "softmax", *, renorm: bool = True, scale: float = 1.0,
+                 n_groups: int = 1, topk_groups: int = 1, group_score: str = "top2"):
+        if score not in _SCORES or group_score not in _GROUP_SCORES:
+            raise ValueError("score is 'softmax' or 'sigmoid', group_score 'max' or 'top2'")
+        super().__init__(_SCORES[score], bool(renorm), scale, n_groups, topk_groups,
+                         _GROUP_SCORES[group_score])
+
+
+class BmoeTensor(ctypes.Structure):
+    """bmoe_tensor: one entry of a gradient list."""
+    _fields_ = [("data", ctypes.c_void_p), ("count", ctypes.c_size_t), ("dtype", ctypes.c_int)]
 
 
 class BmoeError(RuntimeError):
@@ -114,6 +140,29 @@ def lib():
         L.bmoe_router.restype = c_int
         L.bmoe_router_timed.argtypes = L.bmoe_router.argtypes + [vp]
         L.bmoe_router_timed.restype = c_int
+        L.bmoe_router_logits.argtypes = [c_int, c_int, c_int, c_int, vp, vp, vp, vp]
+        L.bmoe_router_logits.restype = c_int
+        L.bmoe_route.argtypes = [c_int, c_int, c_int, c_int, vp, vp, vp, vp, vp, vp]
+        L.bmoe_route.restype = c_int
+        L.bmoe_route_backward.argtypes = [c_int, c_int, c_int, c_int, vp, vp, vp, vp, vp, vp]
+        L.bmoe_route_backward.restype = c_int
+        L.bmoe_route_balance_workspace_bytes.argtypes = [c_int, c_int, c_int]
+        L.bmoe_route_balance_workspace_bytes.restype = c_sz
+        L.bmoe_route_balance.argtypes = [c_int, c_int, c_int, vp, c_int, c_f, vp, vp, vp, c_sz, vp]
+        L.bmoe_route_balance.restype = c_int
+        L.bmoe_router_backward_workspace_bytes.argtypes = [c_int, c_int, c_int, c_int, c_int]
+        L.bmoe_router_backward_workspace_bytes.restype = c_sz
+        L.bmoe_router_backward.argtypes = [c_int, c_int, c_int, c_int, c_int, vp, vp, vp, vp, vp,
+                                           vp, vp, vp, vp, vp, c_sz, vp]
+        L.bmoe_router_backward.restype = c_int
+        L.bmoe_grad_workspace_bytes.argtypes = [c_int]
+        L.bmoe_grad_workspace_bytes.restype = c_sz
+        L.bmoe_grad_norm.argtypes = [c_int, vp, vp, vp, c_sz, vp]
+        L.bmoe_grad_norm.restype = c_int
+        L.bmoe_grad_scale.argtypes = [c_int, vp, vp, vp, c_f, vp]
+        L.bmoe_grad_scale.restype = c_int
+        L.bmoe_grad_clip.argtypes = [c_int, vp, vp, c_f, vp, vp, c_sz, vp]
+        L.bmoe_grad_clip.restype = c_int
         L.bmoe_backward_timed.argtypes = L.bmoe_backward.argtypes + [vp]
         L.bmoe_backward_timed.restype = c_int
         L.bmoe_backward_kernel_count.argtypes = [c_int, c_int, c_int, c_int, c_int]
@@ -126,6 +175,14 @@ def lib():
 
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def _nbytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def _stream(stream=None):
@@ -390,6 +447,63 @@ def bmoe_router_timed(dt: int, T: int, d: int, n_experts: int, k: int, x, w_rout
                                    _ptr(gates), _ptr(logits), _ptr(ws), nb, _stream(stream), ev)
 
 
+def bmoe_router_logits(dt: int, T: int, d: int, n_experts: int, x, w_router, logits,
+                       stream=None) -> int:
+    return lib().bmoe_router_logits(dt, T, d, n_experts, _ptr(x), _ptr(w_router), _ptr(logits),
+                                    _stream(stream))
+
+
+def bmoe_route(dt: int, T: int, n_experts: int, k: int, spec, logits, bias, ids, gates,
+               stream=None) -> int:
+    return lib().bmoe_route(dt, T, n_experts, k, _ref(spec), _ptr(logits), _ptr(bias), _ptr(ids),
+                            _ptr(gates), _stream(stream))
+
+
+def bmoe_route_backward(dt: int, T: int, n_experts: int, k: int, spec, logits, ids, dgates,
+                        dlogits, stream=None) -> int:
+    return lib().bmoe_route_backward(dt, T, n_experts, k, _ref(spec), _ptr(logits), _ptr(ids),
+                                     _ptr(dgates), _ptr(dlogits), _stream(stream))
+
+
+def bmoe_route_balance_workspace_bytes(T: int, n_experts: int, k: int) -> int:
+    return lib().bmoe_route_balance_workspace_bytes(T, n_experts, k)
+
+
+def bmoe_route_balance(T: int, n_experts: int, k: int, ids, accumulate: bool, rate: float, load,
+                       bias, ws, stream=None) -> int:
+    return lib().bmoe_route_balance(T, n_experts, k, _ptr(ids), int(accumulate), rate, _ptr(load),
+                                    _ptr(bias), _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def bmoe_router_backward_workspace_bytes(dt: int, T: int, d: int, n_experts: int, k: int) -> int:
+    return lib().bmoe_router_backward_workspace_bytes(dt, T, d, n_experts, k)
+
+
+def bmoe_router_backward(dt: int, T: int, d: int, n_experts: int, k: int, spec, x, w_router,
+                         logits, ids, dgates, dx_add, dx, dw, ws, stream=None) -> int:
+    return lib().bmoe_router_backward(dt, T, d, n_experts, k, _ref(spec), _ptr(x), _ptr(w_router),
+                                      _ptr(logits), _ptr(ids), _ptr(dgates), _ptr(dx_add),
+                                      _ptr(dx), _ptr(dw), _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def bmoe_grad_workspace_bytes(n: int) -> int:
+    return lib().bmoe_grad_workspace_bytes(n)
+
+
+def bmoe_grad_norm(n: int, grads, norm, ws, stream=None) -> int:
+    """``grads`` (and ``out`` below): ctypes arrays of BmoeTensor, or None."""
+    return lib().bmoe_grad_norm(n, grads, _ptr(norm), _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def bmoe_grad_scale(n: int, grads, out, norm, max_norm: float, stream=None) -> int:
+    return lib().bmoe_grad_scale(n, grads, out, _ptr(norm), max_norm, _stream(stream))
+
+
+def bmoe_grad_clip(n: int, grads, out, max_norm: float, norm, ws, stream=None) -> int:
+    return lib().bmoe_grad_clip(n, grads, out, max_norm, _ptr(norm), _ptr(ws), _nbytes(ws),
+                                _stream(stream))
+
+
 # ---- conveniences over the entry points (allocation + error checks) -------
 
 def dtype_code(t: torch.Tensor) -> int:
@@ -588,3 +702,207 @@ def backward_kept(x: torch.Tensor, gates: torch.Tensor, n_experts: int, w_packed
                                   out["dgates"], out["dtheta"], out["dphi"], out["dw"], kept, ws,
                                   stream), "bmoe_backward_kept")
         return out
+
+
+# ---- routing from logits and the rest of a training step ---------------------
+
+@contextlib.contextmanager
+def _device_of(device, stream):
+    with torch.cuda.device(device), _on(stream):
+        yield
+
+
+def _at(t: torch.Tensor, stream):
+    """Make t's device (and `stream`, one of that device) current for a call."""
+    if not t.is_cuda:
+        raise ValueError("the library works on GPU tensors")
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"the stream is of {stream.device}, the tensors are on {t.device}")
+    if stream is None and t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return _device_of(t.device, stream)
+
+
+def _like(name: str, t: torch.Tensor, dtype, shape, device) -> torch.Tensor:
+    """t itself, checked: dtype, shape, device and contiguous storage."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', strided'}")
+    return t
+
+
+def _matrix(name: str, t: torch.Tensor) -> torch.Tensor:
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous matrix, got shape {tuple(t.shape)}")
+    return t
+
+
+def router_logits(x: torch.Tensor, w_router: torch.Tensor, *, logits=None,
+                  stream=None) -> torch.Tensor:
+    """fp32 [T][N] = x w_router^T: the logits of route(), for route_logits()."""
+    T, d = _matrix("x", x).shape
+    N = w_router.shape[0]
+    dt = dtype_code(x)
+    _like("w_router", w_router, x.dtype, (N, d), x.device)
+    with _at(x, stream):
+        if logits is None:
+            logits = torch.empty(T, N, dtype=torch.float32, device=x.device)
+        _like("logits", logits, torch.float32, (T, N), x.device)
+        _check(bmoe_router_logits(dt, T, d, N, x, w_router, logits, stream), "bmoe_router_logits")
+        return logits
+
+
+def route_logits(logits: torch.Tensor, k: int, spec: Optional[RouteSpec] = None, *, bias=None,
+                 ids=None, gates=None, stream=None):
+    """(ids int32 [T][k], gates fp32 [T][k]) of the k experts each row of
+    logits (fp32 or bf16 [T][N]) chooses under `spec` (default: softmax gates
+    renormalised over the chosen, as route()); `bias` fp32 [N] moves the choice."""
+    T, N = _matrix("logits", logits).shape
+    dt = dtype_code(logits)
+    dev = logits.device
+    if spec is None:
+        spec = RouteSpec()
+    with _at(logits, stream):
+        if bias is not None:
+            _like("bias", bias, torch.float32, (N,), dev)
+        if ids is None:
+            ids = torch.empty(T, k, dtype=torch.int32, device=dev)
+        if gates is None:
+            gates = torch.empty(T, k, dtype=torch.float32, device=dev)
+        _like("ids", ids, torch.int32, (T, k), dev)
+        _like("gates", gates, torch.float32, (T, k), dev)
+        _check(bmoe_route(dt, T, N, k, spec, logits, bias, ids, gates, stream), "bmoe_route")
+        return ids, gates
+
+
+def route_logits_backward(logits: torch.Tensor, ids: torch.Tensor, dgates: torch.Tensor,
+                          spec: Optional[RouteSpec] = None, *, dlogits=None,
+                          stream=None) -> torch.Tensor:
+    """dlogits fp32 [T][N] of sum(dgates * gates) for route_logits()'s gates."""
+    T, N = _matrix("logits", logits).shape
+    k = _matrix("ids", ids).shape[1]
+    dt = dtype_code(logits)
+    dev = logits.device
+    if spec is None:
+        spec = RouteSpec()
+    _like("ids", ids, torch.int32, (T, k), dev)
+    _like("dgates", dgates, torch.float32, (T, k), dev)
+    with _at(logits, stream):
+        if dlogits is None:
+            dlogits = torch.empty(T, N, dtype=torch.float32, device=dev)
+        _like("dlogits", dlogits, torch.float32, (T, N), dev)
+        _check(bmoe_route_backward(dt, T, N, k, spec, logits, ids, dgates, dlogits, stream),
+               "bmoe_route_backward")
+        return dlogits
+
+
+def route_balance(ids: torch.Tensor, load: torch.Tensor, *, bias=None, rate: float = 0.0,
+                  accumulate: bool = False, stream=None) -> torch.Tensor:
+    """Counts ids [T][k] into load int32 [N] (added to it with `accumulate`)
+    and, with a bias fp32 [N], moves it by `rate` against the loads, in place.
+    Returns load."""
+    T, k = _matrix("ids", ids).shape
+    N = load.numel()
+    _like("ids", ids, torch.int32, (T, k), load.device)
+    _like("load", load, torch.int32, (N,), load.device)
+    with _at(load, stream):
+        if bias is not None:
+            _like("bias", bias, torch.float32, (N,), load.device)
+        n = bmoe_route_balance_workspace_bytes(T, N, k)
+        if n == 0:
+            raise BmoeError(2, "bmoe_route_balance_workspace_bytes")
+        ws = torch.empty(n, dtype=torch.uint8, device=load.device)
+        _check(bmoe_route_balance(T, N, k, ids, accumulate, rate, load, bias, ws, stream),
+               "bmoe_route_balance")
+        return load
+
+
+def router_backward(x: torch.Tensor, w_router: torch.Tensor, logits: torch.Tensor,
+                    ids: torch.Tensor, dgates: torch.Tensor, spec: Optional[RouteSpec] = None, *,
+                    dx_add=None, dx=None, dw=None, stream=None) -> dict:
+    """Gradients of sum(dgates * gates) for gates = route_logits(x w_router^T):
+    dict of dx (dtype of x; plus `dx_add`, e.g. backward()'s dx) and dw fp32
+    [N][d]. logits: the fp32 ones of router_logits() or route()."""
+    T, d = _matrix("x", x).shape
+    N = w_router.shape[0]
+    k = _matrix("ids", ids).shape[1]
+    dt = dtype_code(x)
+    dev = x.device
+    if spec is None:
+        spec = RouteSpec()
+    _like("w_router", w_router, x.dtype, (N, d), dev)
+    _like("logits", logits, torch.float32, (T, N), dev)
+    _like("ids", ids, torch.int32, (T, k), dev)
+    _like("dgates", dgates, torch.float32, (T, k), dev)
+    with _at(x, stream):
+        if dx_add is not None:
+            _like("dx_add", dx_add, x.dtype, (T, d), dev)
+        if dx is None:
+            dx = torch.empty_like(x)
+        if dw is None:
+            dw = torch.empty(N, d, dtype=torch.float32, device=dev)
+        _like("dx", dx, x.dtype, (T, d), dev)
+        _like("dw", dw, torch.float32, (N, d), dev)
+        n = bmoe_router_backward_workspace_bytes(dt, T, d, N, k)
+        if n == 0:
+            raise BmoeError(2, "bmoe_router_backward_workspace_bytes")
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        _check(bmoe_router_backward(dt, T, d, N, k, spec, x, w_router, logits, ids, dgates,
+                                    dx_add, dx, dw, ws, stream), "bmoe_router_backward")
+        return {"dx": dx, "dw": dw}
+
+
+def _grad_list(name: str, tensors, device):
+    arr = (BmoeTensor * len(tensors))()
+    for e, t in zip(arr, tensors):
+        if t.device != device or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous tensors on one device")
+        e.data, e.count, e.dtype = t.data_ptr(), t.numel(), dtype_code(t)
+    return arr
+
+
+def _grad_call(grads, out, stream):
+    grads = list(grads)
+    if not grads:
+        raise ValueError("no gradients")
+    dev = grads[0].device
+    arr = _grad_list("grads", grads, dev)
+    if out is None:
+        return grads, arr, None
+    out = list(out)
+    if len(out) != len(grads):
+        raise ValueError("out must have one tensor per gradient")
+    return grads, arr, _grad_list("out", out, dev)
+
+
+def grad_norm(grads, *, stream=None) -> torch.Tensor:
+    """fp32 scalar tensor: the 2-norm over all entries of all `grads` (fp32 or
+    bf16 tensors of one GPU), summed in 64 bits."""
+    grads, arr, _ = _grad_call(grads, None, stream)
+    with _at(grads[0], stream):
+        norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
+        ws = torch.empty(bmoe_grad_workspace_bytes(len(arr)), dtype=torch.uint8, device=norm.device)
+        _check(bmoe_grad_norm(len(arr), arr, norm, ws, stream), "bmoe_grad_norm")
+        return norm
+
+
+def scale_grads(grads, norm: torch.Tensor, max_norm: float, *, out=None, stream=None) -> None:
+    """grads * max_norm / norm where max_norm < norm < inf, in place or to
+    `out`: clip_grads() with a norm at hand (e.g. summed over ranks)."""
+    grads, arr, oarr = _grad_call(grads, out, stream)
+    _like("norm", norm, torch.float32, (), grads[0].device)
+    with _at(grads[0], stream):
+        _check(bmoe_grad_scale(len(arr), arr, oarr, norm, max_norm, stream), "bmoe_grad_scale")
+
+
+def clip_grads(grads, max_norm: float, *, out=None, stream=None) -> torch.Tensor:
+    """Scale `grads` so that their global 2-norm is at most max_norm, in place
+    or to `out` (tensors of the same types and sizes). Returns the norm before
+    clipping; one that is not finite leaves the gradients as they are."""
+    grads, arr, oarr = _grad_call(grads, out, stream)
+    with _at(grads[0], stream):
+        norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
+        ws = torch.empty(bmoe_grad_workspace_bytes(len(arr)), dtype=torch.uint8, device=norm.device)
+        _check(bmoe_grad_clip(len(arr), arr, oarr, max_norm, norm, ws, stream), "bmoe_grad_clip")
+        return norm

@@ -801,6 +801,7 @@ const char* bmoe_status_str(bmoe_status s) {
     case BMOE_E_WORKSPACE: return "workspace missing or too small";
     case BMOE_E_HIP: return "HIP runtime error";
     case BMOE_E_ALIGN: return "pointer not 16-byte aligned";
+    case BMOE_E_VALUE: return "argument outside its range, or written tensors that share memory";
   }
   return "unknown status";
 }

@@ -206,4 +206,51 @@ hipError_t launch_router_logits(bmoe_dtype dt, int T, int d, int N, const void* 
 hipError_t launch_topk(const float* logits, int T, int N, int k, int32_t* ids, float* gates,
                        hipStream_t s, const KernelTiming& t = {});
 
+// ---- routing from logits ---------------------------------------------------------
+// bmoe_route_spec, checked: 1 <= keep <= groups <= 64, groups divides N and
+// the kept groups hold at least k experts.
+struct RouteSpec {
+  int score, renorm;
+  float scale;
+  int groups, keep, group_score;
+};
+// ids, gates [T][k] from logits [T][N] (dtype dt) and bias [N] (may be NULL).
+hipError_t launch_route(bmoe_dtype dt, int T, int N, int k, const RouteSpec& sp,
+                        const void* logits, const float* bias, int32_t* ids, float* gates,
+                        hipStream_t s);
+// dlogits fp32 [T][N] from dgates [T][k].
+hipError_t launch_route_bwd(bmoe_dtype dt, int T, int N, int k, const RouteSpec& sp,
+                            const void* logits, const int32_t* ids, const float* dgates,
+                            float* dlogits, hipStream_t s);
+// load [N] = (accumulate ? load : 0) + counts of the M ids; bias (may be
+// NULL) [N] += rate * sign(sum(load) / N - load).
+hipError_t launch_balance(long long M, int N, const int32_t* ids, int accumulate, float rate,
+                          int32_t* load, float* bias, hipStream_t s);
+// Gradient of the router's product from dl [T][N]: dx = dx_add (may be NULL)
+// + dl W, dw [N][d] fp32 = dl^T x.
+hipError_t launch_router_bwd(bmoe_dtype dt, int T, int d, int N, const void* x, const void* w,
+                             const float* dl, const void* dx_add, void* dx, float* dw,
+                             hipStream_t s);
+
+// ---- gradient lists ----------------------------------------------------------------
+struct GradEntry {
+  const void* src;
+  void* dst;
+  size_t count;
+  int bf16;
+};
+constexpr int kGradTab = 112;     // entries per launch, in its kernel arguments
+constexpr int kGradParts = 1024;  // partial sums per launch, at most
+struct GradTable {
+  int n;
+  GradEntry t[kGradTab];
+};
+// Sums of squares of the table's tensors: *n_part partial sums to part.
+hipError_t launch_grad_sq(const GradTable& tab, double* part, int* n_part, hipStream_t s);
+// norm = sqrt(sum of part[0 .. n_part)), added in order.
+hipError_t launch_grad_norm(const double* part, int n_part, float* norm, hipStream_t s);
+// dst = src * (max_norm / norm where max_norm < norm < infinity, else 1).
+hipError_t launch_grad_scale(const GradTable& tab, const float* norm, float max_norm, int in_place,
+                             hipStream_t s);
+
 }  // namespace bmoe

@@ -58,7 +58,10 @@ typedef enum {
   BMOE_E_EXPERT = 5,     /* device: an expert id outside [0, N) */
   BMOE_E_WORKSPACE = 6,  /* workspace NULL or smaller than required */
   BMOE_E_HIP = 7,        /* a HIP runtime call failed */
-  BMOE_E_ALIGN = 8       /* a pointer is not 16-byte aligned */
+  BMOE_E_ALIGN = 8,      /* a pointer is not 16-byte aligned */
+  BMOE_E_VALUE = 9       /* a field of a bmoe_route_spec or a scalar argument
+                            outside its range, or gradient tensors that share
+                            memory where one of them is written */
 } bmoe_status;
 
 /* Storage of the shared substrate: 2-bit words (bmoe_pack_ternary) or the
@@ -399,6 +402,139 @@ bmoe_status bmoe_router(bmoe_dtype dt, int T, int d, int n_experts, int k, const
 bmoe_status bmoe_router_timed(bmoe_dtype dt, int T, int d, int n_experts, int k, const void* x,
                               const void* w_router, int32_t* ids, float* gates, float* logits,
                               void* ws, size_t ws_bytes, void* stream, void* const* events);
+
+/* The logits of bmoe_router alone (its first launch): fp32 [T][N]. */
+bmoe_status bmoe_router_logits(bmoe_dtype dt, int T, int d, int n_experts, const void* x,
+                               const void* w_router, float* logits, void* stream);
+
+/*
+ * Routing from logits, for the routers that bmoe_router does not cover: other
+ * scores, a bias that balances the experts' loads, expert groups and a choice
+ * of normalisation. For token t with logits l_e, e < N:
+ *   scores   s = softmax(l) over the N experts, or sigmoid(l) of each
+ *   choice   c_e = s_e + bias_e (bias NULL: 0); an expert with l_e = -inf is
+ *            masked: s_e = 0, c_e = -inf
+ *   groups   the experts in n_groups equal runs of consecutive ids; a group's
+ *            score is its largest c (BMOE_GROUP_MAX) or the sum of its two
+ *            largest (BMOE_GROUP_TOP2; masked experts left out, one alone
+ *            counts by itself, none is -inf). The topk_groups groups with the
+ *            largest score are kept, the lower group on ties.
+ *   ids      the k experts of the kept groups with the largest c, in
+ *            descending order, the lower id on ties
+ *   gates    scale * s_id, or with renorm scale * s_id / (sum of the k s)
+ * The choice and its order are those of the scores and sums taken in 64 bits;
+ * without a bias they are those of the logits (the scores rise with them).
+ * The k ids of a token are distinct and in [0, N) for any input: masked
+ * experts come after all others and have gate 0, and a token with nothing
+ * else has gates 0. A NaN logit (for the softmax also a +inf one) makes that
+ * token's gates NaN; experts with a NaN c come last.
+ *   dt      element type of logits [T][N].
+ *   spec    score, renorm, a finite scale, n_groups in [1, 64] that divides N,
+ *           topk_groups in [1, n_groups] with topk_groups * N / n_groups >= k
+ *           (BMOE_E_VALUE otherwise; n_groups = topk_groups = 1: no groups).
+ *   bias    fp32 [N] or NULL. It moves the choice only, never the gates.
+ *   ids     int32 [T][k], gates fp32 [T][k]: bmoe_forward's inputs.
+ * 1 <= N <= 4096, 1 <= k <= min(N, 64), T * k < 2^31. T = 0 is a no-op. No
+ * workspace.
+ */
+typedef enum { BMOE_SCORE_SOFTMAX = 0, BMOE_SCORE_SIGMOID = 1 } bmoe_score;
+typedef enum { BMOE_GROUP_MAX = 0, BMOE_GROUP_TOP2 = 1 } bmoe_group_score;
+typedef struct {
+  int score;       /* bmoe_score */
+  int renorm;      /* nonzero: the k gates of a token sum to scale */
+  float scale;
+  int n_groups, topk_groups;
+  int group_score; /* bmoe_group_score */
+} bmoe_route_spec;
+bmoe_status bmoe_route(bmoe_dtype dt, int T, int n_experts, int k, const bmoe_route_spec* spec,
+                       const void* logits, const float* bias, int32_t* ids, float* gates,
+                       void* stream);
+
+/*
+ * Gradient of bmoe_route's gates with respect to the logits (the choice is
+ * piecewise constant, so it, the bias and the groups have none): dlogits fp32
+ * [T][N], overwritten, from logits, ids and dgates fp32 [T][k]. Entries that
+ * no gate depends on are 0: all but the k chosen ones, except for softmax
+ * scores without renorm, where every score of the row moves every gate. An id
+ * outside [0, N) contributes nothing (a padded pick); an id listed twice adds
+ * up. T = 0 is a no-op.
+ */
+bmoe_status bmoe_route_backward(bmoe_dtype dt, int T, int n_experts, int k,
+                                const bmoe_route_spec* spec, const void* logits,
+                                const int32_t* ids, const float* dgates, float* dlogits,
+                                void* stream);
+
+/*
+ * Balance of the experts' loads without an auxiliary loss: counts the routed
+ * rows of each expert and moves the bias of the choice by one step against
+ * its load.
+ *   load  int32 [N]: overwritten with the counts of ids [T][k], or (accumulate
+ *         nonzero) those added to what it holds, for batches in parts.
+ *   bias  fp32 [N] or NULL (count only): bias_e += rate * sign(mean - load_e)
+ *         with the mean of the final loads over the N experts, compared
+ *         exactly. rate finite (BMOE_E_VALUE).
+ * An id outside [0, N) is not counted. T = 0 counts nothing (ids may be NULL)
+ * and still writes load and bias. Loads must stay below 2^31. ws: at least
+ * bmoe_route_balance_workspace_bytes().
+ */
+size_t bmoe_route_balance_workspace_bytes(int T, int n_experts, int k);
+bmoe_status bmoe_route_balance(int T, int n_experts, int k, const int32_t* ids, int accumulate,
+                               float rate, int32_t* load, float* bias, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/*
+ * Backward of the router (logits = x W_r^T, then bmoe_route): from dgates (of
+ * bmoe_backward) the gradients of x and of the router's weight.
+ *   x, w_router  as bmoe_router, logits fp32 [T][N] and ids as the forward's.
+ *   dx_add  [T][d] or NULL: added to the gradient (bmoe_backward's dx, so that
+ *           dx holds both); may be dx itself, and overlaps it in no other way.
+ *   dx      [T][d], dtype dt: dx_add + sum_e dl_te W_r[e], summed in fp32 and
+ *           rounded once.
+ *   dw      fp32 [N][d]: sum over t of dl_te x_t, the same bits each run.
+ * dl is bmoe_route_backward's dlogits (ids outside [0, N) contribute nothing).
+ * d a power of two in [16, 8192]; T = 0 leaves dx and sets dw to 0. ws: at
+ * least bmoe_router_backward_workspace_bytes().
+ */
+size_t bmoe_router_backward_workspace_bytes(bmoe_dtype dt, int T, int d, int n_experts, int k);
+bmoe_status bmoe_router_backward(bmoe_dtype dt, int T, int d, int n_experts, int k,
+                                 const bmoe_route_spec* spec, const void* x, const void* w_router,
+                                 const float* logits, const int32_t* ids, const float* dgates,
+                                 const void* dx_add, void* dx, float* dw, void* ws,
+                                 size_t ws_bytes, void* stream);
+
+/*
+ * Global norm of many gradients and clipping by it.
+ *   norm = sqrt(sum of g^2 over all entries of all tensors), fp32, summed in
+ *          64 bits (squares neither overflow nor vanish) in a fixed order
+ *   out  = g * max_norm / norm where max_norm < norm < infinity, else g
+ * A norm that is not finite clips nothing: the gradients pass through and the
+ * norm tells the caller.
+ *   grads  host array of n tensors: device pointer (aligned to its element),
+ *          count >= 0 entries, BMOE_F32 or BMOE_BF16. Read before the call
+ *          returns. bf16 results are rounded once.
+ *   out    host array of n tensors of the same types and counts, or NULL:
+ *          in place. An out tensor may be its own grad; any other sharing of
+ *          memory with a written tensor is refused (BMOE_E_VALUE).
+ *   norm   device fp32: written by bmoe_grad_norm and bmoe_grad_clip, read by
+ *          bmoe_grad_scale (where ranks hold parts of the gradients, each
+ *          takes bmoe_grad_norm, the squares are summed over the ranks, and
+ *          each scales by the root). bmoe_grad_clip is bmoe_grad_norm then
+ *          bmoe_grad_scale, bit for bit.
+ *   max_norm > 0 (BMOE_E_VALUE otherwise; +inf: never clips).
+ * ws: at least bmoe_grad_workspace_bytes(n), 16-byte aligned.
+ */
+typedef struct {
+  void* data;
+  size_t count;
+  bmoe_dtype dtype;
+} bmoe_tensor;
+size_t bmoe_grad_workspace_bytes(int n);
+bmoe_status bmoe_grad_norm(int n, const bmoe_tensor* grads, float* norm, void* ws, size_t ws_bytes,
+                           void* stream);
+bmoe_status bmoe_grad_scale(int n, const bmoe_tensor* grads, const bmoe_tensor* out,
+                            const float* norm, float max_norm, void* stream);
+bmoe_status bmoe_grad_clip(int n, const bmoe_tensor* grads, const bmoe_tensor* out, float max_norm,
+                           float* norm, void* ws, size_t ws_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* bmoe_status_str(bmoe_status s);
