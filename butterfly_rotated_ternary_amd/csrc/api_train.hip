@@ -45,6 +45,22 @@ bool pow2_d16(int d) { return d >= 16 && d <= 8192 && (d & (d - 1)) == 0; }
 
 size_t elem(bmoe_dtype dt) { return dt == BMOE_BF16 ? 2 : 4; }
 
+struct PairsLayout {
+  size_t list, off, part, total;
+  int tokens, ranges;
+};
+PairsLayout router_pairs_layout(int T, int d, int N, int k) {
+  PairsLayout l;
+  l.tokens = router_range_tokens(T, d, N);
+  l.ranges = T > 0 ? (T + l.tokens - 1) / l.tokens : 1;
+  const size_t list_bytes = up256((size_t)T * k * sizeof(int2));
+  l.list = list_bytes;
+  l.off = l.list + list_bytes;
+  l.part = l.off + up256((size_t)l.ranges * (N + 1) * sizeof(int32_t));
+  l.total = l.part + (l.ranges > 1 ? up256((size_t)l.ranges * N * d * sizeof(float)) : 0);
+  return l;
+}
+
 // The list of a gradient call: types, NULLs, alignment to the element, and
 // (where it is written) no two written tensors, and no written and another
 // read tensor, that share bytes. `out` may repeat `grads` entry by entry.
@@ -214,7 +230,10 @@ size_t bmoe_router_backward_workspace_bytes(bmoe_dtype dt, int T, int d, int n_e
       n_experts > kMaxExperts || k < 1 || k > n_experts || k > kMaxPicks || T < 0 ||
       (long long)T * k > INT_MAX)
     return 0;
-  return up256((size_t)T * n_experts * sizeof(float)) + 256;
+  // dl [T][N], or the picks' pairs and lists and the dW of the token ranges
+  const size_t dense = up256((size_t)T * n_experts * sizeof(float));
+  const size_t sparse = router_pairs_layout(T, d, n_experts, k).total;
+  return (dense > sparse ? dense : sparse) + 256;
 }
 
 bmoe_status bmoe_router_backward(bmoe_dtype dt, int T, int d, int n_experts, int k,
@@ -234,6 +253,21 @@ bmoe_status bmoe_router_backward(bmoe_dtype dt, int T, int d, int n_experts, int
   for (const void* p : ptrs)
     if (!ok16(p)) return BMOE_E_ALIGN;
   hipStream_t s = static_cast<hipStream_t>(stream);
+  if (T > 0 && !(sp.score == BMOE_SCORE_SOFTMAX && !sp.renorm)) {
+    const PairsLayout l = router_pairs_layout(T, d, n_experts, k);
+    char* base = static_cast<char*>(ws);
+    RouterPairs rp;
+    rp.pairs = reinterpret_cast<int2*>(base);
+    rp.list = reinterpret_cast<int2*>(base + l.list);
+    rp.off = reinterpret_cast<int32_t*>(base + l.off);
+    rp.tokens = l.tokens;
+    rp.ranges = l.ranges;
+    if (launch_route_pairs(T, n_experts, k, sp, logits, ids, dgates, rp, s) != hipSuccess ||
+        launch_router_bwd_sparse(dt, T, d, n_experts, k, x, w_router, rp, dx_add, dx, dw,
+                                 reinterpret_cast<float*>(base + l.part), s) != hipSuccess)
+      return BMOE_E_HIP;
+    return BMOE_OK;
+  }
   float* dl = static_cast<float*>(ws);
   if (T > 0 &&
       launch_route_bwd(BMOE_F32, T, n_experts, k, sp, logits, ids, dgates, dl, s) != hipSuccess)

@@ -226,6 +226,27 @@ hipError_t launch_route_bwd(bmoe_dtype dt, int T, int N, int k, const RouteSpec&
 // NULL) [N] += rate * sign(sum(load) / N - load).
 hipError_t launch_balance(long long M, int N, const int32_t* ids, int accumulate, float rate,
                           int32_t* load, float* bias, hipStream_t s);
+// dl as k pairs (expert id, coefficient's bits) per token, for the specs under
+// which only the picks move (not softmax without renorm), and the same by
+// range of `tokens` tokens and expert: list entries (token, coefficient) of
+// expert e of range r at off[r][e] .. off[r][e + 1], in token order. A pick
+// outside the experts, or whose coefficient is 0, has coefficient 0 in pairs
+// and is not listed. T >= 1.
+struct RouterPairs {
+  int2* pairs;   // [T][k]
+  int2* list;    // [T * k]
+  int32_t* off;  // [ranges][N + 1]
+  int tokens, ranges;
+};
+int router_range_tokens(int T, int d, int N);
+hipError_t launch_route_pairs(int T, int N, int k, const RouteSpec& sp, const float* logits,
+                              const int32_t* ids, const float* dgates, const RouterPairs& rp,
+                              hipStream_t s);
+// The router product's gradient from them; part: fp32 [ranges][N][d] scratch
+// (unused with one range).
+hipError_t launch_router_bwd_sparse(bmoe_dtype dt, int T, int d, int N, int k, const void* x,
+                                    const void* w, const RouterPairs& rp, const void* dx_add,
+                                    void* dx, float* dw, float* part, hipStream_t s);
 // Gradient of the router's product from dl [T][N]: dx = dx_add (may be NULL)
 // + dl W, dw [N][d] fp32 = dl^T x.
 hipError_t launch_router_bwd(bmoe_dtype dt, int T, int d, int N, const void* x, const void* w,

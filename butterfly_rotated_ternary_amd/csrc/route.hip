@@ -181,6 +181,26 @@ __global__ __launch_bounds__(256) void route_kernel(const T* logits, const float
 }
 
 // ---- gradient of the gates --------------------------------------------------------
+// What pick (id, u) of its LPT lanes' token adds to dl[id], for the specs
+// under which only the picks move. l: the pick's logit, -inf for no pick.
+template <int LPT>
+__device__ __forceinline__ double pick_grad(double l, double u, const RouteSpec& sp) {
+  const bool softmax = sp.score == BMOE_SCORE_SOFTMAX;
+  double v;
+  if (sp.renorm) {
+    const double mc = sub_max<LPT>(l);
+    const double shift = softmax ? mc : fmin(mc, 0.0);
+    const double w = l == -INFINITY ? 0.0 : softmax ? exp(l - shift) : sigmoid_shifted(l, shift);
+    const double sum = sub_sum<LPT>(w);
+    const double p = sum > 0.0 ? w / sum : 0.0;
+    v = p * (u - sub_sum<LPT>(u * p));
+    if (!softmax) v *= 1.0 / (1.0 + exp(l));
+  } else {
+    v = u * (1.0 / (1.0 + exp(-l))) * (1.0 / (1.0 + exp(l)));
+  }
+  return l == -INFINITY ? 0.0 : v;
+}
+
 // One wave per token; lane j < k holds pick j. With u_j the gates' gradient
 // times scale:
 //   renormalised:  dl_j = p_j (u_j - sum_i u_i p_i) [ (1 - s_j) ],  p = s / sum
@@ -201,21 +221,10 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const i
   const bool pick = id >= 0 && id < N;
   const float l = pick ? ld_logit(row + id) : -INFINITY;
   const float u = pick ? sp.scale * dgates[tok * k + lane] : 0.f;
-  double m = -INFINITY, total = 0.0, v;  // v: this pick's dl, or its u * s below
+  double m = -INFINITY, total = 0.0, v = u;  // v: this pick's dl, or (dense) its u
   const bool dense = softmax && !sp.renorm;
-  if (sp.renorm) {
-    const double mc = sub_max<64>((double)l);
-    const double shift = softmax ? mc : fmin(mc, 0.0);
-    const double w = l == -INFINITY ? 0.0
-                     : softmax ? exp((double)l - shift) : sigmoid_shifted((double)l, shift);
-    const double sum = sub_sum<64>(w);
-    const double p = sum > 0.0 ? w / sum : 0.0;
-    const double d = sub_sum<64>(u * p);
-    v = p * (u - d);
-    if (!softmax) v *= 1.0 / (1.0 + exp((double)l));
-  } else if (!softmax) {
-    const double s = 1.0 / (1.0 + exp(-(double)l));
-    v = u * s * (1.0 / (1.0 + exp((double)l)));
+  if (!dense) {
+    v = pick_grad<64>((double)l, (double)u, sp);
   } else {
     for (int e = lane; e < N; e += 64) m = fmax(m, (double)ld_logit(row + e));
     m = sub_max<64>(m);
@@ -224,7 +233,6 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const i
       total += x == -INFINITY ? 0.0 : exp(x - m);
     }
     total = sub_sum<64>(total);
-    v = u;
   }
   if (!pick || l == -INFINITY) v = 0.0;
   double d = 0.0;
@@ -242,6 +250,88 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const i
       a = x == -INFINITY ? 0.0 : exp(x - m) / total * (a - d);
     }
     out[e] = (float)a;
+  }
+}
+
+// The picks' (id, coefficient) pairs of one range of tokens, and the same
+// listed by expert (stable): one workgroup per range. Each wave owns a
+// contiguous share of the range's picks; equal experts within 64 picks are
+// ranked by ballots over the id's bits.
+template <int LPT, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void route_pairs_kernel(
+    const float* logits, const int32_t* ids, const float* dgates, int T_, int N, int k, int nbits,
+    RouteSpec sp, RouterPairs rp) {
+  extern __shared__ int cur[];  // [WAVES][N]: counts, then cursors
+  __shared__ int wsum[WAVES];
+  constexpr int kThreads = WAVES * 64;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const size_t t0 = (size_t)blockIdx.x * rp.tokens;
+  const int nt = (int)min((size_t)rp.tokens, (size_t)T_ - t0);
+  for (int i = tid; i < WAVES * N; i += kThreads) cur[i] = 0;
+  const int q = tid % LPT;
+  for (int i = tid / LPT; i - tid / LPT < nt; i += kThreads / LPT) {
+    const size_t tok = t0 + i;
+    const bool mine = i < nt && q < k;
+    const int id = mine ? ids[tok * k + q] : -1;
+    const bool pick = id >= 0 && id < N;
+    const float l = pick ? logits[tok * N + id] : -INFINITY;
+    const float u = pick ? sp.scale * dgates[tok * k + q] : 0.f;
+    const float v = (float)pick_grad<LPT>((double)l, (double)u, sp);
+    if (mine) rp.pairs[tok * k + q] = make_int2(pick ? id : 0, __float_as_int(pick ? v : 0.f));
+  }
+  __syncthreads();
+
+  const int M = nt * k;
+  const int2* pairs = rp.pairs + t0 * k;
+  const int share = ((M + WAVES - 1) / WAVES + 63) / 64 * 64;
+  const int wb = min(M, wave * share), we = min(M, wb + share);
+  int* mycur = cur + wave * N;
+  for (int r = wb + lane; r < we; r += 64) {
+    const int2 p = pairs[r];
+    if (__int_as_float(p.y) != 0.f) atomicAdd(&mycur[p.x], 1);
+  }
+  __syncthreads();
+  // exclusive scan over (expert, wave); a thread owns consecutive experts
+  const int per = (N + kThreads - 1) / kThreads;
+  const int lo = min(N, tid * per), hi = min(N, lo + per);
+  int seg = 0;
+  for (int e = lo; e < hi; ++e)
+    for (int w = 0; w < WAVES; ++w) seg += cur[w * N + e];
+  const int incl = wave_incl_scan(seg);
+  if (lane == 63) wsum[wave] = incl;
+  __syncthreads();
+  int run = (int)(t0 * k) + incl - seg;
+  for (int w = 0; w < wave; ++w) run += wsum[w];
+  int32_t* off = rp.off + (size_t)blockIdx.x * (N + 1);
+  for (int e = lo; e < hi; ++e) {
+    off[e] = run;
+    for (int w = 0; w < WAVES; ++w) {
+      const int c = cur[w * N + e];
+      cur[w * N + e] = run;
+      run += c;
+    }
+  }
+  if (tid == kThreads - 1) off[N] = run;
+  __syncthreads();
+  const uint64_t lt = (1ull << lane) - 1;
+  for (int base = wb; base < we; base += 64) {
+    const int r = base + lane;
+    const int2 p = r < we ? pairs[r] : make_int2(0, 0);
+    const bool valid = r < we && __int_as_float(p.y) != 0.f;
+    uint64_t mask = __ballot(valid);
+    for (int b = 0; b < nbits; ++b) {
+      const bool bit = (p.x >> b) & 1;
+      const uint64_t bal = __ballot(bit);
+      mask &= bit ? bal : ~bal;
+    }
+    const int rank = __popcll(mask & lt), grp = __popcll(mask);
+    const int at = valid ? mycur[p.x] : 0;
+    __builtin_amdgcn_wave_barrier();
+    if (valid) {
+      rp.list[at + rank] = make_int2((int)(t0 + r / k), p.y);
+      if (rank == grp - 1) mycur[p.x] = at + grp;
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -309,6 +399,27 @@ hipError_t launch_route_bwd(bmoe_dtype dt, int T, int N, int k, const RouteSpec&
                          static_cast<const uint16_t*>(logits), ids, dgates, T, N, k, sp, dlogits);
   return launch_kernel(route_bwd_kernel<float>, grid, block, 0, s, KernelTiming{},
                        static_cast<const float*>(logits), ids, dgates, T, N, k, sp, dlogits);
+}
+
+hipError_t launch_route_pairs(int T, int N, int k, const RouteSpec& sp, const float* logits,
+                              const int32_t* ids, const float* dgates, const RouterPairs& rp,
+                              hipStream_t s) {
+  int nbits = 0;
+  while ((1 << nbits) < N) ++nbits;
+  // 16 waves while their cursors take 32 KB at most, else 4 (64 KB at 4096)
+#define BMOE_PAIRS(LPT)                                                                        \
+  return N <= 512 ? launch_kernel(route_pairs_kernel<LPT, 16>, dim3(rp.ranges), dim3(1024),    \
+                                  16 * N * 4, s, KernelTiming{}, logits, ids, dgates, T, N, k, \
+                                  nbits, sp, rp)                                               \
+                  : launch_kernel(route_pairs_kernel<LPT, 4>, dim3(rp.ranges), dim3(256),      \
+                                  4 * N * 4, s, KernelTiming{}, logits, ids, dgates, T, N, k,  \
+                                  nbits, sp, rp)
+  if (k <= 2) BMOE_PAIRS(2);
+  if (k <= 4) BMOE_PAIRS(4);
+  if (k <= 8) BMOE_PAIRS(8);
+  if (k <= 16) BMOE_PAIRS(16);
+  BMOE_PAIRS(64);
+#undef BMOE_PAIRS
 }
 
 hipError_t launch_balance(long long M, int N, const int32_t* ids, int accumulate, float rate,

@@ -90,6 +90,167 @@ __global__ __launch_bounds__(256) void router_dw_kernel(const float* dl, const T
     }
 }
 
+// ---- sparse dl -------------------------------------------------------------------
+// Where only the k picks of a token move (every spec but softmax without
+// renorm), dl is k pairs (id, coefficient) per token: 4 T k d flops instead of
+// 4 T N d, no rounding of dl, rows of W and of dW picked by id. The tokens are
+// cut into ranges; within each the pairs are also listed by expert, in token
+// order (launch_route_pairs). One launch does both products:
+//
+// dx: a thread takes 16 bytes of a row; the k rows of W come from L2.
+// dW: a workgroup takes one expert, one range and up to 64 V columns (V values
+//     per 16 bytes). Its row slots (4, more where a row is narrower than a
+//     wave) walk the expert's list a slot apart, each lane with V sums in
+//     registers; the slots' sums are added in slot order through LDS, the
+//     ranges' by the join kernel, so the order of every sum is fixed. The
+//     workgroups of a range run together and all walk the tokens upwards, so
+//     the k readers of a row of x meet in L2.
+template <typename T>
+struct SparseArgs {
+  const int2* pairs;   // [T][k]
+  const int2* list;    // (token, coefficient), by range and expert
+  const int32_t* off;  // [ranges][N + 1] into list
+  const T* x;
+  const T* w;
+  const T* dx_add;
+  T* dx;
+  float* dw;  // [ranges][N][d] (one range: the result itself)
+  int T_, d, N, k;
+  int chunks, n_dw_blocks;  // column chunks of a row; workgroups of the dW role
+};
+
+template <typename T, bool WIDE>
+__device__ __forceinline__ void sparse_dw(const SparseArgs<T>& p, float* sums) {
+  constexpr int V = 16 / sizeof(T);
+  const int chunk = blockIdx.x % p.chunks, re = blockIdx.x / p.chunks;
+  const int e = re % p.N, range = re / p.N;
+  const int lpr = WIDE ? 64 : p.d / V;  // lanes per row
+  const int slots = 256 / lpr;
+  const int slot = WIDE ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : threadIdx.x / lpr;
+  const int col = threadIdx.x % lpr * V;
+  const int c = chunk * 64 * V + col;
+  const int32_t* off = p.off + (size_t)range * (p.N + 1) + e;
+  const int lo = off[0], hi = off[1];
+  const T* x = p.x + c;
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  constexpr int kU = 8;  // rows in flight per lane
+  int q = lo + slot;
+  for (; q + (kU - 1) * slots < hi; q += kU * slots) {
+    int2 ent[kU];
+    float v[kU][V];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) ent[u] = p.list[q + u * slots];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) load16(x + (size_t)ent[u].x * p.d, v[u]);
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = fmaf(__int_as_float(ent[u].y), v[u][i], acc[i]);
+  }
+  for (; q < hi; q += slots) {
+    const int2 ent = p.list[q];
+    float v[V];
+    load16(x + (size_t)ent.x * p.d, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = fmaf(__int_as_float(ent.y), v[i], acc[i]);
+  }
+  // sums[slot][col]
+  const int cols = lpr * V;
+#pragma unroll
+  for (int i = 0; i < V; ++i) sums[slot * cols + col + i] = acc[i];
+  __syncthreads();
+  float* dst = p.dw + ((size_t)range * p.N + e) * p.d + chunk * 64 * V;
+  for (int i = threadIdx.x; i < cols; i += 256) {
+    float a = sums[i];
+    for (int r = 1; r < slots; ++r) a += sums[r * cols + i];
+    dst[i] = a;
+  }
+}
+
+template <typename T, bool WIDE>
+__device__ __forceinline__ void sparse_dx(const SparseArgs<T>& p, unsigned block) {
+  constexpr int V = 16 / sizeof(T);
+  const int per_row = p.d / V;
+  const size_t u = (size_t)block * 256 + threadIdx.x;
+  if (u >= (size_t)p.T_ * per_row) return;
+  size_t t = u / per_row;
+  // a wave's 64 threads share a row: its pairs come as scalars
+  if (WIDE) t = (size_t)__builtin_amdgcn_readfirstlane((int)t);
+  const int c = (int)(u % per_row) * V;
+  float acc[V], v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  for (int j = 0; j < p.k; ++j) {
+    const int2 pr = p.pairs[t * p.k + j];
+    const float f = __int_as_float(pr.y);
+    if (f == 0.f) continue;
+    load16(p.w + (size_t)pr.x * p.d + c, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = fmaf(f, v[i], acc[i]);
+  }
+  if (p.dx_add) {
+    load16(p.dx_add + t * p.d + c, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] += v[i];
+  }
+  store16(acc, p.dx + t * p.d + c, 1.f);
+}
+
+template <typename T, bool WIDE>
+__global__ __launch_bounds__(256) void router_sparse_kernel(SparseArgs<T> p) {
+  __shared__ float sums[256 * (16 / sizeof(T))];
+  if ((int)blockIdx.x < p.n_dw_blocks) sparse_dw<T, WIDE>(p, sums);
+  else sparse_dx<T, WIDE>(p, blockIdx.x - p.n_dw_blocks);
+}
+
+// dw = the ranges' sums, added in order.
+__global__ __launch_bounds__(256) void router_dw_join_kernel(const float4* part, int S, size_t n4,
+                                                             float4* dw) {
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  float4 a = part[i];
+#pragma unroll 4
+  for (int s = 1; s < S; ++s) {
+    const float4 b = part[(size_t)s * n4 + i];
+    a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+  }
+  dw[i] = a;
+}
+
+template <typename T>
+hipError_t sparse_t(int Tn, int d, int N, int k, const T* x, const T* w, const RouterPairs& rp,
+                    const T* dx_add, T* dx, float* dw, float* part, hipStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  SparseArgs<T> p;
+  p.pairs = rp.pairs;
+  p.list = rp.list;
+  p.off = rp.off;
+  p.x = x;
+  p.w = w;
+  p.dx_add = dx_add;
+  p.dx = dx;
+  p.dw = rp.ranges == 1 ? dw : part;
+  p.T_ = Tn;
+  p.d = d;
+  p.N = N;
+  p.k = k;
+  p.chunks = (d + 64 * V - 1) / (64 * V);
+  p.n_dw_blocks = p.chunks * N * rp.ranges;
+  const size_t units = (size_t)Tn * (d / V);
+  const dim3 grid((unsigned)(p.n_dw_blocks + (units + 255) / 256));
+  hipError_t e = d >= 64 * V ? launch_kernel(router_sparse_kernel<T, true>, grid, dim3(256), 0, s,
+                                             KernelTiming{}, p)
+                             : launch_kernel(router_sparse_kernel<T, false>, grid, dim3(256), 0, s,
+                                             KernelTiming{}, p);
+  if (e != hipSuccess || rp.ranges == 1) return e;
+  const size_t n4 = (size_t)N * d / 4;
+  return launch_kernel(router_dw_join_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s,
+                       KernelTiming{}, reinterpret_cast<const float4*>(part), rp.ranges, n4,
+                       reinterpret_cast<float4*>(dw));
+}
+
 template <typename T>
 hipError_t bwd_t(int Tn, int d, int N, const T* x, const T* w, const float* dl, const T* dx_add,
                  T* dx, float* dw, hipStream_t s) {
@@ -103,6 +264,26 @@ hipError_t bwd_t(int Tn, int d, int N, const T* x, const T* w, const float* dl, 
 }
 
 }  // namespace
+
+// Tokens per range: 4096 at most, and shorter (down to 128) until the dW role
+// has 2048 workgroups.
+int router_range_tokens(int T, int d, int N) {
+  const int chunks = (d + 511) / 512;
+  int r = 4096;
+  while (r > 128 && (long long)((T + r - 1) / r) * N * chunks < 2048) r /= 2;
+  return r;
+}
+
+hipError_t launch_router_bwd_sparse(bmoe_dtype dt, int T, int d, int N, int k, const void* x,
+                                    const void* w, const RouterPairs& rp, const void* dx_add,
+                                    void* dx, float* dw, float* part, hipStream_t s) {
+  if (dt == BMOE_BF16)
+    return sparse_t(T, d, N, k, static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w),
+                    rp, static_cast<const uint16_t*>(dx_add), static_cast<uint16_t*>(dx), dw, part,
+                    s);
+  return sparse_t(T, d, N, k, static_cast<const float*>(x), static_cast<const float*>(w), rp,
+                  static_cast<const float*>(dx_add), static_cast<float*>(dx), dw, part, s);
+}
 
 hipError_t launch_router_bwd(bmoe_dtype dt, int T, int d, int N, const void* x, const void* w,
                              const float* dl, const void* dx_add, void* dx, float* dw,
