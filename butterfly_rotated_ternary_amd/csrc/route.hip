@@ -96,16 +96,9 @@ __device__ __forceinline__ uint64_t own_bits(uint64_t ballot) {
 // ---- order-preserving keys -----------------------------------------------------
 // Unsigned integers in the order of the reals: 0 = not a candidate (taken, or
 // of a group that is not kept), 1 = NaN (after -inf), -0 = +0.
-__device__ __forceinline__ uint32_t key_of(float c) {
-  const int32_t b = __float_as_int(c + 0.f);
-  return c != c ? 1u : (uint32_t)b ^ ((uint32_t)(b >> 31) | 0x80000000u);
-}
 __device__ __forceinline__ uint64_t key_of(double c) {
   const int64_t b = __double_as_longlong(c + 0.0);
   return c != c ? 1ull : (uint64_t)b ^ ((uint64_t)(b >> 63) | 0x8000000000000000ull);
-}
-__device__ __forceinline__ float value_of(uint32_t k) {
-  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
 // ---- scores ----------------------------------------------------------------------
@@ -113,15 +106,12 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 // product with log2 e, that constant, the unit's last place); a difference v
 // brings |v| 2^-24 more.
 __device__ __forceinline__ float exp_of(float v) { return __builtin_amdgcn_exp2f(v * kLog2e); }
-__device__ __forceinline__ double exp_of(double v) { return exp(v); }
 __device__ __forceinline__ float inv_of(float v) { return __builtin_amdgcn_rcpf(v); }
-__device__ __forceinline__ double inv_of(double v) { return 1.0 / v; }
 
 // Sigmoid of l times e^(-shift), shift <= 0 and 0 unless every l of interest
 // is negative: ratios of such scores keep their bits where all are tiny.
-template <typename R>
-__device__ __forceinline__ R sigmoid_shifted(R l, R shift) {
-  return l >= R(0) ? inv_of(R(1) + exp_of(-l)) : exp_of(l - shift) * inv_of(R(1) + exp_of(l));
+__device__ __forceinline__ float sigmoid_shifted(float l, float shift) {
+  return l >= 0.f ? inv_of(1.f + exp_of(-l)) : exp_of(l - shift) * inv_of(1.f + exp_of(l));
 }
 
 template <typename T>
@@ -130,18 +120,22 @@ __device__ __forceinline__ float ld_logit(const T* p) {
   else return *p;
 }
 
-// This lane's PER consecutive values of a row of n from `base` on, `fill`
-// past its end. VEC: n is a multiple of the vector's length.
+// This lane's values p[0 .. cnt), cnt <= PER, `fill` past them. VEC: p is
+// aligned to, and cnt a multiple of, the vector's length.
 template <int PER, bool VEC, typename T>
-__device__ __forceinline__ void ld_row(const T* row, int base, int n, float fill,
-                                       float (&v)[PER]) {
+__device__ __forceinline__ void ld_row(const T* src, int cnt, float fill, float (&v)[PER]) {
   constexpr int W = 16 / sizeof(T) < PER ? 16 / sizeof(T) : PER;  // values per load
   if constexpr (VEC && W > 1) {
 #pragma unroll
     for (int i = 0; i < PER; i += W) {
-      const bool in = base + i < n;
-      const T* p = row + (in ? base + i : 0);
       float f[W];
+      const T* p = src + i;
+      const bool in = i < cnt;
+      if (!in) {
+#pragma unroll
+        for (int u = 0; u < W; ++u) v[i + u] = fill;
+        continue;
+      }
       if constexpr (sizeof(T) == 4) {
         if constexpr (W == 4) {
           const float4 x = *reinterpret_cast<const float4*>(p);
@@ -168,165 +162,256 @@ __device__ __forceinline__ void ld_row(const T* row, int base, int n, float fill
         }
       }
 #pragma unroll
-      for (int u = 0; u < W; ++u) v[i + u] = in ? f[u] : fill;
+      for (int u = 0; u < W; ++u) v[i + u] = f[u];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const bool in = base + i < n;
-      const float f = ld_logit(row + (in ? base + i : 0));
-      v[i] = in ? f : fill;
+      v[i] = fill;
+      if (i < cnt) v[i] = ld_logit(src + i);
     }
   }
 }
 
 // ---- the choice ------------------------------------------------------------------
-// k picks of one token by its LPT lanes, PER experts per lane (lane q holds
-// experts q PER ... q PER + PER - 1, so the lowest lane has the lowest ids).
-// Returns pick j's id in lane j. In fp32 (R = float) scores are a few units
-// off, so *unsure is set for a token whose picks, or kept groups, are not
-// further apart than the errors allow (bounded below); the caller then decides
-// that token with R = double. Without a bias the keys are the logits
-// themselves and nothing is unsure but sums of two scores.
-template <int LPT, int PER, typename R, typename T>
-__device__ __forceinline__ int choose(const T* row, const float* bias, const float (&l)[PER],
-                                      const float (&b)[PER], int base, int N, int k,
-                                      const RouteSpec& sp, float lmax, bool* unsure) {
-  constexpr bool kFast = sizeof(R) == 4;
-  using K = decltype(key_of(R(0)));
-  const bool biased = bias != nullptr;
-  const int q = threadIdx.x % LPT;
+// A token's lanes and its experts: LPT lanes, PER consecutive experts per lane.
+// With groups, a group takes lpg lanes (a power of two), so its lanes hold no
+// other group's experts; the lowest lanes still hold the lowest ids.
+struct LaneMap {
+  int lpg;  // lanes per group; 0: the map does not fit, every token goes the exact way
+};
+template <int LPT, int PER>
+LaneMap lane_map(int N, int groups) {
+  LaneMap m;
+  const int size = N / groups;
+  m.lpg = 1;
+  while (m.lpg * PER < size && m.lpg < LPT) m.lpg *= 2;
+  if (groups == 1) m.lpg = LPT;
+  if (m.lpg * PER < size || groups * m.lpg > LPT) m.lpg = 0;
+  return m;
+}
+
+// Group scores from the lanes' two largest choices: (a, a2) over `lpg` lanes.
+template <int LPT>
+__device__ __forceinline__ void top2_lanes(float& a, float& a2, int lpg) {
+  auto merge = [&](uint32_t ob, uint32_t ob2) {
+    const float o = __uint_as_float(ob), o2 = __uint_as_float(ob2);
+    a2 = fmaxf(fminf(a, o), fmaxf(a2, o2));
+    a = fmaxf(a, o);
+  };
+  if (lpg > 1) merge(partner<1>(__float_as_uint(a)), partner<1>(__float_as_uint(a2)));
+  if (lpg > 2) merge(partner<2>(__float_as_uint(a)), partner<2>(__float_as_uint(a2)));
+  if (lpg > 4) merge(partner<4>(__float_as_uint(a)), partner<4>(__float_as_uint(a2)));
+  if (lpg > 8) merge(partner<8>(__float_as_uint(a)), partner<8>(__float_as_uint(a2)));
+  if constexpr (LPT == 64) {
+    if (lpg > 16) merge(__shfl_xor(__float_as_uint(a), 16, 64), __shfl_xor(__float_as_uint(a2), 16, 64));
+    if (lpg > 32) merge(__shfl_xor(__float_as_uint(a), 32, 64), __shfl_xor(__float_as_uint(a2), 32, 64));
+  }
+}
+
+// The picks of one token in 64 bits, by a whole wave: lane q holds experts
+// q PER ... q PER + PER - 1. Returns pick j's id in lane j.
+template <int PER, typename T>
+__device__ int choose_exact(const T* row, const float* bias, int N, int k, const RouteSpec& sp) {
+  const int q = threadIdx.x & 63, base = q * PER;
   const bool softmax = sp.score == BMOE_SCORE_SOFTMAX;
-  const bool scored = biased || (sp.groups > 1 && sp.group_score == BMOE_GROUP_TOP2);
-  const R m = softmax ? (R)lmax : R(0);
-  // A score s of a logit at distance x from m is off by s u (3 |x| + A) at
-  // most: the difference, its product with log2 e and that constant, then the
-  // exponential's, sum's (PER + 6 additions) and quotient's last places.
-  constexpr float kA = PER + 24;
-  R c[PER], smax = R(1);
-  if (scored) {
-    R inv = R(1);
+  double c[PER], m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      c[i] = softmax ? (l[i] == -INFINITY ? R(0) : exp_of((R)l[i] - m))
-                     : inv_of(R(1) + exp_of(-(R)l[i]));
+  for (int i = 0; i < PER; ++i) {
+    c[i] = base + i < N ? (double)ld_logit(row + base + i) : -INFINITY;
+    m = fmax(m, c[i]);
+  }
+  if (bias || (sp.groups > 1 && sp.group_score == BMOE_GROUP_TOP2)) {
+    double total = 1.0;
     if (softmax) {
-      R total = R(0);
+      m = sub_max<64>(m);
+      total = 0.0;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) total += c[i];
-      inv = R(1) / sub_sum<LPT>(total);
-      smax = inv;
+      for (int i = 0; i < PER; ++i) total += c[i] == -INFINITY ? 0.0 : exp(c[i] - m);
+      total = sub_sum<64>(total);
     }
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      c[i] = l[i] == -INFINITY ? R(-INFINITY) : c[i] * inv + (R)b[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) c[i] = (R)l[i];
+    for (int i = 0; i < PER; ++i) {
+      const double s = softmax ? exp(c[i] - m) / total : 1.0 / (1.0 + exp(-c[i]));
+      c[i] = c[i] == -INFINITY ? -INFINITY
+                               : s + (bias && base + i < N ? (double)bias[base + i] : 0.0);
+    }
   }
-
   uint64_t keep = 1;  // bit g: group g is kept
   const int size = N / sp.groups;
   if (sp.groups > 1) {
-    R mine = R(-INFINITY), slack = R(0);  // lane g: the score of group g, its error
+    double mine = -INFINITY;  // lane g: the score of group g
     for (int g = 0; g < sp.groups; ++g) {
-      R a = R(-INFINITY), a2 = R(-INFINITY);  // the two largest
+      double a = -INFINITY, a2 = -INFINITY;  // the two largest
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const R v = base + i >= g * size && base + i < (g + 1) * size ? c[i] : R(-INFINITY);
+        const double v = base + i >= g * size && base + i < (g + 1) * size ? c[i] : -INFINITY;
         if (v > a) { a2 = a; a = v; }
         else if (v > a2) a2 = v;
       }
-#pragma unroll
-      for (int o = LPT / 2; o >= 1; o >>= 1) {
-        const R oa = __shfl_xor(a, o, 64), ob = __shfl_xor(a2, o, 64);
+      for (int o = 32; o >= 1; o >>= 1) {
+        const double oa = __shfl_xor(a, o, 64), ob = __shfl_xor(a2, o, 64);
         a2 = fmax(fmin(a, oa), a > oa ? a2 : ob);
         a = fmax(a, oa);
       }
-      const bool one = sp.group_score == BMOE_GROUP_MAX || a2 == R(-INFINITY);
-      if (q == g) {
-        mine = one ? a : a + a2;
-        if (kFast && scored)
-          slack = R(kU) * (R(2) * smax * R(kA + 1.f) + R(3) * (fabs(a) + (one ? R(0) : fabs(a2))));
-      }
+      if (q == g) mine = sp.group_score == BMOE_GROUP_MAX || a2 == -INFINITY ? a : a + a2;
     }
     int rank = 0;
     for (int h = 0; h < sp.groups; ++h) {
-      const R v = __shfl(mine, (threadIdx.x & 63) / LPT * LPT + h, 64);
+      const double v = __shfl(mine, h, 64);
       rank += v > mine || (v == mine && h < q);
     }
-    const bool kept = q < sp.groups && rank < sp.keep;
-    keep = own_bits<LPT>(__ballot(kept));
-    if constexpr (kFast) {
-      if (scored) {
-        // the lowest that a kept group, and the highest that another can be
-        const float lowest = -sub_max<LPT>(kept ? -(mine - slack) : -INFINITY);
-        const float highest =
-            sub_max<LPT>(q < sp.groups && !kept ? mine + slack : -INFINITY);
-        *unsure |= !(lowest > highest);
-      }
-    }
+    keep = __ballot(q < sp.groups && rank < sp.keep);
   }
-
-  K key[PER];
+  uint64_t key[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = base + i;
     const bool in = e < N && (sp.groups == 1 || (keep >> (e / size) & 1u));
-    key[i] = in ? key_of(biased ? c[i] : (R)l[i]) : K(0);
+    // without a bias the experts' order is that of their logits
+    key[i] = !in ? 0 : bias ? key_of(c[i]) : key_of((double)ld_logit(row + e));
   }
-
-  // k rounds: the largest key, the lower id on ties
   int id = 0;
-  K top = 0;
   for (int j = 0; j < k; ++j) {
-    K best = key[0];
+    uint64_t best = 0;
 #pragma unroll
-    for (int i = 1; i < PER; ++i) best = key[i] > best ? key[i] : best;
-    best = sub_max<LPT>(best);
+    for (int i = 0; i < PER; ++i) best = key[i] > best ? key[i] : best;
+    best = sub_max<64>(best);
     uint32_t at = 0x7fffffff;
 #pragma unroll
     for (int i = PER - 1; i >= 0; --i) at = key[i] == best ? (uint32_t)(base + i) : at;
-    at = sub_min<LPT>(at);
+    at = sub_min<64>(at);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = at == (uint32_t)(base + i) ? K(0) : key[i];
-    if (q == j) {
-      id = (int)at;
-      top = best;
+    for (int i = 0; i < PER; ++i) key[i] = at == (uint32_t)(base + i) ? 0 : key[i];
+    if (q == j) id = (int)at;
+  }
+  return id;
+}
+
+// The picks in fp32: pick j's id in lane j. *unsure is set for a token whose
+// picks, or kept groups, are not further apart than the errors allow (bounded
+// below), or that has no k finite choices: it goes the exact way. Without a
+// bias the choices are the logits themselves, and only sums of two scores can
+// be unsure. l, b: this lane's `cnt` logits and biases from expert `base` on
+// (-inf and 0 past them).
+template <int LPT, int PER, typename T>
+__device__ __forceinline__ int choose(const T* row, const float* bias, const float (&l)[PER],
+                                      const float (&b)[PER], float bmax, int base, int k,
+                                      const RouteSpec& sp, int lpg, float m, bool& unsure) {
+  const int q = threadIdx.x % LPT, here = threadIdx.x & 63, sub = here / LPT * LPT;
+  const bool softmax = sp.score == BMOE_SCORE_SOFTMAX;
+  // A score s of a logit at distance x from m is off by s u (3 |x| + A) at
+  // most: the difference, its product with log2 e and that constant, then the
+  // exponential's, sum's (PER + 6 additions) and quotient's last places. The
+  // sigmoid has x = |l| and none of the sum.
+  constexpr float kA = PER + 24;
+  float c[PER], smax = 1.f;
+  const bool scored = bias || (sp.groups > 1 && sp.group_score == BMOE_GROUP_TOP2);
+  if (!scored) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) c[i] = l[i];
+  } else if (softmax) {
+    float total = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      c[i] = exp_of(l[i] - m);  // (a row of -inf: NaN, unsure below)
+      total += c[i];
+    }
+    smax = 1.f / sub_sum<LPT>(total);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      c[i] = l[i] == -INFINITY ? -INFINITY : fmaf(c[i], smax, b[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      c[i] = l[i] == -INFINITY ? -INFINITY : inv_of(1.f + exp_of(-l[i])) + b[i];
+  }
+
+  if (sp.groups > 1) {
+    float a = -INFINITY, a2 = -INFINITY;  // the two largest
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      a2 = fmaxf(a2, fminf(a, c[i]));
+      a = fmaxf(a, c[i]);
+    }
+    top2_lanes<LPT>(a, a2, lpg);
+    const bool one = sp.group_score == BMOE_GROUP_MAX || a2 == -INFINITY;
+    const float score = one ? a : a + a2;
+    const int g = q / lpg;
+    int rank = 0;
+    for (int h = 0; h < sp.groups; ++h) {
+      const float v = __shfl(score, sub + h * lpg, 64);
+      rank += v > score || (v == score && h < g);
+    }
+    const bool real = g < sp.groups, kept = real && rank < sp.keep;
+    if (scored) {
+      const float slack = kU * (2.f * smax * (kA + 2.f) + 3.f * (fabsf(a) + (one ? 0.f : fabsf(a2))));
+      // the lowest that a kept group, and the highest that another can be
+      const float lowest = -sub_max<LPT>(kept ? slack - score : -INFINITY);
+      const float highest = sub_max<LPT>(real && !kept ? score + slack : -INFINITY);
+      unsure |= !(lowest > highest);
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      c[i] = !kept ? -INFINITY : bias ? c[i] : l[i];
     }
   }
-  if constexpr (kFast) {
-    if (biased) {
-      // Each pick's choice minus its error has to be above the next pick's
-      // plus that one's, and the last's above every expert left. Experts of
-      // the same logit and bias tie exactly, and so do equal infinities: the
-      // ids have ordered those.
-      auto err = [&](float cv, float lv, float bv) {
-        const float s = fabsf(cv - bv), x = softmax ? lmax - lv : fabsf(lv);
-        return kU * (s * (3.f * x + kA) + 3.f * fabsf(cv));
-      };
-      auto ties = [](float c0, float l0, float b0, float c1, float l1, float b1) {
-        return (l0 == l1 && b0 == b1) || (c0 == c1 && fabsf(c0) == INFINITY);
-      };
-      const bool pick = q < k;
-      const float lj = pick ? ld_logit(row + id) : 0.f, bj = pick ? bias[id] : 0.f;
-      const float cj = value_of(top);
-      const float ej = fabsf(cj) == INFINITY ? 0.f : err(cj, lj, bj);
-      const int here = threadIdx.x & 63, last = here / LPT * LPT + k - 1;
-      const float cn = __shfl(cj, here + 1, 64), en = __shfl(ej, here + 1, 64);
-      const float ln = __shfl(lj, here + 1, 64), bn = __shfl(bj, here + 1, 64);
-      bool ok = q >= k - 1 || ties(cj, lj, bj, cn, ln, bn) || cj - ej > cn + en;
-      const float ck = __shfl(cj, last, 64), ek = __shfl(ej, last, 64);
-      const float lk = __shfl(lj, last, 64), bk = __shfl(bj, last, 64);
-      float left = -INFINITY;
+
+  // k rounds: the largest choice, the lower id on ties
+  int id = base;
+  float cj = -INFINITY;
+  for (int j = 0; j < k; ++j) {
+    float best = c[0];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const float cv = value_of(key[i]);
-        if (key[i] != 0 && !ties(ck, lk, bk, cv, l[i], b[i]))
-          left = fmaxf(left, fabsf(cv) == INFINITY ? cv : cv + err(cv, l[i], b[i]));
-      }
-      ok &= left == -INFINITY ? ck == ck : ck - ek > left;
-      *unsure |= !ok;
+    for (int i = 1; i < PER; ++i) best = fmaxf(best, c[i]);
+    best = sub_max<LPT>(best);
+    int at = 0x3fffffff;
+#pragma unroll
+    for (int i = PER - 1; i >= 0; --i) at = c[i] == best ? i : at;
+    const uint32_t first = sub_min<LPT>((uint32_t)(base + at));
+    const int out = first == (uint32_t)(base + at) ? at : -1;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) c[i] = out == i ? -INFINITY : c[i];
+    if (q == j) {
+      id = (int)first;
+      cj = best;
+    }
+  }
+  const bool pick = q < k;
+  unsure |= pick && !(fabsf(cj) < INFINITY);
+  if (bias) {
+    // Each pick's choice minus its error has to be above the next pick's plus
+    // that one's, and the last's above every expert left. Experts of the same
+    // logit and bias tie exactly, and the ids have ordered those.
+    auto err = [&](float cv, float lv, float bv) {
+      const float x = softmax ? m - lv : fabsf(lv);
+      return kU * (fabsf(cv - bv) * (3.f * x + kA) + 3.f * fabsf(cv));
+    };
+    const bool fine = pick && fabsf(cj) < INFINITY;
+    const float lj = fine ? ld_logit(row + id) : 0.f, bj = fine ? bias[id] : 0.f;
+    const float ej = err(cj, lj, bj);
+    const float cn = __shfl(cj, here + 1, 64), en = __shfl(ej, here + 1, 64);
+    const float ln = __shfl(lj, here + 1, 64), bn = __shfl(bj, here + 1, 64);
+    unsure |= q < k - 1 && !(cj - ej > cn + en) && !(lj == ln && bj == bn);
+    // The experts left: none above `left`, so none's score above S, and none's
+    // error above E (s x <= S (1 + ln(smax / S)) for a score s <= S).
+    float left = c[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) left = fmaxf(left, c[i]);
+    left = sub_max<LPT>(left);
+    const float S = fminf(smax, fmaxf(left + bmax, 1e-30f));
+    const float E = kU * (S * (3.f + 2.1f * __builtin_amdgcn_logf(smax / S) + kA) + 3.f * fabsf(left));
+    const bool clear = q != k - 1 || left == -INFINITY || cj - ej > left + E;
+    if (!__all(clear)) {  // expert by expert, exact ties with the last pick apart
+      const int last = sub + k - 1;
+      const float low = __shfl(cj - ej, last, 64);
+      const float lk = __shfl(lj, last, 64), bk = __shfl(bj, last, 64);
+      bool above = false;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        above |= c[i] != -INFINITY && !(l[i] == lk && b[i] == bk) &&
+                 !(low > c[i] + err(c[i], l[i], b[i]));
+      unsure |= above;
     }
   }
   return id;
@@ -335,21 +420,32 @@ __device__ __forceinline__ int choose(const T* row, const float* bias, const flo
 // ---- routing ----------------------------------------------------------------------
 template <int LPT, int PER, bool VEC, typename T>
 __global__ __launch_bounds__(256) void route_kernel(const T* logits, const float* bias, int T_,
-                                                    int N, int k, RouteSpec sp, int32_t* ids,
-                                                    float* gates) {
+                                                    int N, int k, RouteSpec sp, LaneMap map,
+                                                    int32_t* ids, float* gates) {
   constexpr int kTok = 256 / LPT;  // tokens per workgroup
-  const int q = threadIdx.x % LPT, base = q * PER;
+  const int q = threadIdx.x % LPT;
   const bool softmax = sp.score == BMOE_SCORE_SOFTMAX;
-  float b[PER];
+  // (a map that does not fit: lanes by expert, as without groups)
+  const int groups = map.lpg > 0 ? sp.groups : 1;
+  const int size = N / groups, lpg = map.lpg > 0 ? map.lpg : LPT;
+  const int in_group = q % lpg * PER;  // this lane's first expert within its group
+  const int base = q / lpg * size + in_group;
+  const int cnt = q / lpg < groups ? max(0, min(PER, size - in_group)) : 0;
+  float b[PER], bmax = 0.f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) b[i] = 0.f;
-  if (bias) ld_row<PER, VEC>(bias, base, N, 0.f, b);
+  if (bias) {
+    ld_row<PER, VEC>(bias + base, cnt, 0.f, b);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) bmax = fmaxf(bmax, fabsf(b[i]));
+    bmax = sub_max<LPT>(bmax);
+  }
   for (size_t t0 = (size_t)blockIdx.x * kTok; t0 < (size_t)T_; t0 += (size_t)gridDim.x * kTok) {
     const size_t tok = t0 + threadIdx.x / LPT;
     const bool live = tok < (size_t)T_;
     const T* row = logits + (live ? tok : 0) * N;
     float l[PER];
-    ld_row<PER, VEC>(row, base, N, -INFINITY, l);
+    ld_row<PER, VEC>(row + base, cnt, -INFINITY, l);
     bool bad = false;
     float m = -INFINITY;
 #pragma unroll
@@ -360,11 +456,22 @@ __global__ __launch_bounds__(256) void route_kernel(const T* logits, const float
     m = sub_max<LPT>(m);
     bad = own_bits<LPT>(__ballot(bad)) != 0 || (softmax && m == INFINITY);
 
-    bool unsure = false;
-    int id = choose<LPT, PER, float>(row, bias, l, b, base, N, k, sp, m, &unsure);
-    if (__any(unsure)) id = choose<LPT, PER, double>(row, bias, l, b, base, N, k, sp, m, &unsure);
+    bool unsure = bad || map.lpg == 0;
+    int id = 0;
+    if (map.lpg > 0)
+      id = choose<LPT, PER>(row, bias, l, b, bmax, base, k, sp, lpg, m, unsure);
+    // the exact way, one token at a time by the whole wave
+    uint64_t todo = __ballot(unsure && live);
+    while (todo) {
+      const int sub = (int)__builtin_ctzll(todo) / LPT * LPT;
+      todo &= ~(LPT == 64 ? ~0ull : ((1ull << (LPT & 63)) - 1) << sub);
+      const size_t t = t0 + ((threadIdx.x & ~63) + sub) / LPT;
+      const int x = choose_exact<LPT * PER / 64>(logits + t * N, bias, N, k, sp);
+      const int y = __shfl(x, q, 64);
+      if ((threadIdx.x & 63) / LPT * LPT == sub) id = y;
+    }
 
-    const bool pick = q < k;
+    const bool pick = live && q < k;  // (a lane without a token may hold no id)
     const float lj = pick ? ld_logit(row + id) : -INFINITY;
     float g;
     if (sp.renorm) {
@@ -383,7 +490,7 @@ __global__ __launch_bounds__(256) void route_kernel(const T* logits, const float
     } else {
       g = lj == -INFINITY ? 0.f : inv_of(1.f + exp_of(-lj));
     }
-    if (live && pick) {
+    if (pick) {
       ids[tok * k + q] = id;
       gates[tok * k + q] = bad ? NAN : sp.scale * g;
     }
@@ -443,7 +550,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const i
   }
   if (dense) {
     float l[PER], m = -INFINITY, total = 0.f;
-    ld_row<PER, VEC>(row, base, N, -INFINITY, l);
+    ld_row<PER, VEC>(row + min(base, N), max(0, min(PER, N - base)), -INFINITY, l);
 #pragma unroll
     for (int i = 0; i < PER; ++i) m = fmaxf(m, l[i]);
     m = sub_max<LPT>(m);
@@ -584,31 +691,43 @@ __global__ __launch_bounds__(1024) void balance_kernel(const int32_t* ids, long 
 }
 
 // Lanes per token and experts per lane: 16 lanes (4 tokens per wave) up to 256
-// experts and 16 picks or groups (they sit one per lane), else a whole wave
-// per token.
-#define BMOE_BY_SHAPE(CALL)                          \
-  if (need <= 16 && N <= 64) { CALL(16, 4); }        \
-  if (need <= 16 && N <= 256) { CALL(16, 16); }      \
-  if (N <= 256) { CALL(64, 4); }                     \
-  if (N <= 1024) { CALL(64, 16); }                   \
-  CALL(64, 64)
-
+// experts and 16 picks, else a whole wave per token.
 template <bool VEC, typename T>
 hipError_t route_t(const T* logits, const float* bias, int Tn, int N, int k, const RouteSpec& sp,
                    int32_t* ids, float* gates, hipStream_t s) {
-  const int need = k > sp.groups ? k : sp.groups;
-#define BMOE_CALL(LPT, PER)                                                                     \
-  const unsigned blocks = ((unsigned)Tn + 256 / LPT - 1) / (256 / LPT);                         \
-  return launch_kernel(route_kernel<LPT, PER, VEC, T>, dim3(blocks < 2048 ? blocks : 2048),     \
-                       dim3(256), 0, s, KernelTiming{}, logits, bias, Tn, N, k, sp, ids, gates)
-  BMOE_BY_SHAPE(BMOE_CALL);
+  LaneMap map;
+#define BMOE_CALL(LPT, PER, WHEN)                                                               \
+  if ((WHEN) && N <= LPT * PER && k <= LPT && (map = lane_map<LPT, PER>(N, sp.groups)).lpg) {   \
+    const unsigned blocks = ((unsigned)Tn + 256 / LPT - 1) / (256 / LPT);                       \
+    return launch_kernel(route_kernel<LPT, PER, VEC, T>, dim3(blocks < 2048 ? blocks : 2048),   \
+                         dim3(256), 0, s, KernelTiming{}, logits, bias, Tn, N, k, sp, map, ids, \
+                         gates);                                                                \
+  }
+  const bool few = Tn <= 1024;  // a wave per token still leaves SIMDs without one
+  BMOE_CALL(16, 4, true)
+  BMOE_CALL(16, 16, !few)
+  BMOE_CALL(64, 4, true)
+  BMOE_CALL(16, 16, true)
+  BMOE_CALL(64, 16, true)
+  BMOE_CALL(64, 64, true)
 #undef BMOE_CALL
+  map.lpg = 0;
+  const unsigned blocks = ((unsigned)Tn + 3) / 4;
+  return launch_kernel(route_kernel<64, 64, VEC, T>, dim3(blocks < 2048 ? blocks : 2048),
+                       dim3(256), 0, s, KernelTiming{}, logits, bias, Tn, N, k, sp, map, ids,
+                       gates);
 }
+
+#define BMOE_BY_SHAPE(CALL)                    \
+  if (k <= 16 && N <= 64) { CALL(16, 4); }     \
+  if (k <= 16 && N <= 256) { CALL(16, 16); }   \
+  if (N <= 256) { CALL(64, 4); }               \
+  if (N <= 1024) { CALL(64, 16); }             \
+  CALL(64, 64)
 
 template <bool VEC, typename T>
 hipError_t route_bwd_t(const T* logits, const int32_t* ids, const float* dgates, int Tn, int N,
                        int k, const RouteSpec& sp, float* dlogits, hipStream_t s) {
-  const int need = k;
 #define BMOE_CALL(LPT, PER)                                                                      \
   return launch_kernel(route_bwd_kernel<LPT, PER, VEC, T>,                                       \
                        dim3(((unsigned)Tn + 256 / LPT - 1) / (256 / LPT)), dim3(256), 0, s,      \
@@ -622,15 +741,16 @@ hipError_t route_bwd_t(const T* logits, const int32_t* ids, const float* dgates,
 hipError_t launch_route(bmoe_dtype dt, int T, int N, int k, const RouteSpec& sp,
                         const void* logits, const float* bias, int32_t* ids, float* gates,
                         hipStream_t s) {
-  // whole vectors of a row: 16 bytes of logits (and 4 fp32 of the bias)
+  // whole vectors (16 bytes) of a row and of each group in it
+  const int size = N / sp.groups;
   if (dt == BMOE_BF16) {
     const uint16_t* l = static_cast<const uint16_t*>(logits);
-    return N % 8 == 0 ? route_t<true>(l, bias, T, N, k, sp, ids, gates, s)
-                      : route_t<false>(l, bias, T, N, k, sp, ids, gates, s);
+    return size % 8 == 0 ? route_t<true>(l, bias, T, N, k, sp, ids, gates, s)
+                         : route_t<false>(l, bias, T, N, k, sp, ids, gates, s);
   }
   const float* l = static_cast<const float*>(logits);
-  return N % 4 == 0 ? route_t<true>(l, bias, T, N, k, sp, ids, gates, s)
-                    : route_t<false>(l, bias, T, N, k, sp, ids, gates, s);
+  return size % 4 == 0 ? route_t<true>(l, bias, T, N, k, sp, ids, gates, s)
+                       : route_t<false>(l, bias, T, N, k, sp, ids, gates, s);
 }
 
 hipError_t launch_route_bwd(bmoe_dtype dt, int T, int N, int k, const RouteSpec& sp,
