@@ -174,7 +174,7 @@ def lib():
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _ref(struct):
@@ -185,9 +185,16 @@ def _nbytes(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
+# The current stream's handle without the Stream object around it: 0.1 us of a
+# call instead of 2.7 us (the lookup torch's own generated code uses).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
+    if stream is None and _raw_stream is not None and torch.cuda.is_initialized():
+        return _raw_stream(torch.cuda.current_device())
     s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _on(stream=None):
@@ -853,13 +860,17 @@ def router_backward(x: torch.Tensor, w_router: torch.Tensor, logits: torch.Tenso
         return {"dx": dx, "dw": dw}
 
 
+_CODES = {torch.float32: BMOE_F32, torch.bfloat16: BMOE_BF16}
+
+
 def _grad_list(name: str, tensors, device):
-    arr = (BmoeTensor * len(tensors))()
-    for e, t in zip(arr, tensors):
+    for t in tensors:
+        if t.dtype not in _CODES:
+            raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
         if t.device != device or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous tensors on one device")
-        e.data, e.count, e.dtype = t.data_ptr(), t.numel(), dtype_code(t)
-    return arr
+    return (BmoeTensor * len(tensors))(*[(t.data_ptr(), t.numel(), _CODES[t.dtype])
+                                         for t in tensors])
 
 
 def _grad_call(grads, out, stream):

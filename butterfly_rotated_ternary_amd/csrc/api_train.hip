@@ -68,10 +68,13 @@ bmoe_status check_grads(int n, const bmoe_tensor* grads, const bmoe_tensor* out,
   if (n < 0) return BMOE_E_SHAPE;
   if (n == 0) return BMOE_OK;
   if (!grads) return BMOE_E_NULL;
+  constexpr size_t kMostEntries = (size_t)1 << 40;  // a table's chunk numbers are 32 bits
+  size_t entries = 0;
   for (int i = 0; i < n; ++i) {
     const bmoe_tensor& g = grads[i];
     if (g.dtype != BMOE_F32 && g.dtype != BMOE_BF16) return BMOE_E_DTYPE;
-    if (g.count > (size_t)PTRDIFF_MAX / 8) return BMOE_E_SHAPE;
+    if (g.count > kMostEntries - entries) return BMOE_E_SHAPE;
+    entries += g.count;
     if (g.count && !g.data) return BMOE_E_NULL;
     if (reinterpret_cast<uintptr_t>(g.data) % elem((bmoe_dtype)g.dtype)) return BMOE_E_ALIGN;
     if (out) {
@@ -117,37 +120,42 @@ template <typename F>
 bmoe_status each_table(int n, const bmoe_tensor* grads, const bmoe_tensor* out, F f) {
   GradTable tab;
   tab.n = 0;
+  tab.chunks = 0;
   for (int i = 0; i < n; ++i) {
-    if (grads[i].count)
-      tab.t[tab.n++] = {grads[i].data, out ? out[i].data : grads[i].data, grads[i].count,
-                        grads[i].dtype == BMOE_BF16};
-    if (tab.n == kGradTab || (i == n - 1 && tab.n)) {
+    if (!grads[i].count) continue;
+    const int bf16 = grads[i].dtype == BMOE_BF16;
+    const uint32_t c = grad_chunks(grads[i].data, grads[i].count, bf16);
+    if (tab.n == kGradTab) {
       if (f(tab) != hipSuccess) return BMOE_E_HIP;
       tab.n = 0;
+      tab.chunks = 0;
     }
+    tab.t[tab.n++] = {grads[i].data, out ? out[i].data : grads[i].data, grads[i].count, tab.chunks,
+                      bf16};
+    tab.chunks += c;
   }
-  return BMOE_OK;
+  return !tab.n || f(tab) == hipSuccess ? BMOE_OK : BMOE_E_HIP;
 }
 
-bmoe_status grad_norm_impl(int n, const bmoe_tensor* grads, float* norm, void* ws, hipStream_t s) {
-  double* part = static_cast<double*>(ws);
-  int used = 0;
-  const bmoe_status st = each_table(n, grads, nullptr, [&](const GradTable& t) {
+// Partial sums of the whole list to part; their number to *used.
+bmoe_status grad_sq_impl(int n, const bmoe_tensor* grads, double* part, int* used, hipStream_t s) {
+  *used = 0;
+  return each_table(n, grads, nullptr, [&](const GradTable& t) {
     int np = 0;
-    const hipError_t e = launch_grad_sq(t, part + used, &np, s);
-    used += np;
+    const hipError_t e = launch_grad_sq(t, part + *used, &np, s);
+    *used += np;
     return e;
   });
-  if (st != BMOE_OK) return st;
-  return launch_grad_norm(part, used, norm, s) == hipSuccess ? BMOE_OK : BMOE_E_HIP;
 }
 
+// part not NULL: the norm from its n_part sums, written to *norm.
 bmoe_status grad_scale_impl(int n, const bmoe_tensor* grads, const bmoe_tensor* out,
-                            const float* norm, float max_norm, hipStream_t s) {
+                            const double* part, int n_part, float* norm, float max_norm,
+                            hipStream_t s) {
   bool in_place = true;
   for (int i = 0; out && i < n; ++i) in_place &= out[i].data == grads[i].data || !grads[i].count;
   return each_table(n, grads, out, [&](const GradTable& t) {
-    return launch_grad_scale(t, norm, max_norm, in_place, s);
+    return launch_grad_scale(t, part, n_part, norm, max_norm, in_place, s);
   });
 }
 
@@ -290,7 +298,12 @@ bmoe_status bmoe_grad_norm(int n, const bmoe_tensor* grads, float* norm, void* w
   if (!norm) return BMOE_E_NULL;
   if (!ws || ws_bytes < bmoe_grad_workspace_bytes(n)) return BMOE_E_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(norm) & 3u) || !ok16(ws)) return BMOE_E_ALIGN;
-  return grad_norm_impl(n, grads, norm, ws, static_cast<hipStream_t>(stream));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  double* part = static_cast<double*>(ws);
+  int used = 0;
+  const bmoe_status rs = grad_sq_impl(n, grads, part, &used, s);
+  if (rs != BMOE_OK) return rs;
+  return launch_grad_norm(part, used, norm, s) == hipSuccess ? BMOE_OK : BMOE_E_HIP;
 }
 
 bmoe_status bmoe_grad_scale(int n, const bmoe_tensor* grads, const bmoe_tensor* out,
@@ -300,7 +313,8 @@ bmoe_status bmoe_grad_scale(int n, const bmoe_tensor* grads, const bmoe_tensor* 
   if (!good_max_norm(max_norm)) return BMOE_E_VALUE;
   if (!norm) return BMOE_E_NULL;
   if (reinterpret_cast<uintptr_t>(norm) & 3u) return BMOE_E_ALIGN;
-  return grad_scale_impl(n, grads, out, norm, max_norm, static_cast<hipStream_t>(stream));
+  return grad_scale_impl(n, grads, out, nullptr, 0, const_cast<float*>(norm), max_norm,
+                         static_cast<hipStream_t>(stream));
 }
 
 bmoe_status bmoe_grad_clip(int n, const bmoe_tensor* grads, const bmoe_tensor* out, float max_norm,
@@ -312,8 +326,15 @@ bmoe_status bmoe_grad_clip(int n, const bmoe_tensor* grads, const bmoe_tensor* o
   if (!ws || ws_bytes < bmoe_grad_workspace_bytes(n)) return BMOE_E_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(norm) & 3u) || !ok16(ws)) return BMOE_E_ALIGN;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const bmoe_status rn = grad_norm_impl(n, grads, norm, ws, s);
-  return rn != BMOE_OK ? rn : grad_scale_impl(n, grads, out, norm, max_norm, s);
+  double* part = static_cast<double*>(ws);
+  int used = 0;
+  const bmoe_status rs = grad_sq_impl(n, grads, part, &used, s);
+  if (rs != BMOE_OK) return rs;
+  // One table's partial sums are added by every workgroup of the scaling (16
+  // KB from L2, instead of a launch in between); more tables' once.
+  const bool inside = used > 0 && used <= kGradParts;
+  if (!inside && launch_grad_norm(part, used, norm, s) != hipSuccess) return BMOE_E_HIP;
+  return grad_scale_impl(n, grads, out, inside ? part : nullptr, used, norm, max_norm, s);
 }
 
 }  // extern "C"

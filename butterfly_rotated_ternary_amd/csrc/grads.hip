@@ -3,10 +3,14 @@
 //   norm = sqrt(sum over all tensors and entries of g^2)
 //   out  = g * (max_norm / norm  if max_norm < norm < infinity, else 1)
 // Squares are summed in 64 bits (no overflow, and a sum over 10^9 entries
-// keeps its bits) in an order that the sizes alone fix: thread, wave,
-// workgroup, then the workgroups' partial sums in their order.
-#include <cmath>
-
+// keeps its bits; the fp64 FMA runs at the fp32 rate here, far above what
+// memory delivers) in an order that the sizes and alignments alone fix:
+// thread, wave, workgroup, then the workgroups' partial sums in their order.
+//
+// Bound by HBM: the norm reads every byte once, the scaling reads and writes
+// it once. The tensors are cut into chunks of 256 16-byte vectors, numbered
+// through the list; a workgroup takes a run of consecutive chunks, so it looks
+// its tensor up once, and streams 8 chunks (32 KB) per step.
 #include "common.h"
 #include "kernels.h"
 
@@ -14,6 +18,7 @@ namespace bmoe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAhead = 8;  // vectors in flight per thread
 
 __device__ __forceinline__ double block_sum(double v, double* lds) {
 #pragma unroll
@@ -26,59 +31,215 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
   return s;
 }
 
-__device__ __forceinline__ float ld_grad(const GradEntry& t, size_t i) {
-  return t.bf16 ? bf16_lo(static_cast<const uint16_t*>(t.src)[i])
-                : static_cast<const float*>(t.src)[i];
+// The norm from the partial sums, the same in every workgroup that asks.
+__device__ __forceinline__ float norm_of(const double* part, int n, double* lds) {
+  double acc = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads) acc += part[i];
+  return (float)sqrt(block_sum(acc, lds));
+}
+
+// ---- the entries of one tensor, by 16-byte vectors of its address ----------------
+// Vector v of a tensor holds its entries W v - head ... W v - head + W - 1, W
+// per 16 bytes, head the entries between the aligned address and the first.
+struct Span {
+  const char* src;  // rounded down to 16 bytes
+  char* dst;        // src's offset from it, not rounded
+  long long count;
+  int head, bf16;
+};
+__device__ __forceinline__ Span span_of(const GradEntry& t) {
+  Span s;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(t.src);
+  s.src = reinterpret_cast<const char*>(a & ~(uintptr_t)15);
+  s.dst = static_cast<char*>(t.dst) - (a & 15);
+  s.count = (long long)t.count;
+  s.bf16 = t.bf16;
+  s.head = (int)(a & 15) / (t.bf16 ? 2 : 4);
+  return s;
+}
+
+// Whether all entries of vectors [v0, v1) exist.
+__device__ __forceinline__ bool whole(const Span& s, long long v0, long long v1) {
+  const int w = s.bf16 ? 8 : 4;
+  return v0 * w >= s.head && v1 * w - s.head <= s.count;
+}
+
+// f(value, byte offset) for the entries that vector v has.
+template <typename F>
+__device__ __forceinline__ void each_entry(const Span& s, long long v, F f) {
+  const int w = s.bf16 ? 8 : 4;
+  for (int i = 0; i < w; ++i) {
+    const long long e = v * w + i - s.head;
+    if (e < 0 || e >= s.count) continue;
+    const long long at = v * 16 + i * (16 / w);
+    f(s.bf16 ? bf16_lo(*reinterpret_cast<const uint16_t*>(s.src + at))
+             : *reinterpret_cast<const float*>(s.src + at),
+      at);
+  }
+}
+
+__device__ __forceinline__ double add_sq(double acc, float g) {
+  return fma((double)g, (double)g, acc);
+}
+template <bool BF16>
+__device__ __forceinline__ void add_sq(double& a, double& b, uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF16) {
+      a = add_sq(a, bf16_lo(w[i]));
+      b = add_sq(b, bf16_hi(w[i]));
+    } else {
+      double& x = i & 1 ? b : a;
+      x = add_sq(x, __uint_as_float(w[i]));
+    }
+  }
+}
+
+// Index of the entry that chunk c belongs to.
+__device__ __forceinline__ int find(const GradTable& tab, uint32_t c) {
+  int lo = 0, hi = tab.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (tab.t[mid].first <= c) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// This workgroup's run of chunks.
+__device__ __forceinline__ uint32_t run_start(const GradTable& tab, uint32_t b) {
+  return (uint32_t)((uint64_t)tab.chunks * b / gridDim.x);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void sq_chunks(const Span& s, long long c0, long long c1, double& a,
+                                          double& b) {
+  const uint4* p = reinterpret_cast<const uint4*>(s.src) + threadIdx.x;
+  for (long long c = c0; c < c1;) {
+    if (c + kAhead <= c1 && whole(s, c * 256, (c + kAhead) * 256)) {
+      uint4 v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) v[u] = p[(c + u) * 256];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) add_sq<BF16>(a, b, v[u]);
+      c += kAhead;
+    } else {
+      const long long v = c * 256 + threadIdx.x;
+      if (whole(s, v, v + 1)) add_sq<BF16>(a, b, p[c * 256]);
+      else each_entry(s, v, [&](float g, long long) { a = add_sq(a, g); });
+      ++c;
+    }
+  }
 }
 
 __global__ __launch_bounds__(kThreads) void grad_sq_kernel(GradTable tab, double* part) {
   __shared__ double lds[kThreads / 64];
-  double acc = 0.0;
-  for (int n = 0; n < tab.n; ++n) {
-    const GradEntry t = tab.t[n];
-    for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < t.count;
-         i += (size_t)gridDim.x * kThreads) {
-      const double g = ld_grad(t, i);
-      acc = fma(g, g, acc);
-    }
+  double a = 0.0, b = 0.0;
+  uint32_t c = run_start(tab, blockIdx.x);
+  const uint32_t end = run_start(tab, blockIdx.x + 1);
+  for (int n = find(tab, c); c < end; ++n) {
+    const Span s = span_of(tab.t[n]);
+    const uint32_t first = tab.t[n].first, next = n + 1 < tab.n ? tab.t[n + 1].first : tab.chunks;
+    const uint32_t stop = next < end ? next : end;
+    if (s.bf16) sq_chunks<true>(s, c - first, stop - first, a, b);
+    else sq_chunks<false>(s, c - first, stop - first, a, b);
+    c = stop;
   }
-  const double s = block_sum(acc, lds);
-  if (threadIdx.x == 0) part[blockIdx.x] = s;
+  const double sum = block_sum(a + b, lds);
+  if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
 __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const double* part, int n,
                                                              float* norm) {
   __shared__ double lds[kThreads / 64];
-  double acc = 0.0;
-  for (int i = threadIdx.x; i < n; i += kThreads) acc += part[i];
-  const double s = block_sum(acc, lds);
-  if (threadIdx.x == 0) *norm = (float)sqrt(s);
+  const float v = norm_of(part, n, lds);
+  if (threadIdx.x == 0) *norm = v;
 }
 
-__global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradTable tab, const float* norm,
-                                                              float max_norm, int in_place) {
-  const float nv = *norm;
-  const float coef = nv > max_norm && nv < INFINITY ? max_norm / nv : 1.f;
-  if (in_place && coef == 1.f) return;
-  for (int n = 0; n < tab.n; ++n) {
-    const GradEntry t = tab.t[n];
-    for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < t.count;
-         i += (size_t)gridDim.x * kThreads) {
-      const float v = ld_grad(t, i) * coef;
-      if (t.bf16) static_cast<uint16_t*>(t.dst)[i] = (uint16_t)f32_to_bf16_bits(v);
-      else static_cast<float*>(t.dst)[i] = v;
+__device__ __forceinline__ uint4 scaled(uint4 v, float f, int bf16) {
+  const float c = bf16 ? 1.f : f;
+  uint4 r;
+  if (bf16) {
+    r.x = pack_bf16x2(bf16_lo(v.x) * f, bf16_hi(v.x) * f);
+    r.y = pack_bf16x2(bf16_lo(v.y) * f, bf16_hi(v.y) * f);
+    r.z = pack_bf16x2(bf16_lo(v.z) * f, bf16_hi(v.z) * f);
+    r.w = pack_bf16x2(bf16_lo(v.w) * f, bf16_hi(v.w) * f);
+  } else {
+    r.x = __float_as_uint(__uint_as_float(v.x) * c);
+    r.y = __float_as_uint(__uint_as_float(v.y) * c);
+    r.z = __float_as_uint(__uint_as_float(v.z) * c);
+    r.w = __float_as_uint(__uint_as_float(v.w) * c);
+  }
+  return r;
+}
+
+// Chunks [c0, c1) of a tensor, the last first: what the norm read last is the
+// likeliest to be in the caches still.
+__device__ __forceinline__ void scale_chunks(const Span& s, long long c0, long long c1, float f) {
+  const uint4* p = reinterpret_cast<const uint4*>(s.src) + threadIdx.x;
+  uint4* o = reinterpret_cast<uint4*>(s.dst) + threadIdx.x;
+  const bool same = (reinterpret_cast<uintptr_t>(s.dst) & 15) == 0;  // as aligned as src
+  for (long long c = c1; c > c0;) {
+    if (same && c - kAhead >= c0 && whole(s, (c - kAhead) * 256, c * 256)) {
+      c -= kAhead;
+      uint4 v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) v[u] = p[(c + u) * 256];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) o[(c + u) * 256] = scaled(v[u], f, s.bf16);
+    } else {
+      --c;
+      const long long v = c * 256 + threadIdx.x;
+      if (same && whole(s, v, v + 1)) {
+        o[c * 256] = scaled(p[c * 256], f, s.bf16);
+      } else {
+        each_entry(s, v, [&](float g, long long at) {
+          if (s.bf16) *reinterpret_cast<uint16_t*>(s.dst + at) = (uint16_t)f32_to_bf16_bits(g * f);
+          else *reinterpret_cast<float*>(s.dst + at) = g * f;
+        });
+      }
     }
   }
 }
 
+// norm: read, or (part not NULL) taken from the n_part partial sums and
+// written by the first workgroup.
+__global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradTable tab, const double* part,
+                                                              int n_part, float* norm,
+                                                              float max_norm, int in_place) {
+  __shared__ double lds[kThreads / 64];
+  float nv;
+  if (part) {
+    nv = norm_of(part, n_part, lds);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = nv;
+  } else {
+    nv = *norm;
+  }
+  const float coef = nv > max_norm && nv < INFINITY ? max_norm / nv : 1.f;
+  if (in_place && coef == 1.f) return;
+  uint32_t end = run_start(tab, blockIdx.x + 1);
+  const uint32_t c = run_start(tab, blockIdx.x);
+  for (int n = find(tab, end - 1); end > c; --n) {
+    const uint32_t first = tab.t[n].first;
+    const uint32_t start = first > c ? first : c;
+    scale_chunks(span_of(tab.t[n]), start - first, end - first, coef);
+    end = start;
+  }
+}
+
+// A workgroup per chunk up to what is resident at once.
 int grid_of(const GradTable& tab) {
-  size_t most = 0;
-  for (int n = 0; n < tab.n; ++n) most = tab.t[n].count > most ? tab.t[n].count : most;
-  const size_t g = (most + kThreads - 1) / kThreads;
-  return g < 1 ? 1 : g > kGradParts ? kGradParts : (int)g;
+  return tab.chunks < (uint32_t)kGradParts ? (int)tab.chunks : kGradParts;
 }
 
 }  // namespace
+
+uint32_t grad_chunks(const void* src, size_t count, int bf16) {
+  const size_t w = bf16 ? 8 : 4;
+  const size_t head = (reinterpret_cast<uintptr_t>(src) & 15) / (16 / w);
+  return (uint32_t)(((head + count + w - 1) / w + 255) / 256);
+}
 
 hipError_t launch_grad_sq(const GradTable& tab, double* part, int* n_part, hipStream_t s) {
   *n_part = grid_of(tab);
@@ -91,10 +252,10 @@ hipError_t launch_grad_norm(const double* part, int n_part, float* norm, hipStre
                        n_part, norm);
 }
 
-hipError_t launch_grad_scale(const GradTable& tab, const float* norm, float max_norm, int in_place,
-                             hipStream_t s) {
+hipError_t launch_grad_scale(const GradTable& tab, const double* part, int n_part, float* norm,
+                             float max_norm, int in_place, hipStream_t s) {
   return launch_kernel(grad_scale_kernel, dim3(grid_of(tab)), dim3(kThreads), 0, s, KernelTiming{},
-                       tab, norm, max_norm, in_place);
+                       tab, part, n_part, norm, max_norm, in_place);
 }
 
 }  // namespace bmoe

@@ -258,20 +258,25 @@ struct GradEntry {
   const void* src;
   void* dst;
   size_t count;
+  uint32_t first;  // the table's chunks before this tensor
   int bf16;
 };
 constexpr int kGradTab = 112;     // entries per launch, in its kernel arguments
-constexpr int kGradParts = 1024;  // partial sums per launch, at most
+constexpr int kGradParts = 2048;  // partial sums per launch, at most
 struct GradTable {
   int n;
+  uint32_t chunks;
   GradEntry t[kGradTab];
 };
+// Chunks (256 vectors of 16 bytes) of a tensor.
+uint32_t grad_chunks(const void* src, size_t count, int bf16);
 // Sums of squares of the table's tensors: *n_part partial sums to part.
 hipError_t launch_grad_sq(const GradTable& tab, double* part, int* n_part, hipStream_t s);
 // norm = sqrt(sum of part[0 .. n_part)), added in order.
 hipError_t launch_grad_norm(const double* part, int n_part, float* norm, hipStream_t s);
 // dst = src * (max_norm / norm where max_norm < norm < infinity, else 1).
-hipError_t launch_grad_scale(const GradTable& tab, const float* norm, float max_norm, int in_place,
-                             hipStream_t s);
+// part not NULL: norm is taken from the partial sums, and written.
+hipError_t launch_grad_scale(const GradTable& tab, const double* part, int n_part, float* norm,
+                             float max_norm, int in_place, hipStream_t s);
 
 }  // namespace bmoe

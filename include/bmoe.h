@@ -510,8 +510,8 @@ bmoe_status bmoe_router_backward(bmoe_dtype dt, int T, int d, int n_experts, int
  * A norm that is not finite clips nothing: the gradients pass through and the
  * norm tells the caller.
  *   grads  host array of n tensors: device pointer (aligned to its element),
- *          count >= 0 entries, BMOE_F32 or BMOE_BF16. Read before the call
- *          returns. bf16 results are rounded once.
+ *          count >= 0 entries (2^40 in all at most), BMOE_F32 or BMOE_BF16.
+ *          Read before the call returns. bf16 results are rounded once.
  *   out    host array of n tensors of the same types and counts, or NULL:
  *          in place. An out tensor may be its own grad; any other sharing of
  *          memory with a written tensor is refused (BMOE_E_VALUE).
