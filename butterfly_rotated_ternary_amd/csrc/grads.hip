@@ -10,7 +10,13 @@
 // Bound by HBM: the norm reads every byte once, the scaling reads and writes
 // it once. The tensors are cut into chunks of 256 16-byte vectors, numbered
 // through the list; a workgroup takes a run of consecutive chunks, so it looks
-// its tensor up once, and streams 8 chunks (32 KB) per step.
+// its tensor up once, and streams 8 chunks (32 KB) per step. The scaling walks
+// its run backwards and neither keeps what it loads nor what it stores; the
+// norm's loads stay cached for it up to 256 MB (the last-level cache), above
+// that they stream too. Measured, norm and scaling apart, plain against
+// streaming accesses: 128 MB 84 -> 65 us (73 if the norm streams), 0.96 GB
+// 569 -> 517 us (557 if it does not), against 533 us for its three passes at
+// the rate of a large copy (5.4 TB/s).
 #include "common.h"
 #include "kernels.h"
 
@@ -112,7 +118,15 @@ __device__ __forceinline__ uint32_t run_start(const GradTable& tab, uint32_t b) 
   return (uint32_t)((uint64_t)tab.chunks * b / gridDim.x);
 }
 
-template <bool BF16>
+// Streaming accesses, for data that no cache will hold until its next use.
+__device__ __forceinline__ uint4 ld_once(const uint4* p) {
+  return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)));
+}
+__device__ __forceinline__ void st_once(uint4* p, uint4 v) {
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(p));
+}
+
+template <bool BF16, bool ONCE>
 __device__ __forceinline__ void sq_chunks(const Span& s, long long c0, long long c1, double& a,
                                           double& b) {
   const uint4* p = reinterpret_cast<const uint4*>(s.src) + threadIdx.x;
@@ -120,7 +134,7 @@ __device__ __forceinline__ void sq_chunks(const Span& s, long long c0, long long
     if (c + kAhead <= c1 && whole(s, c * 256, (c + kAhead) * 256)) {
       uint4 v[kAhead];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) v[u] = p[(c + u) * 256];
+      for (int u = 0; u < kAhead; ++u) v[u] = ONCE ? ld_once(p + (c + u) * 256) : p[(c + u) * 256];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) add_sq<BF16>(a, b, v[u]);
       c += kAhead;
@@ -133,6 +147,7 @@ __device__ __forceinline__ void sq_chunks(const Span& s, long long c0, long long
   }
 }
 
+template <bool ONCE>
 __global__ __launch_bounds__(kThreads) void grad_sq_kernel(GradTable tab, double* part) {
   __shared__ double lds[kThreads / 64];
   double a = 0.0, b = 0.0;
@@ -142,8 +157,8 @@ __global__ __launch_bounds__(kThreads) void grad_sq_kernel(GradTable tab, double
     const Span s = span_of(tab.t[n]);
     const uint32_t first = tab.t[n].first, next = n + 1 < tab.n ? tab.t[n + 1].first : tab.chunks;
     const uint32_t stop = next < end ? next : end;
-    if (s.bf16) sq_chunks<true>(s, c - first, stop - first, a, b);
-    else sq_chunks<false>(s, c - first, stop - first, a, b);
+    if (s.bf16) sq_chunks<true, ONCE>(s, c - first, stop - first, a, b);
+    else sq_chunks<false, ONCE>(s, c - first, stop - first, a, b);
     c = stop;
   }
   const double sum = block_sum(a + b, lds);
@@ -158,7 +173,6 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const double* part,
 }
 
 __device__ __forceinline__ uint4 scaled(uint4 v, float f, int bf16) {
-  const float c = bf16 ? 1.f : f;
   uint4 r;
   if (bf16) {
     r.x = pack_bf16x2(bf16_lo(v.x) * f, bf16_hi(v.x) * f);
@@ -166,10 +180,10 @@ __device__ __forceinline__ uint4 scaled(uint4 v, float f, int bf16) {
     r.z = pack_bf16x2(bf16_lo(v.z) * f, bf16_hi(v.z) * f);
     r.w = pack_bf16x2(bf16_lo(v.w) * f, bf16_hi(v.w) * f);
   } else {
-    r.x = __float_as_uint(__uint_as_float(v.x) * c);
-    r.y = __float_as_uint(__uint_as_float(v.y) * c);
-    r.z = __float_as_uint(__uint_as_float(v.z) * c);
-    r.w = __float_as_uint(__uint_as_float(v.w) * c);
+    r.x = __float_as_uint(__uint_as_float(v.x) * f);
+    r.y = __float_as_uint(__uint_as_float(v.y) * f);
+    r.z = __float_as_uint(__uint_as_float(v.z) * f);
+    r.w = __float_as_uint(__uint_as_float(v.w) * f);
   }
   return r;
 }
@@ -185,9 +199,9 @@ __device__ __forceinline__ void scale_chunks(const Span& s, long long c0, long l
       c -= kAhead;
       uint4 v[kAhead];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) v[u] = p[(c + u) * 256];
+      for (int u = 0; u < kAhead; ++u) v[u] = ld_once(p + (c + u) * 256);
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) o[(c + u) * 256] = scaled(v[u], f, s.bf16);
+      for (int u = 0; u < kAhead; ++u) st_once(o + (c + u) * 256, scaled(v[u], f, s.bf16));
     } else {
       --c;
       const long long v = c * 256 + threadIdx.x;
@@ -243,8 +257,10 @@ uint32_t grad_chunks(const void* src, size_t count, int bf16) {
 
 hipError_t launch_grad_sq(const GradTable& tab, double* part, int* n_part, hipStream_t s) {
   *n_part = grid_of(tab);
-  return launch_kernel(grad_sq_kernel, dim3(*n_part), dim3(kThreads), 0, s, KernelTiming{}, tab,
-                       part);
+  const dim3 grid(*n_part), block(kThreads);
+  if (tab.chunks > (256u << 20) / 4096)
+    return launch_kernel(grad_sq_kernel<true>, grid, block, 0, s, KernelTiming{}, tab, part);
+  return launch_kernel(grad_sq_kernel<false>, grid, block, 0, s, KernelTiming{}, tab, part);
 }
 
 hipError_t launch_grad_norm(const double* part, int n_part, float* norm, hipStream_t s) {
