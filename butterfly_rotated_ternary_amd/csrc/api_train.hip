@@ -215,7 +215,7 @@ bmoe_status bmoe_route_backward(bmoe_dtype dt, int T, int n_experts, int k,
 size_t bmoe_route_balance_workspace_bytes(int T, int n_experts, int k) {
   if (n_experts < 1 || n_experts > kMaxExperts || k < 1 || T < 0 || (long long)T * k > INT_MAX)
     return 0;
-  return 256;
+  return up256(balance_part_bytes((long long)T * k, n_experts)) + 256;
 }
 
 bmoe_status bmoe_route_balance(int T, int n_experts, int k, const int32_t* ids, int accumulate,
@@ -228,7 +228,7 @@ bmoe_status bmoe_route_balance(int T, int n_experts, int k, const int32_t* ids, 
   if (!ws || ws_bytes < need) return BMOE_E_WORKSPACE;
   if (!ok16(ids) || !ok16(load) || !ok16(bias) || !ok16(ws)) return BMOE_E_ALIGN;
   return launch_balance((long long)T * k, n_experts, ids, accumulate, rate, load, bias,
-                        static_cast<hipStream_t>(stream)) == hipSuccess
+                        static_cast<int*>(ws), static_cast<hipStream_t>(stream)) == hipSuccess
              ? BMOE_OK
              : BMOE_E_HIP;
 }

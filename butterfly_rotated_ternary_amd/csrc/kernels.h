@@ -224,8 +224,10 @@ hipError_t launch_route_bwd(bmoe_dtype dt, int T, int N, int k, const RouteSpec&
                             float* dlogits, hipStream_t s);
 // load [N] = (accumulate ? load : 0) + counts of the M ids; bias (may be
 // NULL) [N] += rate * sign(sum(load) / N - load).
+// part: scratch of balance_part_bytes(M, N).
+size_t balance_part_bytes(long long M, int N);
 hipError_t launch_balance(long long M, int N, const int32_t* ids, int accumulate, float rate,
-                          int32_t* load, float* bias, hipStream_t s);
+                          int32_t* load, float* bias, int* part, hipStream_t s);
 // dl as k pairs (expert id, coefficient's bits) per token, for the specs under
 // which only the picks move (not softmax without renorm), and the same by
 // range of `tokens` tokens and expert: list entries (token, coefficient) of

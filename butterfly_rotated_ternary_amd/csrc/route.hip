@@ -661,9 +661,57 @@ __global__ __launch_bounds__(WAVES * 64) void route_pairs_kernel(
 }
 
 // ---- loads and the balance bias -----------------------------------------------------
-// One workgroup: a histogram in LDS (integers, so the order does not matter),
-// then bias[e] += rate * sign(mean - load[e]) with the comparison in integers
-// (sum of the loads against N * load).
+// Histograms in LDS (integers, so no order matters), then bias[e] += rate *
+// sign(mean - load[e]) with the comparison in integers (sum of the loads
+// against N * load). Few ids: one workgroup does it all. More: kShares
+// workgroups count a share each and write their histograms; a second launch
+// adds them (no counters to clear, nothing left between calls). Bound by
+// latency: 2^18 ids are 1 MB. Measured at 262144 ids, 256 experts: one
+// workgroup 42 us, shares 12 us (two launches).
+constexpr int kBalanceShares = 64, kBalanceOne = 16384;  // ids that one workgroup takes
+
+__device__ __forceinline__ void count_ids(const int32_t* ids, long long r0, long long r1, int N,
+                                          int* hist) {
+  // r0 is a multiple of 4: 16-byte loads, eight in flight per thread
+  const int4* p = reinterpret_cast<const int4*>(ids);
+  const long long v1 = r1 / 4;
+  auto add = [&](int e) {
+    if (e >= 0 && e < N) atomicAdd(&hist[e], 1);
+  };
+  for (long long v0 = r0 / 4; v0 < v1; v0 += 8 * 1024) {
+    int4 x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const long long v = v0 + u * 1024 + threadIdx.x;
+      x[u] = v < v1 ? p[v] : make_int4(-1, -1, -1, -1);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      add(x[u].x);
+      add(x[u].y);
+      add(x[u].z);
+      add(x[u].w);
+    }
+  }
+  for (long long r = v1 * 4 + threadIdx.x; r < r1; r += 1024) add(ids[r]);
+}
+
+// hist: the experts' loads. Writes load and moves the bias.
+__device__ __forceinline__ void finish_loads(const int* hist, int N, float rate, int32_t* load,
+                                             float* bias, long long* sum) {
+  long long part = 0;
+  for (int e = threadIdx.x; e < N; e += 1024) part += hist[e];
+  if (part) atomicAdd((unsigned long long*)sum, (unsigned long long)part);
+  __syncthreads();
+  for (int e = threadIdx.x; e < N; e += 1024) {
+    load[e] = hist[e];
+    if (bias) {
+      const long long diff = *sum - (long long)N * hist[e];
+      bias[e] += diff > 0 ? rate : diff < 0 ? -rate : 0.f;
+    }
+  }
+}
+
 __global__ __launch_bounds__(1024) void balance_kernel(const int32_t* ids, long long M, int N,
                                                        int accumulate, float rate, int32_t* load,
                                                        float* bias) {
@@ -672,22 +720,43 @@ __global__ __launch_bounds__(1024) void balance_kernel(const int32_t* ids, long 
   if (threadIdx.x == 0) sum = 0;
   for (int e = threadIdx.x; e < N; e += 1024) hist[e] = accumulate ? load[e] : 0;
   __syncthreads();
-  for (long long r = threadIdx.x; r < M; r += 1024) {
-    const int e = ids[r];
-    if (e >= 0 && e < N) atomicAdd(&hist[e], 1);
-  }
+  count_ids(ids, 0, M, N, hist);
   __syncthreads();
-  long long part = 0;
-  for (int e = threadIdx.x; e < N; e += 1024) part += hist[e];
-  if (part) atomicAdd((unsigned long long*)&sum, (unsigned long long)part);
+  finish_loads(hist, N, rate, load, bias, &sum);
+}
+
+// part [kBalanceShares][N]: each workgroup's counts of its share.
+__global__ __launch_bounds__(1024) void balance_count_kernel(const int32_t* ids, long long M,
+                                                             int N, long long share, int* part) {
+  __shared__ int hist[kMaxExperts];
+  for (int e = threadIdx.x; e < N; e += 1024) hist[e] = 0;
   __syncthreads();
-  for (int e = threadIdx.x; e < N; e += 1024) {
-    load[e] = hist[e];
-    if (bias) {
-      const long long diff = sum - (long long)N * hist[e];
-      bias[e] += diff > 0 ? rate : diff < 0 ? -rate : 0.f;
+  const long long r0 = blockIdx.x * share;
+  if (r0 < M) count_ids(ids, r0, r0 + share < M ? r0 + share : M, N, hist);
+  __syncthreads();
+  for (int e = threadIdx.x; e < N; e += 1024) part[(size_t)blockIdx.x * N + e] = hist[e];
+}
+
+__global__ __launch_bounds__(1024) void balance_join_kernel(const int* part, int N, int accumulate,
+                                                            float rate, int32_t* load,
+                                                            float* bias) {
+  __shared__ int hist[kMaxExperts];
+  __shared__ long long sum;
+  if (threadIdx.x == 0) sum = 0;
+  for (int e = threadIdx.x; e < N; e += 1024) hist[e] = accumulate ? load[e] : 0;
+  __syncthreads();
+  // a thread adds several shares of one expert; N threads side by side
+  const int lanes = N < 1024 ? N : 1024, rows = 1024 / lanes;
+  const int row = threadIdx.x / lanes;
+  if (row < rows)
+    for (int e = threadIdx.x % lanes; e < N; e += lanes) {
+      int c = 0;
+#pragma unroll 8
+      for (int w = row; w < kBalanceShares; w += rows) c += part[(size_t)w * N + e];
+      if (c) atomicAdd(&hist[e], c);
     }
-  }
+  __syncthreads();
+  finish_loads(hist, N, rate, load, bias, &sum);
 }
 
 // Lanes per token and experts per lane: 16 lanes (4 tokens per wave) up to 256
@@ -787,10 +856,21 @@ hipError_t launch_route_pairs(int T, int N, int k, const RouteSpec& sp, const fl
 #undef BMOE_PAIRS
 }
 
+size_t balance_part_bytes(long long M, int N) {
+  return M > kBalanceOne ? (size_t)kBalanceShares * N * sizeof(int) : 0;
+}
+
 hipError_t launch_balance(long long M, int N, const int32_t* ids, int accumulate, float rate,
-                          int32_t* load, float* bias, hipStream_t s) {
-  return launch_kernel(balance_kernel, dim3(1), dim3(1024), 0, s, KernelTiming{}, ids, M, N,
-                       accumulate, rate, load, bias);
+                          int32_t* load, float* bias, int* part, hipStream_t s) {
+  if (M <= kBalanceOne)
+    return launch_kernel(balance_kernel, dim3(1), dim3(1024), 0, s, KernelTiming{}, ids, M, N,
+                         accumulate, rate, load, bias);
+  const long long share = ((M + kBalanceShares - 1) / kBalanceShares + 3) / 4 * 4;
+  const hipError_t e = launch_kernel(balance_count_kernel, dim3(kBalanceShares), dim3(1024), 0, s,
+                                     KernelTiming{}, ids, M, N, share, part);
+  if (e != hipSuccess) return e;
+  return launch_kernel(balance_join_kernel, dim3(1), dim3(1024), 0, s, KernelTiming{},
+                       static_cast<const int*>(part), N, accumulate, rate, load, bias);
 }
 
 }  // namespace bmoe
