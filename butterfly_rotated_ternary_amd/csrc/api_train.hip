@@ -61,6 +61,8 @@ PairsLayout router_pairs_layout(int T, int d, int N, int k) {
   return l;
 }
 
+size_t parts_bytes(int T, int N) { return up256((size_t)T * 3 * router_parts_experts(N) * 2); }
+
 // The list of a gradient call: types, NULLs, alignment to the element, and
 // (where it is written) no two written tensors, and no written and another
 // read tensor, that share bytes. `out` may repeat `grads` entry by entry.
@@ -238,8 +240,13 @@ size_t bmoe_router_backward_workspace_bytes(bmoe_dtype dt, int T, int d, int n_e
       n_experts > kMaxExperts || k < 1 || k > n_experts || k > kMaxPicks || T < 0 ||
       (long long)T * k > INT_MAX)
     return 0;
-  // dl [T][N], or the picks' pairs and lists and the dW of the token ranges
-  const size_t dense = up256((size_t)T * n_experts * sizeof(float));
+  // dl [T][N] (its three parts for bf16, with the dW of the token ranges), or
+  // the picks' pairs and lists with the dW of theirs
+  size_t dense = up256((size_t)T * n_experts * sizeof(float));
+  if (dt == BMOE_BF16) {
+    const int S = router_dense_splits(T, d, n_experts);
+    dense = parts_bytes(T, n_experts) + (S > 1 ? (size_t)S * n_experts * d * sizeof(float) : 0);
+  }
   const size_t sparse = router_pairs_layout(T, d, n_experts, k).total;
   return (dense > sparse ? dense : sparse) + 256;
 }
@@ -273,6 +280,17 @@ bmoe_status bmoe_router_backward(bmoe_dtype dt, int T, int d, int n_experts, int
     if (launch_route_pairs(T, n_experts, k, sp, logits, ids, dgates, rp, s) != hipSuccess ||
         launch_router_bwd_sparse(dt, T, d, n_experts, k, x, w_router, rp, dx_add, dx, dw,
                                  reinterpret_cast<float*>(base + l.part), s) != hipSuccess)
+      return BMOE_E_HIP;
+    return BMOE_OK;
+  }
+  if (T > 0 && dt == BMOE_BF16) {
+    uint16_t* parts = static_cast<uint16_t*>(ws);
+    float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + parts_bytes(T, n_experts));
+    if (launch_route_bwd_parts(T, n_experts, k, sp, logits, ids, dgates, parts, s) != hipSuccess ||
+        launch_router_bwd_parts(T, d, n_experts, static_cast<const uint16_t*>(x),
+                                static_cast<const uint16_t*>(w_router), parts,
+                                static_cast<const uint16_t*>(dx_add), static_cast<uint16_t*>(dx),
+                                dw, part, s) != hipSuccess)
       return BMOE_E_HIP;
     return BMOE_OK;
   }

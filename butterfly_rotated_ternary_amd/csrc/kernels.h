@@ -249,6 +249,18 @@ hipError_t launch_route_pairs(int T, int N, int k, const RouteSpec& sp, const fl
 hipError_t launch_router_bwd_sparse(bmoe_dtype dt, int T, int d, int N, int k, const void* x,
                                     const void* w, const RouterPairs& rp, const void* dx_add,
                                     void* dx, float* dw, float* part, hipStream_t s);
+// dl (any spec, fp32 logits) as three bf16 parts [T][Np / 32][3][32] whose sum
+// is dl, Np = router_parts_experts(N), zeros from N on.
+__host__ __device__ inline int router_parts_experts(int N) { return (N + 63) / 64 * 64; }
+hipError_t launch_route_bwd_parts(int T, int N, int k, const RouteSpec& sp, const float* logits,
+                                  const int32_t* ids, const float* dgates, uint16_t* parts,
+                                  hipStream_t s);
+// The router product's gradient from them, bf16 x and W; part: fp32
+// [router_dense_splits][N][d] scratch (unused where that is 1). T >= 1.
+int router_dense_splits(int T, int d, int N);
+hipError_t launch_router_bwd_parts(int T, int d, int N, const uint16_t* x, const uint16_t* w,
+                                   const uint16_t* parts, const uint16_t* dx_add, uint16_t* dx,
+                                   float* dw, float* part, hipStream_t s);
 // Gradient of the router's product from dl [T][N]: dx = dx_add (may be NULL)
 // + dl W, dw [N][d] fp32 = dl^T x.
 hipError_t launch_router_bwd(bmoe_dtype dt, int T, int d, int N, const void* x, const void* w,

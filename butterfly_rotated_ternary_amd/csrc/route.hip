@@ -524,10 +524,14 @@ __device__ __forceinline__ float pick_grad(float l, float u, const RouteSpec& sp
   return l == -INFINITY ? 0.f : v;
 }
 
-template <int LPT, int PER, bool VEC, typename T>
+// dl is written as fp32 [T][N], or (PARTS) as three bf16 parts whose sum is
+// dl to fp32's last bits, for the products on bf16 MFMA: [T][Np / 32][3][32],
+// Np = N rounded up to 64, zeros from N on.
+template <int LPT, int PER, bool VEC, bool PARTS, typename T>
 __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const int32_t* ids,
                                                         const float* dgates, int T_, int N, int k,
-                                                        RouteSpec sp, float* dlogits) {
+                                                        RouteSpec sp, float* dlogits,
+                                                        uint16_t* parts) {
   const int q = threadIdx.x % LPT, base = q * PER;
   const size_t tok = (size_t)blockIdx.x * (256 / LPT) + threadIdx.x / LPT;
   const bool live = tok < (size_t)T_;
@@ -565,6 +569,30 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const i
     for (int i = 0; i < PER; ++i) a[i] = l[i] == 0.f ? 0.f : l[i] * inv * (a[i] - d);
   }
   if (!live) return;
+  if constexpr (PARTS) {
+    const int np = router_parts_experts(N);
+    uint16_t* out = parts + tok * (3 * (size_t)np);
+#pragma unroll
+    for (int i = 0; i < PER; i += 4) {
+      const int e = base + i;
+      if (e >= np) continue;
+      float v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = e + u < N ? a[i + u] : 0.f;
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        uint2 w;
+        w.x = pack_bf16x2(v[0], v[1]);
+        w.y = pack_bf16x2(v[2], v[3]);
+        *reinterpret_cast<uint2*>(out + (e / 32 * 3 + p) * 32 + e % 32) = w;
+        v[0] -= bf16_lo(w.x);
+        v[1] -= bf16_hi(w.x);
+        v[2] -= bf16_lo(w.y);
+        v[3] -= bf16_hi(w.y);
+      }
+    }
+    return;
+  }
   float* out = dlogits + tok * N;
   if constexpr (VEC && PER % 4 == 0) {
 #pragma unroll
@@ -794,13 +822,14 @@ hipError_t route_t(const T* logits, const float* bias, int Tn, int N, int k, con
   if (N <= 1024) { CALL(64, 16); }             \
   CALL(64, 64)
 
-template <bool VEC, typename T>
+template <bool VEC, bool PARTS, typename T>
 hipError_t route_bwd_t(const T* logits, const int32_t* ids, const float* dgates, int Tn, int N,
-                       int k, const RouteSpec& sp, float* dlogits, hipStream_t s) {
+                       int k, const RouteSpec& sp, float* dlogits, uint16_t* parts,
+                       hipStream_t s) {
 #define BMOE_CALL(LPT, PER)                                                                      \
-  return launch_kernel(route_bwd_kernel<LPT, PER, VEC, T>,                                       \
+  return launch_kernel(route_bwd_kernel<LPT, PER, VEC, PARTS, T>,                                \
                        dim3(((unsigned)Tn + 256 / LPT - 1) / (256 / LPT)), dim3(256), 0, s,      \
-                       KernelTiming{}, logits, ids, dgates, Tn, N, k, sp, dlogits)
+                       KernelTiming{}, logits, ids, dgates, Tn, N, k, sp, dlogits, parts)
   BMOE_BY_SHAPE(BMOE_CALL);
 #undef BMOE_CALL
 }
@@ -827,12 +856,19 @@ hipError_t launch_route_bwd(bmoe_dtype dt, int T, int N, int k, const RouteSpec&
                             float* dlogits, hipStream_t s) {
   if (dt == BMOE_BF16) {
     const uint16_t* l = static_cast<const uint16_t*>(logits);
-    return N % 8 == 0 ? route_bwd_t<true>(l, ids, dgates, T, N, k, sp, dlogits, s)
-                      : route_bwd_t<false>(l, ids, dgates, T, N, k, sp, dlogits, s);
+    return N % 8 == 0 ? route_bwd_t<true, false>(l, ids, dgates, T, N, k, sp, dlogits, nullptr, s)
+                      : route_bwd_t<false, false>(l, ids, dgates, T, N, k, sp, dlogits, nullptr, s);
   }
   const float* l = static_cast<const float*>(logits);
-  return N % 4 == 0 ? route_bwd_t<true>(l, ids, dgates, T, N, k, sp, dlogits, s)
-                    : route_bwd_t<false>(l, ids, dgates, T, N, k, sp, dlogits, s);
+  return N % 4 == 0 ? route_bwd_t<true, false>(l, ids, dgates, T, N, k, sp, dlogits, nullptr, s)
+                    : route_bwd_t<false, false>(l, ids, dgates, T, N, k, sp, dlogits, nullptr, s);
+}
+
+hipError_t launch_route_bwd_parts(int T, int N, int k, const RouteSpec& sp, const float* logits,
+                                  const int32_t* ids, const float* dgates, uint16_t* parts,
+                                  hipStream_t s) {
+  return N % 4 == 0 ? route_bwd_t<true, true>(logits, ids, dgates, T, N, k, sp, nullptr, parts, s)
+                    : route_bwd_t<false, true>(logits, ids, dgates, T, N, k, sp, nullptr, parts, s);
 }
 
 hipError_t launch_route_pairs(int T, int N, int k, const RouteSpec& sp, const float* logits,

@@ -251,6 +251,216 @@ hipError_t sparse_t(int Tn, int d, int N, int k, const T* x, const T* w, const R
                        reinterpret_cast<float4*>(dw));
 }
 
+// ---- dense dl, bf16: MFMA ----------------------------------------------------------
+// dl as three bf16 parts (their products with bf16 x and W are exact, so only
+// the fp32 sums round): three MFMAs per fragment into one accumulator.
+// Operands whose reduction index is the row index of their matrix go through
+// LDS tiles of padded rows and gfx950's transposing read: lane l gets column
+// l % 32 and rows 8 (l / 32) + 0..7 of a 16-row slice from two reads. Rows are
+// padded so that four neighbours start 64 bytes apart in the banks.
+typedef short rb_v4s __attribute__((ext_vector_type(4)));
+typedef uint64_t rb_u64x2 __attribute__((ext_vector_type(2)));
+
+// Byte offset of this lane's first read for the 32 columns from col, slice 0.
+template <int STRIDE>
+__device__ __forceinline__ uint32_t tr_offset(int col, int lane) {
+  const int gr = lane >> 4, L = lane & 15;
+  return (uint32_t)((8 * (gr >> 1) + (L >> 2)) * STRIDE + (col + 16 * (gr & 1) + 4 * (L & 3)) * 2);
+}
+template <int STRIDE>
+__device__ __forceinline__ bf16x8 tr_read(const char* p) {
+  typedef __attribute__((address_space(3))) rb_v4s lds_v4s;
+  const rb_v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)p);
+  const rb_v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * STRIDE));
+  const rb_u64x2 x = {__builtin_bit_cast(uint64_t, lo), __builtin_bit_cast(uint64_t, hi)};
+  return __builtin_bit_cast(bf16x8, x);
+}
+
+// dx: 128 tokens x 128 columns per workgroup, 4 waves of 64 x 64. W goes to LDS
+// 64 experts at a time; the parts come straight from memory (16 bytes of
+// consecutive experts per lane). The tile leaves through LDS, so dx_add and dx
+// move in 128-byte pieces of a row.
+constexpr int kDxStrideW = 128 * 2 + 64;
+
+__global__ __launch_bounds__(256) void router_dx_mfma_kernel(const uint16_t* parts,
+                                                             const uint16_t* w,
+                                                             const uint16_t* dx_add, int T_,
+                                                             int d, int N, uint16_t* dx) {
+  __shared__ __attribute__((aligned(16))) char ws[64 * kDxStrideW];
+  __shared__ float tile[4][32][68];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int c0 = blockIdx.x * 128, np = router_parts_experts(N);
+  const size_t t0 = (size_t)blockIdx.y * 128 + wm * 64;
+  const uint16_t* arow[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    size_t t = t0 + 32 * i + (lane & 31);
+    if (t >= (size_t)T_) t = T_ - 1;
+    arow[i] = parts + t * (3 * (size_t)np) + 8 * (lane >> 5);
+  }
+  uint32_t off[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) off[j] = tr_offset<kDxStrideW>(wn * 64 + 32 * j, lane);
+  f32x16 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+
+  for (int e0 = 0; e0 < np; e0 += 64) {
+    uint4 a[4][3][2];
+#pragma unroll
+    for (int sl = 0; sl < 4; ++sl)
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          a[sl][p][i] = *reinterpret_cast<const uint4*>(arow[i] + ((e0 / 32 + sl / 2) * 3 + p) * 32 +
+                                                        sl % 2 * 16);
+    uint4 b[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = (tid + u * 256) / 16, ch = (tid + u * 256) % 16;
+      const int e = e0 + r, c = c0 + ch * 8;
+      b[u] = e < N && c < d ? *reinterpret_cast<const uint4*>(w + (size_t)e * d + c)
+                            : make_uint4(0, 0, 0, 0);
+    }
+    if (e0 > 0) __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = (tid + u * 256) / 16, ch = (tid + u * 256) % 16;
+      *reinterpret_cast<uint4*>(ws + r * kDxStrideW + ch * 16) = b[u];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int sl = 0; sl < 4; ++sl) {
+      bf16x8 bf[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) bf[j] = tr_read<kDxStrideW>(ws + off[j] + sl * 16 * kDxStrideW);
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                __builtin_bit_cast(bf16x8, a[sl][p][i]), bf[j], acc[i][j], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (i > 0) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        tile[wave][8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)][32 * j + (lane & 31)] = acc[i][j][r];
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int row = (u * 64 + lane) / 8, cc = (u * 64 + lane) % 8 * 8;
+      const size_t t = t0 + 32 * i + row;
+      const int c = c0 + wn * 64 + cc;
+      if (t >= (size_t)T_ || c >= d) continue;
+      float v[8], add[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[x] = tile[wave][row][cc + x];
+      if (dx_add) {
+        load16(dx_add + t * d + c, add);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] += add[x];
+      }
+      store16(v, dx + t * d + c, 1.f);
+    }
+  }
+}
+
+// dW: 64 experts x 256 columns per workgroup and range of tokens, 8 waves of
+// 32 x 64, 64 tokens per step; two LDS buffers filled through registers, one
+// barrier per step.
+constexpr int kDwStrideA = 192 * 2 + 64, kDwStrideB = 256 * 2 + 64;
+
+__global__ __launch_bounds__(512) void router_dw_mfma_kernel(const uint16_t* parts,
+                                                             const uint16_t* x, int T_, int d,
+                                                             int N, int tokens_per_split,
+                                                             float* out) {
+  __shared__ __attribute__((aligned(16))) char as[2][64 * kDwStrideA];
+  __shared__ __attribute__((aligned(16))) char bs[2][64 * kDwStrideB];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave >> 2, wn = wave & 3;
+  const int c0 = blockIdx.x * 256, e0 = blockIdx.y * 64, np = router_parts_experts(N);
+  const size_t t0 = (size_t)blockIdx.z * tokens_per_split;
+  const int rows = t0 < (size_t)T_ ? (int)min((size_t)tokens_per_split, (size_t)T_ - t0) : 0;
+  const uint16_t* ap = parts + t0 * (3 * (size_t)np) + e0 * 3;
+  const uint16_t* bp = x + t0 * d + c0;
+  const uint32_t offa = tr_offset<kDwStrideA>(wm * 96, lane);
+  uint32_t offb[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) offb[j] = tr_offset<kDwStrideB>(wn * 64 + 32 * j, lane);
+  f32x16 acc[2] = {f32x16{}, f32x16{}};
+  uint4 ra[3], rb[4];
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+      const int r = r0 + (tid + u * 512) / 24, ch = (tid + u * 512) % 24;
+      ra[u] = r < rows ? *reinterpret_cast<const uint4*>(ap + (size_t)r * 3 * np + ch * 8) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = r0 + (tid + u * 512) / 32, ch = (tid + u * 512) % 32;
+      rb[u] = r < rows && c0 + ch * 8 < d
+                  ? *reinterpret_cast<const uint4*>(bp + (size_t)r * d + ch * 8)
+                  : zero;
+    }
+  };
+  auto store = [&](int buf) {
+#pragma unroll
+    for (int u = 0; u < 3; ++u)
+      *reinterpret_cast<uint4*>(as[buf] + (tid + u * 512) / 24 * kDwStrideA +
+                                (tid + u * 512) % 24 * 16) = ra[u];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      *reinterpret_cast<uint4*>(bs[buf] + (tid + u * 512) / 32 * kDwStrideB +
+                                (tid + u * 512) % 32 * 16) = rb[u];
+  };
+  load(0);
+  store(0);
+  __syncthreads();
+  for (int r0 = 0, buf = 0; r0 < rows; r0 += 64, buf ^= 1) {
+    const bool more = r0 + 64 < rows;
+    if (more) load(r0 + 64);
+#pragma unroll
+    for (int sl = 0; sl < 4; ++sl) {
+      bf16x8 a[3], b[2];
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+        a[p] = tr_read<kDwStrideA>(as[buf] + offa + p * 64 + sl * 16 * kDwStrideA);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        b[j] = tr_read<kDwStrideB>(bs[buf] + offb[j] + sl * 16 * kDwStrideB);
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[p], b[j], acc[j], 0, 0, 0);
+    }
+    if (more) store(buf ^ 1);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int c = c0 + wn * 64 + 32 * j + (lane & 31);
+    if (c >= d) continue;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int e = e0 + wm * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+      if (e < N) out[((size_t)blockIdx.z * N + e) * d + c] = acc[j][r];
+    }
+  }
+}
+
 template <typename T>
 hipError_t bwd_t(int Tn, int d, int N, const T* x, const T* w, const float* dl, const T* dx_add,
                  T* dx, float* dw, hipStream_t s) {
@@ -283,6 +493,41 @@ hipError_t launch_router_bwd_sparse(bmoe_dtype dt, int T, int d, int N, int k, c
                     s);
   return sparse_t(T, d, N, k, static_cast<const float*>(x), static_cast<const float*>(w), rp,
                   static_cast<const float*>(dx_add), static_cast<float*>(dx), dw, part, s);
+}
+
+// Token ranges of the dense dW: one workgroup per CU (its LDS), at least four
+// steps each.
+int router_dense_splits(int T, int d, int N) {
+  const int tiles = (d + 255) / 256 * (router_parts_experts(N) / 64);
+  int S = (256 + tiles - 1) / tiles;
+  const int most = (T + 255) / 256;
+  if (S > most) S = most;
+  return S < 1 ? 1 : S;
+}
+
+hipError_t launch_router_bwd_parts(int T, int d, int N, const uint16_t* x, const uint16_t* w,
+                                   const uint16_t* parts, const uint16_t* dx_add, uint16_t* dx,
+                                   float* dw, float* part, hipStream_t s) {
+  // token tiles on y in launches of 65535 at most
+  for (size_t t = 0; t < (size_t)T; t += (size_t)65535 * 128) {
+    const size_t left = (size_t)T - t, most = (size_t)65535 * 128;
+    const int n = (int)(left < most ? left : most);
+    const hipError_t e = launch_kernel(
+        router_dx_mfma_kernel, dim3((d + 127) / 128, (n + 127) / 128), dim3(256), 0, s,
+        KernelTiming{}, parts + t * 3 * router_parts_experts(N), w,
+        dx_add ? dx_add + t * d : dx_add, n, d, N, dx + t * d);
+    if (e != hipSuccess) return e;
+  }
+  const int S = router_dense_splits(T, d, N);
+  const int per = ((T + S - 1) / S + 63) / 64 * 64;
+  hipError_t e = launch_kernel(router_dw_mfma_kernel,
+                               dim3((d + 255) / 256, router_parts_experts(N) / 64, S), dim3(512),
+                               0, s, KernelTiming{}, parts, x, T, d, N, per, S == 1 ? dw : part);
+  if (e != hipSuccess || S == 1) return e;
+  const size_t n4 = (size_t)N * d / 4;
+  return launch_kernel(router_dw_join_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s,
+                       KernelTiming{}, reinterpret_cast<const float4*>(part), S, n4,
+                       reinterpret_cast<float4*>(dw));
 }
 
 hipError_t launch_router_bwd(bmoe_dtype dt, int T, int d, int N, const void* x, const void* w,
