@@ -323,8 +323,9 @@ __global__ __launch_bounds__(256) void router_dx_mfma_kernel(const uint16_t* par
     for (int u = 0; u < 4; ++u) {
       const int r = (tid + u * 256) / 16, ch = (tid + u * 256) % 16;
       const int e = e0 + r, c = c0 + ch * 8;
-      b[u] = e < N && c < d ? *reinterpret_cast<const uint4*>(w + (size_t)e * d + c)
-                            : make_uint4(0, 0, 0, 0);
+      // (past the end: any row and column; the parts there are 0, and nothing
+      // past d is stored)
+      b[u] = *reinterpret_cast<const uint4*>(w + (size_t)min(e, N - 1) * d + (c < d ? c : 0));
     }
     if (e0 > 0) __syncthreads();
 #pragma unroll
@@ -400,33 +401,41 @@ __global__ __launch_bounds__(512) void router_dw_mfma_kernel(const uint16_t* par
   for (int j = 0; j < 2; ++j) offb[j] = tr_offset<kDwStrideB>(wn * 64 + 32 * j, lane);
   f32x16 acc[2] = {f32x16{}, f32x16{}};
   uint4 ra[3], rb[4];
-  const uint4 zero = make_uint4(0, 0, 0, 0);
+  // Loads of rows or columns past the end go to the last row or to column 0
+  // (no branches between the loads) and become zeros on their way to LDS.
   auto load = [&](int r0) {
 #pragma unroll
     for (int u = 0; u < 3; ++u) {
       const int r = r0 + (tid + u * 512) / 24, ch = (tid + u * 512) % 24;
-      ra[u] = r < rows ? *reinterpret_cast<const uint4*>(ap + (size_t)r * 3 * np + ch * 8) : zero;
+      ra[u] = *reinterpret_cast<const uint4*>(ap + (size_t)min(r, rows - 1) * 3 * np + ch * 8);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int r = r0 + (tid + u * 512) / 32, ch = (tid + u * 512) % 32;
-      rb[u] = r < rows && c0 + ch * 8 < d
-                  ? *reinterpret_cast<const uint4*>(bp + (size_t)r * d + ch * 8)
-                  : zero;
+      rb[u] = *reinterpret_cast<const uint4*>(bp + (size_t)min(r, rows - 1) * d +
+                                              (c0 + ch * 8 < d ? ch * 8 : 0));
     }
   };
-  auto store = [&](int buf) {
-#pragma unroll
-    for (int u = 0; u < 3; ++u)
-      *reinterpret_cast<uint4*>(as[buf] + (tid + u * 512) / 24 * kDwStrideA +
-                                (tid + u * 512) % 24 * 16) = ra[u];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      *reinterpret_cast<uint4*>(bs[buf] + (tid + u * 512) / 32 * kDwStrideB +
-                                (tid + u * 512) % 32 * 16) = rb[u];
+  auto keep = [](uint4 v, bool ok) {
+    return make_uint4(ok ? v.x : 0u, ok ? v.y : 0u, ok ? v.z : 0u, ok ? v.w : 0u);
   };
-  load(0);
-  store(0);
+  auto store = [&](int r0, int buf) {
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+      const int r = (tid + u * 512) / 24, ch = (tid + u * 512) % 24;
+      *reinterpret_cast<uint4*>(as[buf] + r * kDwStrideA + ch * 16) = keep(ra[u], r0 + r < rows);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = (tid + u * 512) / 32, ch = (tid + u * 512) % 32;
+      *reinterpret_cast<uint4*>(bs[buf] + r * kDwStrideB + ch * 16) =
+          keep(rb[u], r0 + r < rows && c0 + ch * 8 < d);
+    }
+  };
+  if (rows > 0) {
+    load(0);
+    store(0, 0);
+  }
   __syncthreads();
   for (int r0 = 0, buf = 0; r0 < rows; r0 += 64, buf ^= 1) {
     const bool more = r0 + 64 < rows;
@@ -446,7 +455,7 @@ __global__ __launch_bounds__(512) void router_dw_mfma_kernel(const uint16_t* par
         for (int j = 0; j < 2; ++j)
           acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[p], b[j], acc[j], 0, 0, 0);
     }
-    if (more) store(buf ^ 1);
+    if (more) store(r0 + 64, buf ^ 1);
     __syncthreads();
   }
 #pragma unroll
