@@ -606,12 +606,40 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const i
   }
 }
 
-// The picks' (id, coefficient) pairs of one range of tokens, and the same
-// listed by expert (stable): one workgroup per range. Each wave owns a
-// contiguous share of the range's picks; equal experts within 64 picks are
-// ranked by ballots over the id's bits.
-template <int LPT, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void route_pairs_kernel(
+// Token i of `nt` from t0 on: its picks' (id, coefficient) pairs, by THREADS
+// threads.
+template <int LPT, int THREADS>
+__device__ __forceinline__ void make_pairs(const float* logits, const int32_t* ids,
+                                           const float* dgates, size_t t0, int nt, int N, int k,
+                                           const RouteSpec& sp, int2* pairs) {
+  const int q = threadIdx.x % LPT;
+  for (int i = threadIdx.x / LPT; i - (int)threadIdx.x / LPT < nt; i += THREADS / LPT) {
+    const size_t tok = t0 + i;
+    const bool mine = i < nt && q < k;
+    const int id = mine ? ids[tok * k + q] : -1;
+    const bool pick = id >= 0 && id < N;
+    const float l = pick ? logits[tok * N + id] : -INFINITY;
+    const float u = pick ? sp.scale * dgates[tok * k + q] : 0.f;
+    const float v = pick_grad<LPT>(l, u, sp);
+    if (mine) pairs[tok * k + q] = make_int2(pick ? id : 0, __float_as_int(pick ? v : 0.f));
+  }
+}
+
+template <int LPT>
+__global__ __launch_bounds__(256) void route_pairs_kernel(const float* logits, const int32_t* ids,
+                                                          const float* dgates, int T_, int N,
+                                                          int k, RouteSpec sp, int2* pairs) {
+  const size_t t0 = (size_t)blockIdx.x * (256 / LPT);
+  const int nt = (int)min((size_t)(256 / LPT), (size_t)T_ - t0);
+  make_pairs<LPT, 256>(logits, ids, dgates, t0, nt, N, k, sp, pairs);
+}
+
+// The pairs of one range of tokens listed by expert (stable): one workgroup
+// per range. Each wave owns a contiguous share of the range's picks; equal
+// experts within 64 picks are ranked by ballots over the id's bits. MAKE: the
+// workgroup makes its range's pairs first (short ranges, one launch less).
+template <int LPT, int WAVES, bool MAKE>
+__global__ __launch_bounds__(WAVES * 64) void route_lists_kernel(
     const float* logits, const int32_t* ids, const float* dgates, int T_, int N, int k, int nbits,
     RouteSpec sp, RouterPairs rp) {
   extern __shared__ int cur[];  // [WAVES][N]: counts, then cursors
@@ -621,17 +649,8 @@ __global__ __launch_bounds__(WAVES * 64) void route_pairs_kernel(
   const size_t t0 = (size_t)blockIdx.x * rp.tokens;
   const int nt = (int)min((size_t)rp.tokens, (size_t)T_ - t0);
   for (int i = tid; i < WAVES * N; i += kThreads) cur[i] = 0;
-  const int q = tid % LPT;
-  for (int i = tid / LPT; i - tid / LPT < nt; i += kThreads / LPT) {
-    const size_t tok = t0 + i;
-    const bool mine = i < nt && q < k;
-    const int id = mine ? ids[tok * k + q] : -1;
-    const bool pick = id >= 0 && id < N;
-    const float l = pick ? logits[tok * N + id] : -INFINITY;
-    const float u = pick ? sp.scale * dgates[tok * k + q] : 0.f;
-    const float v = pick_grad<LPT>(l, u, sp);
-    if (mine) rp.pairs[tok * k + q] = make_int2(pick ? id : 0, __float_as_int(pick ? v : 0.f));
-  }
+  if constexpr (MAKE)
+    make_pairs<LPT, kThreads>(logits, ids, dgates, t0, nt, N, k, sp, rp.pairs);
   __syncthreads();
 
   const int M = nt * k;
@@ -639,6 +658,7 @@ __global__ __launch_bounds__(WAVES * 64) void route_pairs_kernel(
   const int share = ((M + WAVES - 1) / WAVES + 63) / 64 * 64;
   const int wb = min(M, wave * share), we = min(M, wb + share);
   int* mycur = cur + wave * N;
+#pragma unroll 8
   for (int r = wb + lane; r < we; r += 64) {
     const int2 p = pairs[r];
     if (__int_as_float(p.y) != 0.f) atomicAdd(&mycur[p.x], 1);
@@ -876,19 +896,30 @@ hipError_t launch_route_pairs(int T, int N, int k, const RouteSpec& sp, const fl
                               hipStream_t s) {
   int nbits = 0;
   while ((1 << nbits) < N) ++nbits;
+  // Ranges of up to 2048 lanes' worth of picks make their pairs themselves;
+  // longer ones wait too long for their gathers (4096 tokens of 4 picks: 59 us
+  // by 8 workgroups), so a launch over all CUs makes them.
+  const int lpt = k <= 2 ? 2 : k <= 4 ? 4 : k <= 8 ? 8 : k <= 16 ? 16 : 64;
+  const bool make = (long long)rp.tokens * lpt <= 2048;
   // 16 waves while their cursors take 32 KB at most, else 4 (64 KB at 4096)
-#define BMOE_PAIRS(LPT)                                                                        \
-  return N <= 512 ? launch_kernel(route_pairs_kernel<LPT, 16>, dim3(rp.ranges), dim3(1024),    \
-                                  16 * N * 4, s, KernelTiming{}, logits, ids, dgates, T, N, k, \
-                                  nbits, sp, rp)                                               \
-                  : launch_kernel(route_pairs_kernel<LPT, 4>, dim3(rp.ranges), dim3(256),      \
-                                  4 * N * 4, s, KernelTiming{}, logits, ids, dgates, T, N, k,  \
-                                  nbits, sp, rp)
+#define BMOE_LISTS(LPT, WAVES, MAKE)                                                            \
+  launch_kernel(route_lists_kernel<LPT, WAVES, MAKE>, dim3(rp.ranges), dim3(WAVES * 64),        \
+                WAVES * N * 4, s, KernelTiming{}, logits, ids, dgates, T, N, k, nbits, sp, rp)
+#define BMOE_PAIRS(LPT)                                                                         \
+  do {                                                                                          \
+    if (make) return N <= 512 ? BMOE_LISTS(LPT, 16, true) : BMOE_LISTS(LPT, 4, true);           \
+    const hipError_t e =                                                                        \
+        launch_kernel(route_pairs_kernel<LPT>, dim3(((unsigned)T + 256 / LPT - 1) / (256 / LPT)), \
+                      dim3(256), 0, s, KernelTiming{}, logits, ids, dgates, T, N, k, sp, rp.pairs); \
+    if (e != hipSuccess) return e;                                                              \
+    return N <= 512 ? BMOE_LISTS(2, 16, false) : BMOE_LISTS(2, 4, false);                       \
+  } while (0)
   if (k <= 2) BMOE_PAIRS(2);
   if (k <= 4) BMOE_PAIRS(4);
   if (k <= 8) BMOE_PAIRS(8);
   if (k <= 16) BMOE_PAIRS(16);
   BMOE_PAIRS(64);
+#undef BMOE_LISTS
 #undef BMOE_PAIRS
 }
 

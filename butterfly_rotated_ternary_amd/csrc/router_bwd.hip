@@ -135,7 +135,8 @@ __device__ __forceinline__ void sparse_dw(const SparseArgs<T>& p, float* sums) {
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  constexpr int kU = 8;  // rows in flight per lane
+  constexpr int kU = 4;  // rows in flight per lane: 8 take registers that cost the dx role
+                         // more (T = 32768, d = 4096: 295 us of both roles, 4: 236 us)
   int q = lo + slot;
   for (; q + (kU - 1) * slots < hi; q += kU * slots) {
     int2 ent[kU];
@@ -190,12 +191,27 @@ __device__ __forceinline__ void sparse_dx(const SparseArgs<T>& p, unsigned block
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = fmaf(f, v[i], acc[i]);
   }
+  // (streamed, so that W and the dW role's rows of x keep the caches)
   if (p.dx_add) {
-    load16(p.dx_add + t * p.d + c, v);
+    const u32x4 a =
+        __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.dx_add + t * p.d + c));
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] += v[i];
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (V == 8) {
+        acc[2 * i] += bf16_lo(a[i]);
+        acc[2 * i + 1] += bf16_hi(a[i]);
+      } else {
+        acc[i] += __uint_as_float(a[i]);
+      }
+    }
   }
-  store16(acc, p.dx + t * p.d + c, 1.f);
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (V == 8) o[i] = pack_bf16x2(acc[2 * i], acc[2 * i + 1]);
+    else o[i] = __float_as_uint(acc[i]);
+  }
+  __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(p.dx + t * p.d + c));
 }
 
 template <typename T, bool WIDE>
@@ -276,63 +292,66 @@ __device__ __forceinline__ bf16x8 tr_read(const char* p) {
   return __builtin_bit_cast(bf16x8, x);
 }
 
-// dx: 128 tokens x 128 columns per workgroup, 4 waves of 64 x 64. W goes to LDS
+// dx: 64 tokens x 128 columns per workgroup, 4 waves of 32 x 64. W goes to LDS
 // 64 experts at a time; the parts come straight from memory (16 bytes of
-// consecutive experts per lane). The tile leaves through LDS, so dx_add and dx
-// move in 128-byte pieces of a row.
+// consecutive experts per lane), dx_add is under way from the start. The tile
+// leaves through LDS (the W tile's, done with by then), so dx_add and dx move
+// in 128-byte pieces of a row. Small tiles, so that four workgroups share a CU
+// and one's loads run under another's MFMAs: at T = 16384, d = 2048, 64
+// experts 128 x 128 tiles at two per CU took 56 us, these 31 us (134 MB).
 constexpr int kDxStrideW = 128 * 2 + 64;
 
+template <bool ADD>
 __global__ __launch_bounds__(256) void router_dx_mfma_kernel(const uint16_t* parts,
                                                              const uint16_t* w,
-                                                             const uint16_t* dx_add, int T_,
-                                                             int d, int N, uint16_t* dx) {
-  __shared__ __attribute__((aligned(16))) char ws[64 * kDxStrideW];
-  __shared__ float tile[4][32][68];
+                                                             const uint16_t* dx_add, int T_, int d,
+                                                             int N, uint16_t* dx) {
+  __shared__ __attribute__((aligned(16))) float lds[4 * 32 * 68];
+  static_assert(sizeof(lds) >= 64 * kDxStrideW, "the W tile shares it");
+  char* const ws = reinterpret_cast<char*>(lds);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 1, wn = wave & 1;
+  float* const tile = lds + wave * (32 * 68);
   const int c0 = blockIdx.x * 128, np = router_parts_experts(N);
-  const size_t t0 = (size_t)blockIdx.y * 128 + wm * 64;
-  const uint16_t* arow[2];
+  const int t0 = blockIdx.y * 64 + wm * 32;
+  const uint16_t* arow =
+      parts + (size_t)min(t0 + (lane & 31), T_ - 1) * (3 * (size_t)np) + 8 * (lane >> 5);
+  // This lane's piece u of the tile: row (u * 64 + lane) / 8, 8 columns.
+  const int cc = lane % 8 * 8, c = c0 + wn * 64 + cc;
+  u32x4 add[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    size_t t = t0 + 32 * i + (lane & 31);
-    if (t >= (size_t)T_) t = T_ - 1;
-    arow[i] = parts + t * (3 * (size_t)np) + 8 * (lane >> 5);
+  for (int u = 0; u < 4; ++u) {
+    add[u] = u32x4{0u, 0u, 0u, 0u};
+    if constexpr (ADD)
+      add[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
+          dx_add + (size_t)min(t0 + u * 8 + lane / 8, T_ - 1) * d + (c < d ? c : 0)));
   }
   uint32_t off[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) off[j] = tr_offset<kDxStrideW>(wn * 64 + 32 * j, lane);
-  f32x16 acc[2][2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+  f32x16 acc[2] = {f32x16{}, f32x16{}};
 
   for (int e0 = 0; e0 < np; e0 += 64) {
-    uint4 a[4][3][2];
+    u32x4 a[4][3];
 #pragma unroll
     for (int sl = 0; sl < 4; ++sl)
 #pragma unroll
       for (int p = 0; p < 3; ++p)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          a[sl][p][i] = *reinterpret_cast<const uint4*>(arow[i] + ((e0 / 32 + sl / 2) * 3 + p) * 32 +
-                                                        sl % 2 * 16);
-    uint4 b[4];
+        a[sl][p] = *reinterpret_cast<const u32x4*>(arow + ((e0 / 32 + sl / 2) * 3 + p) * 32 +
+                                                   sl % 2 * 16);
+    u32x4 b[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int r = (tid + u * 256) / 16, ch = (tid + u * 256) % 16;
-      const int e = e0 + r, c = c0 + ch * 8;
+      const int e = e0 + (tid + u * 256) / 16, cb = c0 + (tid + u * 256) % 16 * 8;
       // (past the end: any row and column; the parts there are 0, and nothing
       // past d is stored)
-      b[u] = *reinterpret_cast<const uint4*>(w + (size_t)min(e, N - 1) * d + (c < d ? c : 0));
+      b[u] = *reinterpret_cast<const u32x4*>(w + (size_t)min(e, N - 1) * d + (cb < d ? cb : 0));
     }
     if (e0 > 0) __syncthreads();
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int r = (tid + u * 256) / 16, ch = (tid + u * 256) % 16;
-      *reinterpret_cast<uint4*>(ws + r * kDxStrideW + ch * 16) = b[u];
-    }
+    for (int u = 0; u < 4; ++u)
+      *reinterpret_cast<u32x4*>(ws + (tid + u * 256) / 16 * kDxStrideW + (tid + u * 256) % 16 * 16) =
+          b[u];
     __syncthreads();
 #pragma unroll
     for (int sl = 0; sl < 4; ++sl) {
@@ -342,38 +361,30 @@ __global__ __launch_bounds__(256) void router_dx_mfma_kernel(const uint16_t* par
 #pragma unroll
       for (int p = 0; p < 3; ++p)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                __builtin_bit_cast(bf16x8, a[sl][p][i]), bf[j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < 2; ++j)
+          acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a[sl][p]),
+                                                           bf[j], acc[j], 0, 0, 0);
     }
   }
+  __syncthreads();  // W is done with
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (i > 0) __syncthreads();
+  for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int r = 0; r < 16; ++r)
+      tile[(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * 68 + 32 * j + (lane & 31)] = acc[j][r];
+  __syncthreads();
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        tile[wave][8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)][32 * j + (lane & 31)] = acc[i][j][r];
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int row = (u * 64 + lane) / 8, cc = (u * 64 + lane) % 8 * 8;
-      const size_t t = t0 + 32 * i + row;
-      const int c = c0 + wn * 64 + cc;
-      if (t >= (size_t)T_ || c >= d) continue;
-      float v[8], add[8];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) v[x] = tile[wave][row][cc + x];
-      if (dx_add) {
-        load16(dx_add + t * d + c, add);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) v[x] += add[x];
-      }
-      store16(v, dx + t * d + c, 1.f);
-    }
+  for (int u = 0; u < 4; ++u) {
+    const int row = u * 8 + lane / 8, t = t0 + row;
+    if (t >= T_ || c >= d) continue;
+    const float4 v0 = *reinterpret_cast<const float4*>(tile + row * 68 + cc);
+    const float4 v1 = *reinterpret_cast<const float4*>(tile + row * 68 + cc + 4);
+    u32x4 o;
+    o[0] = pack_bf16x2(v0.x + bf16_lo(add[u][0]), v0.y + bf16_hi(add[u][0]));
+    o[1] = pack_bf16x2(v0.z + bf16_lo(add[u][1]), v0.w + bf16_hi(add[u][1]));
+    o[2] = pack_bf16x2(v1.x + bf16_lo(add[u][2]), v1.y + bf16_hi(add[u][2]));
+    o[3] = pack_bf16x2(v1.z + bf16_lo(add[u][3]), v1.w + bf16_hi(add[u][3]));
+    __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(dx + (size_t)t * d + c));
   }
 }
 
@@ -518,13 +529,17 @@ hipError_t launch_router_bwd_parts(int T, int d, int N, const uint16_t* x, const
                                    const uint16_t* parts, const uint16_t* dx_add, uint16_t* dx,
                                    float* dw, float* part, hipStream_t s) {
   // token tiles on y in launches of 65535 at most
-  for (size_t t = 0; t < (size_t)T; t += (size_t)65535 * 128) {
-    const size_t left = (size_t)T - t, most = (size_t)65535 * 128;
+  constexpr size_t most = (size_t)65535 * 64;
+  for (size_t t = 0; t < (size_t)T; t += most) {
+    const size_t left = (size_t)T - t;
     const int n = (int)(left < most ? left : most);
-    const hipError_t e = launch_kernel(
-        router_dx_mfma_kernel, dim3((d + 127) / 128, (n + 127) / 128), dim3(256), 0, s,
-        KernelTiming{}, parts + t * 3 * router_parts_experts(N), w,
-        dx_add ? dx_add + t * d : dx_add, n, d, N, dx + t * d);
+    const dim3 grid((d + 127) / 128, (n + 63) / 64);
+    const uint16_t* p = parts + t * 3 * router_parts_experts(N);
+    const hipError_t e =
+        dx_add ? launch_kernel(router_dx_mfma_kernel<true>, grid, dim3(256), 0, s, KernelTiming{},
+                               p, w, dx_add + t * d, n, d, N, dx + t * d)
+               : launch_kernel(router_dx_mfma_kernel<false>, grid, dim3(256), 0, s, KernelTiming{},
+                               p, w, dx_add, n, d, N, dx + t * d);
     if (e != hipSuccess) return e;
   }
   const int S = router_dense_splits(T, d, N);
