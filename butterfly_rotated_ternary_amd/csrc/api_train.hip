@@ -57,7 +57,8 @@ PairsLayout router_pairs_layout(int T, int d, int N, int k) {
   l.list = list_bytes;
   l.off = l.list + list_bytes;
   l.part = l.off + up256((size_t)l.ranges * (N + 1) * sizeof(int32_t));
-  l.total = l.part + (l.ranges > 1 ? up256((size_t)l.ranges * N * d * sizeof(float)) : 0);
+  const int groups = (l.ranges + 3) / 4;
+  l.total = l.part + (groups > 1 ? up256((size_t)groups * N * d * sizeof(float)) : 0);
   return l;
 }
 

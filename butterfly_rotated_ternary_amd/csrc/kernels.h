@@ -244,8 +244,8 @@ int router_range_tokens(int T, int d, int N);
 hipError_t launch_route_pairs(int T, int N, int k, const RouteSpec& sp, const float* logits,
                               const int32_t* ids, const float* dgates, const RouterPairs& rp,
                               hipStream_t s);
-// The router product's gradient from them; part: fp32 [ranges][N][d] scratch
-// (unused with one range).
+// The router product's gradient from them; part: fp32 [groups][N][d] scratch
+// for the groups of four ranges (unused with one).
 hipError_t launch_router_bwd_sparse(bmoe_dtype dt, int T, int d, int N, int k, const void* x,
                                     const void* w, const RouterPairs& rp, const void* dx_add,
                                     void* dx, float* dw, float* part, hipStream_t s);

@@ -897,17 +897,17 @@ hipError_t launch_route_pairs(int T, int N, int k, const RouteSpec& sp, const fl
   int nbits = 0;
   while ((1 << nbits) < N) ++nbits;
   // Ranges of up to 2048 lanes' worth of picks make their pairs themselves;
-  // longer ones wait too long for their gathers (4096 tokens of 4 picks: 59 us
-  // by 8 workgroups), so a launch over all CUs makes them.
+  // longer ones wait too long for their gathers, so a launch over all CUs makes
+  // them. 16 waves for those while their cursors take 32 KB at most, else 4
+  // (64 KB at 4096 experts).
   const int lpt = k <= 2 ? 2 : k <= 4 ? 4 : k <= 8 ? 8 : k <= 16 ? 16 : 64;
   const bool make = (long long)rp.tokens * lpt <= 2048;
-  // 16 waves while their cursors take 32 KB at most, else 4 (64 KB at 4096)
 #define BMOE_LISTS(LPT, WAVES, MAKE)                                                            \
   launch_kernel(route_lists_kernel<LPT, WAVES, MAKE>, dim3(rp.ranges), dim3(WAVES * 64),        \
                 WAVES * N * 4, s, KernelTiming{}, logits, ids, dgates, T, N, k, nbits, sp, rp)
 #define BMOE_PAIRS(LPT)                                                                         \
   do {                                                                                          \
-    if (make) return N <= 512 ? BMOE_LISTS(LPT, 16, true) : BMOE_LISTS(LPT, 4, true);           \
+    if (make) return BMOE_LISTS(LPT, 4, true);                                                  \
     const hipError_t e =                                                                        \
         launch_kernel(route_pairs_kernel<LPT>, dim3(((unsigned)T + 256 / LPT - 1) / (256 / LPT)), \
                       dim3(256), 0, s, KernelTiming{}, logits, ids, dgates, T, N, k, sp, rp.pairs); \

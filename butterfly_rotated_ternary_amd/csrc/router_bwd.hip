@@ -98,13 +98,17 @@ __global__ __launch_bounds__(256) void router_dw_kernel(const float* dl, const T
 // order (launch_route_pairs). One launch does both products:
 //
 // dx: a thread takes 16 bytes of a row; the k rows of W come from L2.
-// dW: a workgroup takes one expert, one range and up to 64 V columns (V values
-//     per 16 bytes). Its row slots (4, more where a row is narrower than a
-//     wave) walk the expert's list a slot apart, each lane with V sums in
-//     registers; the slots' sums are added in slot order through LDS, the
-//     ranges' by the join kernel, so the order of every sum is fixed. The
-//     workgroups of a range run together and all walk the tokens upwards, so
-//     the k readers of a row of x meet in L2.
+// dW: a workgroup takes one expert, four consecutive ranges (one per wave) and
+//     up to 64 V columns (V values per 16 bytes). Each lane keeps V sums in
+//     registers while its wave walks the expert's list of its range (rows
+//     narrower than a wave: several at once); the sums are added in order
+//     through LDS, those of the groups of ranges by the join kernel, so the
+//     order of every sum is fixed. The workgroups of a group of ranges run
+//     together and walk the tokens upwards, so the k readers of a row of x
+//     meet in L2 (column chunk c goes to XCD c % 8).
+// The workgroups of the roles alternate, so that dx streams from HBM while dW
+// gathers from L2: at T = 32768, d = 4096, 256 experts, top 4 the roles take
+// 122 and 100 us alone, BMOE_ONE_US one after the other, BMOE_MIX_US so.
 template <typename T>
 struct SparseArgs {
   const int2* pairs;   // [T][k]
@@ -114,58 +118,86 @@ struct SparseArgs {
   const T* w;
   const T* dx_add;
   T* dx;
-  float* dw;  // [ranges][N][d] (one range: the result itself)
-  int T_, d, N, k;
-  int chunks, n_dw_blocks;  // column chunks of a row; workgroups of the dW role
+  float* dw;  // [groups of 4 ranges][N][d] (one group: the result itself)
+  int T_, d, N, k, ranges;
+  int chunks;  // column chunks of a row
 };
 
+constexpr int kU = 8;  // rows of x in flight per lane
+
 template <typename T, bool WIDE>
-__device__ __forceinline__ void sparse_dw(const SparseArgs<T>& p, float* sums) {
+__device__ __forceinline__ void sparse_dw(const SparseArgs<T>& p, unsigned block, float* sums) {
   constexpr int V = 16 / sizeof(T);
-  const int chunk = blockIdx.x % p.chunks, re = blockIdx.x / p.chunks;
-  const int e = re % p.N, range = re / p.N;
+  // (blockIdx.x % 8 is the XCD; eight consecutive `block` have all eight)
+  const int chunk = p.chunks == 8 ? blockIdx.x % 8 : block % p.chunks, re = block / p.chunks;
+  const int e = re % p.N, group = re / p.N;
   const int lpr = WIDE ? 64 : p.d / V;  // lanes per row
-  const int slots = 256 / lpr;
-  const int slot = WIDE ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : threadIdx.x / lpr;
-  const int col = threadIdx.x % lpr * V;
+  const int slots = 64 / lpr;           // rows that a wave takes at once
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int slot = WIDE ? 0 : lane / lpr;
+  const int col = lane % lpr * V;
   const int c = chunk * 64 * V + col;
-  const int32_t* off = p.off + (size_t)range * (p.N + 1) + e;
-  const int lo = off[0], hi = off[1];
+  const int range = group * 4 + wave;
+  int lo = 0, hi = 0;
+  if (range < p.ranges) {
+    const int32_t* off = p.off + (size_t)range * (p.N + 1) + e;
+    lo = off[0];
+    hi = off[1];
+  }
   const T* x = p.x + c;
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  constexpr int kU = 4;  // rows in flight per lane: 8 take registers that cost the dx role
-                         // more (T = 32768, d = 4096: 295 us of both roles, 4: 236 us)
-  int q = lo + slot;
-  for (; q + (kU - 1) * slots < hi; q += kU * slots) {
-    int2 ent[kU];
-    float v[kU][V];
+  if constexpr (WIDE) {
+    // 64 list entries at a time, one per lane; their rows by readlane, so only
+    // the rows' own loads wait on memory, kU of them in flight per lane
+    for (int q0 = lo; q0 < hi; q0 += 64) {
+      const int n = min(64, hi - q0);
+      const int2 ent = p.list[q0 + min(lane, n - 1)];
+      auto row = [&](int i) {
+        return *reinterpret_cast<const u32x4*>(
+            x + (size_t)__builtin_amdgcn_readlane(ent.x, i) * p.d);
+      };
+      auto add = [&](u32x4 v, int i) {
+        const float f = __int_as_float(__builtin_amdgcn_readlane(ent.y, i));
 #pragma unroll
-    for (int u = 0; u < kU; ++u) ent[u] = p.list[q + u * slots];
+        for (int u = 0; u < 4; ++u) {
+          if constexpr (V == 8) {
+            acc[2 * u] = fmaf(f, bf16_lo(v[u]), acc[2 * u]);
+            acc[2 * u + 1] = fmaf(f, bf16_hi(v[u]), acc[2 * u + 1]);
+          } else {
+            acc[u] = fmaf(f, __uint_as_float(v[u]), acc[u]);
+          }
+        }
+      };
+      int i = 0;
+      for (; i + kU <= n; i += kU) {
+        u32x4 v[kU];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) load16(x + (size_t)ent[u].x * p.d, v[u]);
+        for (int u = 0; u < kU; ++u) v[u] = row(i + u);
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
+        for (int u = 0; u < kU; ++u) add(v[u], i + u);
+      }
+      for (; i < n; ++i) add(row(i), i);
+    }
+  } else {
+    for (int q = lo + slot; q < hi; q += slots) {
+      const int2 ent = p.list[q];
+      float v[V];
+      load16(x + (size_t)ent.x * p.d, v);
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = fmaf(__int_as_float(ent[u].y), v[u][i], acc[i]);
-  }
-  for (; q < hi; q += slots) {
-    const int2 ent = p.list[q];
-    float v[V];
-    load16(x + (size_t)ent.x * p.d, v);
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = fmaf(__int_as_float(ent.y), v[i], acc[i]);
+      for (int i = 0; i < V; ++i) acc[i] = fmaf(__int_as_float(ent.y), v[i], acc[i]);
+    }
   }
   // sums[slot][col]
   const int cols = lpr * V;
 #pragma unroll
-  for (int i = 0; i < V; ++i) sums[slot * cols + col + i] = acc[i];
+  for (int i = 0; i < V; ++i) sums[(wave * slots + slot) * cols + col + i] = acc[i];
   __syncthreads();
-  float* dst = p.dw + ((size_t)range * p.N + e) * p.d + chunk * 64 * V;
+  float* dst = p.dw + ((size_t)group * p.N + e) * p.d + chunk * 64 * V;
   for (int i = threadIdx.x; i < cols; i += 256) {
     float a = sums[i];
-    for (int r = 1; r < slots; ++r) a += sums[r * cols + i];
+    for (int r = 1; r < 4 * slots; ++r) a += sums[r * cols + i];
     dst[i] = a;
   }
 }
@@ -183,11 +215,30 @@ __device__ __forceinline__ void sparse_dx(const SparseArgs<T>& p, unsigned block
   float acc[V], v[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  for (int j = 0; j < p.k; ++j) {
-    const int2 pr = p.pairs[t * p.k + j];
-    const float f = __int_as_float(pr.y);
+  const int2* pr = p.pairs + t * p.k;
+  const T* w = p.w + c;
+  int j = 0;
+  for (; j + 4 <= p.k; j += 4) {  // four rows of W in flight
+    int2 q[4];
+    bool all = true;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      q[u] = pr[j + u];
+      all &= __int_as_float(q[u].y) != 0.f;
+    }
+    if (!all) break;
+    float r[4][V];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) load16(w + (size_t)q[u].x * p.d, r[u]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = fmaf(__int_as_float(q[u].y), r[u][i], acc[i]);
+  }
+  for (; j < p.k; ++j) {  // the rest, and picks that add nothing
+    const float f = __int_as_float(pr[j].y);
     if (f == 0.f) continue;
-    load16(p.w + (size_t)pr.x * p.d + c, v);
+    load16(w + (size_t)pr[j].x * p.d, v);
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = fmaf(f, v[i], acc[i]);
   }
@@ -215,10 +266,14 @@ __device__ __forceinline__ void sparse_dx(const SparseArgs<T>& p, unsigned block
 }
 
 template <typename T, bool WIDE>
-__global__ __launch_bounds__(256) void router_sparse_kernel(SparseArgs<T> p) {
+__global__ __launch_bounds__(256) void router_sparse_dw_kernel(SparseArgs<T> p) {
   __shared__ float sums[256 * (16 / sizeof(T))];
-  if ((int)blockIdx.x < p.n_dw_blocks) sparse_dw<T, WIDE>(p, sums);
-  else sparse_dx<T, WIDE>(p, blockIdx.x - p.n_dw_blocks);
+  sparse_dw<T, WIDE>(p, blockIdx.x, sums);
+}
+
+template <typename T, bool WIDE>
+__global__ __launch_bounds__(256) void router_sparse_dx_kernel(SparseArgs<T> p) {
+  sparse_dx<T, WIDE>(p, blockIdx.x);
 }
 
 // dw = the ranges' sums, added in order.
@@ -247,23 +302,29 @@ hipError_t sparse_t(int Tn, int d, int N, int k, const T* x, const T* w, const R
   p.w = w;
   p.dx_add = dx_add;
   p.dx = dx;
-  p.dw = rp.ranges == 1 ? dw : part;
+  const int groups = (rp.ranges + 3) / 4;
+  p.ranges = rp.ranges;
+  p.dw = groups == 1 ? dw : part;
   p.T_ = Tn;
   p.d = d;
   p.N = N;
   p.k = k;
   p.chunks = (d + 64 * V - 1) / (64 * V);
-  p.n_dw_blocks = p.chunks * N * rp.ranges;
-  const size_t units = (size_t)Tn * (d / V);
-  const dim3 grid((unsigned)(p.n_dw_blocks + (units + 255) / 256));
-  hipError_t e = d >= 64 * V ? launch_kernel(router_sparse_kernel<T, true>, grid, dim3(256), 0, s,
-                                             KernelTiming{}, p)
-                             : launch_kernel(router_sparse_kernel<T, false>, grid, dim3(256), 0, s,
-                                             KernelTiming{}, p);
-  if (e != hipSuccess || rp.ranges == 1) return e;
+  const dim3 gw(p.chunks * N * groups);
+  const dim3 gx((unsigned)(((size_t)Tn * (d / V) + 255) / 256));
+  const bool wide = d >= 64 * V;
+  hipError_t e = wide ? launch_kernel(router_sparse_dx_kernel<T, true>, gx, dim3(256), 0, s,
+                                      KernelTiming{}, p)
+                      : launch_kernel(router_sparse_dx_kernel<T, false>, gx, dim3(256), 0, s,
+                                      KernelTiming{}, p);
+  if (e != hipSuccess) return e;
+  e = wide ? launch_kernel(router_sparse_dw_kernel<T, true>, gw, dim3(256), 0, s, KernelTiming{}, p)
+           : launch_kernel(router_sparse_dw_kernel<T, false>, gw, dim3(256), 0, s, KernelTiming{},
+                           p);
+  if (e != hipSuccess || groups == 1) return e;
   const size_t n4 = (size_t)N * d / 4;
   return launch_kernel(router_dw_join_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s,
-                       KernelTiming{}, reinterpret_cast<const float4*>(part), rp.ranges, n4,
+                       KernelTiming{}, reinterpret_cast<const float4*>(part), groups, n4,
                        reinterpret_cast<float4*>(dw));
 }
 
@@ -495,12 +556,12 @@ hipError_t bwd_t(int Tn, int d, int N, const T* x, const T* w, const float* dl, 
 
 }  // namespace
 
-// Tokens per range: 4096 at most, and shorter (down to 128) until the dW role
-// has 2048 workgroups.
+// Tokens per range: 1024 at most (four ranges per dW workgroup), and shorter
+// (down to 32) until the dW role has 2048 workgroups.
 int router_range_tokens(int T, int d, int N) {
   const int chunks = (d + 511) / 512;
-  int r = 4096;
-  while (r > 128 && (long long)((T + r - 1) / r) * N * chunks < 2048) r /= 2;
+  int r = 1024;
+  while (r > 32 && (long long)((T + 4 * r - 1) / (4 * r)) * N * chunks < 2048) r /= 2;
   return r;
 }
 
