@@ -106,9 +106,13 @@ __global__ __launch_bounds__(256) void router_dw_kernel(const float* dl, const T
 //     order of every sum is fixed. The workgroups of a group of ranges run
 //     together and walk the tokens upwards, so the k readers of a row of x
 //     meet in L2 (column chunk c goes to XCD c % 8).
-// The workgroups of the roles alternate, so that dx streams from HBM while dW
-// gathers from L2: at T = 32768, d = 4096, 256 experts, top 4 the roles take
-// 122 and 100 us alone, BMOE_ONE_US one after the other, BMOE_MIX_US so.
+// One launch, the dW workgroups first. Measured at T = 32768, d = 4096, 256
+// experts, top 4 (bf16): dW 96 us and dx 117 us in launches of their own (dx
+// moves 537 MB: 100 us at the rate of a large copy; dW gathers 1.07 GB of x
+// through L2), the call 223 us so (235 us at six waves per SIMD instead of
+// eight) and 237 us with two launches; the headline
+// batch 17.8 and 19.8 us. Alternating the roles' workgroups costs dW its hits
+// in L2 (245 us with every third, 257 us with every fifth a dW one).
 template <typename T>
 struct SparseArgs {
   const int2* pairs;   // [T][k]
@@ -121,6 +125,7 @@ struct SparseArgs {
   float* dw;  // [groups of 4 ranges][N][d] (one group: the result itself)
   int T_, d, N, k, ranges;
   int chunks;  // column chunks of a row
+  int n_dw;    // workgroups of the dW role
 };
 
 constexpr int kU = 8;  // rows of x in flight per lane
@@ -266,14 +271,10 @@ __device__ __forceinline__ void sparse_dx(const SparseArgs<T>& p, unsigned block
 }
 
 template <typename T, bool WIDE>
-__global__ __launch_bounds__(256) void router_sparse_dw_kernel(SparseArgs<T> p) {
+__global__ __launch_bounds__(256, 8) void router_sparse_kernel(SparseArgs<T> p) {
   __shared__ float sums[256 * (16 / sizeof(T))];
-  sparse_dw<T, WIDE>(p, blockIdx.x, sums);
-}
-
-template <typename T, bool WIDE>
-__global__ __launch_bounds__(256) void router_sparse_dx_kernel(SparseArgs<T> p) {
-  sparse_dx<T, WIDE>(p, blockIdx.x);
+  if (blockIdx.x < (unsigned)p.n_dw) sparse_dw<T, WIDE>(p, blockIdx.x, sums);
+  else sparse_dx<T, WIDE>(p, blockIdx.x - p.n_dw);
 }
 
 // dw = the ranges' sums, added in order.
@@ -310,17 +311,12 @@ hipError_t sparse_t(int Tn, int d, int N, int k, const T* x, const T* w, const R
   p.N = N;
   p.k = k;
   p.chunks = (d + 64 * V - 1) / (64 * V);
-  const dim3 gw(p.chunks * N * groups);
-  const dim3 gx((unsigned)(((size_t)Tn * (d / V) + 255) / 256));
-  const bool wide = d >= 64 * V;
-  hipError_t e = wide ? launch_kernel(router_sparse_dx_kernel<T, true>, gx, dim3(256), 0, s,
-                                      KernelTiming{}, p)
-                      : launch_kernel(router_sparse_dx_kernel<T, false>, gx, dim3(256), 0, s,
-                                      KernelTiming{}, p);
-  if (e != hipSuccess) return e;
-  e = wide ? launch_kernel(router_sparse_dw_kernel<T, true>, gw, dim3(256), 0, s, KernelTiming{}, p)
-           : launch_kernel(router_sparse_dw_kernel<T, false>, gw, dim3(256), 0, s, KernelTiming{},
-                           p);
+  p.n_dw = p.chunks * N * groups;
+  const dim3 grid(p.n_dw + (unsigned)(((size_t)Tn * (d / V) + 255) / 256));
+  const hipError_t e = d >= 64 * V ? launch_kernel(router_sparse_kernel<T, true>, grid, dim3(256),
+                                                   0, s, KernelTiming{}, p)
+                                   : launch_kernel(router_sparse_kernel<T, false>, grid,
+                                                   dim3(256), 0, s, KernelTiming{}, p);
   if (e != hipSuccess || groups == 1) return e;
   const size_t n4 = (size_t)N * d / 4;
   return launch_kernel(router_dw_join_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s,
@@ -557,11 +553,12 @@ hipError_t bwd_t(int Tn, int d, int N, const T* x, const T* w, const float* dl, 
 }  // namespace
 
 // Tokens per range: 1024 at most (four ranges per dW workgroup), and shorter
-// (down to 32) until the dW role has 2048 workgroups.
+// (down to 32) until the dW role has 4096 workgroups (T = 16384, d = 2048, 64
+// experts: 55 us, with 2048 67 us, with 512 81 us).
 int router_range_tokens(int T, int d, int N) {
   const int chunks = (d + 511) / 512;
   int r = 1024;
-  while (r > 32 && (long long)((T + 4 * r - 1) / (4 * r)) * N * chunks < 2048) r /= 2;
+  while (r > 32 && (long long)((T + 4 * r - 1) / (4 * r)) * N * chunks < 4096) r /= 2;
   return r;
 }
 
