@@ -64,26 +64,38 @@ __device__ __forceinline__ float sub_sum(float v) {
     return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
   }));
 }
-template <int LPT>
-__device__ __forceinline__ double sub_max(double v) {
-#pragma unroll
-  for (int o = LPT / 2; o >= 1; o >>= 1) v = fmax(v, __shfl_xor(v, o, 64));
-  return v;
-}
-template <int LPT>
-__device__ __forceinline__ double sub_sum(double v) {
-#pragma unroll
-  for (int o = LPT / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+// The same for 64-bit values, as two halves.
+template <int LPT, typename F>
+__device__ __forceinline__ uint64_t sub_reduce64(uint64_t v, F f) {
+  auto both = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
+#define BMOE_STEP(O) \
+  if constexpr (LPT > O) v = f(v, both(partner<O>((uint32_t)v), partner<O>((uint32_t)(v >> 32))));
+  BMOE_STEP(1)
+  BMOE_STEP(2)
+  BMOE_STEP(4)
+  BMOE_STEP(8)
+#undef BMOE_STEP
+  if constexpr (LPT >= 32) {
+    const auto l = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
+    const auto h = __builtin_amdgcn_permlane16_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false);
+    v = f(both(l[0], h[0]), both(l[1], h[1]));
+  }
+  if constexpr (LPT >= 64) {
+    const auto l = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
+    const auto h = __builtin_amdgcn_permlane32_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false);
+    v = f(both(l[0], h[0]), both(l[1], h[1]));
+  }
   return v;
 }
 template <int LPT>
 __device__ __forceinline__ uint64_t sub_max(uint64_t v) {
-#pragma unroll
-  for (int o = LPT / 2; o >= 1; o >>= 1) {
-    const uint64_t w = __shfl_xor((unsigned long long)v, o, 64);
-    v = w > v ? w : v;
-  }
-  return v;
+  return sub_reduce64<LPT>(v, [](uint64_t x, uint64_t y) { return x > y ? x : y; });
+}
+template <int LPT>
+__device__ __forceinline__ double sub_sum(double v) {
+  return __longlong_as_double(sub_reduce64<LPT>(__double_as_longlong(v), [](uint64_t x, uint64_t y) {
+    return (uint64_t)__double_as_longlong(__longlong_as_double(x) + __longlong_as_double(y));
+  }));
 }
 
 // Lanes of this lane's token in a ballot, moved to bit 0.
@@ -178,17 +190,19 @@ __device__ __forceinline__ void ld_row(const T* src, int cnt, float fill, float 
 // With groups, a group takes lpg lanes (a power of two), so its lanes hold no
 // other group's experts; the lowest lanes still hold the lowest ids.
 struct LaneMap {
-  int lpg;  // lanes per group; 0: the map does not fit, every token goes the exact way
+  int lpg;    // lanes per group; 0: the map does not fit, every token goes the exact way
+  int lpg64;  // the same where a wave takes one token of LPT PER experts
 };
+inline int lanes_per_group(int lanes, int per, int N, int groups) {
+  const int size = N / groups;
+  int lpg = 1;
+  while (lpg * per < size && lpg < lanes) lpg *= 2;
+  if (groups == 1) lpg = lanes;
+  return lpg * per < size || groups * lpg > lanes ? 0 : lpg;
+}
 template <int LPT, int PER>
 LaneMap lane_map(int N, int groups) {
-  LaneMap m;
-  const int size = N / groups;
-  m.lpg = 1;
-  while (m.lpg * PER < size && m.lpg < LPT) m.lpg *= 2;
-  if (groups == 1) m.lpg = LPT;
-  if (m.lpg * PER < size || groups * m.lpg > LPT) m.lpg = 0;
-  return m;
+  return {lanes_per_group(LPT, PER, N, groups), lanes_per_group(64, LPT * PER / 64, N, groups)};
 }
 
 // Group scores from the lanes' two largest choices: (a, a2) over `lpg` lanes.
@@ -209,67 +223,89 @@ __device__ __forceinline__ void top2_lanes(float& a, float& a2, int lpg) {
   }
 }
 
-// The picks of one token in 64 bits, by a whole wave: lane q holds experts
-// q PER ... q PER + PER - 1. Returns pick j's id in lane j.
+// fp64 score of a logit: e^(l - m) / total, or the sigmoid.
+__device__ __forceinline__ double score64(float l, bool softmax, float m, double total) {
+  return softmax ? exp((double)l - m) / total : 1.0 / (1.0 + exp(-(double)l));
+}
+
+// The picks of one token in 64 bits, by a whole wave, from row; m: the row's
+// largest logit. Lanes by group where `lpg` lanes hold one (0: by expert).
+// Returns pick j's id in lane j. Rare, so what counts is how long one takes
+// (kept on DPP and scalar reads of lanes), not how many instructions.
 template <int PER, typename T>
-__device__ int choose_exact(const T* row, const float* bias, int N, int k, const RouteSpec& sp) {
-  const int q = threadIdx.x & 63, base = q * PER;
+__device__ int choose_exact(const T* row, const float* bias, int N, int k, const RouteSpec& sp,
+                            int lpg, float m) {
+  const int q = threadIdx.x & 63;
   const bool softmax = sp.score == BMOE_SCORE_SOFTMAX;
-  double c[PER], m = -INFINITY;
+  const int size = N / sp.groups;
+  const int mine_g = lpg ? q / lpg : 0, in_group = lpg ? q % lpg * PER : q * PER;
+  const int base = lpg ? mine_g * size + in_group : in_group;
+  const int cnt = lpg ? (mine_g < sp.groups ? min(PER, size - in_group) : 0) : min(PER, N - in_group);
+  float l[PER];
+  double c[PER], total = 1.0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) l[i] = i < cnt ? ld_logit(row + base + i) : -INFINITY;
+  const bool scored = bias || (sp.groups > 1 && sp.group_score == BMOE_GROUP_TOP2);
+  if (scored && softmax) {
+    total = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) total += l[i] == -INFINITY ? 0.0 : exp((double)l[i] - m);
+    total = sub_sum<64>(total);
+  }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    c[i] = base + i < N ? (double)ld_logit(row + base + i) : -INFINITY;
-    m = fmax(m, c[i]);
+    c[i] = l[i];
+    if (scored && l[i] != -INFINITY)
+      c[i] = score64(l[i], softmax, m, total) + (bias ? (double)bias[base + i] : 0.0);
   }
-  if (bias || (sp.groups > 1 && sp.group_score == BMOE_GROUP_TOP2)) {
-    double total = 1.0;
-    if (softmax) {
-      m = sub_max<64>(m);
-      total = 0.0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) total += c[i] == -INFINITY ? 0.0 : exp(c[i] - m);
-      total = sub_sum<64>(total);
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const double s = softmax ? exp(c[i] - m) / total : 1.0 / (1.0 + exp(-c[i]));
-      c[i] = c[i] == -INFINITY ? -INFINITY
-                               : s + (bias && base + i < N ? (double)bias[base + i] : 0.0);
-    }
-  }
-  uint64_t keep = 1;  // bit g: group g is kept
-  const int size = N / sp.groups;
+  uint64_t keep = ~0ull;  // bit g: group g is kept
   if (sp.groups > 1) {
-    double mine = -INFINITY;  // lane g: the score of group g
-    for (int g = 0; g < sp.groups; ++g) {
-      double a = -INFINITY, a2 = -INFINITY;  // the two largest
+    double mine = -INFINITY;  // lane g * max(lpg, 1): the score of group g
+    auto top2 = [&](double& a, double& a2, double v) {
+      if (v > a) { a2 = a; a = v; }
+      else if (v > a2) a2 = v;
+    };
+    auto merge = [&](double& a, double& a2, int o) {
+      const double oa = __shfl_xor(a, o, 64), ob = __shfl_xor(a2, o, 64);
+      a2 = fmax(fmin(a, oa), a > oa ? a2 : ob);
+      a = fmax(a, oa);
+    };
+    const bool by_max = sp.group_score == BMOE_GROUP_MAX;
+    if (lpg) {
+      double a = -INFINITY, a2 = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const double v = base + i >= g * size && base + i < (g + 1) * size ? c[i] : -INFINITY;
-        if (v > a) { a2 = a; a = v; }
-        else if (v > a2) a2 = v;
+      for (int i = 0; i < PER; ++i) top2(a, a2, c[i]);
+      for (int o = 1; o < lpg; o *= 2) merge(a, a2, o);
+      mine = by_max || a2 == -INFINITY ? a : a + a2;
+    } else {
+      for (int g = 0; g < sp.groups; ++g) {
+        double a = -INFINITY, a2 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          top2(a, a2, base + i >= g * size && base + i < (g + 1) * size ? c[i] : -INFINITY);
+        for (int o = 32; o >= 1; o /= 2) merge(a, a2, o);
+        if (q == g) mine = by_max || a2 == -INFINITY ? a : a + a2;
       }
-      for (int o = 32; o >= 1; o >>= 1) {
-        const double oa = __shfl_xor(a, o, 64), ob = __shfl_xor(a2, o, 64);
-        a2 = fmax(fmin(a, oa), a > oa ? a2 : ob);
-        a = fmax(a, oa);
-      }
-      if (q == g) mine = sp.group_score == BMOE_GROUP_MAX || a2 == -INFINITY ? a : a + a2;
     }
+    const int step = lpg ? lpg : 1, g = q / step;
     int rank = 0;
     for (int h = 0; h < sp.groups; ++h) {
-      const double v = __shfl(mine, h, 64);
-      rank += v > mine || (v == mine && h < q);
+      const uint64_t bits = __double_as_longlong(mine);
+      const double v = __longlong_as_double(
+          (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(bits >> 32), h * step) << 32 |
+          (uint32_t)__builtin_amdgcn_readlane((int)bits, h * step));
+      rank += v > mine || (v == mine && h < g);
     }
-    keep = __ballot(q < sp.groups && rank < sp.keep);
+    const bool kept = g < sp.groups && rank < sp.keep;
+    keep = __ballot(kept);
+    if (lpg) keep = kept ? ~0ull : 0;
   }
   uint64_t key[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = base + i;
-    const bool in = e < N && (sp.groups == 1 || (keep >> (e / size) & 1u));
+    const bool in = i < cnt && (sp.groups == 1 || lpg ? keep != 0 : keep >> ((base + i) / size) & 1u);
     // without a bias the experts' order is that of their logits
-    key[i] = !in ? 0 : bias ? key_of(c[i]) : key_of((double)ld_logit(row + e));
+    key[i] = !in ? 0 : bias ? key_of(c[i]) : key_of((double)l[i]);
   }
   int id = 0;
   for (int j = 0; j < k; ++j) {
@@ -288,12 +324,14 @@ __device__ int choose_exact(const T* row, const float* bias, int N, int k, const
   return id;
 }
 
-// The picks in fp32: pick j's id in lane j. *unsure is set for a token whose
-// picks, or kept groups, are not further apart than the errors allow (bounded
-// below), or that has no k finite choices: it goes the exact way. Without a
-// bias the choices are the logits themselves, and only sums of two scores can
-// be unsure. l, b: this lane's `cnt` logits and biases from expert `base` on
-// (-inf and 0 past them).
+// The picks in fp32: pick j's id in lane j. Their errors are bounded below.
+// Picks that are not further apart than that (from one another, or the last
+// from the experts left) are put in order by their fp64 choices, with the next
+// few experts among them; unsure is set for a token whose kept groups are not
+// far enough apart, whose experts left still are not, or that has no k finite
+// choices: choose_exact decides it. Without a bias the choices are the logits
+// themselves, and only sums of two scores can be unsure. l, b: this lane's
+// logits and biases from expert `base` on (-inf and 0 past its last).
 template <int LPT, int PER, typename T>
 __device__ __forceinline__ int choose(const T* row, const float* bias, const float (&l)[PER],
                                       const float (&b)[PER], float bmax, int base, int k,
@@ -357,28 +395,30 @@ __device__ __forceinline__ int choose(const T* row, const float* bias, const flo
     }
   }
 
-  // k rounds: the largest choice, the lower id on ties
+  // rounds: the largest choice, the lower id on ties; pick j to lane j
   int id = base;
   float cj = -INFINITY;
-  for (int j = 0; j < k; ++j) {
-    float best = c[0];
+  auto rounds = [&](int j0, int j1) {
+    for (int j = j0; j < j1; ++j) {
+      float best = c[0];
 #pragma unroll
-    for (int i = 1; i < PER; ++i) best = fmaxf(best, c[i]);
-    best = sub_max<LPT>(best);
-    int at = 0x3fffffff;
+      for (int i = 1; i < PER; ++i) best = fmaxf(best, c[i]);
+      best = sub_max<LPT>(best);
+      int at = 0x3fffffff;
 #pragma unroll
-    for (int i = PER - 1; i >= 0; --i) at = c[i] == best ? i : at;
-    const uint32_t first = sub_min<LPT>((uint32_t)(base + at));
-    const int out = first == (uint32_t)(base + at) ? at : -1;
+      for (int i = PER - 1; i >= 0; --i) at = c[i] == best ? i : at;
+      const uint32_t first = sub_min<LPT>((uint32_t)(base + at));
+      const int out = first == (uint32_t)(base + at) ? at : -1;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) c[i] = out == i ? -INFINITY : c[i];
-    if (q == j) {
-      id = (int)first;
-      cj = best;
+      for (int i = 0; i < PER; ++i) c[i] = out == i ? -INFINITY : c[i];
+      if (q == j) {
+        id = (int)first;
+        cj = best;
+      }
     }
-  }
-  const bool pick = q < k;
-  unsure |= pick && !(fabsf(cj) < INFINITY);
+  };
+  rounds(0, k);
+  unsure |= q < k && !(fabsf(cj) < INFINITY);
   if (bias) {
     // Each pick's choice minus its error has to be above the next pick's plus
     // that one's, and the last's above every expert left. Experts of the same
@@ -387,31 +427,65 @@ __device__ __forceinline__ int choose(const T* row, const float* bias, const flo
       const float x = softmax ? m - lv : fabsf(lv);
       return kU * (fabsf(cv - bv) * (3.f * x + kA) + 3.f * fabsf(cv));
     };
-    const bool fine = pick && fabsf(cj) < INFINITY;
+    const bool fine = q < k && fabsf(cj) < INFINITY;
     const float lj = fine ? ld_logit(row + id) : 0.f, bj = fine ? bias[id] : 0.f;
     const float ej = err(cj, lj, bj);
     const float cn = __shfl(cj, here + 1, 64), en = __shfl(ej, here + 1, 64);
     const float ln = __shfl(lj, here + 1, 64), bn = __shfl(bj, here + 1, 64);
-    unsure |= q < k - 1 && !(cj - ej > cn + en) && !(lj == ln && bj == bn);
+    const bool close = q < k - 1 && !(cj - ej > cn + en) && !(lj == ln && bj == bn);
     // The experts left: none above `left`, so none's score above S, and none's
     // error above E (s x <= S (1 + ln(smax / S)) for a score s <= S).
-    float left = c[0];
+    auto above = [&]() {  // the highest that an expert left can be
+      float left = c[0];
 #pragma unroll
-    for (int i = 1; i < PER; ++i) left = fmaxf(left, c[i]);
-    left = sub_max<LPT>(left);
-    const float S = fminf(smax, fmaxf(left + bmax, 1e-30f));
-    const float E = kU * (S * (3.f + 2.1f * __builtin_amdgcn_logf(smax / S) + kA) + 3.f * fabsf(left));
-    const bool clear = q != k - 1 || left == -INFINITY || cj - ej > left + E;
-    if (!__all(clear)) {  // expert by expert, exact ties with the last pick apart
+      for (int i = 1; i < PER; ++i) left = fmaxf(left, c[i]);
+      left = sub_max<LPT>(left);
+      const float S = fminf(smax, fmaxf(left + bmax, 1e-30f));
+      const float E =
+          kU * (S * (3.f + 2.1f * __builtin_amdgcn_logf(smax / S) + kA) + 3.f * fabsf(left));
+      return left == -INFINITY ? left : left + E;
+    };
+    const float high = above();
+    bool below = q != k - 1 || cj - ej > high;
+    if (!__all(below)) {  // expert by expert, exact ties with the last pick apart
       const int last = sub + k - 1;
       const float low = __shfl(cj - ej, last, 64);
       const float lk = __shfl(lj, last, 64), bk = __shfl(bj, last, 64);
-      bool above = false;
+      below = true;
 #pragma unroll
       for (int i = 0; i < PER; ++i)
-        above |= c[i] != -INFINITY && !(l[i] == lk && b[i] == bk) &&
-                 !(low > c[i] + err(c[i], l[i], b[i]));
-      unsure |= above;
+        below &= c[i] == -INFINITY || (l[i] == lk && b[i] == bk) ||
+                 low > c[i] + err(c[i], l[i], b[i]);
+    }
+    const bool reorder = own_bits<LPT>(__ballot(close)) != 0;
+    const bool more = own_bits<LPT>(__ballot(!below)) != 0;
+    if (__any(reorder || more)) {
+      // fp64 choices of the picks and the next ones, ranked by them. Enough if
+      // the picks are sure to be among these: k of them are above `low`.
+      const int n = min(k + 3, LPT);
+      rounds(k, n);
+      const float low = -sub_max<LPT>(q < k ? ej - cj : -INFINITY);
+      const float rest = above();
+      unsure |= more && !(low > rest);
+      double total = 1.0;
+      if (softmax) {
+        total = 0.0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) total += l[i] == -INFINITY ? 0.0 : exp((double)l[i] - m);
+        total = sub_sum<LPT>(total);
+      }
+      const bool cand = q < n && fabsf(cj) < INFINITY;
+      const float lc = cand ? ld_logit(row + id) : 0.f;
+      const double v = cand ? score64(lc, softmax, m, total) + (double)bias[id] : -INFINITY;
+      int rank = 0;
+      for (int j = 0; j < n; ++j) {
+        const double w = __shfl(v, sub + j, 64);
+        const int wi = __shfl(id, sub + j, 64);
+        rank += w > v || (w == v && wi < id);
+      }
+      // candidate of rank r to lane r
+      const int to = reorder || more ? (cand ? rank : q) : q;
+      id = __builtin_amdgcn_ds_permute((sub + to) * 4, id);
     }
   }
   return id;
@@ -466,7 +540,8 @@ __global__ __launch_bounds__(256) void route_kernel(const T* logits, const float
       const int sub = (int)__builtin_ctzll(todo) / LPT * LPT;
       todo &= ~(LPT == 64 ? ~0ull : ((1ull << (LPT & 63)) - 1) << sub);
       const size_t t = t0 + ((threadIdx.x & ~63) + sub) / LPT;
-      const int x = choose_exact<LPT * PER / 64>(logits + t * N, bias, N, k, sp);
+      const int x = choose_exact<LPT * PER / 64>(logits + t * N, bias, N, k, sp, map.lpg64,
+                                                 __shfl(m, sub, 64));
       const int y = __shfl(x, q, 64);
       if ((threadIdx.x & 63) / LPT * LPT == sub) id = y;
     }
@@ -828,7 +903,7 @@ hipError_t route_t(const T* logits, const float* bias, int Tn, int N, int k, con
   BMOE_CALL(64, 16, true)
   BMOE_CALL(64, 64, true)
 #undef BMOE_CALL
-  map.lpg = 0;
+  map.lpg = map.lpg64 = 0;
   const unsigned blocks = ((unsigned)Tn + 3) / 4;
   return launch_kernel(route_kernel<64, 64, VEC, T>, dim3(blocks < 2048 ? blocks : 2048),
                        dim3(256), 0, s, KernelTiming{}, logits, bias, Tn, N, k, sp, map, ids,
