@@ -217,7 +217,7 @@ __device__ __forceinline__ void top2_lanes(float& a, float& a2, int lpg) {
   if (lpg > 2) merge(partner<2>(__float_as_uint(a)), partner<2>(__float_as_uint(a2)));
   if (lpg > 4) merge(partner<4>(__float_as_uint(a)), partner<4>(__float_as_uint(a2)));
   if (lpg > 8) merge(partner<8>(__float_as_uint(a)), partner<8>(__float_as_uint(a2)));
-  if constexpr (LPT == 64) {
+  if constexpr (LPT >= 32) {
     if (lpg > 16) merge(__shfl_xor(__float_as_uint(a), 16, 64), __shfl_xor(__float_as_uint(a2), 16, 64));
     if (lpg > 32) merge(__shfl_xor(__float_as_uint(a), 32, 64), __shfl_xor(__float_as_uint(a2), 32, 64));
   }
@@ -342,7 +342,7 @@ __device__ __forceinline__ int choose(const T* row, const float* bias, const flo
   // most: the difference, its product with log2 e and that constant, then the
   // exponential's, sum's (PER + 6 additions) and quotient's last places. The
   // sigmoid has x = |l| and none of the sum.
-  constexpr float kA = PER + 24;
+  const float kA = softmax ? PER + 24 : 8;
   float c[PER], smax = 1.f;
   const bool scored = bias || (sp.groups > 1 && sp.group_score == BMOE_GROUP_TOP2);
   if (!scored) {
@@ -395,9 +395,102 @@ __device__ __forceinline__ int choose(const T* row, const float* bias, const flo
     }
   }
 
-  // rounds: the largest choice, the lower id on ties; pick j to lane j
+  auto err = [&](float cv, float lv, float bv) {
+    const float x = softmax ? m - lv : fabsf(lv);
+    return kU * (fabsf(cv - bv) * (3.f * x + kA) + 3.f * fabsf(cv));
+  };
+  // The highest that an expert can be whose choice is `left` at most: no such
+  // expert's score is above S, and none's error above E (s x <= S (1 + ln(smax
+  // / S)) for a score s <= S).
+  auto ceiling = [&](float left) {
+    const float S = fminf(smax, fmaxf(left + bmax, 1e-30f));
+    const float E =
+        kU * (S * (3.f + 2.1f * __builtin_amdgcn_logf(smax / S) + kA) + 3.f * fabsf(left));
+    return left == -INFINITY ? left : left + E;
+  };
   int id = base;
   float cj = -INFINITY;
+
+  // Many experts per lane: each lane sorts integer keys (the choice's bits in
+  // order, the last ones replaced by the place in the lane, so a comparison is
+  // a min and a max) into its four largest; a round then looks at the lanes'
+  // heads only. The keys order choices that differ above the replaced bits;
+  // whatever they leave open (equal ones, a lane that gave all four, choices
+  // closer than their errors) sends the wave to the rounds below.
+  if constexpr (PER >= 16) {
+    constexpr uint32_t kLow = PER - 1;
+    uint32_t h[4], f[4];
+    auto order = [](uint32_t& x, uint32_t& y) {  // x >= y
+      const uint32_t a = x > y ? x : y;
+      y = x > y ? y : x;
+      x = a;
+    };
+#pragma unroll
+    for (int i0 = 0; i0 < PER; i0 += 4) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int32_t bits = __float_as_int(c[i0 + u]);
+        f[u] = (((uint32_t)bits ^ ((uint32_t)(bits >> 31) | 0x80000000u)) & ~kLow) |
+               (kLow - (i0 + u));
+      }
+      order(f[0], f[1]);
+      order(f[2], f[3]);
+      order(f[0], f[2]);
+      order(f[1], f[3]);
+      order(f[1], f[2]);
+      if (i0 == 0) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) h[u] = f[u];
+      } else {  // the four largest of two sorted fours, sorted
+#pragma unroll
+        for (int u = 0; u < 4; ++u) h[u] = h[u] > f[3 - u] ? h[u] : f[3 - u];
+        order(h[0], h[2]);
+        order(h[1], h[3]);
+        order(h[0], h[1]);
+        order(h[2], h[3]);
+      }
+    }
+    uint32_t prev = 0xffffffffu, kj = 0;
+    bool open = false;
+    for (int j = 0; j < k; ++j) {
+      const uint32_t v = h[0] & ~kLow;
+      const uint32_t best = sub_max<LPT>(v);
+      const uint32_t mine = v == best ? (uint32_t)base + kLow - (h[0] & kLow) : 0x7fffffffu;
+      const uint32_t first = sub_min<LPT>(mine);
+      const bool out = mine == first;
+      open |= best == prev || (out && h[1] == 0);
+      prev = best;
+      h[0] = out ? h[1] : h[0];
+      h[1] = out ? h[2] : h[1];
+      h[2] = out ? h[3] : h[2];
+      h[3] = out ? 0u : h[3];
+      if (q == j) {
+        id = (int)first;
+        kj = best;
+      }
+    }
+    const uint32_t next = sub_max<LPT>(h[0] & ~kLow);
+    open |= next == prev;
+    const uint32_t low_key = kj & 0x80000000u ? kj ^ 0x80000000u : ~kj;
+    const bool pick = q < k;
+    open |= pick && !(fabsf(__uint_as_float(low_key)) < INFINITY);
+    if (bias && !__any(open)) {
+      // the picks' choices again, without the places in their last bits
+      const float lj = pick ? ld_logit(row + id) : 0.f, bj = pick ? bias[id] : 0.f;
+      cj = (softmax ? exp_of(lj - m) * smax : inv_of(1.f + exp_of(-lj))) + bj;
+      const float ej = err(cj, lj, bj);
+      const float cn = __shfl(cj, here + 1, 64), en = __shfl(ej, here + 1, 64);
+      // (a key is short of its choice by less than PER units in the last place)
+      const uint32_t up = next | kLow;
+      const float left = __uint_as_float(up & 0x80000000u ? up ^ 0x80000000u : ~up);
+      const float high = ceiling(left);
+      open |= pick && !(cj - ej > (q < k - 1 ? cn + en : high));
+    }
+    if (!__any(open)) return id;
+  }
+
+  // rounds: the largest choice, the lower id on ties; pick j to lane j
+  id = base;
   auto rounds = [&](int j0, int j1) {
     for (int j = j0; j < j1; ++j) {
       float best = c[0];
@@ -423,27 +516,17 @@ __device__ __forceinline__ int choose(const T* row, const float* bias, const flo
     // Each pick's choice minus its error has to be above the next pick's plus
     // that one's, and the last's above every expert left. Experts of the same
     // logit and bias tie exactly, and the ids have ordered those.
-    auto err = [&](float cv, float lv, float bv) {
-      const float x = softmax ? m - lv : fabsf(lv);
-      return kU * (fabsf(cv - bv) * (3.f * x + kA) + 3.f * fabsf(cv));
-    };
     const bool fine = q < k && fabsf(cj) < INFINITY;
     const float lj = fine ? ld_logit(row + id) : 0.f, bj = fine ? bias[id] : 0.f;
     const float ej = err(cj, lj, bj);
     const float cn = __shfl(cj, here + 1, 64), en = __shfl(ej, here + 1, 64);
     const float ln = __shfl(lj, here + 1, 64), bn = __shfl(bj, here + 1, 64);
     const bool close = q < k - 1 && !(cj - ej > cn + en) && !(lj == ln && bj == bn);
-    // The experts left: none above `left`, so none's score above S, and none's
-    // error above E (s x <= S (1 + ln(smax / S)) for a score s <= S).
     auto above = [&]() {  // the highest that an expert left can be
       float left = c[0];
 #pragma unroll
       for (int i = 1; i < PER; ++i) left = fmaxf(left, c[i]);
-      left = sub_max<LPT>(left);
-      const float S = fminf(smax, fmaxf(left + bmax, 1e-30f));
-      const float E =
-          kU * (S * (3.f + 2.1f * __builtin_amdgcn_logf(smax / S) + kA) + 3.f * fabsf(left));
-      return left == -INFINITY ? left : left + E;
+      return ceiling(sub_max<LPT>(left));
     };
     const float high = above();
     bool below = q != k - 1 || cj - ej > high;
@@ -883,7 +966,7 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const int* part, int
 }
 
 // Lanes per token and experts per lane: 16 lanes (4 tokens per wave) up to 256
-// experts and 16 picks, else a whole wave per token.
+// experts and 16 picks, 32 up to 512 and 32, else a whole wave per token.
 template <bool VEC, typename T>
 hipError_t route_t(const T* logits, const float* bias, int Tn, int N, int k, const RouteSpec& sp,
                    int32_t* ids, float* gates, hipStream_t s) {
@@ -900,6 +983,7 @@ hipError_t route_t(const T* logits, const float* bias, int Tn, int N, int k, con
   BMOE_CALL(16, 16, !few)
   BMOE_CALL(64, 4, true)
   BMOE_CALL(16, 16, true)
+  BMOE_CALL(32, 16, !few)
   BMOE_CALL(64, 16, true)
   BMOE_CALL(64, 64, true)
 #undef BMOE_CALL
