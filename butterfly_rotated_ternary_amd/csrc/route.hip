@@ -190,8 +190,10 @@ __device__ __forceinline__ void ld_row(const T* src, int cnt, float fill, float 
 // With groups, a group takes lpg lanes (a power of two), so its lanes hold no
 // other group's experts; the lowest lanes still hold the lowest ids.
 struct LaneMap {
-  int lpg;    // lanes per group; 0: the map does not fit, every token goes the exact way
+  int lpg;    // lanes per group; 0: the map does not fit
   int lpg64;  // the same where a wave takes one token of LPT PER experts
+  int shift;  // log2 lpg
+  int size;   // experts per group
 };
 inline int lanes_per_group(int lanes, int per, int N, int groups) {
   const int size = N / groups;
@@ -202,7 +204,10 @@ inline int lanes_per_group(int lanes, int per, int N, int groups) {
 }
 template <int LPT, int PER>
 LaneMap lane_map(int N, int groups) {
-  return {lanes_per_group(LPT, PER, N, groups), lanes_per_group(64, LPT * PER / 64, N, groups)};
+  const int lpg = lanes_per_group(LPT, PER, N, groups);
+  int shift = 0;
+  while (1 << shift < lpg) ++shift;
+  return {lpg, lanes_per_group(64, LPT * PER / 64, N, groups), shift, N / groups};
 }
 
 // Group scores from the lanes' two largest choices: (a, a2) over `lpg` lanes.
@@ -324,18 +329,16 @@ __device__ int choose_exact(const T* row, const float* bias, int N, int k, const
   return id;
 }
 
-// The picks in fp32: pick j's id in lane j. Their errors are bounded below.
-// Picks that are not further apart than that (from one another, or the last
-// from the experts left) are put in order by their fp64 choices, with the next
-// few experts among them; unsure is set for a token whose kept groups are not
-// far enough apart, whose experts left still are not, or that has no k finite
-// choices: choose_exact decides it. Without a bias the choices are the logits
-// themselves, and only sums of two scores can be unsure. l, b: this lane's
+// The picks in fp32: pick j's id in lane j. `open` is set for a token that fp32
+// does not decide: kept groups or picks closer than the errors bounded below,
+// no k finite choices, six picks from one lane of many experts;
+// choose_exact then decides it. Without a bias the choices are the logits
+// themselves, and only sums of two scores have errors. l, b: this lane's
 // logits and biases from expert `base` on (-inf and 0 past its last).
 template <int LPT, int PER, typename T>
 __device__ __forceinline__ int choose(const T* row, const float* bias, const float (&l)[PER],
                                       const float (&b)[PER], float bmax, int base, int k,
-                                      const RouteSpec& sp, int lpg, float m, bool& unsure) {
+                                      const RouteSpec& sp, const LaneMap& map, float m, bool& open) {
   const int q = threadIdx.x % LPT, here = threadIdx.x & 63, sub = here / LPT * LPT;
   const bool softmax = sp.score == BMOE_SCORE_SOFTMAX;
   // A score s of a logit at distance x from m is off by s u (3 |x| + A) at
@@ -352,7 +355,7 @@ __device__ __forceinline__ int choose(const T* row, const float* bias, const flo
     float total = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      c[i] = exp_of(l[i] - m);  // (a row of -inf: NaN, unsure below)
+      c[i] = exp_of(l[i] - m);  // (a row of -inf: NaN, left open below)
       total += c[i];
     }
     smax = 1.f / sub_sum<LPT>(total);
@@ -372,13 +375,13 @@ __device__ __forceinline__ int choose(const T* row, const float* bias, const flo
       a2 = fmaxf(a2, fminf(a, c[i]));
       a = fmaxf(a, c[i]);
     }
-    top2_lanes<LPT>(a, a2, lpg);
+    top2_lanes<LPT>(a, a2, map.lpg);
     const bool one = sp.group_score == BMOE_GROUP_MAX || a2 == -INFINITY;
     const float score = one ? a : a + a2;
-    const int g = q / lpg;
+    const int g = q >> map.shift;
     int rank = 0;
     for (int h = 0; h < sp.groups; ++h) {
-      const float v = __shfl(score, sub + h * lpg, 64);
+      const float v = __shfl(score, sub + (h << map.shift), 64);
       rank += v > score || (v == score && h < g);
     }
     const bool real = g < sp.groups, kept = real && rank < sp.keep;
@@ -387,7 +390,7 @@ __device__ __forceinline__ int choose(const T* row, const float* bias, const flo
       // the lowest that a kept group, and the highest that another can be
       const float lowest = -sub_max<LPT>(kept ? slack - score : -INFINITY);
       const float highest = sub_max<LPT>(real && !kept ? score + slack : -INFINITY);
-      unsure |= !(lowest > highest);
+      open |= !(lowest > highest);
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -408,173 +411,149 @@ __device__ __forceinline__ int choose(const T* row, const float* bias, const flo
         kU * (S * (3.f + 2.1f * __builtin_amdgcn_logf(smax / S) + kA) + 3.f * fabsf(left));
     return left == -INFINITY ? left : left + E;
   };
-  int id = base;
-  float cj = -INFINITY;
-
-  // Many experts per lane: each lane sorts integer keys (the choice's bits in
-  // order, the last ones replaced by the place in the lane, so a comparison is
-  // a min and a max) into its four largest; a round then looks at the lanes'
-  // heads only. The keys order choices that differ above the replaced bits;
-  // whatever they leave open (equal ones, a lane that gave all four, choices
-  // closer than their errors) sends the wave to the rounds below.
-  if constexpr (PER >= 16) {
-    constexpr uint32_t kLow = PER - 1;
-    uint32_t h[4], f[4];
-    auto order = [](uint32_t& x, uint32_t& y) {  // x >= y
-      const uint32_t a = x > y ? x : y;
-      y = x > y ? y : x;
-      x = a;
-    };
+  // Each lane sorts integer keys (the choice's bits in order, the last ones
+  // replaced by the place in the lane, so that a comparison is a min and a max)
+  // into its kDepth largest; a round looks at the lanes' heads only. Keys equal
+  // above the replaced bits go by id.
+  constexpr uint32_t kLow = PER - 1;
+  constexpr int kDepth = PER < 6 ? PER : 6;
+  uint32_t h[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  auto order = [](uint32_t& x, uint32_t& y) {  // x >= y
+    const uint32_t hi = x > y ? x : y;
+    y = x > y ? y : x;
+    x = hi;
+  };
+  auto four = [&](uint32_t* f, int i0) {  // the lane's choices i0 .. i0 + 3, sorted
 #pragma unroll
-    for (int i0 = 0; i0 < PER; i0 += 4) {
+    for (int u = 0; u < 4; ++u) {
+      const int32_t bits = __float_as_int(c[i0 + u]);
+      f[u] = (((uint32_t)bits ^ ((uint32_t)(bits >> 31) | 0x80000000u)) & ~kLow) | (kLow - (i0 + u));
+    }
+    order(f[0], f[1]);
+    order(f[2], f[3]);
+    order(f[0], f[2]);
+    order(f[1], f[3]);
+    order(f[1], f[2]);
+  };
+  auto merge8 = [&](uint32_t (&f)[8]) {  // sorts a bitonic eight
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int32_t bits = __float_as_int(c[i0 + u]);
-        f[u] = (((uint32_t)bits ^ ((uint32_t)(bits >> 31) | 0x80000000u)) & ~kLow) |
-               (kLow - (i0 + u));
-      }
-      order(f[0], f[1]);
-      order(f[2], f[3]);
-      order(f[0], f[2]);
-      order(f[1], f[3]);
-      order(f[1], f[2]);
+    for (int u = 0; u < 4; ++u) order(f[u], f[u + 4]);
+#pragma unroll
+    for (int u = 0; u < 8; u += 4) {
+      order(f[u], f[u + 2]);
+      order(f[u + 1], f[u + 3]);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; u += 2) order(f[u], f[u + 1]);
+  };
+  if constexpr (PER == 4) {
+    four(h, 0);
+  } else {
+#pragma unroll
+    for (int i0 = 0; i0 < PER; i0 += 8) {
+      uint32_t f[8], g[4];
+      four(f, i0);
+      four(g, i0 + 4);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) f[4 + u] = g[3 - u];
+      merge8(f);
       if (i0 == 0) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) h[u] = f[u];
-      } else {  // the four largest of two sorted fours, sorted
+        for (int u = 0; u < 8; ++u) h[u] = f[u];
+      } else {  // the eight largest of two sorted eights, sorted
 #pragma unroll
-        for (int u = 0; u < 4; ++u) h[u] = h[u] > f[3 - u] ? h[u] : f[3 - u];
-        order(h[0], h[2]);
-        order(h[1], h[3]);
-        order(h[0], h[1]);
-        order(h[2], h[3]);
+        for (int u = 0; u < 8; ++u) h[u] = h[u] > f[7 - u] ? h[u] : f[7 - u];
+        merge8(h);
       }
     }
-    uint32_t prev = 0xffffffffu, kj = 0;
-    bool open = false;
-    for (int j = 0; j < k; ++j) {
-      const uint32_t v = h[0] & ~kLow;
-      const uint32_t best = sub_max<LPT>(v);
-      const uint32_t mine = v == best ? (uint32_t)base + kLow - (h[0] & kLow) : 0x7fffffffu;
-      const uint32_t first = sub_min<LPT>(mine);
-      const bool out = mine == first;
-      open |= best == prev || (out && h[1] == 0);
-      prev = best;
-      h[0] = out ? h[1] : h[0];
-      h[1] = out ? h[2] : h[1];
-      h[2] = out ? h[3] : h[2];
-      h[3] = out ? 0u : h[3];
-      if (q == j) {
-        id = (int)first;
-        kj = best;
-      }
-    }
-    const uint32_t next = sub_max<LPT>(h[0] & ~kLow);
-    open |= next == prev;
-    const uint32_t low_key = kj & 0x80000000u ? kj ^ 0x80000000u : ~kj;
-    const bool pick = q < k;
-    open |= pick && !(fabsf(__uint_as_float(low_key)) < INFINITY);
-    if (bias && !__any(open)) {
-      // the picks' choices again, without the places in their last bits
-      const float lj = pick ? ld_logit(row + id) : 0.f, bj = pick ? bias[id] : 0.f;
-      cj = (softmax ? exp_of(lj - m) * smax : inv_of(1.f + exp_of(-lj))) + bj;
-      const float ej = err(cj, lj, bj);
-      const float cn = __shfl(cj, here + 1, 64), en = __shfl(ej, here + 1, 64);
-      // (a key is short of its choice by less than PER units in the last place)
-      const uint32_t up = next | kLow;
-      const float left = __uint_as_float(up & 0x80000000u ? up ^ 0x80000000u : ~up);
-      const float high = ceiling(left);
-      open |= pick && !(cj - ej > (q < k - 1 ? cn + en : high));
-    }
-    if (!__any(open)) return id;
   }
-
-  // rounds: the largest choice, the lower id on ties; pick j to lane j
-  id = base;
-  auto rounds = [&](int j0, int j1) {
-    for (int j = j0; j < j1; ++j) {
-      float best = c[0];
-#pragma unroll
-      for (int i = 1; i < PER; ++i) best = fmaxf(best, c[i]);
-      best = sub_max<LPT>(best);
-      int at = 0x3fffffff;
-#pragma unroll
-      for (int i = PER - 1; i >= 0; --i) at = c[i] == best ? i : at;
-      const uint32_t first = sub_min<LPT>((uint32_t)(base + at));
-      const int out = first == (uint32_t)(base + at) ? at : -1;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) c[i] = out == i ? -INFINITY : c[i];
-      if (q == j) {
-        id = (int)first;
-        cj = best;
-      }
-    }
+  auto value_of = [](uint32_t k0) {
+    return __uint_as_float(k0 & 0x80000000u ? k0 ^ 0x80000000u : ~k0);
   };
-  rounds(0, k);
-  unsure |= q < k && !(fabsf(cj) < INFINITY);
-  if (bias) {
-    // Each pick's choice minus its error has to be above the next pick's plus
-    // that one's, and the last's above every expert left. Experts of the same
-    // logit and bias tie exactly, and the ids have ordered those.
-    const bool fine = q < k && fabsf(cj) < INFINITY;
-    const float lj = fine ? ld_logit(row + id) : 0.f, bj = fine ? bias[id] : 0.f;
-    const float ej = err(cj, lj, bj);
-    const float cn = __shfl(cj, here + 1, 64), en = __shfl(ej, here + 1, 64);
-    const float ln = __shfl(lj, here + 1, 64), bn = __shfl(bj, here + 1, 64);
-    const bool close = q < k - 1 && !(cj - ej > cn + en) && !(lj == ln && bj == bn);
-    auto above = [&]() {  // the highest that an expert left can be
-      float left = c[0];
+  int id = 0, id_next = 0;  // pick q's, and that of the pick after it
+  uint32_t key = 0, key_next = 0;
+  for (int j = 0; j <= k; ++j) {
+    const uint32_t v = h[0] & ~kLow;
+    const uint32_t best = sub_max<LPT>(v);
+    const uint32_t mine = v == best ? (uint32_t)base + kLow - (h[0] & kLow) : 0x7fffffffu;
+    const uint32_t first = sub_min<LPT>(mine);
+    const bool out = mine == first;
+    if (PER > kDepth) open |= out && h[1] == 0;  // all its six are given
+    // (a bit select: written as a choice between two entries it is compiled
+    // as an indexed read of h, eleven instructions each)
+    const uint32_t gone = out ? ~0u : 0u;
 #pragma unroll
-      for (int i = 1; i < PER; ++i) left = fmaxf(left, c[i]);
-      return ceiling(sub_max<LPT>(left));
+    for (int u = 0; u + 1 < kDepth; ++u) h[u] = (h[u] & ~gone) | (h[u + 1] & gone);
+    h[kDepth - 1] &= ~gone;
+    if (q == j) {
+      id = (int)first;
+      key = best;
+    }
+    if (q == j - 1) {
+      id_next = (int)first;
+      key_next = best;
+    }
+  }
+  const uint32_t left = sub_max<LPT>(h[0] & ~kLow);  // of the experts after those
+
+  // Each pick has to be above the one after it, errors and replaced bits
+  // aside, and the last pick above all that is left. Experts of the same logit
+  // and bias tie exactly, and the ids have ordered those.
+  const bool pick = q < k, last = q == k - 1;
+  const float vj = value_of(key), vn = value_of(key_next);
+  const bool fine = pick && fabsf(vj) < INFINITY, more = fine && fabsf(vn) < INFINITY;
+  open |= pick && !fine;
+  const float lj = fine ? ld_logit(row + id) : 0.f, ln = more ? ld_logit(row + id_next) : 0.f;
+  if (!bias) {
+    open |= more && !(lj >= ln);
+    open |= last && key == left;
+  } else {
+    const float bj = fine ? bias[id] : 0.f, bn = more ? bias[id_next] : 0.f;
+    auto choice = [&](float lv, float bv) {
+      return (softmax ? exp_of(lv - m) * smax : inv_of(1.f + exp_of(-lv))) + bv;
     };
-    const float high = above();
-    bool below = q != k - 1 || cj - ej > high;
-    if (!__all(below)) {  // expert by expert, exact ties with the last pick apart
-      const int last = sub + k - 1;
-      const float low = __shfl(cj - ej, last, 64);
-      const float lk = __shfl(lj, last, 64), bk = __shfl(bj, last, 64);
-      below = true;
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        below &= c[i] == -INFINITY || (l[i] == lk && b[i] == bk) ||
-                 low > c[i] + err(c[i], l[i], b[i]);
-    }
-    const bool reorder = own_bits<LPT>(__ballot(close)) != 0;
-    const bool more = own_bits<LPT>(__ballot(!below)) != 0;
-    if (__any(reorder || more)) {
-      // fp64 choices of the picks and the next ones, ranked by them. Enough if
-      // the picks are sure to be among these: k of them are above `low`.
-      const int n = min(k + 3, LPT);
-      rounds(k, n);
-      const float low = -sub_max<LPT>(q < k ? ej - cj : -INFINITY);
-      const float rest = above();
-      unsure |= more && !(low > rest);
-      double total = 1.0;
-      if (softmax) {
-        total = 0.0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) total += l[i] == -INFINITY ? 0.0 : exp((double)l[i] - m);
-        total = sub_sum<LPT>(total);
-      }
-      const bool cand = q < n && fabsf(cj) < INFINITY;
-      const float lc = cand ? ld_logit(row + id) : 0.f;
-      const double v = cand ? score64(lc, softmax, m, total) + (double)bias[id] : -INFINITY;
-      int rank = 0;
-      for (int j = 0; j < n; ++j) {
-        const double w = __shfl(v, sub + j, 64);
-        const int wi = __shfl(id, sub + j, 64);
-        rank += w > v || (w == v && wi < id);
-      }
-      // candidate of rank r to lane r
-      const int to = reorder || more ? (cand ? rank : q) : q;
-      id = __builtin_amdgcn_ds_permute((sub + to) * 4, id);
-    }
+    auto err = [&](float cv, float lv, float bv) {
+      const float x = softmax ? m - lv : fabsf(lv);
+      return kU * (fabsf(cv - bv) * (3.f * x + kA) + 3.f * fabsf(cv));
+    };
+    const float cj = choice(lj, bj), cn = choice(ln, bn);
+    const float low = cj - err(cj, lj, bj);
+    open |= more && !(low > cn + err(cn, ln, bn)) && !(lj == ln && bj == bn);
+    // None left has a choice above `up`, so none a score above S, and none an
+    // error above E (s x <= S (1 + ln(smax / S)) for a score s <= S).
+    const float up = value_of(left | kLow);
+    const float S = fminf(smax, fmaxf(up + bmax, 1e-30f));
+    const float E = kU * (S * (3.f + 2.1f * __builtin_amdgcn_logf(smax / S) + kA) + 3.f * fabsf(up));
+    open |= last && up > -INFINITY && !(low > up + E);
   }
   return id;
 }
 
+// Gate of pick q < k of a token (lj: its logit, -inf where there is none).
+// total: the row's sum of e^(l - m), for softmax gates without renorm.
+template <int LPT>
+__device__ __forceinline__ float gate_of(float lj, const RouteSpec& sp, float m, float total) {
+  const bool softmax = sp.score == BMOE_SCORE_SOFTMAX;
+  float g;
+  if (sp.renorm) {
+    const float mc = sub_max<LPT>(lj);
+    const float shift = softmax ? mc : fminf(mc, 0.f);
+    const float u = lj == -INFINITY ? 0.f
+                    : softmax ? exp_of(lj - shift) : sigmoid_shifted(lj, shift);
+    const float sum = sub_sum<LPT>(u);
+    g = sum > 0.f ? u / sum : 0.f;
+  } else if (softmax) {
+    g = lj == -INFINITY ? 0.f : exp_of(lj - m) / total;
+  } else {
+    g = lj == -INFINITY ? 0.f : inv_of(1.f + exp_of(-lj));
+  }
+  return sp.scale * g;
+}
+
 // ---- routing ----------------------------------------------------------------------
+// Tokens that fp32 leaves open (well under 1 in 100 of ordinary ones) are
+// decided one at a time by the whole wave. In a launch of their own after this
+// one they cost more (at 32768 tokens of 256 experts 24 us for that launch).
 template <int LPT, int PER, bool VEC, typename T>
 __global__ __launch_bounds__(256) void route_kernel(const T* logits, const float* bias, int T_,
                                                     int N, int k, RouteSpec sp, LaneMap map,
@@ -582,12 +561,9 @@ __global__ __launch_bounds__(256) void route_kernel(const T* logits, const float
   constexpr int kTok = 256 / LPT;  // tokens per workgroup
   const int q = threadIdx.x % LPT;
   const bool softmax = sp.score == BMOE_SCORE_SOFTMAX;
-  // (a map that does not fit: lanes by expert, as without groups)
-  const int groups = map.lpg > 0 ? sp.groups : 1;
-  const int size = N / groups, lpg = map.lpg > 0 ? map.lpg : LPT;
-  const int in_group = q % lpg * PER;  // this lane's first expert within its group
-  const int base = q / lpg * size + in_group;
-  const int cnt = q / lpg < groups ? max(0, min(PER, size - in_group)) : 0;
+  const int in_group = (q & (map.lpg - 1)) * PER;  // this lane's first expert within its group
+  const int base = (q >> map.shift) * map.size + in_group;
+  const int cnt = q >> map.shift < sp.groups ? max(0, min(PER, map.size - in_group)) : 0;
   float b[PER], bmax = 0.f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) b[i] = 0.f;
@@ -604,21 +580,24 @@ __global__ __launch_bounds__(256) void route_kernel(const T* logits, const float
     float l[PER];
     ld_row<PER, VEC>(row + base, cnt, -INFINITY, l);
     bool bad = false;
-    float m = -INFINITY;
+    float m = -INFINITY, total = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       bad |= l[i] != l[i];
       m = fmaxf(m, l[i]);
     }
     m = sub_max<LPT>(m);
-    bad = own_bits<LPT>(__ballot(bad)) != 0 || (softmax && m == INFINITY);
+    if (softmax && !sp.renorm) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) total += l[i] == -INFINITY ? 0.f : exp_of(l[i] - m);
+      total = sub_sum<LPT>(total);
+    }
+    const bool has_nan = own_bits<LPT>(__ballot(bad)) != 0;
 
-    bool unsure = bad || map.lpg == 0;
-    int id = 0;
-    if (map.lpg > 0)
-      id = choose<LPT, PER>(row, bias, l, b, bmax, base, k, sp, lpg, m, unsure);
-    // the exact way, one token at a time by the whole wave
-    uint64_t todo = __ballot(unsure && live);
+    bool open = has_nan || m == INFINITY || !(bmax < INFINITY);
+    int id = choose<LPT, PER>(row, bias, l, b, bmax, base, k, sp, map, m, open);
+    uint64_t todo = __ballot(open && live);
+    const bool pick = live && q < k;  // (a lane without a token may hold no id)
     while (todo) {
       const int sub = (int)__builtin_ctzll(todo) / LPT * LPT;
       todo &= ~(LPT == 64 ? ~0ull : ((1ull << (LPT & 63)) - 1) << sub);
@@ -628,30 +607,48 @@ __global__ __launch_bounds__(256) void route_kernel(const T* logits, const float
       const int y = __shfl(x, q, 64);
       if ((threadIdx.x & 63) / LPT * LPT == sub) id = y;
     }
-
-    const bool pick = live && q < k;  // (a lane without a token may hold no id)
-    const float lj = pick ? ld_logit(row + id) : -INFINITY;
-    float g;
-    if (sp.renorm) {
-      const float mc = sub_max<LPT>(lj);
-      const float shift = softmax ? mc : fminf(mc, 0.f);
-      const float u = lj == -INFINITY ? 0.f
-                      : softmax ? exp_of(lj - shift) : sigmoid_shifted(lj, shift);
-      const float sum = sub_sum<LPT>(u);
-      g = sum > 0.f ? u / sum : 0.f;
-    } else if (softmax) {
-      float total = 0.f;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) total += l[i] == -INFINITY ? 0.f : exp_of(l[i] - m);
-      total = sub_sum<LPT>(total);
-      g = lj == -INFINITY ? 0.f : exp_of(lj - m) / total;
-    } else {
-      g = lj == -INFINITY ? 0.f : inv_of(1.f + exp_of(-lj));
-    }
+    const bool nan = has_nan || (softmax && m == INFINITY);
+    const float g = gate_of<LPT>(pick ? ld_logit(row + id) : -INFINITY, sp, m, total);
     if (pick) {
       ids[tok * k + q] = id;
-      gates[tok * k + q] = bad ? NAN : sp.scale * g;
+      gates[tok * k + q] = nan ? NAN : g;
     }
+  }
+}
+
+// Every token in 64 bits, a wave each: groups whose lanes route_kernel does not
+// have (more than 32 groups of more than 64 experts).
+template <typename T>
+__global__ __launch_bounds__(256) void route_exact_kernel(const T* logits, const float* bias,
+                                                          int T_, int N, int k, RouteSpec sp,
+                                                          int32_t* ids, float* gates) {
+  constexpr int PER = 64;
+  const int q = threadIdx.x & 63;
+  const bool softmax = sp.score == BMOE_SCORE_SOFTMAX;
+  const size_t t = (size_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= (size_t)T_) return;  // whole wave
+  const T* row = logits + t * N;
+  float m = -INFINITY, total = 0.f;
+  bool nan = false;
+  for (int e = q; e < N; e += 64) {
+    const float l = ld_logit(row + e);
+    nan |= l != l;
+    m = fmaxf(m, l);
+  }
+  m = sub_max<64>(m);
+  nan = __any(nan) || (softmax && m == INFINITY);
+  if (softmax && !sp.renorm) {
+    for (int e = q; e < N; e += 64) {
+      const float l = ld_logit(row + e);
+      total += l == -INFINITY ? 0.f : exp_of(l - m);
+    }
+    total = sub_sum<64>(total);
+  }
+  const int id = choose_exact<PER>(row, bias, N, k, sp, 0, m);
+  const float g = gate_of<64>(q < k ? ld_logit(row + id) : -INFINITY, sp, m, total);
+  if (q < k) {
+    ids[t * k + q] = id;
+    gates[t * k + q] = nan ? NAN : g;
   }
 }
 
@@ -970,6 +967,7 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const int* part, int
 template <bool VEC, typename T>
 hipError_t route_t(const T* logits, const float* bias, int Tn, int N, int k, const RouteSpec& sp,
                    int32_t* ids, float* gates, hipStream_t s) {
+  const bool few = Tn <= 1024;  // a wave per token still leaves SIMDs without one
   LaneMap map;
 #define BMOE_CALL(LPT, PER, WHEN)                                                               \
   if ((WHEN) && N <= LPT * PER && k <= LPT && (map = lane_map<LPT, PER>(N, sp.groups)).lpg) {   \
@@ -978,20 +976,16 @@ hipError_t route_t(const T* logits, const float* bias, int Tn, int N, int k, con
                          dim3(256), 0, s, KernelTiming{}, logits, bias, Tn, N, k, sp, map, ids, \
                          gates);                                                                \
   }
-  const bool few = Tn <= 1024;  // a wave per token still leaves SIMDs without one
   BMOE_CALL(16, 4, true)
   BMOE_CALL(16, 16, !few)
   BMOE_CALL(64, 4, true)
   BMOE_CALL(16, 16, true)
-  BMOE_CALL(32, 16, !few)
+  BMOE_CALL(32, 16, true)
   BMOE_CALL(64, 16, true)
   BMOE_CALL(64, 64, true)
 #undef BMOE_CALL
-  map.lpg = map.lpg64 = 0;
-  const unsigned blocks = ((unsigned)Tn + 3) / 4;
-  return launch_kernel(route_kernel<64, 64, VEC, T>, dim3(blocks < 2048 ? blocks : 2048),
-                       dim3(256), 0, s, KernelTiming{}, logits, bias, Tn, N, k, sp, map, ids,
-                       gates);
+  return launch_kernel(route_exact_kernel<T>, dim3(((unsigned)Tn + 3) / 4), dim3(256), 0, s,
+                       KernelTiming{}, logits, bias, Tn, N, k, sp, ids, gates);
 }
 
 #define BMOE_BY_SHAPE(CALL)                    \
