@@ -491,7 +491,9 @@ bmoe_status bmoe_route_balance(int T, int n_experts, int k, const int32_t* ids, 
  *   dx      [T][d], dtype dt: dx_add + sum_e dl_te W_r[e], summed in fp32 and
  *           rounded once.
  *   dw      fp32 [N][d]: sum over t of dl_te x_t, the same bits each run.
- * dl is bmoe_route_backward's dlogits (ids outside [0, N) contribute nothing).
+ * dl is bmoe_route_backward's dlogits. Ids outside [0, N) contribute nothing:
+ * a padded token's x may hold anything, except for softmax scores without
+ * renorm, whose products take every row (its dl is 0, so x has to be finite).
  * d a power of two in [16, 8192]; T = 0 leaves dx and sets dw to 0. ws: at
  * least bmoe_router_backward_workspace_bytes().
  */

@@ -78,6 +78,12 @@ CASES = [  # T, N, k, dtype, bias, groups
     (1000, 8, 2, "bf16", True, (4, 2, "top2")), (31, 12, 3, "f32", True, (12, 4, "top2")),
     (20, 64, 64, "f32", True, None), (12, 48, 6, "f32", True, (8, 1, "max")),
     (5000, 128, 4, "f32", True, (4, 2, "top2")), (70, 512, 8, "bf16", True, (16, 4, "max")),
+    # more than 1024 tokens: other lanes per token; groups that end inside a lane's
+    # experts, and ones that no lane layout holds
+    (1500, 216, 7, "bf16", True, (8, 3, "top2")), (1100, 500, 20, "f32", True, (4, 2, "max")),
+    (1300, 300, 33, "f32", True, (3, 1, "top2")), (1025, 250, 16, "bf16", False, (10, 4, "top2")),
+    (5, 4092, 7, "f32", True, (33, 4, "top2")), (3, 4092, 64, "bf16", False, (44, 2, "max")),
+    (1031, 17, 16, "f32", True, (1, 1, "max")),
 ]
 
 
@@ -327,6 +333,58 @@ def test_balance_matches_oracle(T, N, k):
     # counting only
     bmoe.route_balance(idd, load)
     assert np.array_equal(load.cpu().numpy(), rl)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_more_logits_than_32_bits_count(dt):
+    """Rows on both sides of the 2^31st logit and the last ones, of a batch with
+    more logits than 32 bits count; and their gradient's."""
+    N, k = 256, 3
+    T = 2 ** 31 // N + 5000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    logits = torch.empty(T, N, dtype=torch.bfloat16 if dt == "bf16" else torch.float32,
+                         device="cuda")
+    logits.normal_(generator=g)
+    sp = bmoe.RouteSpec("sigmoid", scale=1.5)
+    print(f"[route] T={T} N={N} {dt}", flush=True)
+    ids, gates = bmoe.route_logits(logits, k, sp)
+    dg = torch.randn(T, k, generator=g, device="cuda")
+    dl = bmoe.route_logits_backward(logits, ids, dg, sp)
+    rows = torch.cat([torch.arange(2 ** 31 // N - 40, 2 ** 31 // N + 40),
+                      torch.arange(T - 40, T)]).cuda()
+    l = logits[rows].double().cpu().numpy()
+    oid, og = O.route_logits(l, k, score="sigmoid", scale=1.5)
+    idn = ids[rows].cpu().numpy()
+    assert np.array_equal(idn, oid)
+    assert (np.abs(gates[rows].double().cpu().numpy() - og) <= eps_of(l) * og).all()
+    dgn = dg[rows].cpu().numpy()
+    ref = O.route_logits_backward(l, idn, dgn, score="sigmoid", scale=1.5)
+    tol = 4 * eps_of(l) * grad_scale(l, idn, dgn, "sigmoid", True, 1.5) + 2.0 ** -126
+    assert (np.abs(dl[rows].double().cpu().numpy() - ref) <= tol).all()
+
+
+def test_two_streams_at_once():
+    """Independent calls on two streams, in flight together, equal the same
+    calls made alone."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    sp = bmoe.RouteSpec("sigmoid", n_groups=4, topk_groups=2)
+    ls = [torch.randn(20000, 128, generator=g, device="cuda") for _ in range(2)]
+    b = torch.randn(128, generator=g, device="cuda") * 0.1
+    alone = [bmoe.route_logits(l, 4, sp, bias=b) for l in ls]
+    loads = [bmoe.route_balance(a[0], torch.zeros(128, dtype=torch.int32, device="cuda"))
+             for a in alone]
+    torch.cuda.synchronize()
+    ss = [torch.cuda.Stream() for _ in range(2)]
+    both = [None, None]
+    for _ in range(3):
+        for i, s in enumerate(ss):
+            r = bmoe.route_logits(ls[i], 4, sp, bias=b, stream=s)
+            ld = torch.empty(128, dtype=torch.int32, device="cuda")
+            bmoe.route_balance(r[0], ld, stream=s)
+            both[i] = (*r, ld)
+    torch.cuda.synchronize()
+    for a, l, r in zip(alone, loads, both):
+        assert torch.equal(a[0], r[0]) and torch.equal(a[1], r[1]) and torch.equal(l, r[2])
 
 
 # ---- graphs --------------------------------------------------------------------

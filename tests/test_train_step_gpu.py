@@ -103,6 +103,104 @@ def test_router_backward_same_bits_each_run():
         assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dw"], b["dw"])
 
 
+def test_router_backward_padded_rows_do_not_spread():
+    """A padded token (ids -1) may hold anything, NaN and infinities included:
+    it changes neither dW nor other rows, and its own dx is dx_add."""
+    T, d, N, k = 300, 512, 16, 2
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(T, d, generator=g, device="cuda").bfloat16()
+    w = torch.randn(N, d, generator=g, device="cuda").bfloat16()
+    l = torch.randn(T, N, generator=g, device="cuda")
+    ids, _ = bmoe.route_logits(l, k)
+    dg = torch.randn(T, k, generator=g, device="cuda")
+    add = torch.randn(T, d, generator=g, device="cuda").bfloat16()
+    pad = torch.arange(T, device="cuda") % 7 == 3
+    for dt in (torch.bfloat16, torch.float32):
+        xs, ws, adds = x.to(dt), w.to(dt), add.to(dt)
+        ids2, xz, xn = ids.clone(), xs.clone(), xs.clone()
+        ids2[pad] = -1
+        xz[pad] = 0
+        xn[pad] = float("nan")
+        for spec in (("softmax", True), ("sigmoid", False), ("sigmoid", True)):
+            sp = bmoe.RouteSpec(spec[0], renorm=spec[1])
+            a = bmoe.router_backward(xz, ws, l, ids2, dg, sp, dx_add=adds)
+            b = bmoe.router_backward(xn, ws, l, ids2, dg, sp, dx_add=adds)
+            assert torch.equal(a["dw"], b["dw"]) and torch.equal(a["dx"], b["dx"])
+            assert torch.equal(a["dx"][pad], adds[pad])
+
+
+@pytest.mark.parametrize("spec", [("sigmoid", True), ("softmax", False)], ids=str)
+def test_router_backward_captured_and_replayed(spec):
+    T, d, N, k = 700, 256, 32, 2
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.randn(T, d, device="cuda").bfloat16()
+    w = torch.randn(N, d, generator=g, device="cuda").bfloat16()
+    l = torch.randn(T, N, device="cuda")
+    dg = torch.randn(T, k, device="cuda")
+    sp = bmoe.RouteSpec(spec[0], renorm=spec[1])
+
+    def step():
+        ids, _ = bmoe.route_logits(l, k, sp)
+        return bmoe.router_backward(x, w, l, ids, dg, sp, dx_add=x)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(4):
+        for t in (x, l, dg):
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = step()
+        assert torch.equal(out["dx"], ref["dx"]) and torch.equal(out["dw"], ref["dw"]), i
+
+
+@pytest.mark.parametrize("spec", [("sigmoid", True), ("softmax", False)], ids=str)
+def test_router_backward_more_values_than_32_bits_count(spec):
+    """x with more than 2^31 values; only a few far rows have a gradient, so dW
+    is theirs alone, and the other rows' dx is dx_add."""
+    d, N, k = 2048, 8, 2
+    T = 2 ** 31 // d + 3000
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.empty(T, d, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    w_dev, w = rounded(np.random.default_rng(1).normal(0, 1, (N, d)) / math.sqrt(d), "bf16")
+    l_dev, _ = rounded(np.zeros((1, N)), "f32")
+    l_dev = torch.randn(T, N, generator=g, device="cuda")
+    sp = bmoe.RouteSpec(spec[0], renorm=spec[1])
+    ids, _ = bmoe.route_logits(l_dev, k, sp)
+    rows = torch.tensor([0, 5, 2 ** 31 // d - 1, 2 ** 31 // d, 2 ** 31 // d + 1, T - 1],
+                        device="cuda")
+    dg = torch.zeros(T, k, device="cuda")
+    dg[rows] = torch.randn(len(rows), k, generator=g, device="cuda")
+    print(f"[router_backward] T={T} d={d} {spec}", flush=True)
+    out = bmoe.router_backward(x, w_dev, l_dev, ids, dg, sp, dx_add=x)
+    l = l_dev[rows].double().cpu().numpy()
+    xr, idn, dgn = x[rows].double().cpu().numpy(), ids[rows].cpu().numpy(), dg[rows].cpu().numpy()
+    ref = O.router_backward(xr, w, l, idn, dgn, dx_add=xr, score=spec[0], renorm=spec[1])
+    A = grad_scale(l, idn, dgn, *spec, 1.0)
+    sx = np.abs(xr) * (N + 1) * U + ((4 * eps_of(l) + (N + 2) * U) * A) @ np.abs(w)
+    err = np.abs(out["dx"][rows].double().cpu().numpy() - ref["dx"])
+    assert (err <= sx + HALF["bf16"] * (np.abs(ref["dx"]) + sx)).all()
+    sw = ((4 * eps_of(l) + (len(rows) + 2) * U) * A).T @ np.abs(xr)
+    assert (np.abs(out["dw"].double().cpu().numpy() - ref["dw"]) <= sw + 2.0 ** -126).all()
+    out["dx"][rows] = x[rows]
+    assert torch.equal(out["dx"], x)
+
+
+def test_norm_of_more_values_than_32_bits_count():
+    n = 2 ** 31 + 12345
+    t = torch.empty(n, dtype=torch.bfloat16, device="cuda")
+    t.fill_(0.5)
+    t[-1] = 1024.0
+    ref = math.sqrt(0.25 * (n - 1) + 1024.0 ** 2)
+    assert abs(float(bmoe.grad_norm([t[3:], t[:3].clone()])) - ref) <= (U + 2.0 ** -40) * ref
+    half = float(np.float32(ref / 2))
+    bmoe.clip_grads([t], half)   # a factor of 1/2 to within three roundings of fp32
+    assert t[0] == 0.25 and t[n // 2] == 0.25 and t[2 ** 31] == 0.25 and t[-1] == 512.0
+
+
 # ---- gradient lists --------------------------------------------------------------
 
 def make_list(sizes, rng, scale=1.0, offset=0):
