@@ -62,6 +62,7 @@ PairsLayout router_pairs_layout(int T, int d, int N, int k) {
   return l;
 }
 
+size_t dl_bytes(int T, int N) { return up256((size_t)T * N * sizeof(float)); }
 size_t parts_bytes(int T, int N) { return up256((size_t)T * 3 * router_parts_experts(N) * 2); }
 
 // The list of a gradient call: types, NULLs, alignment to the element, and
@@ -241,13 +242,13 @@ size_t bmoe_router_backward_workspace_bytes(bmoe_dtype dt, int T, int d, int n_e
       n_experts > kMaxExperts || k < 1 || k > n_experts || k > kMaxPicks || T < 0 ||
       (long long)T * k > INT_MAX)
     return 0;
-  // dl [T][N] (its three parts for bf16, with the dW of the token ranges), or
+  // dl [T][N] (its three parts for bf16) with the dW of the token ranges, or
   // the picks' pairs and lists with the dW of theirs
-  size_t dense = up256((size_t)T * n_experts * sizeof(float));
-  if (dt == BMOE_BF16) {
-    const int S = router_dense_splits(T, d, n_experts);
-    dense = parts_bytes(T, n_experts) + (S > 1 ? (size_t)S * n_experts * d * sizeof(float) : 0);
-  }
+  const int S = dt == BMOE_BF16 ? router_dense_splits(T, d, n_experts)
+                                : router_f32_splits(T, d, n_experts);
+  const size_t dense =
+      (dt == BMOE_BF16 ? parts_bytes(T, n_experts) : dl_bytes(T, n_experts)) +
+      (S > 1 ? (size_t)S * n_experts * d * sizeof(float) : 0);
   const size_t sparse = router_pairs_layout(T, d, n_experts, k).total;
   return (dense > sparse ? dense : sparse) + 256;
 }
@@ -295,11 +296,16 @@ bmoe_status bmoe_router_backward(bmoe_dtype dt, int T, int d, int n_experts, int
       return BMOE_E_HIP;
     return BMOE_OK;
   }
+  // fp32, or no tokens (dw = 0, whatever x's type)
   float* dl = static_cast<float*>(ws);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + dl_bytes(T, n_experts));
   if (T > 0 &&
       launch_route_bwd(BMOE_F32, T, n_experts, k, sp, logits, ids, dgates, dl, s) != hipSuccess)
     return BMOE_E_HIP;
-  return launch_router_bwd(dt, T, d, n_experts, x, w_router, dl, dx_add, dx, dw, s) == hipSuccess
+  return launch_router_bwd_f32(T, d, n_experts, static_cast<const float*>(x),
+                               static_cast<const float*>(w_router), dl,
+                               static_cast<const float*>(dx_add), static_cast<float*>(dx), dw,
+                               part, s) == hipSuccess
              ? BMOE_OK
              : BMOE_E_HIP;
 }

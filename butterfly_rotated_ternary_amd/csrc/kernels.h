@@ -261,11 +261,12 @@ int router_dense_splits(int T, int d, int N);
 hipError_t launch_router_bwd_parts(int T, int d, int N, const uint16_t* x, const uint16_t* w,
                                    const uint16_t* parts, const uint16_t* dx_add, uint16_t* dx,
                                    float* dw, float* part, hipStream_t s);
-// Gradient of the router's product from dl [T][N]: dx = dx_add (may be NULL)
-// + dl W, dw [N][d] fp32 = dl^T x.
-hipError_t launch_router_bwd(bmoe_dtype dt, int T, int d, int N, const void* x, const void* w,
-                             const float* dl, const void* dx_add, void* dx, float* dw,
-                             hipStream_t s);
+// The router product's gradient from dl fp32 [T][N], fp32 x and W; part: fp32
+// [router_f32_splits][N][d] scratch (unused where that is 1). T = 0: dw = 0.
+int router_f32_splits(int T, int d, int N);
+hipError_t launch_router_bwd_f32(int T, int d, int N, const float* x, const float* w,
+                                 const float* dl, const float* dx_add, float* dx, float* dw,
+                                 float* part, hipStream_t s);
 
 // ---- gradient lists ----------------------------------------------------------------
 struct GradEntry {

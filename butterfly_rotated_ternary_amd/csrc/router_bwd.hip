@@ -2,93 +2,13 @@
 // logits dl [T][N] (fp32):
 //   dx[t][c] = dx_add[t][c] + sum_e dl[t][e] W_r[e][c]
 //   dW[e][c] = sum_t dl[t][e] x[t][c]
-// fp32 FMA, 64 x 64 outputs per workgroup, 4 x 4 per thread, the reduction in
-// chunks of 16 through LDS, in ascending order.
+// Three ways: from the picks alone where only they move (sparse), on bf16 MFMA
+// with dl in three bf16 parts (dense, bf16), on fp32 MFMA (dense, fp32).
 #include "common.h"
 #include "kernels.h"
 
 namespace bmoe {
 namespace {
-
-constexpr int kRb = 16;
-
-template <typename T>
-__device__ __forceinline__ float ld_act(const T* p) {
-  if constexpr (sizeof(T) == 2) return bf16_lo(*reinterpret_cast<const uint16_t*>(p));
-  else return *p;
-}
-template <typename T>
-__device__ __forceinline__ void st_act(T* p, float v) {
-  if constexpr (sizeof(T) == 2) *p = (uint16_t)f32_to_bf16_bits(v);
-  else *p = v;
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void router_dx_kernel(const float* dl, const T* w,
-                                                        const T* dx_add, int T_, int d, int N,
-                                                        T* dx) {
-  __shared__ float as[kRb][65], bs[kRb][65];
-  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
-  const int t0 = blockIdx.x * 64, c0 = blockIdx.y * 64;
-  float acc[4][4] = {};
-  for (int e0 = 0; e0 < N; e0 += kRb) {
-    for (int u = tid; u < 64 * kRb; u += 256) {
-      const int r = u / kRb, ke = u % kRb;
-      as[ke][r] = t0 + r < T_ && e0 + ke < N ? dl[(size_t)(t0 + r) * N + e0 + ke] : 0.f;
-      const int kb = u / 64, cb = u % 64;
-      bs[kb][cb] = e0 + kb < N && c0 + cb < d ? ld_act(w + (size_t)(e0 + kb) * d + c0 + cb) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kRb; ++u)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[u][ty + 16 * i], bs[u][tx + 16 * j], acc[i][j]);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int t = t0 + ty + 16 * i, c = c0 + tx + 16 * j;
-      if (t >= T_ || c >= d) continue;
-      const size_t o = (size_t)t * d + c;
-      st_act(dx + o, acc[i][j] + (dx_add ? ld_act(dx_add + o) : 0.f));
-    }
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void router_dw_kernel(const float* dl, const T* x, int T_, int d,
-                                                        int N, float* dw) {
-  __shared__ float as[kRb][65], bs[kRb][65];
-  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
-  const int e0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
-  float acc[4][4] = {};
-  for (int t0 = 0; t0 < T_; t0 += kRb) {
-    for (int u = tid; u < 64 * kRb; u += 256) {
-      const int r = u / 64, c = u % 64;
-      const bool ok = t0 + r < T_;
-      as[r][c] = ok && e0 + c < N ? dl[(size_t)(t0 + r) * N + e0 + c] : 0.f;
-      bs[r][c] = ok && c0 + c < d ? ld_act(x + (size_t)(t0 + r) * d + c0 + c) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kRb; ++u)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[u][ty + 16 * i], bs[u][tx + 16 * j], acc[i][j]);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int e = e0 + ty + 16 * i, c = c0 + tx + 16 * j;
-      if (e < N && c < d) dw[(size_t)e * d + c] = acc[i][j];
-    }
-}
 
 // ---- sparse dl -------------------------------------------------------------------
 // Where only the k picks of a token move (every spec but softmax without
@@ -538,16 +458,119 @@ __global__ __launch_bounds__(512) void router_dw_mfma_kernel(const uint16_t* par
   }
 }
 
-template <typename T>
-hipError_t bwd_t(int Tn, int d, int N, const T* x, const T* w, const float* dl, const T* dx_add,
-                 T* dx, float* dw, hipStream_t s) {
-  const hipError_t e =
-      Tn == 0 ? hipSuccess :
-      launch_kernel(router_dx_kernel<T>, dim3(((unsigned)Tn + 63) / 64, (d + 63) / 64), dim3(256), 0, s,
-                    KernelTiming{}, dl, w, dx_add, Tn, d, N, dx);
-  if (e != hipSuccess) return e;
-  return launch_kernel(router_dw_kernel<T>, dim3((d + 63) / 64, (N + 63) / 64), dim3(256), 0, s,
-                       KernelTiming{}, dl, x, Tn, d, N, dw);
+// ---- dense dl, fp32: fp32 MFMA ------------------------------------------------------
+// v_mfma_f32_32x32x2_f32: lane l gives element (l % 32, l / 32) of A and (l / 32,
+// l % 32) of B, straight from memory. Exact fp32 products at 1/16 of the bf16
+// rate; the split of both operands into bf16 parts (six products) would be
+// faster and is left out, fp32 layers being small here.
+//
+// dx: 64 tokens x 128 columns per workgroup, 4 waves of 32 x 64. Eight experts
+// per step: half h of the wave takes experts 4 h .. 4 h + 3 of them (any order
+// of a sum's terms will do, as long as A and B agree), so its dl come as one
+// 16-byte load (VEC: N is a multiple of 4).
+template <bool VEC>
+__global__ __launch_bounds__(256) void router_dx_f32_kernel(const float* dl, const float* w,
+                                                            const float* dx_add, int T_, int d,
+                                                            int N, float* dx) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int half = lane >> 5, col = lane & 31;
+  const size_t t0 = (size_t)blockIdx.x * 64 + wave / 2 * 32;
+  const int c0 = blockIdx.y * 128 + wave % 2 * 64;
+  const float* row = dl + min(t0 + col, (size_t)T_ - 1) * N;
+  const int ca = min(c0 + col, d - 1), cb = min(c0 + 32 + col, d - 1);
+  f32x16 acc[2] = {f32x16{}, f32x16{}};
+  for (int e0 = 0; e0 < N; e0 += 8) {
+    float a[4], b0[4], b1[4];
+    const int eh = e0 + 4 * half;
+    if constexpr (VEC) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(row + min(eh, N - 4));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = row[min(eh + i, N - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float* we = w + (size_t)min(eh + i, N - 1) * d;
+      b0[i] = we[ca];
+      b1[i] = we[cb];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = eh + i < N;
+      const float x = in ? a[i] : 0.f;
+      acc[0] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, in ? b0[i] : 0.f, acc[0], 0, 0, 0);
+      acc[1] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, in ? b1[i] : 0.f, acc[1], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const size_t t = t0 + 8 * (r >> 2) + 4 * half + (r & 3);
+      const int c = c0 + 32 * j + col;
+      if (t < (size_t)T_ && c < d) dx[t * d + c] = acc[j][r] + (dx_add ? dx_add[t * d + c] : 0.f);
+    }
+}
+
+// dW: 64 experts x 64 columns per wave and range of tokens, two tokens per MFMA
+// step, eight steps loaded ahead.
+constexpr int kF32Rows = 16;
+
+__global__ __launch_bounds__(64) void router_dw_f32_kernel(const float* dl, const float* x, int T_,
+                                                           int d, int N, int tokens_per_split,
+                                                           float* out) {
+  const int lane = threadIdx.x, half = lane >> 5, col = lane & 31;
+  const int c0 = blockIdx.x * 64, e0 = blockIdx.y * 64;
+  const size_t t0 = (size_t)blockIdx.z * tokens_per_split;
+  const size_t t1 = min(t0 + tokens_per_split, (size_t)T_);
+  int e[2], c[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    e[i] = min(e0 + 32 * i + col, N - 1);
+    c[i] = min(c0 + 32 * i + col, d - 1);
+  }
+  f32x16 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+  for (size_t t = t0; t < t1; t += kF32Rows) {
+    float a[8][2], b[8][2];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const size_t tr = min(t + 2 * u + half, t1 - 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        a[u][i] = dl[tr * N + e[i]];
+        b[u][i] = x[tr * d + c[i]];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const bool in = t + 2 * u + half < t1;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        a[u][i] = in ? a[u][i] : 0.f;
+        b[u][i] = in ? b[u][i] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(a[u][i], b[u][j], acc[i][j], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int ee = e0 + 32 * i + 8 * (r >> 2) + 4 * half + (r & 3), cc = c0 + 32 * j + col;
+        if (ee < N && cc < d) out[((size_t)blockIdx.z * N + ee) * d + cc] = acc[i][j][r];
+      }
 }
 
 }  // namespace
@@ -612,14 +635,35 @@ hipError_t launch_router_bwd_parts(int T, int d, int N, const uint16_t* x, const
                        reinterpret_cast<float4*>(dw));
 }
 
-hipError_t launch_router_bwd(bmoe_dtype dt, int T, int d, int N, const void* x, const void* w,
-                             const float* dl, const void* dx_add, void* dx, float* dw,
-                             hipStream_t s) {
-  if (dt == BMOE_BF16)
-    return bwd_t(T, d, N, static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w), dl,
-                 static_cast<const uint16_t*>(dx_add), static_cast<uint16_t*>(dx), dw, s);
-  return bwd_t(T, d, N, static_cast<const float*>(x), static_cast<const float*>(w), dl,
-               static_cast<const float*>(dx_add), static_cast<float*>(dx), dw, s);
+// Token ranges of the fp32 dW: 2048 waves, at least 128 tokens each.
+int router_f32_splits(int T, int d, int N) {
+  const int tiles = (d + 63) / 64 * ((N + 63) / 64);
+  int S = (2048 + tiles - 1) / tiles;
+  const int most = (T + 127) / 128;
+  if (S > most) S = most;
+  return S < 1 ? 1 : S;
+}
+
+hipError_t launch_router_bwd_f32(int T, int d, int N, const float* x, const float* w,
+                                 const float* dl, const float* dx_add, float* dx, float* dw,
+                                 float* part, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  const dim3 gx(((unsigned)T + 63) / 64, (d + 127) / 128);
+  if (T > 0)
+    e = N % 4 == 0 ? launch_kernel(router_dx_f32_kernel<true>, gx, dim3(256), 0, s, KernelTiming{},
+                                   dl, w, dx_add, T, d, N, dx)
+                   : launch_kernel(router_dx_f32_kernel<false>, gx, dim3(256), 0, s,
+                                   KernelTiming{}, dl, w, dx_add, T, d, N, dx);
+  if (e != hipSuccess) return e;
+  const int S = router_f32_splits(T, d, N);
+  const int per = ((T + S - 1) / S + kF32Rows - 1) / kF32Rows * kF32Rows;
+  e = launch_kernel(router_dw_f32_kernel, dim3((d + 63) / 64, (N + 63) / 64, S), dim3(64), 0, s,
+                    KernelTiming{}, dl, x, T, d, N, per, S == 1 ? dw : part);
+  if (e != hipSuccess || S == 1) return e;
+  const size_t n4 = (size_t)N * d / 4;
+  return launch_kernel(router_dw_join_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s,
+                       KernelTiming{}, reinterpret_cast<const float4*>(part), S, n4,
+                       reinterpret_cast<float4*>(dw));
 }
 
 }  // namespace bmoe
