@@ -254,6 +254,14 @@ hipError_t sparse_t(int Tn, int d, int N, int k, const T* x, const T* w, const R
 typedef short rb_v4s __attribute__((ext_vector_type(4)));
 typedef uint64_t rb_u64x2 __attribute__((ext_vector_type(2)));
 
+// Work item of this workgroup: XCD x (workgroups are dealt to the eight in turn)
+// takes a run of consecutive items, the column tiles of the same tokens, so
+// that those tokens' parts are fetched into one L2 only.
+__device__ __forceinline__ unsigned xcd_item() {
+  const unsigned b = blockIdx.x, n = gridDim.x;
+  return n % 8 == 0 ? b % 8 * (n / 8) + b / 8 : b;
+}
+
 // Byte offset of this lane's first read for the 32 columns from col, slice 0.
 template <int STRIDE>
 __device__ __forceinline__ uint32_t tr_offset(int col, int lane) {
@@ -289,8 +297,9 @@ __global__ __launch_bounds__(256) void router_dx_mfma_kernel(const uint16_t* par
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 1, wn = wave & 1;
   float* const tile = lds + wave * (32 * 68);
-  const int c0 = blockIdx.x * 128, np = router_parts_experts(N);
-  const int t0 = blockIdx.y * 64 + wm * 32;
+  const unsigned item = xcd_item(), tiles = (d + 127) / 128;
+  const int c0 = item % tiles * 128, np = router_parts_experts(N);
+  const int t0 = (int)(item / tiles) * 64 + wm * 32;
   const uint16_t* arow =
       parts + (size_t)min(t0 + (lane & 31), T_ - 1) * (3 * (size_t)np) + 8 * (lane >> 5);
   // This lane's piece u of the tile: row (u * 64 + lane) / 8, 8 columns.
@@ -378,8 +387,11 @@ __global__ __launch_bounds__(512) void router_dw_mfma_kernel(const uint16_t* par
   __shared__ __attribute__((aligned(16))) char bs[2][64 * kDwStrideB];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 2, wn = wave & 3;
-  const int c0 = blockIdx.x * 256, e0 = blockIdx.y * 64, np = router_parts_experts(N);
-  const size_t t0 = (size_t)blockIdx.z * tokens_per_split;
+  const int np = router_parts_experts(N);
+  const unsigned item = xcd_item(), tiles_c = (d + 255) / 256, tiles = tiles_c * (np / 64);
+  const unsigned split = item / tiles, tile = item % tiles;
+  const int c0 = tile % tiles_c * 256, e0 = tile / tiles_c * 64;
+  const size_t t0 = (size_t)split * tokens_per_split;
   const int rows = t0 < (size_t)T_ ? (int)min((size_t)tokens_per_split, (size_t)T_ - t0) : 0;
   const uint16_t* ap = parts + t0 * (3 * (size_t)np) + e0 * 3;
   const uint16_t* bp = x + t0 * d + c0;
@@ -388,46 +400,60 @@ __global__ __launch_bounds__(512) void router_dw_mfma_kernel(const uint16_t* par
 #pragma unroll
   for (int j = 0; j < 2; ++j) offb[j] = tr_offset<kDwStrideB>(wn * 64 + 32 * j, lane);
   f32x16 acc[2] = {f32x16{}, f32x16{}};
-  uint4 ra[3], rb[4];
-  // Loads of rows or columns past the end go to the last row or to column 0
-  // (no branches between the loads) and become zeros on their way to LDS.
-  auto load = [&](int r0) {
+  u32x4 ra[2][3] = {}, rb[2][4] = {};
+  // This thread's pieces of a step: offsets in the step's rows of the parts and
+  // of x, and in LDS.
+  int row_a[3], row_b[4];
+  uint32_t at_a[3], at_b[4], lds_a[3], lds_b[4];
 #pragma unroll
-    for (int u = 0; u < 3; ++u) {
-      const int r = r0 + (tid + u * 512) / 24, ch = (tid + u * 512) % 24;
-      ra[u] = *reinterpret_cast<const uint4*>(ap + (size_t)min(r, rows - 1) * 3 * np + ch * 8);
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int r = r0 + (tid + u * 512) / 32, ch = (tid + u * 512) % 32;
-      rb[u] = *reinterpret_cast<const uint4*>(bp + (size_t)min(r, rows - 1) * d +
-                                              (c0 + ch * 8 < d ? ch * 8 : 0));
-    }
-  };
-  auto keep = [](uint4 v, bool ok) {
-    return make_uint4(ok ? v.x : 0u, ok ? v.y : 0u, ok ? v.z : 0u, ok ? v.w : 0u);
-  };
-  auto store = [&](int r0, int buf) {
-#pragma unroll
-    for (int u = 0; u < 3; ++u) {
-      const int r = (tid + u * 512) / 24, ch = (tid + u * 512) % 24;
-      *reinterpret_cast<uint4*>(as[buf] + r * kDwStrideA + ch * 16) = keep(ra[u], r0 + r < rows);
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int r = (tid + u * 512) / 32, ch = (tid + u * 512) % 32;
-      *reinterpret_cast<uint4*>(bs[buf] + r * kDwStrideB + ch * 16) =
-          keep(rb[u], r0 + r < rows && c0 + ch * 8 < d);
-    }
-  };
-  if (rows > 0) {
-    load(0);
-    store(0, 0);
+  for (int u = 0; u < 3; ++u) {
+    const int ch = (tid + u * 512) % 24;
+    row_a[u] = (tid + u * 512) / 24;
+    at_a[u] = (uint32_t)(row_a[u] * 3 * np + ch * 8);
+    lds_a[u] = row_a[u] * kDwStrideA + ch * 16;
   }
-  __syncthreads();
-  for (int r0 = 0, buf = 0; r0 < rows; r0 += 64, buf ^= 1) {
-    const bool more = r0 + 64 < rows;
-    if (more) load(r0 + 64);
+  const int ch_b = tid % 32;
+  const bool in_d = c0 + ch_b * 8 < d;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    row_b[u] = (tid + u * 512) / 32;
+    at_b[u] = (uint32_t)(row_b[u] * d + (in_d ? ch_b * 8 : 0));
+    lds_b[u] = row_b[u] * kDwStrideB + ch_b * 16;
+  }
+  // Rows past the end load the last row and become zeros on their way to LDS,
+  // as do columns past d. Every step issues the same loads, without a branch:
+  // only then do the compiler's waits for one step's leave the next in flight.
+  auto load = [&](int r0, u32x4 (&a)[3], u32x4 (&b)[4]) {
+    r0 = min(r0, rows - 1);
+    const uint16_t* pa = ap + (size_t)r0 * 3 * np;
+    const uint16_t* pb = bp + (size_t)r0 * d;
+    const int most = rows - 1 - r0;
+#pragma unroll
+    for (int u = 0; u < 3; ++u)
+      a[u] = *reinterpret_cast<const u32x4*>(
+          pa + (at_a[u] - (uint32_t)(max(0, row_a[u] - most) * 3 * np)));
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      b[u] = *reinterpret_cast<const u32x4*>(pb +
+                                             (at_b[u] - (uint32_t)(max(0, row_b[u] - most) * d)));
+  };
+  auto store = [&](int r0, int buf, const u32x4 (&a)[3], const u32x4 (&b)[4]) {
+    const int left = rows - r0;
+    const bool all = left >= 64 && c0 + 256 <= d;
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+      u32x4 v = a[u];
+      if (!all && row_a[u] >= left) v = u32x4{0u, 0u, 0u, 0u};
+      *reinterpret_cast<u32x4*>(as[buf] + lds_a[u]) = v;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      u32x4 v = b[u];
+      if (!all && (row_b[u] >= left || !in_d)) v = u32x4{0u, 0u, 0u, 0u};
+      *reinterpret_cast<u32x4*>(bs[buf] + lds_b[u]) = v;
+    }
+  };
+  auto multiply = [&](int buf) {
 #pragma unroll
     for (int sl = 0; sl < 4; ++sl) {
       bf16x8 a[3], b[2];
@@ -443,8 +469,23 @@ __global__ __launch_bounds__(512) void router_dw_mfma_kernel(const uint16_t* par
         for (int j = 0; j < 2; ++j)
           acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[p], b[j], acc[j], 0, 0, 0);
     }
-    if (more) store(r0 + 64, buf ^ 1);
-    __syncthreads();
+  };
+  // Step r0 is in LDS buffer (r0 / 64) % 2 while the next two are under way to
+  // registers. Steps past the end add zeros.
+  if (rows > 0) {
+    load(0, ra[0], rb[0]);
+    load(64, ra[1], rb[1]);
+    store(0, 0, ra[0], rb[0]);
+    for (int r0 = 0; r0 < rows; r0 += 128) {
+      load(r0 + 128, ra[0], rb[0]);
+      lds_barrier();
+      multiply(0);
+      store(r0 + 64, 1, ra[1], rb[1]);
+      load(r0 + 192, ra[1], rb[1]);
+      lds_barrier();
+      multiply(1);
+      store(r0 + 128, 0, ra[0], rb[0]);
+    }
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -453,7 +494,7 @@ __global__ __launch_bounds__(512) void router_dw_mfma_kernel(const uint16_t* par
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const int e = e0 + wm * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-      if (e < N) out[((size_t)blockIdx.z * N + e) * d + c] = acc[j][r];
+      if (e < N) out[((size_t)split * N + e) * d + c] = acc[j][r];
     }
   }
 }
@@ -609,25 +650,17 @@ int router_dense_splits(int T, int d, int N) {
 hipError_t launch_router_bwd_parts(int T, int d, int N, const uint16_t* x, const uint16_t* w,
                                    const uint16_t* parts, const uint16_t* dx_add, uint16_t* dx,
                                    float* dw, float* part, hipStream_t s) {
-  // token tiles on y in launches of 65535 at most
-  constexpr size_t most = (size_t)65535 * 64;
-  for (size_t t = 0; t < (size_t)T; t += most) {
-    const size_t left = (size_t)T - t;
-    const int n = (int)(left < most ? left : most);
-    const dim3 grid((d + 127) / 128, (n + 63) / 64);
-    const uint16_t* p = parts + t * 3 * router_parts_experts(N);
-    const hipError_t e =
-        dx_add ? launch_kernel(router_dx_mfma_kernel<true>, grid, dim3(256), 0, s, KernelTiming{},
-                               p, w, dx_add + t * d, n, d, N, dx + t * d)
-               : launch_kernel(router_dx_mfma_kernel<false>, grid, dim3(256), 0, s, KernelTiming{},
-                               p, w, dx_add, n, d, N, dx + t * d);
-    if (e != hipSuccess) return e;
-  }
+  const dim3 gx(((unsigned)T + 63) / 64 * ((d + 127) / 128));
+  hipError_t e = dx_add ? launch_kernel(router_dx_mfma_kernel<true>, gx, dim3(256), 0, s,
+                                        KernelTiming{}, parts, w, dx_add, T, d, N, dx)
+                        : launch_kernel(router_dx_mfma_kernel<false>, gx, dim3(256), 0, s,
+                                        KernelTiming{}, parts, w, dx_add, T, d, N, dx);
+  if (e != hipSuccess) return e;
   const int S = router_dense_splits(T, d, N);
   const int per = ((T + S - 1) / S + 63) / 64 * 64;
-  hipError_t e = launch_kernel(router_dw_mfma_kernel,
-                               dim3((d + 255) / 256, router_parts_experts(N) / 64, S), dim3(512),
-                               0, s, KernelTiming{}, parts, x, T, d, N, per, S == 1 ? dw : part);
+  e = launch_kernel(router_dw_mfma_kernel,
+                    dim3((d + 255) / 256 * (router_parts_experts(N) / 64) * S), dim3(512), 0, s,
+                    KernelTiming{}, parts, x, T, d, N, per, S == 1 ? dw : part);
   if (e != hipSuccess || S == 1) return e;
   const size_t n4 = (size_t)N * d / 4;
   return launch_kernel(router_dw_join_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s,
