@@ -63,7 +63,9 @@ PairsLayout router_pairs_layout(int T, int d, int N, int k) {
 }
 
 size_t dl_bytes(int T, int N) { return up256((size_t)T * N * sizeof(float)); }
-size_t parts_bytes(int T, int N) { return up256((size_t)T * 3 * router_parts_experts(N) * 2); }
+size_t parts_bytes(int T, int N) {
+  return up256(((size_t)T + 31) / 32 * 32 * 3 * router_parts_experts(N) * 2);
+}
 
 // The list of a gradient call: types, NULLs, alignment to the element, and
 // (where it is written) no two written tensors, and no written and another

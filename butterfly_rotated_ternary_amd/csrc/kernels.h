@@ -249,8 +249,10 @@ hipError_t launch_route_pairs(int T, int N, int k, const RouteSpec& sp, const fl
 hipError_t launch_router_bwd_sparse(bmoe_dtype dt, int T, int d, int N, int k, const void* x,
                                     const void* w, const RouterPairs& rp, const void* dx_add,
                                     void* dx, float* dw, float* part, hipStream_t s);
-// dl (any spec, fp32 logits) as three bf16 parts [T][Np / 32][3][32] whose sum
-// is dl, Np = router_parts_experts(N), zeros from N on.
+// dl (any spec, fp32 logits) as three bf16 parts whose sum is dl, in the order
+// of v_mfma_f32_32x32x16_bf16's A operand: [T / 32][Np / 16][part][64 lanes][8],
+// lane l = token l % 32, experts 8 (l / 32) .. + 7 of the sixteen; Np = N
+// rounded up to 64, zeros from N on; tokens from T on are not written.
 __host__ __device__ inline int router_parts_experts(int N) { return (N + 63) / 64 * 64; }
 hipError_t launch_route_bwd_parts(int T, int N, int k, const RouteSpec& sp, const float* logits,
                                   const int32_t* ids, const float* dgates, uint16_t* parts,

@@ -680,8 +680,7 @@ __device__ __forceinline__ float pick_grad(float l, float u, const RouteSpec& sp
 }
 
 // dl is written as fp32 [T][N], or (PARTS) as three bf16 parts whose sum is
-// dl to fp32's last bits, for the products on bf16 MFMA: [T][Np / 32][3][32],
-// Np = N rounded up to 64, zeros from N on.
+// dl to fp32's last bits, in the order of MFMA operands (router_parts_*).
 template <int LPT, int PER, bool VEC, bool PARTS, typename T>
 __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const int32_t* ids,
                                                         const float* dgates, int T_, int N, int k,
@@ -726,7 +725,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const i
   if (!live) return;
   if constexpr (PARTS) {
     const int np = router_parts_experts(N);
-    uint16_t* out = parts + tok * (3 * (size_t)np);
+    uint16_t* out = parts + tok / 32 * (96 * (size_t)np) + tok % 32 * 8;
 #pragma unroll
     for (int i = 0; i < PER; i += 4) {
       const int e = base + i;
@@ -739,7 +738,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const i
         uint2 w;
         w.x = pack_bf16x2(v[0], v[1]);
         w.y = pack_bf16x2(v[2], v[3]);
-        *reinterpret_cast<uint2*>(out + (e / 32 * 3 + p) * 32 + e % 32) = w;
+        *reinterpret_cast<uint2*>(out + (e / 16 * 3 + p) * 512 + e % 16 / 8 * 256 + e % 8) = w;
         v[0] -= bf16_lo(w.x);
         v[1] -= bf16_hi(w.x);
         v[2] -= bf16_lo(w.y);

@@ -278,8 +278,9 @@ __device__ __forceinline__ bf16x8 tr_read(const char* p) {
 }
 
 // dx: 64 tokens x 128 columns per workgroup, 4 waves of 32 x 64. W goes to LDS
-// 64 experts at a time; the parts come straight from memory (16 bytes of
-// consecutive experts per lane), dx_add is under way from the start. The tile
+// 64 experts at a time; the parts come straight from memory, stored in operand
+// order (by token and expert the call took 73 us, 11 more), dx_add is under way
+// from the start. The tile
 // leaves through LDS (the W tile's, done with by then), so dx_add and dx move
 // in 128-byte pieces of a row. Small tiles, so that four workgroups share a CU
 // and one's loads run under another's MFMAs: at T = 16384, d = 2048, 64
@@ -300,8 +301,8 @@ __global__ __launch_bounds__(256) void router_dx_mfma_kernel(const uint16_t* par
   const unsigned item = xcd_item(), tiles = (d + 127) / 128;
   const int c0 = item % tiles * 128, np = router_parts_experts(N);
   const int t0 = (int)(item / tiles) * 64 + wm * 32;
-  const uint16_t* arow =
-      parts + (size_t)min(t0 + (lane & 31), T_ - 1) * (3 * (size_t)np) + 8 * (lane >> 5);
+  // (tokens past the end: whatever is there, in rows that are not stored)
+  const uint16_t* ablock = parts + (size_t)(min(t0, T_ - 1) / 32) * (96 * (size_t)np) + lane * 8;
   // This lane's piece u of the tile: row (u * 64 + lane) / 8, 8 columns.
   const int cc = lane % 8 * 8, c = c0 + wn * 64 + cc;
   u32x4 add[4];
@@ -323,8 +324,8 @@ __global__ __launch_bounds__(256) void router_dx_mfma_kernel(const uint16_t* par
     for (int sl = 0; sl < 4; ++sl)
 #pragma unroll
       for (int p = 0; p < 3; ++p)
-        a[sl][p] = *reinterpret_cast<const u32x4*>(arow + ((e0 / 32 + sl / 2) * 3 + p) * 32 +
-                                                   sl % 2 * 16);
+        a[sl][p] =
+            *reinterpret_cast<const u32x4*>(ablock + ((size_t)(e0 / 16 + sl) * 3 + p) * 512);
     u32x4 b[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -393,7 +394,7 @@ __global__ __launch_bounds__(512) void router_dw_mfma_kernel(const uint16_t* par
   const int c0 = tile % tiles_c * 256, e0 = tile / tiles_c * 64;
   const size_t t0 = (size_t)split * tokens_per_split;
   const int rows = t0 < (size_t)T_ ? (int)min((size_t)tokens_per_split, (size_t)T_ - t0) : 0;
-  const uint16_t* ap = parts + t0 * (3 * (size_t)np) + e0 * 3;
+  const uint16_t* ap = parts + t0 / 32 * (96 * (size_t)np) + (size_t)(e0 / 16) * 1536;
   const uint16_t* bp = x + t0 * d + c0;
   const uint32_t offa = tr_offset<kDwStrideA>(wm * 96, lane);
   uint32_t offb[2];
@@ -407,10 +408,13 @@ __global__ __launch_bounds__(512) void router_dw_mfma_kernel(const uint16_t* par
   uint32_t at_a[3], at_b[4], lds_a[3], lds_b[4];
 #pragma unroll
   for (int u = 0; u < 3; ++u) {
-    const int ch = (tid + u * 512) % 24;
-    row_a[u] = (tid + u * 512) / 24;
-    at_a[u] = (uint32_t)(row_a[u] * 3 * np + ch * 8);
-    lds_a[u] = row_a[u] * kDwStrideA + ch * 16;
+    // 16 bytes of the step's two token blocks, four slices of sixteen experts,
+    // three parts and 64 lanes: a token's eight experts of one part
+    const int piece = tid + u * 512, l = piece % 64, part = piece / 64 % 3;
+    const int sl = piece / 192 % 4, e = sl * 16 + l / 32 * 8;
+    row_a[u] = piece / 768 * 32 + l % 32;
+    at_a[u] = (uint32_t)((sl * 3 + part) * 512 + l * 8);
+    lds_a[u] = row_a[u] * kDwStrideA + (e / 32 * 96 + part * 32 + e % 32) * 2;
   }
   const int ch_b = tid % 32;
   const bool in_d = c0 + ch_b * 8 < d;
@@ -425,13 +429,13 @@ __global__ __launch_bounds__(512) void router_dw_mfma_kernel(const uint16_t* par
   // only then do the compiler's waits for one step's leave the next in flight.
   auto load = [&](int r0, u32x4 (&a)[3], u32x4 (&b)[4]) {
     r0 = min(r0, rows - 1);
-    const uint16_t* pa = ap + (size_t)r0 * 3 * np;
     const uint16_t* pb = bp + (size_t)r0 * d;
     const int most = rows - 1 - r0;
 #pragma unroll
-    for (int u = 0; u < 3; ++u)
-      a[u] = *reinterpret_cast<const u32x4*>(
-          pa + (at_a[u] - (uint32_t)(max(0, row_a[u] - most) * 3 * np)));
+    for (int u = 0; u < 3; ++u) {  // (a block holds 32 tokens: those past the end are there)
+      const int block = min(r0 / 32 + row_a[u] / 32, (rows - 1) / 32);
+      a[u] = *reinterpret_cast<const u32x4*>(ap + (size_t)block * (96 * (size_t)np) + at_a[u]);
+    }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       b[u] = *reinterpret_cast<const u32x4*>(pb +
