@@ -45,6 +45,11 @@ bool pow2_d16(int d) { return d >= 16 && d <= 8192 && (d & (d - 1)) == 0; }
 
 size_t elem(bmoe_dtype dt) { return dt == BMOE_BF16 ? 2 : 4; }
 
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + b_bytes && y < x + a_bytes;
+}
+
 struct PairsLayout {
   size_t list, off, part, total;
   int tokens, ranges;
@@ -52,7 +57,7 @@ struct PairsLayout {
 PairsLayout router_pairs_layout(int T, int d, int N, int k) {
   PairsLayout l;
   l.tokens = router_range_tokens(T, d, N);
-  l.ranges = T > 0 ? (T + l.tokens - 1) / l.tokens : 1;
+  l.ranges = T > 0 ? (int)(((long long)T + l.tokens - 1) / l.tokens) : 1;
   const size_t list_bytes = up256((size_t)T * k * sizeof(int2));
   l.list = list_bytes;
   l.off = l.list + list_bytes;
@@ -271,6 +276,10 @@ bmoe_status bmoe_router_backward(bmoe_dtype dt, int T, int d, int n_experts, int
   const void* ptrs[] = {x, w_router, logits, ids, dgates, dx_add, dx, dw, ws};
   for (const void* p : ptrs)
     if (!ok16(p)) return BMOE_E_ALIGN;
+  // dx is written while x is read; dx_add is read entry by entry before dx is
+  const size_t x_bytes = (size_t)T * d * elem(dt);
+  if (overlap(dx, x_bytes, x, x_bytes) || (dx_add != dx && overlap(dx, x_bytes, dx_add, x_bytes)))
+    return BMOE_E_VALUE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (T > 0 && !(sp.score == BMOE_SCORE_SOFTMAX && !sp.renorm)) {
     const PairsLayout l = router_pairs_layout(T, d, n_experts, k);

@@ -398,19 +398,6 @@ __device__ __forceinline__ int choose(const T* row, const float* bias, const flo
     }
   }
 
-  auto err = [&](float cv, float lv, float bv) {
-    const float x = softmax ? m - lv : fabsf(lv);
-    return kU * (fabsf(cv - bv) * (3.f * x + kA) + 3.f * fabsf(cv));
-  };
-  // The highest that an expert can be whose choice is `left` at most: no such
-  // expert's score is above S, and none's error above E (s x <= S (1 + ln(smax
-  // / S)) for a score s <= S).
-  auto ceiling = [&](float left) {
-    const float S = fminf(smax, fmaxf(left + bmax, 1e-30f));
-    const float E =
-        kU * (S * (3.f + 2.1f * __builtin_amdgcn_logf(smax / S) + kA) + 3.f * fabsf(left));
-    return left == -INFINITY ? left : left + E;
-  };
   // Each lane sorts integer keys (the choice's bits in order, the last ones
   // replaced by the place in the lane, so that a comparison is a min and a max)
   // into its kDepth largest; a round looks at the lanes' heads only. Keys equal
@@ -865,8 +852,8 @@ __global__ __launch_bounds__(WAVES * 64) void route_lists_kernel(
 // ---- loads and the balance bias -----------------------------------------------------
 // Histograms in LDS (integers, so no order matters), then bias[e] += rate *
 // sign(mean - load[e]) with the comparison in integers (sum of the loads
-// against N * load). Few ids: one workgroup does it all. More: kShares
-// workgroups count a share each and write their histograms; a second launch
+// against N * load). Few ids: one workgroup does it all. More: 64 workgroups
+// count a share each and write their histograms; a second launch
 // adds them (no counters to clear, nothing left between calls). Bound by
 // latency: 2^18 ids are 1 MB. Measured at 262144 ids, 256 experts: one
 // workgroup 42 us, shares 12 us (two launches).

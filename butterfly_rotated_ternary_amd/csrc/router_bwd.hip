@@ -280,9 +280,8 @@ __device__ __forceinline__ bf16x8 tr_read(const char* p) {
 // dx: 64 tokens x 128 columns per workgroup, 4 waves of 32 x 64. W goes to LDS
 // 64 experts at a time; the parts come straight from memory, stored in operand
 // order (by token and expert the call took 73 us, 11 more), dx_add is under way
-// from the start. The tile
-// leaves through LDS (the W tile's, done with by then), so dx_add and dx move
-// in 128-byte pieces of a row. Small tiles, so that four workgroups share a CU
+// from the start. The tile leaves through LDS (the W tile's, done with by
+// then), so dx_add and dx move in 128-byte pieces of a row. Small tiles, so that four workgroups share a CU
 // and one's loads run under another's MFMAs: at T = 16384, d = 2048, 64
 // experts 128 x 128 tiles at two per CU took 56 us, these 31 us (134 MB).
 constexpr int kDxStrideW = 128 * 2 + 64;
@@ -626,7 +625,7 @@ __global__ __launch_bounds__(64) void router_dw_f32_kernel(const float* dl, cons
 int router_range_tokens(int T, int d, int N) {
   const int chunks = (d + 511) / 512;
   int r = 1024;
-  while (r > 32 && (long long)((T + 4 * r - 1) / (4 * r)) * N * chunks < 4096) r /= 2;
+  while (r > 32 && ((long long)T + 4 * r - 1) / (4 * r) * N * chunks < 4096) r /= 2;
   return r;
 }
 
@@ -646,7 +645,7 @@ hipError_t launch_router_bwd_sparse(bmoe_dtype dt, int T, int d, int N, int k, c
 int router_dense_splits(int T, int d, int N) {
   const int tiles = (d + 255) / 256 * (router_parts_experts(N) / 64);
   int S = (256 + tiles - 1) / tiles;
-  const int most = (T + 255) / 256;
+  const int most = (int)(((long long)T + 255) / 256);
   if (S > most) S = most;
   return S < 1 ? 1 : S;
 }
@@ -661,7 +660,7 @@ hipError_t launch_router_bwd_parts(int T, int d, int N, const uint16_t* x, const
                                         KernelTiming{}, parts, w, dx_add, T, d, N, dx);
   if (e != hipSuccess) return e;
   const int S = router_dense_splits(T, d, N);
-  const int per = ((T + S - 1) / S + 63) / 64 * 64;
+  const int per = (int)((((long long)T + S - 1) / S + 63) / 64 * 64);
   e = launch_kernel(router_dw_mfma_kernel,
                     dim3((d + 255) / 256 * (router_parts_experts(N) / 64) * S), dim3(512), 0, s,
                     KernelTiming{}, parts, x, T, d, N, per, S == 1 ? dw : part);
@@ -676,7 +675,7 @@ hipError_t launch_router_bwd_parts(int T, int d, int N, const uint16_t* x, const
 int router_f32_splits(int T, int d, int N) {
   const int tiles = (d + 63) / 64 * ((N + 63) / 64);
   int S = (2048 + tiles - 1) / tiles;
-  const int most = (T + 127) / 128;
+  const int most = (int)(((long long)T + 127) / 128);
   if (S > most) S = most;
   return S < 1 ? 1 : S;
 }
@@ -693,7 +692,7 @@ hipError_t launch_router_bwd_f32(int T, int d, int N, const float* x, const floa
                                    KernelTiming{}, dl, w, dx_add, T, d, N, dx);
   if (e != hipSuccess) return e;
   const int S = router_f32_splits(T, d, N);
-  const int per = ((T + S - 1) / S + kF32Rows - 1) / kF32Rows * kF32Rows;
+  const int per = (int)((((long long)T + S - 1) / S + kF32Rows - 1) / kF32Rows * kF32Rows);
   e = launch_kernel(router_dw_f32_kernel, dim3((d + 63) / 64, (N + 63) / 64, S), dim3(64), 0, s,
                     KernelTiming{}, dl, x, T, d, N, per, S == 1 ? dw : part);
   if (e != hipSuccess || S == 1) return e;

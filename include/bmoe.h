@@ -60,8 +60,8 @@ typedef enum {
   BMOE_E_HIP = 7,        /* a HIP runtime call failed */
   BMOE_E_ALIGN = 8,      /* a pointer is not 16-byte aligned */
   BMOE_E_VALUE = 9       /* a field of a bmoe_route_spec or a scalar argument
-                            outside its range, or gradient tensors that share
-                            memory where one of them is written */
+                            outside its range, or tensors that share memory
+                            where one of them is written */
 } bmoe_status;
 
 /* Storage of the shared substrate: 2-bit words (bmoe_pack_ternary) or the
@@ -487,9 +487,10 @@ bmoe_status bmoe_route_balance(int T, int n_experts, int k, const int32_t* ids, 
  * bmoe_backward) the gradients of x and of the router's weight.
  *   x, w_router  as bmoe_router, logits fp32 [T][N] and ids as the forward's.
  *   dx_add  [T][d] or NULL: added to the gradient (bmoe_backward's dx, so that
- *           dx holds both); may be dx itself, and overlaps it in no other way.
+ *           dx holds both); may be dx itself.
  *   dx      [T][d], dtype dt: dx_add + sum_e dl_te W_r[e], summed in fp32 and
- *           rounded once.
+ *           rounded once. Sharing memory with x, or with part of dx_add, is
+ *           refused (BMOE_E_VALUE).
  *   dw      fp32 [N][d]: sum over t of dl_te x_t, the same bits each run.
  * dl is bmoe_route_backward's dlogits. Ids outside [0, N) contribute nothing:
  * a padded token's x may hold anything, except for softmax scores without

@@ -83,6 +83,7 @@ def test_router_backward_refuses():
              dw=A, ws=A, wb=big):
         return bmoe.lib().bmoe_router_backward(dt, T, d, N, k, sp or spec(), x, w, lg, ids, dg,
                                                add, dx, dw, ws, wb, None)
+    B = A + 0x10000
     assert call(dt=3) == DTYPE and call(d=100) == SHAPE and call(N=0) == SHAPE
     assert call(sp=spec(n_groups=3)) == VALUE
     for name in ("x", "w", "lg", "ids", "dg", "dx", "dw"):
@@ -90,6 +91,9 @@ def test_router_backward_refuses():
         assert call(**{name: A + 8}) == ALIGN, name
     assert call(add=A + 8) == ALIGN
     assert call(ws=None) == WS and call(wb=16) == WS
+    # dx on x, or on part of dx_add (4 x 64 bf16 values are 512 bytes)
+    assert call() == VALUE and call(dx=B, x=B + 496) == VALUE and call(dx=B, x=B - 496) == VALUE
+    assert call(dx=B, add=B + 256) == VALUE and call(dx=B, add=B - 496) == VALUE
 
 
 def test_router_logits_refuses():
@@ -184,3 +188,16 @@ def test_wrappers_refuse_before_the_library():
     with pytest.raises(ValueError):
         bmoe.router_backward(x, torch.zeros(5, 7), x, torch.zeros(4, 2, dtype=torch.int32),
                              torch.zeros(4, 2))
+
+
+def test_workspace_sizes_at_the_largest_token_counts():
+    """Sizes for token counts next to 2^31 neither wrap nor shrink."""
+    n = bmoe.bmoe_router_backward_workspace_bytes
+    top = 2 ** 31 - 1
+    for dt in (BF, F32):
+        last = 0
+        for T in (1, 1000, 1 << 20, 1 << 30, top - 4096, top):
+            got = n(dt, T, 16, 8, 1)
+            assert got >= max(last, T * 8 * 4), (dt, T)
+            last = got
+    assert bmoe.bmoe_route_balance_workspace_bytes(top, 64, 1) >= 64 * 4
