@@ -376,12 +376,14 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     ss = [torch.cuda.Stream() for _ in range(2)]
     both = [None, None]
+    # each stream's own loads: one freed here would go to the other stream
+    # while its kernel still runs
+    ld = [torch.empty(128, dtype=torch.int32, device="cuda") for _ in range(2)]
     for _ in range(3):
         for i, s in enumerate(ss):
             r = bmoe.route_logits(ls[i], 4, sp, bias=b, stream=s)
-            ld = torch.empty(128, dtype=torch.int32, device="cuda")
-            bmoe.route_balance(r[0], ld, stream=s)
-            both[i] = (*r, ld)
+            bmoe.route_balance(r[0], ld[i], stream=s)
+            both[i] = (*r, ld[i])
     torch.cuda.synchronize()
     for a, l, r in zip(alone, loads, both):
         assert torch.equal(a[0], r[0]) and torch.equal(a[1], r[1]) and torch.equal(l, r[2])
