@@ -673,7 +673,14 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const i
                                                         const float* dgates, int T_, int N, int k,
                                                         RouteSpec sp, float* dlogits,
                                                         uint16_t* parts) {
-  const int q = threadIdx.x % LPT, base = q * PER;
+  // Lanes of a token side by side in memory: slot i of lane q is expert
+  // q QUAD + off(i). (No order among lanes matters here, as it does for the
+  // choice. PER consecutive experts per lane, 16-byte pieces 64 bytes apart,
+  // took 18.0 us instead of 11.4 at T = 32768, N = 256, dense: 67 MB.)
+  constexpr int QUAD = VEC || PARTS ? 4 : 1;
+  static_assert(PER % 4 == 0, "whole quads");
+  auto off = [](int i) { return i / QUAD * (QUAD * LPT) + i % QUAD; };
+  const int q = threadIdx.x % LPT, base = q * QUAD;
   const size_t tok = (size_t)blockIdx.x * (256 / LPT) + threadIdx.x / LPT;
   const bool live = tok < (size_t)T_;
   const T* row = logits + (live ? tok : 0) * N;
@@ -691,11 +698,18 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const i
     const int at = __shfl(id, sub + j, 64) - base;
     const float vj = __shfl(v, sub + j, 64);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) a[i] += at == i ? vj : 0.f;
+    for (int i = 0; i < PER; ++i) a[i] += at == off(i) ? vj : 0.f;
   }
   if (dense) {
     float l[PER], m = -INFINITY, total = 0.f;
-    ld_row<PER, VEC>(row + min(base, N), max(0, min(PER, N - base)), -INFINITY, l);
+#pragma unroll
+    for (int i = 0; i < PER; i += QUAD) {
+      const int e = base + off(i);
+      float f[QUAD];
+      ld_row<QUAD, VEC>(row + min(e, N), max(0, min(QUAD, N - e)), -INFINITY, f);
+#pragma unroll
+      for (int u = 0; u < QUAD; ++u) l[i + u] = f[u];
+    }
 #pragma unroll
     for (int i = 0; i < PER; ++i) m = fmaxf(m, l[i]);
     m = sub_max<LPT>(m);
@@ -715,7 +729,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const i
     uint16_t* out = parts + tok / 32 * (96 * (size_t)np) + tok % 32 * 8;
 #pragma unroll
     for (int i = 0; i < PER; i += 4) {
-      const int e = base + i;
+      const int e = base + off(i);
       if (e >= np) continue;
       float v[4];
 #pragma unroll
@@ -735,15 +749,14 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const i
     return;
   }
   float* out = dlogits + tok * N;
-  if constexpr (VEC && PER % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < PER; i += 4)
-      if (base + i < N)
-        *reinterpret_cast<float4*>(out + base + i) = make_float4(a[i], a[i + 1], a[i + 2], a[i + 3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (base + i < N) out[base + i] = a[i];
+  for (int i = 0; i < PER; i += QUAD) {
+    const int e = base + off(i);
+    if (e >= N) continue;
+    if constexpr (QUAD == 4)
+      *reinterpret_cast<float4*>(out + e) = make_float4(a[i], a[i + 1], a[i + 2], a[i + 3]);
+    else
+      out[e] = a[i];
   }
 }
 
