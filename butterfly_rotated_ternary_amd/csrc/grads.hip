@@ -103,7 +103,8 @@ __device__ __forceinline__ void add_sq(double& a, double& b, uint4 v) {
 }
 
 // Index of the entry that chunk c belongs to.
-__device__ __forceinline__ int find(const GradTable& tab, uint32_t c) {
+template <typename Table>
+__device__ __forceinline__ int find(const Table& tab, uint32_t c) {
   int lo = 0, hi = tab.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
@@ -114,7 +115,8 @@ __device__ __forceinline__ int find(const GradTable& tab, uint32_t c) {
 }
 
 // This workgroup's run of chunks.
-__device__ __forceinline__ uint32_t run_start(const GradTable& tab, uint32_t b) {
+template <typename Table>
+__device__ __forceinline__ uint32_t run_start(const Table& tab, uint32_t b) {
   return (uint32_t)((uint64_t)tab.chunks * b / gridDim.x);
 }
 
@@ -147,8 +149,8 @@ __device__ __forceinline__ void sq_chunks(const Span& s, long long c0, long long
   }
 }
 
-template <bool ONCE>
-__global__ __launch_bounds__(kThreads) void grad_sq_kernel(GradTable tab, double* part) {
+template <bool ONCE, typename Table>
+__global__ __launch_bounds__(kThreads) void grad_sq_kernel(Table tab, double* part) {
   __shared__ double lds[kThreads / 64];
   double a = 0.0, b = 0.0;
   uint32_t c = run_start(tab, blockIdx.x);
@@ -219,7 +221,8 @@ __device__ __forceinline__ void scale_chunks(const Span& s, long long c0, long l
 
 // norm: read, or (part not NULL) taken from the n_part partial sums and
 // written by the first workgroup.
-__global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradTable tab, const double* part,
+template <typename Table>
+__global__ __launch_bounds__(kThreads) void grad_scale_kernel(Table tab, const double* part,
                                                               int n_part, float* norm,
                                                               float max_norm, int in_place) {
   __shared__ double lds[kThreads / 64];
@@ -242,6 +245,21 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradTable tab, con
   }
 }
 
+// A table of few tensors: kernel arguments of 4.5 KB cost each launch about
+// 0.5 us of host time, which short lists wait for (one layer's four tensors:
+// 17.5 us a call, 18.6 with the large table).
+constexpr int kFew = 8;
+struct FewTable {
+  int n;
+  uint32_t chunks;
+  GradEntry t[kFew];
+};
+FewTable few(const GradTable& tab) {
+  FewTable r{tab.n, tab.chunks, {}};
+  for (int i = 0; i < tab.n; ++i) r.t[i] = tab.t[i];
+  return r;
+}
+
 // A workgroup per chunk up to what is resident at once.
 int grid_of(const GradTable& tab) {
   return tab.chunks < (uint32_t)kGradParts ? (int)tab.chunks : kGradParts;
@@ -259,8 +277,13 @@ hipError_t launch_grad_sq(const GradTable& tab, double* part, int* n_part, hipSt
   *n_part = grid_of(tab);
   const dim3 grid(*n_part), block(kThreads);
   if (tab.chunks > (256u << 20) / 4096)
-    return launch_kernel(grad_sq_kernel<true>, grid, block, 0, s, KernelTiming{}, tab, part);
-  return launch_kernel(grad_sq_kernel<false>, grid, block, 0, s, KernelTiming{}, tab, part);
+    return launch_kernel(grad_sq_kernel<true, GradTable>, grid, block, 0, s, KernelTiming{}, tab,
+                         part);
+  if (tab.n <= kFew)
+    return launch_kernel(grad_sq_kernel<false, FewTable>, grid, block, 0, s, KernelTiming{},
+                         few(tab), part);
+  return launch_kernel(grad_sq_kernel<false, GradTable>, grid, block, 0, s, KernelTiming{}, tab,
+                       part);
 }
 
 hipError_t launch_grad_norm(const double* part, int n_part, float* norm, hipStream_t s) {
@@ -270,8 +293,12 @@ hipError_t launch_grad_norm(const double* part, int n_part, float* norm, hipStre
 
 hipError_t launch_grad_scale(const GradTable& tab, const double* part, int n_part, float* norm,
                              float max_norm, int in_place, hipStream_t s) {
-  return launch_kernel(grad_scale_kernel, dim3(grid_of(tab)), dim3(kThreads), 0, s, KernelTiming{},
-                       tab, part, n_part, norm, max_norm, in_place);
+  const dim3 grid(grid_of(tab)), block(kThreads);
+  if (tab.n <= kFew)
+    return launch_kernel(grad_scale_kernel<FewTable>, grid, block, 0, s, KernelTiming{}, few(tab),
+                         part, n_part, norm, max_norm, in_place);
+  return launch_kernel(grad_scale_kernel<GradTable>, grid, block, 0, s, KernelTiming{}, tab, part,
+                       n_part, norm, max_norm, in_place);
 }
 
 }  // namespace bmoe
