@@ -510,8 +510,8 @@ bmoe_status bmoe_router_backward(bmoe_dtype dt, int T, int d, int n_experts, int
  *   norm = sqrt(sum of g^2 over all entries of all tensors), fp32, summed in
  *          64 bits (squares neither overflow nor vanish) in a fixed order
  *   out  = g * max_norm / norm where max_norm < norm < infinity, else g
- * A norm that is not finite clips nothing: the gradients pass through and the
- * norm tells the caller.
+ * (max_norm / norm is one fp32 division). A norm that is not finite clips
+ * nothing: the gradients pass through and the norm tells the caller.
  *   grads  host array of n tensors: device pointer (aligned to its element),
  *          count >= 0 entries (2^40 in all at most), BMOE_F32 or BMOE_BF16.
  *          Read before the call returns. bf16 results are rounded once.
