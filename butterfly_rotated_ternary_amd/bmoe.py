@@ -755,7 +755,8 @@ def router_logits(x: torch.Tensor, w_router: torch.Tensor, *, logits=None,
     with _at(x, stream):
         if logits is None:
             logits = torch.empty(T, N, dtype=torch.float32, device=x.device)
-        _like("logits", logits, torch.float32, (T, N), x.device)
+        else:
+            _like("logits", logits, torch.float32, (T, N), x.device)
         _check(bmoe_router_logits(dt, T, d, N, x, w_router, logits, stream), "bmoe_router_logits")
         return logits
 
@@ -775,10 +776,12 @@ def route_logits(logits: torch.Tensor, k: int, spec: Optional[RouteSpec] = None,
             _like("bias", bias, torch.float32, (N,), dev)
         if ids is None:
             ids = torch.empty(T, k, dtype=torch.int32, device=dev)
+        else:
+            _like("ids", ids, torch.int32, (T, k), dev)
         if gates is None:
             gates = torch.empty(T, k, dtype=torch.float32, device=dev)
-        _like("ids", ids, torch.int32, (T, k), dev)
-        _like("gates", gates, torch.float32, (T, k), dev)
+        else:
+            _like("gates", gates, torch.float32, (T, k), dev)
         _check(bmoe_route(dt, T, N, k, spec, logits, bias, ids, gates, stream), "bmoe_route")
         return ids, gates
 
@@ -798,7 +801,8 @@ def route_logits_backward(logits: torch.Tensor, ids: torch.Tensor, dgates: torch
     with _at(logits, stream):
         if dlogits is None:
             dlogits = torch.empty(T, N, dtype=torch.float32, device=dev)
-        _like("dlogits", dlogits, torch.float32, (T, N), dev)
+        else:
+            _like("dlogits", dlogits, torch.float32, (T, N), dev)
         _check(bmoe_route_backward(dt, T, N, k, spec, logits, ids, dgates, dlogits, stream),
                "bmoe_route_backward")
         return dlogits
@@ -847,10 +851,12 @@ def router_backward(x: torch.Tensor, w_router: torch.Tensor, logits: torch.Tenso
             _like("dx_add", dx_add, x.dtype, (T, d), dev)
         if dx is None:
             dx = torch.empty_like(x)
+        else:
+            _like("dx", dx, x.dtype, (T, d), dev)
         if dw is None:
             dw = torch.empty(N, d, dtype=torch.float32, device=dev)
-        _like("dx", dx, x.dtype, (T, d), dev)
-        _like("dw", dw, torch.float32, (N, d), dev)
+        else:
+            _like("dw", dw, torch.float32, (N, d), dev)
         n = bmoe_router_backward_workspace_bytes(dt, T, d, N, k)
         if n == 0:
             raise BmoeError(2, "bmoe_router_backward_workspace_bytes")
