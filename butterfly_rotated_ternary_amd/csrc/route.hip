@@ -194,6 +194,7 @@ struct LaneMap {
   int lpg64;  // the same where a wave takes one token of LPT PER experts
   int shift;  // log2 lpg
   int size;   // experts per group
+  bool fits() const { return lpg && lpg64; }
 };
 inline int lanes_per_group(int lanes, int per, int N, int groups) {
   const int size = N / groups;
@@ -228,44 +229,61 @@ __device__ __forceinline__ void top2_lanes(float& a, float& a2, int lpg) {
   }
 }
 
-// fp64 score of a logit: e^(l - m) / total, or the sigmoid.
-__device__ __forceinline__ double score64(float l, bool softmax, float m, double total) {
-  return softmax ? exp((double)l - m) / total : 1.0 / (1.0 + exp(-(double)l));
-}
-
 // The picks of one token in 64 bits, by a whole wave, from row; m: the row's
-// largest logit. Lanes by group where `lpg` lanes hold one (0: by expert).
-// Returns pick j's id in lane j. Rare, so what counts is how long one takes
-// (kept on DPP and scalar reads of lanes), not how many instructions.
-template <int PER, typename T>
+// largest logit. LANES: `lpg` lanes hold a group each, else a lane's experts
+// may be of several. Returns pick j's id in lane j. Rare, so its code is seldom
+// in the instruction cache and fetching that is what one costs: it is kept
+// short (the exponential and the quotient once each, in loops that turn the
+// lane's values around) and on DPP and scalar reads of lanes.
+template <int PER, bool LANES, typename T>
 __device__ int choose_exact(const T* row, const float* bias, int N, int k, const RouteSpec& sp,
                             int lpg, float m) {
   const int q = threadIdx.x & 63;
   const bool softmax = sp.score == BMOE_SCORE_SOFTMAX;
   const int size = N / sp.groups;
-  const int mine_g = lpg ? q / lpg : 0, in_group = lpg ? q % lpg * PER : q * PER;
-  const int base = lpg ? mine_g * size + in_group : in_group;
-  const int cnt = lpg ? (mine_g < sp.groups ? min(PER, size - in_group) : 0) : min(PER, N - in_group);
+  const int mine_g = LANES ? q / lpg : 0, in_group = LANES ? q % lpg * PER : q * PER;
+  const int base = LANES ? mine_g * size + in_group : in_group;
+  const int cnt =
+      LANES ? (mine_g < sp.groups ? min(PER, size - in_group) : 0) : min(PER, N - in_group);
   float l[PER];
-  double c[PER], total = 1.0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) l[i] = i < cnt ? ld_logit(row + base + i) : -INFINITY;
-  const bool scored = bias || (sp.groups > 1 && sp.group_score == BMOE_GROUP_TOP2);
-  if (scored && softmax) {
-    total = 0.0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) total += l[i] == -INFINITY ? 0.0 : exp((double)l[i] - m);
-    total = sub_sum<64>(total);
-  }
+  double c[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
+    const float v = ld_logit(row + min(base + i, N - 1));
+    l[i] = i < cnt ? v : -INFINITY;
     c[i] = l[i];
-    if (scored && l[i] != -INFINITY)
-      c[i] = score64(l[i], softmax, m, total) + (bias ? (double)bias[base + i] : 0.0);
+  }
+  if (bias || (sp.groups > 1 && sp.group_score == BMOE_GROUP_TOP2)) {
+    // f(l, c, slot) for each slot in turn, its result the slot's new c
+    auto each = [&](auto f) {
+#pragma unroll 1
+      for (int i = 0; i < PER; ++i) {
+        const float l0 = l[0];
+        const double c0 = f(l0, c[0], i);
+#pragma unroll
+        for (int u = 0; u + 1 < PER; ++u) {
+          l[u] = l[u + 1];
+          c[u] = c[u + 1];
+        }
+        l[PER - 1] = l0;
+        c[PER - 1] = c0;
+      }
+    };
+    double total = 0.0;
+    each([&](float v, double, int) {
+      const double e = exp(softmax ? (double)v - m : -(double)v);
+      total += v == -INFINITY ? 0.0 : e;
+      return e;
+    });
+    total = softmax ? sub_sum<64>(total) : 1.0;
+    each([&](float v, double e, int i) {
+      const double s = (softmax ? e : 1.0) / (softmax ? total : 1.0 + e);
+      return v == -INFINITY ? -INFINITY : s + (bias ? (double)bias[min(base + i, N - 1)] : 0.0);
+    });
   }
   uint64_t keep = ~0ull;  // bit g: group g is kept
   if (sp.groups > 1) {
-    double mine = -INFINITY;  // lane g * max(lpg, 1): the score of group g
+    double mine = -INFINITY;  // lane g * lpg (LANES) or g: the score of group g
     auto top2 = [&](double& a, double& a2, double v) {
       if (v > a) { a2 = a; a = v; }
       else if (v > a2) a2 = v;
@@ -276,7 +294,7 @@ __device__ int choose_exact(const T* row, const float* bias, int N, int k, const
       a = fmax(a, oa);
     };
     const bool by_max = sp.group_score == BMOE_GROUP_MAX;
-    if (lpg) {
+    if constexpr (LANES) {
       double a = -INFINITY, a2 = -INFINITY;
 #pragma unroll
       for (int i = 0; i < PER; ++i) top2(a, a2, c[i]);
@@ -292,7 +310,7 @@ __device__ int choose_exact(const T* row, const float* bias, int N, int k, const
         if (q == g) mine = by_max || a2 == -INFINITY ? a : a + a2;
       }
     }
-    const int step = lpg ? lpg : 1, g = q / step;
+    const int step = LANES ? lpg : 1, g = q / step;
     int rank = 0;
     for (int h = 0; h < sp.groups; ++h) {
       const uint64_t bits = __double_as_longlong(mine);
@@ -303,12 +321,12 @@ __device__ int choose_exact(const T* row, const float* bias, int N, int k, const
     }
     const bool kept = g < sp.groups && rank < sp.keep;
     keep = __ballot(kept);
-    if (lpg) keep = kept ? ~0ull : 0;
+    if (LANES) keep = kept ? ~0ull : 0;
   }
   uint64_t key[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const bool in = i < cnt && (sp.groups == 1 || lpg ? keep != 0 : keep >> ((base + i) / size) & 1u);
+    const bool in = i < cnt && (sp.groups == 1 || LANES ? keep != 0 : keep >> ((base + i) / size) & 1u);
     // without a bias the experts' order is that of their logits
     key[i] = !in ? 0 : bias ? key_of(c[i]) : key_of((double)l[i]);
   }
@@ -560,46 +578,49 @@ __global__ __launch_bounds__(256) void route_kernel(const T* logits, const float
     for (int i = 0; i < PER; ++i) bmax = fmaxf(bmax, fabsf(b[i]));
     bmax = sub_max<LPT>(bmax);
   }
-  for (size_t t0 = (size_t)blockIdx.x * kTok; t0 < (size_t)T_; t0 += (size_t)gridDim.x * kTok) {
-    const size_t tok = t0 + threadIdx.x / LPT;
-    const bool live = tok < (size_t)T_;
-    const T* row = logits + (live ? tok : 0) * N;
-    float l[PER];
-    ld_row<PER, VEC>(row + base, cnt, -INFINITY, l);
-    bool bad = false;
-    float m = -INFINITY, total = 0.f;
+  // (No loop over tokens: in one the compiler keeps the conditions on spec and
+  // shape as masks, more than there are scalar registers; their spills made
+  // the 32768 x 256 case 26.0 us instead of 23.4.)
+  const size_t t0 = ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * kTok;
+  if (t0 >= (size_t)T_) return;
+  const size_t tok = t0 + threadIdx.x / LPT;
+  const bool live = tok < (size_t)T_;
+  const T* row = logits + (live ? tok : 0) * N;
+  float l[PER];
+  ld_row<PER, VEC>(row + base, cnt, -INFINITY, l);
+  bool bad = false;
+  float m = -INFINITY, total = 0.f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      bad |= l[i] != l[i];
-      m = fmaxf(m, l[i]);
-    }
-    m = sub_max<LPT>(m);
-    if (softmax && !sp.renorm) {
+  for (int i = 0; i < PER; ++i) {
+    bad |= l[i] != l[i];
+    m = fmaxf(m, l[i]);
+  }
+  m = sub_max<LPT>(m);
+  if (softmax && !sp.renorm) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) total += l[i] == -INFINITY ? 0.f : exp_of(l[i] - m);
-      total = sub_sum<LPT>(total);
-    }
-    const bool has_nan = own_bits<LPT>(__ballot(bad)) != 0;
+    for (int i = 0; i < PER; ++i) total += l[i] == -INFINITY ? 0.f : exp_of(l[i] - m);
+    total = sub_sum<LPT>(total);
+  }
+  const bool has_nan = own_bits<LPT>(__ballot(bad)) != 0;
 
-    bool open = has_nan || m == INFINITY || !(bmax < INFINITY);
-    int id = choose<LPT, PER>(row, bias, l, b, bmax, base, k, sp, map, m, open);
-    uint64_t todo = __ballot(open && live);
-    const bool pick = live && q < k;  // (a lane without a token may hold no id)
-    while (todo) {
-      const int sub = (int)__builtin_ctzll(todo) / LPT * LPT;
-      todo &= ~(LPT == 64 ? ~0ull : ((1ull << (LPT & 63)) - 1) << sub);
-      const size_t t = t0 + ((threadIdx.x & ~63) + sub) / LPT;
-      const int x = choose_exact<LPT * PER / 64>(logits + t * N, bias, N, k, sp, map.lpg64,
-                                                 __shfl(m, sub, 64));
-      const int y = __shfl(x, q, 64);
-      if ((threadIdx.x & 63) / LPT * LPT == sub) id = y;
-    }
-    const bool nan = has_nan || (softmax && m == INFINITY);
-    const float g = gate_of<LPT>(pick ? ld_logit(row + id) : -INFINITY, sp, m, total);
-    if (pick) {
-      ids[tok * k + q] = id;
-      gates[tok * k + q] = nan ? NAN : g;
-    }
+  bool open = has_nan || m == INFINITY || !(bmax < INFINITY);
+  int id = choose<LPT, PER>(row, bias, l, b, bmax, base, k, sp, map, m, open);
+  uint64_t todo = __ballot(open && live);
+  const bool pick = live && q < k;  // (a lane without a token may hold no id)
+  while (todo) {
+    const int sub = (int)__builtin_ctzll(todo) / LPT * LPT;
+    todo &= ~(LPT == 64 ? ~0ull : ((1ull << (LPT & 63)) - 1) << sub);
+    const size_t t = t0 + ((threadIdx.x & ~63) + sub) / LPT;
+    const int x = choose_exact<LPT * PER / 64, true>(logits + t * N, bias, N, k, sp, map.lpg64,
+                                               __shfl(m, sub, 64));
+    const int y = __shfl(x, q, 64);
+    if ((threadIdx.x & 63) / LPT * LPT == sub) id = y;
+  }
+  const bool nan = has_nan || (softmax && m == INFINITY);
+  const float g = gate_of<LPT>(pick ? ld_logit(row + id) : -INFINITY, sp, m, total);
+  if (pick) {
+    ids[tok * k + q] = id;
+    gates[tok * k + q] = nan ? NAN : g;
   }
 }
 
@@ -631,7 +652,7 @@ __global__ __launch_bounds__(256) void route_exact_kernel(const T* logits, const
     }
     total = sub_sum<64>(total);
   }
-  const int id = choose_exact<PER>(row, bias, N, k, sp, 0, m);
+  const int id = choose_exact<PER, false>(row, bias, N, k, sp, 0, m);
   const float g = gate_of<64>(q < k ? ld_logit(row + id) : -INFINITY, sp, m, total);
   if (q < k) {
     ids[t * k + q] = id;
@@ -969,11 +990,11 @@ hipError_t route_t(const T* logits, const float* bias, int Tn, int N, int k, con
   const bool few = Tn <= 1024;  // a wave per token still leaves SIMDs without one
   LaneMap map;
 #define BMOE_CALL(LPT, PER, WHEN)                                                               \
-  if ((WHEN) && N <= LPT * PER && k <= LPT && (map = lane_map<LPT, PER>(N, sp.groups)).lpg) {   \
+  if ((WHEN) && N <= LPT * PER && k <= LPT && (map = lane_map<LPT, PER>(N, sp.groups)).fits()) { \
     const unsigned blocks = ((unsigned)Tn + 256 / LPT - 1) / (256 / LPT);                       \
-    return launch_kernel(route_kernel<LPT, PER, VEC, T>, dim3(blocks < 2048 ? blocks : 2048),   \
-                         dim3(256), 0, s, KernelTiming{}, logits, bias, Tn, N, k, sp, map, ids, \
-                         gates);                                                                \
+    const dim3 grid(blocks < 65536 ? blocks : 65536, (blocks + 65535) / 65536);                 \
+    return launch_kernel(route_kernel<LPT, PER, VEC, T>, grid, dim3(256), 0, s, KernelTiming{}, \
+                         logits, bias, Tn, N, k, sp, map, ids, gates);                          \
   }
   BMOE_CALL(16, 4, true)
   BMOE_CALL(16, 16, !few)
