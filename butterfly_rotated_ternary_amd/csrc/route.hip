@@ -347,12 +347,14 @@ __device__ int choose_exact(const T* row, const float* bias, int N, int k, const
   return id;
 }
 
-// The picks in fp32: pick j's id in lane j. `open` is set for a token that fp32
-// does not decide: kept groups or picks closer than the errors bounded below,
-// no k finite choices, six picks from one lane of many experts;
-// choose_exact then decides it. Without a bias the choices are the logits
-// themselves, and only sums of two scores have errors. l, b: this lane's
-// logits and biases from expert `base` on (-inf and 0 past its last).
+// The picks: pick j's id in lane j. fp32 finds them and the one after them,
+// 64 bits put those in order. `open` is set for a token that this does not
+// decide: kept groups, or the last pick and the experts not looked at again,
+// closer than the errors bounded below, no k finite choices, a seventh pick from
+// one lane; choose_exact then decides it. Without a bias the
+// choices are the logits themselves, and only sums of two scores have errors.
+// l, b: this lane's logits and biases from expert `base` on (-inf and 0 past
+// its last).
 template <int LPT, int PER, typename T>
 __device__ __forceinline__ int choose(const T* row, const float* bias, const float (&l)[PER],
                                       const float (&b)[PER], float bmax, int base, int k,
@@ -363,7 +365,7 @@ __device__ __forceinline__ int choose(const T* row, const float* bias, const flo
   // most: the difference, its product with log2 e and that constant, then the
   // exponential's, sum's (PER + 6 additions) and quotient's last places. The
   // sigmoid has x = |l| and none of the sum.
-  const float kA = softmax ? PER + 24 : 8;
+  const float kA = softmax ? PER + 26 : 8;
   float c[PER], smax = 1.f;
   const bool scored = bias || (sp.groups > 1 && sp.group_score == BMOE_GROUP_TOP2);
   if (!scored) {
@@ -475,15 +477,16 @@ __device__ __forceinline__ int choose(const T* row, const float* bias, const flo
   auto value_of = [](uint32_t k0) {
     return __uint_as_float(k0 & 0x80000000u ? k0 ^ 0x80000000u : ~k0);
   };
-  int id = 0, id_next = 0;  // pick q's, and that of the pick after it
-  uint32_t key = 0, key_next = 0;
+  // the largest that a lane's list does not hold
+  const uint32_t spare = PER > kDepth ? h[kDepth] & ~kLow : 0;
+  int id = 0;  // pick q's; in lane k (if there is one) the expert's after the picks
+  uint32_t key = 0, beyond = 0;
   for (int j = 0; j <= k; ++j) {
     const uint32_t v = h[0] & ~kLow;
     const uint32_t best = sub_max<LPT>(v);
     const uint32_t mine = v == best ? (uint32_t)base + kLow - (h[0] & kLow) : 0x7fffffffu;
     const uint32_t first = sub_min<LPT>(mine);
     const bool out = mine == first;
-    if (PER > kDepth) open |= out && h[1] == 0;  // all its six are given
     // (a bit select: written as a choice between two entries it is compiled
     // as an indexed read of h, eleven instructions each)
     const uint32_t gone = out ? ~0u : 0u;
@@ -494,43 +497,59 @@ __device__ __forceinline__ int choose(const T* row, const float* bias, const flo
       id = (int)first;
       key = best;
     }
-    if (q == j - 1) {
-      id_next = (int)first;
-      key_next = best;
+    if (j == LPT) beyond = best;
+  }
+  // the largest of the experts that no lane has
+  const uint32_t left = max(sub_max<LPT>(h[0] ? h[0] & ~kLow : spare), beyond);
+
+  // The candidates in 64 bits, a lane each, and put in order: keys equal above
+  // the replaced bits, or off by the errors of c, may have them wrong. The sum
+  // behind a softmax's scores is off by kA u still.
+  const bool pick = q < k, last = q == k - 1;
+  const float v32 = value_of(key);
+  const bool fine = q <= k && fabsf(v32) < INFINITY;
+  open |= pick && !fine;
+  const float lq = fine ? ld_logit(row + id) : 0.f;
+  double s = 0.0, v = fine ? (double)lq : -INFINITY;
+  if (bias) {
+    const float bq = fine ? bias[id] : 0.f;
+    const double e = exp(softmax ? (double)lq - m : -(double)lq);
+    s = softmax ? e * (double)smax : 1.0 / (1.0 + e);
+    v = fine ? s + (double)bq : -INFINITY;
+  }
+  const bool follows = pick && q + 1 < LPT;  // the next lane has a candidate
+  auto wrong = [&] {
+    const double vn = __shfl(v, (here + 1) & 63, 64);
+    const int in = __shfl(id, (here + 1) & 63, 64);
+    return follows && !(v > vn || (v == vn && id < in));
+  };
+  for (int pass = 0; pass <= k && __any(wrong()); ++pass) {  // odd-even transposition
+    const int other = (q + pass) & 1 ? q - 1 : q + 1;
+    const bool two = other >= 0 && max(q, other) <= k && other < LPT;
+    const int from = two ? sub + other : here;
+    const double vo = __shfl(v, from, 64), so = __shfl(s, from, 64);
+    const int io = __shfl(id, from, 64);
+    const bool before = v > vo || (v == vo && id < io);
+    if (two && before != (other > q)) {
+      v = vo;
+      s = so;
+      id = io;
     }
   }
-  const uint32_t left = sub_max<LPT>(h[0] & ~kLow);  // of the experts after those
-
-  // Each pick has to be above the one after it, errors and replaced bits
-  // aside, and the last pick above all that is left. Experts of the same logit
-  // and bias tie exactly, and the ids have ordered those.
-  const bool pick = q < k, last = q == k - 1;
-  const float vj = value_of(key), vn = value_of(key_next);
-  const bool fine = pick && fabsf(vj) < INFINITY, more = fine && fabsf(vn) < INFINITY;
-  open |= pick && !fine;
-  const float lj = fine ? ld_logit(row + id) : 0.f, ln = more ? ld_logit(row + id_next) : 0.f;
-  if (!bias) {
-    open |= more && !(lj >= ln);
-    open |= last && key == left;
-  } else {
-    const float bj = fine ? bias[id] : 0.f, bn = more ? bias[id_next] : 0.f;
-    auto choice = [&](float lv, float bv) {
-      return (softmax ? exp_of(lv - m) * smax : inv_of(1.f + exp_of(-lv))) + bv;
-    };
-    auto err = [&](float cv, float lv, float bv) {
-      const float x = softmax ? m - lv : fabsf(lv);
-      return kU * (fabsf(cv - bv) * (3.f * x + kA) + 3.f * fabsf(cv));
-    };
-    const float cj = choice(lj, bj), cn = choice(ln, bn);
-    const float low = cj - err(cj, lj, bj);
-    open |= more && !(low > cn + err(cn, ln, bn)) && !(lj == ln && bj == bn);
-    // None left has a choice above `up`, so none a score above S, and none an
-    // error above E (s x <= S (1 + ln(smax / S)) for a score s <= S).
-    const float up = value_of(left | kLow);
-    const float S = fminf(smax, fmaxf(up + bmax, 1e-30f));
-    const float E = kU * (S * (3.f + 2.1f * __builtin_amdgcn_logf(smax / S) + kA) + 3.f * fabsf(up));
-    open |= last && up > -INFINITY && !(low > up + E);
+  if (bias && softmax) {
+    const double dv = v - __shfl(v, (here + 1) & 63, 64), ds = s - __shfl(s, (here + 1) & 63, 64);
+    open |= follows && !(dv > fabs(ds) * (double)(kA * kU) + 1e-15) && !(dv == 0.0 && ds == 0.0);
   }
+  // None left has a choice above `up`, so none a score above S, and none an
+  // error above E (s x <= S (1 + ln(smax / S)) for a score s <= S).
+  const float up = value_of(left | kLow);
+  double bound = up, low = v;
+  if (bias) {
+    const float S = fminf(smax, fmaxf(up + bmax, 1e-30f));
+    bound += kU * (S * (3.f + 2.1f * __builtin_amdgcn_logf(smax / S) + kA) + 3.f * fabsf(up));
+    if (softmax) low -= s * (double)(kA * kU);
+  }
+  open |= last && up > -INFINITY && !(low > bound);
   return id;
 }
 
