@@ -9,6 +9,7 @@ from test_codegen import _asm, _functions, _kernels, pytestmark  # noqa: F401
 
 @pytest.mark.parametrize("src,names", [
     ("grads.hip", ["grad_sq_kernel", "grad_scale_kernel"]),
+    ("route.hip", ["route_kernel", "route_bwd_kernel", "route_exact_kernel"]),
     ("router_bwd.hip", ["router_sparse_kernel", "router_dx_mfma_kernel", "router_dw_mfma_kernel",
                         "router_dx_f32_kernel", "router_dw_f32_kernel"]),
 ])
