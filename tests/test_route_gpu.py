@@ -157,6 +157,45 @@ def test_route_near_ties_are_decided_in_64_bits(score, N, k):
                                                         group_score="max"))
 
 
+@pytest.mark.parametrize("T,N,k", [(40, 64, 8), (1100, 64, 16), (40, 256, 8), (1100, 256, 8),
+                                   (1100, 255, 16), (1100, 500, 20), (1100, 510, 32),
+                                   (30, 66, 64)])
+@pytest.mark.parametrize("spec", SPECS, ids=lambda s: f"{s[0]}-{'renorm' if s[1] else 'plain'}")
+def test_route_close_logits_in_any_order(T, N, k, spec):
+    """Every logit has two others one and two steps of fp32 above it, at random
+    places: the scores of the three agree to fp32's last bits, or in fp32."""
+    rng = np.random.default_rng(T + N + k)
+    v = rng.normal(0, 1, (T, (N + 2) // 3)).astype(np.float32)
+    up = np.nextafter(v, np.float32(9))
+    l = np.concatenate([v, up, np.nextafter(up, np.float32(9))], axis=1)
+    l = rng.permuted(l, axis=1)[:, :N]
+    l_dev, l = rounded(l, "f32")
+    check_route(l_dev, l, k, spec)
+    check_route(l_dev, l, k, spec, np.full(N, 0.25, np.float32))
+    if N % 5 == 0 and k <= N // 5 * 2:
+        check_route(l_dev, l, k, spec, np.full(N, -0.5, np.float32),
+                    dict(n_groups=5, topk_groups=2))
+
+
+@pytest.mark.parametrize("T,N,k", [(20, 256, 12), (1100, 256, 8), (1100, 256, 16), (1100, 500, 20),
+                                   (20, 1000, 16), (20, 4000, 40)])
+@pytest.mark.parametrize("spec", SPECS, ids=lambda s: f"{s[0]}-{'renorm' if s[1] else 'plain'}")
+def test_route_picks_from_consecutive_experts(T, N, k, spec):
+    """Most picks, or all, from a run of consecutive experts, anywhere."""
+    rng = np.random.default_rng(T + N + k)
+    l = rng.normal(0, 1, (T, N))
+    for t in range(T):
+        n = int(rng.integers(4, 20))
+        at = int(rng.integers(0, N - n + 1))
+        l[t, at:at + n] += 4.0
+    l_dev, l = rounded(l, "f32")
+    check_route(l_dev, l, k, spec)
+    check_route(l_dev, l, k, spec, rng.uniform(0, 0.1, N).astype(np.float32))
+    if N % 4 == 0:
+        check_route(l_dev, l, k, spec, rng.uniform(0, 0.1, N).astype(np.float32),
+                    dict(n_groups=4, topk_groups=1))
+
+
 def test_route_exact_ties_of_equal_experts():
     """Equal logits with equal biases tie exactly: the lower id goes first."""
     rng = np.random.default_rng(4)
