@@ -23,6 +23,25 @@ hipError_t launch_kernel(F kernel, dim3 grid, dim3 block, uint32_t shmem, hipStr
   return hipGetLastError();
 }
 
+// Grids of many workgroups in one dimension: HIP takes fewer than 2^32 threads
+// per grid dimension, so the workgroups come in rows of 2^20 along another
+// one (y; z where y is in use) and take their number from both. Workgroups
+// past the last one exit.
+constexpr int kGridRowBits = 20;
+inline dim3 grid_rows(size_t blocks) {
+  const size_t row = (size_t)1 << kGridRowBits;
+  return blocks <= row ? dim3((unsigned)blocks)
+                       : dim3((unsigned)row, (unsigned)((blocks + row - 1) / row));
+}
+inline dim3 grid_rows_z(size_t blocks, unsigned y) {
+  const dim3 g = grid_rows(blocks);
+  return dim3(g.x, y, g.y);
+}
+__device__ __forceinline__ unsigned grid_block() { return blockIdx.y << kGridRowBits | blockIdx.x; }
+__device__ __forceinline__ unsigned grid_block_z() {
+  return blockIdx.z << kGridRowBits | blockIdx.x;
+}
+
 struct RouteTables {
   int32_t* offsets;  // [N+1]
   int32_t* perm;     // [M] sorted slot -> routed index

@@ -605,7 +605,7 @@ __global__ __launch_bounds__(256) void route_kernel(const T* logits, const float
   // (No loop over tokens: in one the compiler keeps the conditions on spec and
   // shape as masks, more than there are scalar registers; their spills made
   // the 32768 x 256 case 26.0 us instead of 23.4.)
-  const size_t t0 = ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * kTok;
+  const size_t t0 = (size_t)grid_block() * kTok;
   if (t0 >= (size_t)T_) return;
   const size_t tok = t0 + threadIdx.x / LPT;
   const bool live = tok < (size_t)T_;
@@ -657,7 +657,7 @@ __global__ __launch_bounds__(256) void route_exact_kernel(const T* logits, const
   constexpr int PER = 64;
   const int q = threadIdx.x & 63;
   const bool softmax = sp.score == BMOE_SCORE_SOFTMAX;
-  const size_t t = (size_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const size_t t = (size_t)grid_block() * 4 + (threadIdx.x >> 6);
   if (t >= (size_t)T_) return;  // whole wave
   const T* row = logits + t * N;
   float m = -INFINITY, total = 0.f;
@@ -726,7 +726,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const i
   static_assert(PER % 4 == 0, "whole quads");
   auto off = [](int i) { return i / QUAD * (QUAD * LPT) + i % QUAD; };
   const int q = threadIdx.x % LPT, base = q * QUAD;
-  const size_t tok = (size_t)blockIdx.x * (256 / LPT) + threadIdx.x / LPT;
+  const size_t tok = (size_t)grid_block() * (256 / LPT) + threadIdx.x / LPT;
   const bool live = tok < (size_t)T_;
   const T* row = logits + (live ? tok : 0) * N;
   const bool dense = sp.score == BMOE_SCORE_SOFTMAX && !sp.renorm;
@@ -828,7 +828,8 @@ template <int LPT>
 __global__ __launch_bounds__(256) void route_pairs_kernel(const float* logits, const int32_t* ids,
                                                           const float* dgates, int T_, int N,
                                                           int k, RouteSpec sp, int2* pairs) {
-  const size_t t0 = (size_t)blockIdx.x * (256 / LPT);
+  const size_t t0 = (size_t)grid_block() * (256 / LPT);
+  if (t0 >= (size_t)T_) return;
   const int nt = (int)min((size_t)(256 / LPT), (size_t)T_ - t0);
   make_pairs<LPT, 256>(logits, ids, dgates, t0, nt, N, k, sp, pairs);
 }
@@ -1006,6 +1007,12 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const int* part, int
   finish_loads(hist, N, rate, load, bias, &sum);
 }
 
+// Workgroups of 256 threads for T tokens of `lanes` lanes each.
+inline dim3 token_grid(int T, int lanes) {
+  const unsigned per = 256 / lanes;
+  return grid_rows(((unsigned)T + per - 1) / per);
+}
+
 // Lanes per token and experts per lane: 16 lanes (4 tokens per wave) up to 256
 // experts and 16 picks, 32 up to 512 and 32, else a whole wave per token.
 template <bool VEC, typename T>
@@ -1015,10 +1022,8 @@ hipError_t route_t(const T* logits, const float* bias, int Tn, int N, int k, con
   LaneMap map;
 #define BMOE_CALL(LPT, PER, WHEN)                                                               \
   if ((WHEN) && N <= LPT * PER && k <= LPT && (map = lane_map<LPT, PER>(N, sp.groups)).fits()) { \
-    const unsigned blocks = ((unsigned)Tn + 256 / LPT - 1) / (256 / LPT);                       \
-    const dim3 grid(blocks < 65536 ? blocks : 65536, (blocks + 65535) / 65536);                 \
-    return launch_kernel(route_kernel<LPT, PER, VEC, T>, grid, dim3(256), 0, s, KernelTiming{}, \
-                         logits, bias, Tn, N, k, sp, map, ids, gates);                          \
+    return launch_kernel(route_kernel<LPT, PER, VEC, T>, token_grid(Tn, LPT), dim3(256), 0, s,  \
+                         KernelTiming{}, logits, bias, Tn, N, k, sp, map, ids, gates);          \
   }
   BMOE_CALL(16, 4, true)
   BMOE_CALL(16, 16, !few)
@@ -1028,7 +1033,7 @@ hipError_t route_t(const T* logits, const float* bias, int Tn, int N, int k, con
   BMOE_CALL(64, 16, true)
   BMOE_CALL(64, 64, true)
 #undef BMOE_CALL
-  return launch_kernel(route_exact_kernel<T>, dim3(((unsigned)Tn + 3) / 4), dim3(256), 0, s,
+  return launch_kernel(route_exact_kernel<T>, token_grid(Tn, 64), dim3(256), 0, s,
                        KernelTiming{}, logits, bias, Tn, N, k, sp, ids, gates);
 }
 
@@ -1045,8 +1050,8 @@ hipError_t route_bwd_t(const T* logits, const int32_t* ids, const float* dgates,
                        hipStream_t s) {
 #define BMOE_CALL(LPT, PER)                                                                      \
   return launch_kernel(route_bwd_kernel<LPT, PER, VEC, PARTS, T>,                                \
-                       dim3(((unsigned)Tn + 256 / LPT - 1) / (256 / LPT)), dim3(256), 0, s,      \
-                       KernelTiming{}, logits, ids, dgates, Tn, N, k, sp, dlogits, parts)
+                       token_grid(Tn, LPT), dim3(256), 0, s, KernelTiming{}, logits, ids,        \
+                       dgates, Tn, N, k, sp, dlogits, parts)
   BMOE_BY_SHAPE(BMOE_CALL);
 #undef BMOE_CALL
 }
@@ -1106,8 +1111,8 @@ hipError_t launch_route_pairs(int T, int N, int k, const RouteSpec& sp, const fl
   do {                                                                                          \
     if (make) return BMOE_LISTS(LPT, 4, true);                                                  \
     const hipError_t e =                                                                        \
-        launch_kernel(route_pairs_kernel<LPT>, dim3(((unsigned)T + 256 / LPT - 1) / (256 / LPT)), \
-                      dim3(256), 0, s, KernelTiming{}, logits, ids, dgates, T, N, k, sp, rp.pairs); \
+        launch_kernel(route_pairs_kernel<LPT>, token_grid(T, LPT), dim3(256), 0, s,             \
+                      KernelTiming{}, logits, ids, dgates, T, N, k, sp, rp.pairs);              \
     if (e != hipSuccess) return e;                                                              \
     return N <= 512 ? BMOE_LISTS(2, 16, false) : BMOE_LISTS(2, 4, false);                       \
   } while (0)

@@ -44,8 +44,8 @@ struct SparseArgs {
   T* dx;
   float* dw;  // [groups of 4 ranges][N][d] (one group: the result itself)
   int T_, d, N, k, ranges;
-  int chunks;  // column chunks of a row
-  int n_dw;    // workgroups of the dW role
+  int chunks;     // column chunks of a row
+  unsigned n_dw;  // workgroups of the dW role
 };
 
 constexpr int kU = 8;  // rows of x in flight per lane
@@ -193,8 +193,9 @@ __device__ __forceinline__ void sparse_dx(const SparseArgs<T>& p, unsigned block
 template <typename T, bool WIDE>
 __global__ __launch_bounds__(256, 8) void router_sparse_kernel(SparseArgs<T> p) {
   __shared__ float sums[256 * (16 / sizeof(T))];
-  if (blockIdx.x < (unsigned)p.n_dw) sparse_dw<T, WIDE>(p, blockIdx.x, sums);
-  else sparse_dx<T, WIDE>(p, blockIdx.x - p.n_dw);
+  const unsigned block = grid_block();
+  if (block < p.n_dw) sparse_dw<T, WIDE>(p, block, sums);
+  else sparse_dx<T, WIDE>(p, block - p.n_dw);
 }
 
 // dw = the ranges' sums, added in order.
@@ -231,8 +232,8 @@ hipError_t sparse_t(int Tn, int d, int N, int k, const T* x, const T* w, const R
   p.N = N;
   p.k = k;
   p.chunks = (d + 64 * V - 1) / (64 * V);
-  p.n_dw = p.chunks * N * groups;
-  const dim3 grid(p.n_dw + (unsigned)(((size_t)Tn * (d / V) + 255) / 256));
+  p.n_dw = (unsigned)p.chunks * N * groups;
+  const dim3 grid = grid_rows(p.n_dw + ((size_t)Tn * (d / V) + 255) / 256);
   const hipError_t e = d >= 64 * V ? launch_kernel(router_sparse_kernel<T, true>, grid, dim3(256),
                                                    0, s, KernelTiming{}, p)
                                    : launch_kernel(router_sparse_kernel<T, false>, grid,
@@ -518,7 +519,8 @@ __global__ __launch_bounds__(256) void router_dx_f32_kernel(const float* dl, con
                                                             int N, float* dx) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int half = lane >> 5, col = lane & 31;
-  const size_t t0 = (size_t)blockIdx.x * 64 + wave / 2 * 32;
+  const size_t t0 = (size_t)grid_block_z() * 64 + wave / 2 * 32;
+  if (t0 >= (size_t)T_) return;  // (no barrier below)
   const int c0 = blockIdx.y * 128 + wave % 2 * 64;
   const float* row = dl + min(t0 + col, (size_t)T_ - 1) * N;
   const int ca = min(c0 + col, d - 1), cb = min(c0 + 32 + col, d - 1);
@@ -684,7 +686,7 @@ hipError_t launch_router_bwd_f32(int T, int d, int N, const float* x, const floa
                                  const float* dl, const float* dx_add, float* dx, float* dw,
                                  float* part, hipStream_t s) {
   hipError_t e = hipSuccess;
-  const dim3 gx(((unsigned)T + 63) / 64, (d + 127) / 128);
+  const dim3 gx = grid_rows_z(((unsigned)T + 63) / 64, (d + 127) / 128);
   if (T > 0)
     e = N % 4 == 0 ? launch_kernel(router_dx_f32_kernel<true>, gx, dim3(256), 0, s, KernelTiming{},
                                    dl, w, dx_add, T, d, N, dx)

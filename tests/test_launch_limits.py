@@ -1,0 +1,82 @@
+"""Calls with the largest token counts that the header takes are launched with
+grids that HIP takes (CPU only: launches are recorded, none is made). HIP
+refuses a grid dimension of 2^32 or more threads, and a call that fails there
+may have enqueued its first kernels already."""
+import shutil
+
+import pytest
+
+from butterfly_rotated_ternary_amd import bmoe
+from launches import record
+
+BF, F32 = bmoe.BMOE_BF16, bmoe.BMOE_F32
+A, LOTS = 1 << 40, 1 << 62  # an aligned address; more workspace than any call asks for
+TOP = 2 ** 31 - 1
+DENSE, SPARSE = dict(score="softmax", renorm=False), dict(score="sigmoid", renorm=True)
+
+pytestmark = pytest.mark.skipif(not shutil.which("g++"), reason="g++ not available")
+
+
+def logits(dt, T, d, N):
+    return "bmoe_router_logits", [dt, T, d, N, A, A, A, None]
+
+
+def router(dt, T, d, N, k):
+    return "bmoe_router", [dt, T, d, N, k, A, A, A, A, A, A, LOTS, None]
+
+
+def route(dt, T, N, k, spec):
+    return "bmoe_route", [dt, T, N, k, spec, A, None, A, A, None]
+
+
+def route_bwd(dt, T, N, k, spec):
+    return "bmoe_route_backward", [dt, T, N, k, spec, A, A, A, A, None]
+
+
+def router_bwd(dt, T, d, N, k, spec):
+    return "bmoe_router_backward", [dt, T, d, N, k, spec, A, 2 * A, 3 * A, 4 * A, 5 * A, 6 * A,
+                                    7 * A, 8 * A, 9 * A, LOTS, None]
+
+
+def groups(n, keep):
+    return dict(score="sigmoid", n_groups=n, topk_groups=keep)
+
+
+# (call, workgroups that the first launches need at least); tokens per
+# workgroup of the kernels: 16 where 16 lanes take one, 4 where a wave does
+CASES = [
+    (route(F32, TOP, 1, 1, SPARSE), [TOP // 16]),
+    (route(BF, (1 << 27) - 1, 17, 16, SPARSE), [1 << 23]),
+    (route(BF, (1 << 26) + 3, 33 * 66, 4, groups(33, 4)), [1 << 24]),
+    (route_bwd(F32, (1 << 28) - 1, 4, 1, SPARSE), [1 << 24]),
+    (route_bwd(F32, 1 << 28, 4, 1, SPARSE), [1 << 24]),
+    (route_bwd(F32, TOP, 1, 1, DENSE), [TOP // 16]),
+    (route_bwd(BF, 1 << 26, 17, 17, SPARSE), [1 << 24]),
+    (route_bwd(F32, TOP // 64, 300, 64, DENSE), [TOP // 256]),
+    # picks only: pairs, lists, then the products of both roles (16 bytes a thread), join
+    (router_bwd(F32, (1 << 26) + 1, 16, 17, 17, SPARSE), [1 << 24, 1 << 16, 1 << 20]),
+    (router_bwd(BF, 1 << 24, 2048, 8, 1, SPARSE), [1 << 14, 1 << 24]),
+    (router_bwd(BF, (1 << 24) - 5, 4096, 256, 2, SPARSE), [1 << 14, 1 << 25]),
+    (router_bwd(F32, 1 << 23, 2048, 8, 4, SPARSE), [1 << 17, 1 << 13, 1 << 24]),
+    # dense: dl, then dx in 64-token tiles
+    (router_bwd(F32, 1 << 30, 16, 1, 1, DENSE), [1 << 26, 1 << 24]),
+    (router_bwd(F32, TOP, 16, 1, 1, DENSE), [TOP // 16, TOP // 64]),
+    (router_bwd(BF, 1 << 28, 16, 4, 1, DENSE), [1 << 24, 1 << 22]),
+]
+
+
+@pytest.fixture(scope="module")
+def recorded(tmp_path_factory):
+    return record([c for c, _ in CASES], tmp_path_factory.mktemp("launches"))
+
+
+@pytest.mark.parametrize("i", range(len(CASES)), ids=lambda i: f"{CASES[i][0][0]}-{i}")
+def test_largest_calls_have_legal_grids(i, recorded):
+    (name, args), need = CASES[i]
+    status, ls = recorded[i]
+    assert status == 0 and len(ls) >= len(need)
+    for l in ls:
+        assert l.legal(), (name, args[:5], l)
+    for l, n in zip(ls, need):
+        # all of them there, and no more than the rows' last one left over
+        assert n <= l.workgroups, (name, args[:5], l, n)
