@@ -238,7 +238,8 @@ __global__ __launch_bounds__(64) void logits_mfma_narrow_kernel(const uint16_t* 
                                                                 int N, float* logits) {
   constexpr int NU = KC / 16;
   const int lane = threadIdx.x;
-  const int t0 = blockIdx.x * 32, e0 = blockIdx.y * 32;
+  if (grid_block_z() > (unsigned)(T - 1) / 32) return;
+  const int t0 = grid_block_z() * 32, e0 = blockIdx.y * 32;
   const int row = lane & 31, half = lane >> 5;
   const int t = min(t0 + row, T - 1), e = e0 + row;
   const bool ok = e < N;
@@ -265,7 +266,8 @@ __global__ __launch_bounds__(256) void logits_f32_kernel(const float* x, const f
   __shared__ float xs[32][65];
   __shared__ float ws_[32][65];
   const int tid = threadIdx.x;
-  const int t0 = blockIdx.x * 64, e0 = blockIdx.y * 64;
+  if (grid_block_z() > (unsigned)(T - 1) / 64) return;
+  const int t0 = grid_block_z() * 64, e0 = blockIdx.y * 64;
   const int ty = tid / 16, tx = tid % 16;
   float acc[4][4] = {};
   const int kc = d < 32 ? d : 32;
@@ -312,7 +314,8 @@ template <int PER>
 __global__ __launch_bounds__(256) void topk_kernel(const float* logits, int T, int N, int k,
                                                    int32_t* ids, float* gates) {
   const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (grid_block() > (unsigned)(T - 1) / 4) return;
+  const int t = grid_block() * 4 + (threadIdx.x >> 6);
   if (t >= T) return;  // whole wave
   const float* lt = logits + (size_t)t * N;
   float v[PER];
@@ -364,8 +367,8 @@ __global__ __launch_bounds__(256) void topk_kernel(const float* logits, int T, i
 template <int PER>
 hipError_t launch_topk_per(const float* logits, int T, int N, int k, int32_t* ids, float* gates,
                            hipStream_t s, const KernelTiming& tm) {
-  return launch_kernel(topk_kernel<PER>, dim3((T + 3) / 4), dim3(256), 0, s, tm, logits, T, N, k,
-                       ids, gates);
+  return launch_kernel(topk_kernel<PER>, grid_rows(((unsigned)T + 3) / 4), dim3(256), 0, s, tm,
+                       logits, T, N, k, ids, gates);
 }
 
 }  // namespace
@@ -373,14 +376,16 @@ hipError_t launch_topk_per(const float* logits, int T, int N, int k, int32_t* id
 hipError_t launch_router_logits(bmoe_dtype dt, int T, int d, int N, const void* x,
                                 const void* w, float* logits, hipStream_t s,
                                 const KernelTiming& tm) {
+  // token tiles of `rows`; T + rows may pass 31 bits
+  auto tiles = [&](unsigned rows) { return ((unsigned)T + rows - 1) / rows; };
   if (dt == BMOE_F32)
-    return launch_kernel(logits_f32_kernel, dim3((T + 63) / 64, (N + 63) / 64), dim3(256), 0, s, tm,
-                         static_cast<const float*>(x), static_cast<const float*>(w), T, d, N,
+    return launch_kernel(logits_f32_kernel, grid_rows_z(tiles(64), (N + 63) / 64), dim3(256), 0, s,
+                         tm, static_cast<const float*>(x), static_cast<const float*>(w), T, d, N,
                          logits);
   const uint16_t* xb = static_cast<const uint16_t*>(x);
   const uint16_t* wb = static_cast<const uint16_t*>(w);
   if (d < 64) {
-    const dim3 g2((T + 31) / 32, (N + 31) / 32);
+    const dim3 g2 = grid_rows_z(tiles(32), (N + 31) / 32);
     if (d == 32)
       return launch_kernel(logits_mfma_narrow_kernel<32>, g2, dim3(64), 0, s, tm, xb, wb, T, d, N,
                            logits);
@@ -391,8 +396,8 @@ hipError_t launch_router_logits(bmoe_dtype dt, int T, int d, int N, const void* 
   // flight measured fastest at d = 512 and one at d = 4096 (where the extra
   // registers cost occupancy). With N <= 64 the register kernel below is
   // faster at every measured size.
-  if (d >= 64 && N > 64 && (long long)((T + 127) / 128) * ((N + 127) / 128) >= 256) {
-    const dim3 gl((N + 127) / 128, (T + 127) / 128);
+  if (d >= 64 && N > 64 && (long long)tiles(128) * ((N + 127) / 128) >= 256) {
+    const dim3 gl((N + 127) / 128, tiles(128));
     if (d >= 2048)
       return launch_kernel(logits_lds_kernel<128, 128, 1>, gl, dim3(256), 0, s, tm, xb, wb, T, d,
                            N, logits);
@@ -403,8 +408,8 @@ hipError_t launch_router_logits(bmoe_dtype dt, int T, int d, int N, const void* 
   // when that already gives at least 512 workgroups, else a 4-way k split.
   const int G = N > 64 ? 4 : N > 32 ? 2 : 1;
   const int ny = (N + 32 * G - 1) / (32 * G);
-  const bool split = d >= 256 && (long long)((T + 127) / 128) * ny < 512;
-  const dim3 gr(split ? (T + 31) / 32 : (T + 127) / 128, ny);
+  const bool split = d >= 256 && (long long)tiles(128) * ny < 512;
+  const dim3 gr(split ? tiles(32) : tiles(128), ny);
 #define BMOE_LOGITS(GG, SS) \
   launch_kernel(logits_mfma_kernel<GG, SS>, gr, dim3(256), 0, s, tm, xb, wb, T, d, N, logits)
   if (G == 4) return split ? BMOE_LOGITS(4, true) : BMOE_LOGITS(4, false);

@@ -65,7 +65,6 @@ class Launch:
         """Within what HIP and the chip take: fewer than 2^32 threads per
         dimension, no empty dimension, at most 1024 threads and 160 KB."""
         return (all(g > 0 and b > 0 and g * b < 1 << 32 for g, b in zip(self.grid, self.block))
-                and self.grid[1] < 1 << 16 and self.grid[2] < 1 << 16
                 and self.block[0] * self.block[1] * self.block[2] <= 1024 and self.lds <= 160 << 10)
 
     def __repr__(self):

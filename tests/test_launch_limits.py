@@ -62,6 +62,12 @@ CASES = [
     (router_bwd(F32, 1 << 30, 16, 1, 1, DENSE), [1 << 26, 1 << 24]),
     (router_bwd(F32, TOP, 16, 1, 1, DENSE), [TOP // 16, TOP // 64]),
     (router_bwd(BF, 1 << 28, 16, 4, 1, DENSE), [1 << 24, 1 << 22]),
+    (logits(F32, 1 << 30, 16, 1), [1 << 24]),
+    (logits(F32, TOP, 16, 70), [2 * (TOP // 64)]),
+    (logits(BF, TOP, 16, 1), [TOP // 32]),
+    (logits(BF, TOP, 64, 65), [TOP // 128]),
+    (router(F32, 1 << 26, 16, 8, 2), [1 << 20, 1 << 24]),
+    (router(BF, TOP // 2, 64, 16, 2), [TOP // 256, TOP // 8]),
 ]
 
 

@@ -129,3 +129,26 @@ def test_route_of_groups_that_no_lane_layout_holds():
     oid, og = O.route_logits(l64, k, score="sigmoid", n_groups=33, topk_groups=5)
     assert np.array_equal(ids[rows].cpu().numpy(), oid)
     assert (np.abs(gates[rows].double().cpu().numpy() - og) <= eps_of(l64) * og).all()
+
+
+@pytest.mark.parametrize("dt,T", [(torch.float32, (1 << 26) + 70), (torch.bfloat16, (1 << 25) + 35)],
+                         ids=["f32", "bf16"])
+def test_plain_router(dt, T):
+    """Logits of more than 2^20 tiles of tokens, and as many workgroups of the
+    choice. A logit is a sum of 16 terms, its products in bf16 exact."""
+    d, N, k = 16, 3, 2
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(T, d, generator=g, device="cuda").to(dt)
+    w = torch.randn(N, d, generator=g, device="cuda").to(dt)
+    print(f"[router] T={T} d={d} N={N} {dt}", flush=True)
+    ids, gates, logits = bmoe.route(x, w, k, want_logits=True)
+    assert torch.equal(bmoe.router_logits(x, w), logits)
+    for r in parts(T):
+        ref = x[r].double() @ w.double().t().contiguous()
+        mag = x[r].double().abs() @ w.double().abs().t().contiguous()
+        l64 = logits[r].double()
+        assert ((l64 - ref).abs() <= 17 * U * mag).all()
+        want = torch.sort(l64, dim=1, descending=True, stable=True).indices[:, :k]
+        assert torch.equal(ids[r].long(), want)
+        wg = torch.softmax(l64.gather(1, want), 1)
+        assert ((gates[r].double() - wg).abs() <= eps(l64) * wg).all()
