@@ -689,10 +689,12 @@ __global__ __launch_bounds__(256) void route_exact_kernel(const T* logits, const
 //   renormalised:  dl_j = p_j (u_j - sum_i u_i p_i) [ (1 - s_j) ],  p = s / sum
 //   sigmoid:       dl_j = u_j s_j (1 - s_j)
 //   softmax:       dl_e = s_e (sum over j with id_j = e of u_j  -  sum_i u_i s_i)
-// An id outside [0, N) contributes nothing; equal ids add up in their order.
+// An id outside [0, N) contributes nothing; equal ids add up in their order. Nor
+// does a masked pick, whose gate is constant: what arrives as its gradient may
+// be NaN or infinite, so it becomes 0 before any product.
 
 // What pick (l, u) of its LPT lanes' token adds to its logit's gradient, for
-// the specs under which only the picks move. l = -inf: no pick, or masked.
+// the specs under which only the picks move. l = -inf: no pick, or masked (u 0).
 template <int LPT>
 __device__ __forceinline__ float pick_grad(float l, float u, const RouteSpec& sp) {
   const bool softmax = sp.score == BMOE_SCORE_SOFTMAX;
@@ -733,11 +735,12 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const i
   const int id = live && q < k ? ids[tok * k + q] : -1;
   const bool pick = id >= 0 && id < N;
   const float lj = pick ? ld_logit(row + id) : -INFINITY;
-  const float u = pick ? sp.scale * dgates[tok * k + q] : 0.f;
+  const float dg = pick ? dgates[tok * k + q] : 0.f;
+  const float u = lj == -INFINITY ? 0.f : sp.scale * dg;
   float a[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) a[i] = 0.f;
-  const float v = dense ? (lj == -INFINITY ? 0.f : u) : pick_grad<LPT>(lj, u, sp);
+  const float v = dense ? u : pick_grad<LPT>(lj, u, sp);
   const int sub = (threadIdx.x & 63) / LPT * LPT;
   for (int j = 0; j < k; ++j) {
     const int at = __shfl(id, sub + j, 64) - base;
@@ -818,7 +821,8 @@ __device__ __forceinline__ void make_pairs(const float* logits, const int32_t* i
     const int id = mine ? ids[tok * k + q] : -1;
     const bool pick = id >= 0 && id < N;
     const float l = pick ? logits[tok * N + id] : -INFINITY;
-    const float u = pick ? sp.scale * dgates[tok * k + q] : 0.f;
+    const float dg = pick ? dgates[tok * k + q] : 0.f;
+    const float u = l == -INFINITY ? 0.f : sp.scale * dg;
     const float v = pick_grad<LPT>(l, u, sp);
     if (mine) pairs[tok * k + q] = make_int2(pick ? id : 0, __float_as_int(pick ? v : 0.f));
   }

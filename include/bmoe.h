@@ -456,8 +456,8 @@ bmoe_status bmoe_route(bmoe_dtype dt, int T, int n_experts, int k, const bmoe_ro
  * [T][N], overwritten, from logits, ids and dgates fp32 [T][k]. Entries that
  * no gate depends on are 0: all but the k chosen ones, except for softmax
  * scores without renorm, where every score of the row moves every gate. An id
- * outside [0, N) contributes nothing (a padded pick); an id listed twice adds
- * up. T = 0 is a no-op.
+ * outside [0, N) contributes nothing (a padded pick), nor does a masked one,
+ * whatever its dgates; an id listed twice adds up. T = 0 is a no-op.
  */
 bmoe_status bmoe_route_backward(bmoe_dtype dt, int T, int n_experts, int k,
                                 const bmoe_route_spec* spec, const void* logits,

@@ -13,7 +13,8 @@ Readings (the pages describe a top-k mixture of experts without a router):
   ones; ties go to the lower group, then to the lower expert;
 * gates: scale * score, or scale * score / sum of the chosen scores (0 where
   all chosen are masked); a NaN logit, or +inf for the softmax, makes the
-  token's gates NaN.
+  token's gates NaN;
+* a pick outside the experts, or a masked one, has no gradient.
 """
 from __future__ import annotations
 
@@ -100,7 +101,8 @@ def route_logits_backward(logits, ids, dgates, *, score="softmax", renorm=True, 
     s = scores(l, score)
     out = np.zeros((T, N))
     for t in range(T):
-        js = [j for j in range(k) if 0 <= ids[t, j] < N]
+        # (a masked pick's gate is constant)
+        js = [j for j in range(k) if 0 <= ids[t, j] < N and l[t, ids[t, j]] != -np.inf]
         e = [int(ids[t, j]) for j in js]
         u = scale * np.asarray([dgates[t, j] for j in js], dtype=np.float64)
         sj = s[t, e]

@@ -217,3 +217,16 @@ def test_choice_matches_a_loop():
             kept = sorted(range(G), key=lambda g: (-val[g], g))[:keep]
             cand = [e for e in range(N) if e // (N // G) in kept]
             assert ids[t].tolist() == sorted(cand, key=lambda e: (-c[t, e], e))[:k]
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True),
+                                          ("sigmoid", False)])
+def test_gradient_at_a_masked_pick_counts_nothing(score, renorm, bad):
+    l = np.array([[0.5, -np.inf, 1.0, -1.0], [-np.inf, -np.inf, 2.0, 0.0]])
+    ids = np.array([[0, 1, 2], [0, 2, 1]], dtype=np.int32)
+    dg = np.array([[1.0, 0.0, -2.0], [0.0, 3.0, 0.0]])
+    want = O.route_logits_backward(l, ids, dg, score=score, renorm=renorm)
+    dg[0, 1] = dg[1, 0] = dg[1, 2] = bad
+    assert np.array_equal(O.route_logits_backward(l, ids, dg, score=score, renorm=renorm), want)
+    assert np.isfinite(want).all()
