@@ -704,7 +704,7 @@ __device__ __forceinline__ float pick_grad(float l, float u, const RouteSpec& sp
     const float shift = softmax ? mc : fminf(mc, 0.f);
     const float w = l == -INFINITY ? 0.f : softmax ? exp_of(l - shift) : sigmoid_shifted(l, shift);
     const float sum = sub_sum<LPT>(w);
-    const float p = sum > 0.f ? w / sum : 0.f;
+    const float p = sum == 0.f ? 0.f : w / sum;  // (a NaN stays one)
     v = p * (u - sub_sum<LPT>(u * p));
     if (!softmax) v *= inv_of(1.f + exp_of(l));
   } else {
@@ -766,10 +766,12 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const i
       l[i] = l[i] == -INFINITY ? 0.f : exp_of(l[i] - m);
       total += l[i];
     }
-    const float inv = 1.f / sub_sum<LPT>(total);
+    total = sub_sum<LPT>(total);
+    const float inv = 1.f / total;
+    const float none = total != total ? total : 0.f;  // a NaN or +inf logit: NaN, not 0
     const float d = sub_sum<LPT>(lj == -INFINITY ? 0.f : u * (exp_of(lj - m) * inv));
 #pragma unroll
-    for (int i = 0; i < PER; ++i) a[i] = l[i] == 0.f ? 0.f : l[i] * inv * (a[i] - d);
+    for (int i = 0; i < PER; ++i) a[i] = l[i] == 0.f ? none : l[i] * inv * (a[i] - d);
   }
   if (!live) return;
   if constexpr (PARTS) {

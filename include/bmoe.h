@@ -457,7 +457,10 @@ bmoe_status bmoe_route(bmoe_dtype dt, int T, int n_experts, int k, const bmoe_ro
  * no gate depends on are 0: all but the k chosen ones, except for softmax
  * scores without renorm, where every score of the row moves every gate. An id
  * outside [0, N) contributes nothing (a padded pick), nor does a masked one,
- * whatever its dgates; an id listed twice adds up. T = 0 is a no-op.
+ * whatever its dgates; an id listed twice adds up. Where a NaN logit (for the
+ * softmax also a +inf one) makes gates NaN, so is their gradient, as far as it
+ * reads that logit: with renorm the token's picks if it is one of them, for the
+ * full softmax the row, for plain sigmoids that pick. T = 0 is a no-op.
  */
 bmoe_status bmoe_route_backward(bmoe_dtype dt, int T, int n_experts, int k,
                                 const bmoe_route_spec* spec, const void* logits,

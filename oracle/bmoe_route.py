@@ -108,7 +108,7 @@ def route_logits_backward(logits, ids, dgates, *, score="softmax", renorm=True, 
         sj = s[t, e]
         if renorm:
             tot = sj.sum()
-            if not tot > 0:
+            if tot == 0:
                 continue
             # d g_j / d s_i = (delta_ij - p_j) / tot
             ds = (u - (u * sj).sum() / tot) / tot

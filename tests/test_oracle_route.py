@@ -230,3 +230,13 @@ def test_gradient_at_a_masked_pick_counts_nothing(score, renorm, bad):
     dg[0, 1] = dg[1, 0] = dg[1, 2] = bad
     assert np.array_equal(O.route_logits_backward(l, ids, dg, score=score, renorm=renorm), want)
     assert np.isfinite(want).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gradient_through_a_nan_pick_is_nan(score):
+    """Renormalised gates of a token with a NaN among its picks are NaN, and so
+    is their gradient."""
+    l = np.array([[0.5, np.nan, 1.0, -1.0], [0.5, 0.0, 1.0, -1.0]])
+    ids = np.array([[0, 1], [0, 1]], dtype=np.int32)
+    g = O.route_logits_backward(l, ids, np.ones((2, 2)), score=score, renorm=True)
+    assert np.isnan(g[0, :2]).all() and np.isfinite(g[1]).all()

@@ -60,3 +60,38 @@ def test_gradient_of_a_masked_pick_does_not_spread(spec, bad):
             dg[t, j] = bad
     ref = check(l, ids, dg, spec)
     assert np.isfinite(ref).all() and (ref[4::5] == 0).all() and (ref[1::5] != 0).any()
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("spec", SPECS, ids=str)
+def test_gradient_through_a_pick_that_is_not_a_number(spec, bad):
+    """A NaN among a token's picked logits (softmax: or an infinity) makes its
+    gates NaN, and their gradient too, not 0: the picks' where they are
+    renormalised, the row's for the full softmax, the pick's alone for plain
+    sigmoids. Other rows keep theirs. A sigmoid of +inf is 1, its slope 0."""
+    rng = np.random.default_rng(2)
+    T, N, k = 30, 16, 3
+    l = rng.normal(0, 1, (T, N))
+    ids = np.argsort(rng.random((T, N)), axis=1)[:, :k].astype(np.int32)
+    dg = rng.normal(0, 1, (T, k)).astype(np.float32)
+    l[np.arange(0, T, 3), ids[::3, 1]] = bad
+    l_dev, _ = rounded(l, "f32")
+    is_nan = np.zeros((T, N), dtype=bool)
+    if spec[0] == "softmax" or math.isnan(bad):
+        if not spec[1]:
+            if spec[0] == "softmax":
+                is_nan[::3] = True
+            else:
+                is_nan[np.arange(0, T, 3), ids[::3, 1]] = True
+        else:
+            np.put_along_axis(is_nan[::3], ids[::3].astype(np.int64), True, axis=1)
+    got, *dx = gradient(l_dev, ids, dg, spec)
+    assert (np.isnan(got) == is_nan).all()
+    for v in dx:
+        assert (np.isnan(v).all(axis=1) == is_nan.any(axis=1)).all()
+    with np.errstate(all="ignore"):
+        ref = O.route_logits_backward(l, ids, dg, score=spec[0], renorm=spec[1], scale=1.5)
+    rows = np.arange(T) % 3 != 0
+    tol = 4 * eps_of(l[rows]) * grad_scale(l[rows], ids[rows], dg[rows], *spec, 1.5) + 2.0 ** -126
+    assert (np.abs(got - ref)[rows] <= tol).all()
+    assert (np.isnan(ref) == is_nan).all()
