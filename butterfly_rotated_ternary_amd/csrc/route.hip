@@ -772,6 +772,12 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const T* logits, const i
     const float d = sub_sum<LPT>(lj == -INFINITY ? 0.f : u * (exp_of(lj - m) * inv));
 #pragma unroll
     for (int i = 0; i < PER; ++i) a[i] = l[i] == 0.f ? none : l[i] * inv * (a[i] - d);
+    // a row without a pick is 0 whatever it holds (a branch, rarely taken: in the
+    // line above the condition cost 0.5 of 11.5 us)
+    if (own_bits<LPT>(__ballot(lj != -INFINITY)) == 0) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) a[i] = 0.f;
+    }
   }
   if (!live) return;
   if constexpr (PARTS) {

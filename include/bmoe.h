@@ -457,10 +457,11 @@ bmoe_status bmoe_route(bmoe_dtype dt, int T, int n_experts, int k, const bmoe_ro
  * no gate depends on are 0: all but the k chosen ones, except for softmax
  * scores without renorm, where every score of the row moves every gate. An id
  * outside [0, N) contributes nothing (a padded pick), nor does a masked one,
- * whatever its dgates; an id listed twice adds up. Where a NaN logit (for the
- * softmax also a +inf one) makes gates NaN, so is their gradient, as far as it
- * reads that logit: with renorm the token's picks if it is one of them, for the
- * full softmax the row, for plain sigmoids that pick. T = 0 is a no-op.
+ * whatever its dgates; an id listed twice adds up. A token without other picks
+ * has gradient 0, whatever its logits and dgates. Else, where a NaN logit (for
+ * the softmax also a +inf one) makes gates NaN, so is their gradient, as far as
+ * it reads that logit: with renorm the token's picks if it is one of them, for
+ * the full softmax the row, for plain sigmoids that pick. T = 0 is a no-op.
  */
 bmoe_status bmoe_route_backward(bmoe_dtype dt, int T, int n_experts, int k,
                                 const bmoe_route_spec* spec, const void* logits,
@@ -496,8 +497,9 @@ bmoe_status bmoe_route_balance(int T, int n_experts, int k, const int32_t* ids, 
  *           refused (BMOE_E_VALUE).
  *   dw      fp32 [N][d]: sum over t of dl_te x_t, the same bits each run.
  * dl is bmoe_route_backward's dlogits. Ids outside [0, N) contribute nothing:
- * a padded token's x may hold anything, except for softmax scores without
- * renorm, whose products take every row (its dl is 0, so x has to be finite).
+ * a padded token's logits and dgates may hold anything, and so may its x,
+ * except for softmax scores without renorm, whose products take every row (its
+ * dl is 0, so x has to be finite).
  * d a power of two in [16, 8192]; T = 0 leaves dx and sets dw to 0. ws: at
  * least bmoe_router_backward_workspace_bytes().
  */

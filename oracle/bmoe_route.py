@@ -103,6 +103,8 @@ def route_logits_backward(logits, ids, dgates, *, score="softmax", renorm=True, 
     for t in range(T):
         # (a masked pick's gate is constant)
         js = [j for j in range(k) if 0 <= ids[t, j] < N and l[t, ids[t, j]] != -np.inf]
+        if not js:
+            continue
         e = [int(ids[t, j]) for j in js]
         u = scale * np.asarray([dgates[t, j] for j in js], dtype=np.float64)
         sj = s[t, e]

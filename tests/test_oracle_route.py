@@ -240,3 +240,12 @@ def test_gradient_through_a_nan_pick_is_nan(score):
     ids = np.array([[0, 1], [0, 1]], dtype=np.int32)
     g = O.route_logits_backward(l, ids, np.ones((2, 2)), score=score, renorm=True)
     assert np.isnan(g[0, :2]).all() and np.isfinite(g[1]).all()
+
+
+def test_gradient_of_a_row_without_picks_is_zero_whatever_its_logits():
+    l = np.array([[np.nan, 1.0, 2.0], [np.inf, 0.0, 1.0], [np.nan, -np.inf, 0.0], [0.0, 1.0, 2.0]])
+    ids = np.array([[-1, 3], [-1, -1], [1, -1], [0, 1]], dtype=np.int32)
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            g = O.route_logits_backward(l, ids, np.ones((4, 2)), score=score, renorm=renorm)
+            assert (g[:3] == 0).all() and np.isfinite(g[3]).all()

@@ -95,3 +95,25 @@ def test_gradient_through_a_pick_that_is_not_a_number(spec, bad):
     tol = 4 * eps_of(l[rows]) * grad_scale(l[rows], ids[rows], dg[rows], *spec, 1.5) + 2.0 ** -126
     assert (np.abs(got - ref)[rows] <= tol).all()
     assert (np.isnan(ref) == is_nan).all()
+
+
+@pytest.mark.parametrize("N", [16, 64, 512, 2048])
+@pytest.mark.parametrize("spec", SPECS, ids=str)
+def test_gradient_of_padded_rows_whatever_they_hold(spec, N):
+    """Rows all of whose picks are padded (or masked) have no gradient, also
+    where their logits and dgates are NaN or infinite, and change no other's."""
+    rng = np.random.default_rng(N)
+    T, k = 60, 4
+    l = rng.normal(0, 1, (T, N))
+    ids = np.argsort(rng.random((T, N)), axis=1)[:, :k].astype(np.int32)
+    dg = rng.normal(0, 1, (T, k)).astype(np.float32)
+    pad = np.arange(T) % 3 == 1
+    ids[pad] = [-1, N, -7, 2 ** 31 - 1]
+    clean = gradient(rounded(l, "f32")[0], ids, dg, spec)
+    l[pad] = rng.choice([math.nan, math.inf, -math.inf, 0.0], (pad.sum(), N))
+    dg[pad] = rng.choice([math.nan, math.inf, 1.0], (pad.sum(), k))
+    l[4, :4] = -math.inf
+    ids[4] = [0, 2, -1, 3]     # masked ones count as none
+    got = gradient(rounded(l, "f32")[0], ids, dg, spec)
+    for a, b in zip(got, clean):
+        assert (a[pad] == 0).all() and (a[~pad] == b[~pad]).all()
