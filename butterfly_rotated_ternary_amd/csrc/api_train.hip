@@ -47,7 +47,7 @@ size_t elem(bmoe_dtype dt) { return dt == BMOE_BF16 ? 2 : 4; }
 
 bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + b_bytes && y < x + a_bytes;
+  return a && b && a_bytes && b_bytes && x < y + b_bytes && y < x + a_bytes;
 }
 
 struct PairsLayout {
@@ -276,10 +276,26 @@ bmoe_status bmoe_router_backward(bmoe_dtype dt, int T, int d, int n_experts, int
   const void* ptrs[] = {x, w_router, logits, ids, dgates, dx_add, dx, dw, ws};
   for (const void* p : ptrs)
     if (!ok16(p)) return BMOE_E_ALIGN;
-  // dx is written while x is read; dx_add is read entry by entry before dx is
-  const size_t x_bytes = (size_t)T * d * elem(dt);
-  if (overlap(dx, x_bytes, x, x_bytes) || (dx_add != dx && overlap(dx, x_bytes, dx_add, x_bytes)))
-    return BMOE_E_VALUE;
+  // what is written while others are read shares no byte with them; dx_add is
+  // read entry by entry before dx is written
+  struct Span {
+    const void* p;
+    size_t bytes;
+  };
+  const size_t x_bytes = (size_t)T * d * elem(dt), w_entries = (size_t)n_experts * d;
+  const Span written[] = {{dx, x_bytes}, {dw, w_entries * sizeof(float)}, {ws, need}};
+  const Span read[] = {{x, x_bytes},
+                       {w_router, w_entries * elem(dt)},
+                       {logits, (size_t)T * n_experts * sizeof(float)},
+                       {ids, (size_t)T * k * sizeof(int32_t)},
+                       {dgates, (size_t)T * k * sizeof(float)},
+                       {dx_add == dx ? nullptr : dx_add, x_bytes}};
+  for (const Span& a : written) {
+    for (const Span& b : read)
+      if (overlap(a.p, a.bytes, b.p, b.bytes)) return BMOE_E_VALUE;
+    for (const Span& b : written)
+      if (&a != &b && overlap(a.p, a.bytes, b.p, b.bytes)) return BMOE_E_VALUE;
+  }
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (T > 0 && !(sp.score == BMOE_SCORE_SOFTMAX && !sp.renorm)) {
     const PairsLayout l = router_pairs_layout(T, d, n_experts, k);

@@ -493,9 +493,10 @@ bmoe_status bmoe_route_balance(int T, int n_experts, int k, const int32_t* ids, 
  *   dx_add  [T][d] or NULL: added to the gradient (bmoe_backward's dx, so that
  *           dx holds both); may be dx itself.
  *   dx      [T][d], dtype dt: dx_add + sum_e dl_te W_r[e], summed in fp32 and
- *           rounded once. Sharing memory with x, or with part of dx_add, is
- *           refused (BMOE_E_VALUE).
+ *           rounded once.
  *   dw      fp32 [N][d]: sum over t of dl_te x_t, the same bits each run.
+ * dx, dw and ws share no memory with each other or with what is read, dx_add
+ * aside where it is all of dx (BMOE_E_VALUE).
  * dl is bmoe_route_backward's dlogits. Ids outside [0, N) contribute nothing:
  * a padded token's logits and dgates may hold anything, and so may its x,
  * except for softmax scores without renorm, whose products take every row (its

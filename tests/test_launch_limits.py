@@ -86,3 +86,46 @@ def test_largest_calls_have_legal_grids(i, recorded):
     for l, n in zip(ls, need):
         # all of them there, and no more than the rows' last one left over
         assert n <= l.workgroups, (name, args[:5], l, n)
+
+
+def spans(T, d, N, k, e, ws):
+    """Bytes of the router backward's tensors, in the order of its pointers."""
+    return dict(x=T * d * e, w=N * d * e, logits=4 * T * N, ids=4 * T * k, dgates=4 * T * k,
+                dx_add=T * d * e, dx=T * d * e, dw=4 * N * d, ws=ws)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_router_backward_refuses_shared_memory(dt, tmp_path):
+    """What is written (dx, dw, the workspace) shares no byte with another
+    tensor; the exception is dx_add, which dx may be. Nothing is launched."""
+    T, d, N, k = 40, 64, 8, 2
+    size = spans(T, d, N, k, 2 if dt == BF else 4,
+                 bmoe.bmoe_router_backward_workspace_bytes(dt, T, d, N, k))
+    names = list(size)
+    far = {n: A + (i << 30) for i, n in enumerate(names)}
+    calls, want = [], []
+
+    def add(status, **moved):
+        p = {**far, **moved}
+        calls.append(("bmoe_router_backward", [dt, T, d, N, k, SPARSE, *(p[n] for n in names),
+                                               size["ws"], None]))
+        want.append(status)
+
+    add(0)
+    add(0, dx_add=far["dx"])
+    add(0, dx_add=None)
+    add(0, w=far["x"])                                   # both only read
+    for a in ("dx", "dw", "ws"):
+        for b in names:
+            if a == b:
+                continue
+            first = far[b] + size[b] // 16 * 16 - 16     # b's last 16 bytes
+            add(9, **{a: first})
+            add(9, **{a: far[b] - size[a] // 16 * 16 + 16})
+            add(0, **{a: far[b] + (size[b] + 15) // 16 * 16})
+            add(0, **{a: far[b] - (size[a] + 15) // 16 * 16})
+            if (a, b) != ("dx", "dx_add"):
+                add(9, **{a: far[b]})
+    got = record(calls, tmp_path)
+    assert [s for s, _ in got] == want
+    assert all(len(l) >= 2 if s == 0 else not l for (s, l) in got)
