@@ -8,6 +8,7 @@ import pytest
 
 from butterfly_rotated_ternary_amd import bmoe
 from launches import record
+from range_cases import CASES as RANGES
 
 BF, F32 = bmoe.BMOE_BF16, bmoe.BMOE_F32
 A, LOTS = 1 << 40, 1 << 62  # an aligned address; more workspace than any call asks for
@@ -129,3 +130,15 @@ def test_router_backward_refuses_shared_memory(dt, tmp_path):
     got = record(calls, tmp_path)
     assert [s for s, _ in got] == want
     assert all(len(l) >= 2 if s == 0 else not l for (s, l) in got)
+
+
+def test_long_ranges_take_the_paths_that_their_cases_name(tmp_path):
+    """The shapes whose results the GPU tests compare run the launches meant."""
+    got = record([router_bwd(dt, *c[:4], SPARSE) for c in RANGES for dt in (BF, F32)], tmp_path)
+    for i, (status, ls) in enumerate(got):
+        T, d, N, k, threads, ranges, pairs = RANGES[i // 2]
+        groups_ = (ranges + 3) // 4
+        assert status == 0
+        assert len(ls) == pairs + 2 + (groups_ > 1), (RANGES[i // 2], ls)
+        lists = ls[pairs]
+        assert (lists.workgroups, lists.block[0]) == (ranges, threads), (RANGES[i // 2], ls)
