@@ -151,9 +151,13 @@ bmoe_status each_table(int n, const bmoe_tensor* grads, const bmoe_tensor* out, 
 // Partial sums of the whole list to part; their number to *used.
 bmoe_status grad_sq_impl(int n, const bmoe_tensor* grads, double* part, int* used, hipStream_t s) {
   *used = 0;
+  size_t chunks = 0;  // of the whole list: the scaling comes after all of its tables
+  for (int i = 0; i < n; ++i)
+    if (grads[i].count)
+      chunks += grad_chunks(grads[i].data, grads[i].count, grads[i].dtype == BMOE_BF16);
   return each_table(n, grads, nullptr, [&](const GradTable& t) {
     int np = 0;
-    const hipError_t e = launch_grad_sq(t, part + *used, &np, s);
+    const hipError_t e = launch_grad_sq(t, chunks, part + *used, &np, s);
     *used += np;
     return e;
   });

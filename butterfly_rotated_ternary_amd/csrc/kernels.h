@@ -307,7 +307,9 @@ struct GradTable {
 // Chunks (256 vectors of 16 bytes) of a tensor.
 uint32_t grad_chunks(const void* src, size_t count, int bf16);
 // Sums of squares of the table's tensors: *n_part partial sums to part.
-hipError_t launch_grad_sq(const GradTable& tab, double* part, int* n_part, hipStream_t s);
+// list_chunks: those of all tables of the list.
+hipError_t launch_grad_sq(const GradTable& tab, size_t list_chunks, double* part, int* n_part,
+                          hipStream_t s);
 // norm = sqrt(sum of part[0 .. n_part)), added in order.
 hipError_t launch_grad_norm(const double* part, int n_part, float* norm, hipStream_t s);
 // dst = src * (max_norm / norm where max_norm < norm < infinity, else 1).

@@ -16,21 +16,23 @@ STUB = r"""
 #include <vector>
 struct dim3 { unsigned x, y, z; };
 static std::vector<unsigned long long> seen;
-static int note(dim3 g, dim3 b, size_t lds) {
+static int note(const void* f, dim3 g, dim3 b, size_t lds) {
   for (unsigned long long v : {(unsigned long long)g.x, (unsigned long long)g.y,
                                (unsigned long long)g.z, (unsigned long long)b.x,
                                (unsigned long long)b.y, (unsigned long long)b.z,
-                               (unsigned long long)lds})
+                               (unsigned long long)lds, (unsigned long long)f})
     seen.push_back(v);
   return 0;
 }
 extern "C" {
-int hipExtLaunchKernel(const void*, dim3 g, dim3 b, void**, size_t lds, void*, void*, void*, int) {
-  return note(g, b, lds);
+int hipExtLaunchKernel(const void* f, dim3 g, dim3 b, void**, size_t lds, void*, void*, void*, int) {
+  return note(f, g, b, lds);
 }
-int hipLaunchKernel(const void*, dim3 g, dim3 b, void**, size_t lds, void*) { return note(g, b, lds); }
+int hipLaunchKernel(const void* f, dim3 g, dim3 b, void**, size_t lds, void*) {
+  return note(f, g, b, lds);
+}
 int hipGetLastError() { return 0; }
-size_t seen_count() { return seen.size() / 7; }
+size_t seen_count() { return seen.size() / 8; }
 const unsigned long long* seen_data() { return seen.data(); }
 void seen_clear() { seen.clear(); }
 }
@@ -44,11 +46,12 @@ stub.seen_data.restype = ctypes.POINTER(ctypes.c_ulonglong)
 from butterfly_rotated_ternary_amd import bmoe
 out = []
 for name, args in json.load(sys.stdin):
-    args = [ctypes.byref(bmoe.RouteSpec(**a)) if isinstance(a, dict) else a for a in args]
+    args = [ctypes.byref(bmoe.RouteSpec(**a)) if isinstance(a, dict) else
+            (bmoe.BmoeTensor * len(a))(*map(tuple, a)) if isinstance(a, list) else a for a in args]
     stub.seen_clear()
     status = getattr(bmoe.lib(), name)(*args)
     d = stub.seen_data()
-    out.append([status, [[d[7 * i + j] for j in range(7)] for i in range(stub.seen_count())]])
+    out.append([status, [[d[8 * i + j] for j in range(8)] for i in range(stub.seen_count())]])
 print(json.dumps(out))
 """
 
@@ -56,6 +59,7 @@ print(json.dumps(out))
 class Launch:
     def __init__(self, v):
         self.grid, self.block, self.lds = tuple(v[:3]), tuple(v[3:6]), v[6]
+        self.kernel = v[7]  # equal for launches of one kernel within a recording
 
     @property
     def workgroups(self):
@@ -73,7 +77,8 @@ class Launch:
 
 def record(calls, tmp_path):
     """[(status, [Launch])] of calls [(entry point, [arguments])]; a dict among
-    the arguments is a RouteSpec's."""
+    the arguments is a RouteSpec's, a list one of bmoe_tensor (address, entries,
+    type)."""
     src, lib = os.path.join(tmp_path, "stub.cpp"), os.path.join(tmp_path, "stub.so")
     with open(src, "w") as f:
         f.write(STUB)

@@ -142,3 +142,20 @@ def test_long_ranges_take_the_paths_that_their_cases_name(tmp_path):
         assert len(ls) == pairs + 2 + (groups_ > 1), (RANGES[i // 2], ls)
         lists = ls[pairs]
         assert (lists.workgroups, lists.block[0]) == (ranges, threads), (RANGES[i // 2], ls)
+
+
+def test_norm_streams_by_the_bytes_of_the_whole_list(tmp_path):
+    """A list above 256 MB does not fit the last-level cache until the scaling
+    reads it, however many tables of 112 tensors it takes."""
+    def norm(counts):
+        tensors = [[A + (i << 32), n, F32] for i, n in enumerate(counts)]
+        return "bmoe_grad_norm", [len(tensors), tensors, A, A, LOTS, None]
+
+    one_big, one_small = [70 << 20], [60 << 20] + [4] * 20
+    got = record([norm(one_big), norm(one_small), norm([1 << 20] * 300), norm([1 << 17] * 300),
+                  norm([100] * 112 + [70 << 20]), norm([100] * 9)], tmp_path)
+    assert all(s == 0 for s, _ in got)
+    big, small, many_big, many_small, mixed, few = ([l.kernel for l in ls[:-1]] for _, ls in got)
+    assert len(big) == 1 and len(small) == 1 and big != small and few == small
+    assert many_big == big * 3 and mixed == big * 2
+    assert set(many_small) == set(small)
