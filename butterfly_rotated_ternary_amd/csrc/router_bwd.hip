@@ -25,7 +25,9 @@ namespace {
 //     through LDS, those of the groups of ranges by the join kernel, so the
 //     order of every sum is fixed. The workgroups of a group of ranges run
 //     together and walk the tokens upwards, so the k readers of a row of x
-//     meet in L2 (column chunk c goes to XCD c % 8).
+//     meet in the caches: in one L2 where a row has eight column chunks or
+//     more (workgroups go to the eight XCDs in turn, so chunk c to XCD c % 8),
+//     else in two to eight of them and the last-level cache.
 // One launch, the dW workgroups first. Measured at T = 32768, d = 4096, 256
 // experts, top 4 (bf16): dW 96 us and dx 117 us in launches of their own (dx
 // moves 537 MB: 100 us at the rate of a large copy; dW gathers 1.07 GB of x
@@ -44,7 +46,7 @@ struct SparseArgs {
   T* dx;
   float* dw;  // [groups of 4 ranges][N][d] (one group: the result itself)
   int T_, d, N, k, ranges;
-  int chunks;     // column chunks of a row
+  int chunks;     // column chunks of a row (a power of two, as d)
   unsigned n_dw;  // workgroups of the dW role
 };
 
@@ -53,8 +55,7 @@ constexpr int kU = 8;  // rows of x in flight per lane
 template <typename T, bool WIDE>
 __device__ __forceinline__ void sparse_dw(const SparseArgs<T>& p, unsigned block, float* sums) {
   constexpr int V = 16 / sizeof(T);
-  // (blockIdx.x % 8 is the XCD; eight consecutive `block` have all eight)
-  const int chunk = p.chunks == 8 ? blockIdx.x % 8 : block % p.chunks, re = block / p.chunks;
+  const int chunk = block & (p.chunks - 1), re = block >> __builtin_ctz(p.chunks);
   const int e = re % p.N, group = re / p.N;
   const int lpr = WIDE ? 64 : p.d / V;  // lanes per row
   const int slots = 64 / lpr;           // rows that a wave takes at once
