@@ -32,8 +32,8 @@ namespace {
 // experts, top 4 (bf16): dW 96 us and dx 117 us in launches of their own (dx
 // moves 537 MB: 100 us at the rate of a large copy; dW gathers 1.07 GB of x
 // through L2), the call 223 us so (235 us at six waves per SIMD instead of
-// eight) and 237 us with two launches; the headline
-// batch 17.8 and 19.8 us. Alternating the roles' workgroups costs dW its hits
+// eight) and 237 us with two launches; T = 4096, d = 512, 64 experts, top 2
+// 16.8 to 17.8 and 19.8 us. Alternating the roles' workgroups costs dW its hits
 // in L2 (245 us with every third, 257 us with every fifth a dW one).
 template <typename T>
 struct SparseArgs {
@@ -283,8 +283,9 @@ __device__ __forceinline__ bf16x8 tr_read(const char* p) {
 // 64 experts at a time; the parts come straight from memory, stored in operand
 // order (by token and expert the call took 73 us, 11 more), dx_add is under way
 // from the start. The tile leaves through LDS (the W tile's, done with by
-// then), so dx_add and dx move in 128-byte pieces of a row. Small tiles, so that four workgroups share a CU
-// and one's loads run under another's MFMAs: at T = 16384, d = 2048, 64
+// then), so dx_add and dx move in 128-byte pieces of a row. Small tiles, so that
+// several workgroups share a CU and one's loads run under another's MFMAs:
+// three with dx_add (132 registers), four without. At T = 16384, d = 2048, 64
 // experts 128 x 128 tiles at two per CU took 56 us, these 31 us (134 MB).
 constexpr int kDxStrideW = 128 * 2 + 64;
 
@@ -507,8 +508,9 @@ __global__ __launch_bounds__(512) void router_dw_mfma_kernel(const uint16_t* par
 // ---- dense dl, fp32: fp32 MFMA ------------------------------------------------------
 // v_mfma_f32_32x32x2_f32: lane l gives element (l % 32, l / 32) of A and (l / 32,
 // l % 32) of B, straight from memory. Exact fp32 products at 1/16 of the bf16
-// rate; the split of both operands into bf16 parts (six products) would be
-// faster and is left out, fp32 layers being small here.
+// rate: 226 to 231 us at T = 16384, d = 2048, 64 experts, three times what its
+// bytes take. The split of both operands into bf16 parts (six products) would
+// be faster and is left out, fp32 layers being small here.
 //
 // dx: 64 tokens x 128 columns per workgroup, 4 waves of 32 x 64. Eight experts
 // per step: half h of the wave takes experts 4 h .. 4 h + 3 of them (any order

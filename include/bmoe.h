@@ -422,8 +422,9 @@ bmoe_status bmoe_router_logits(bmoe_dtype dt, int T, int d, int n_experts, const
  *   ids      the k experts of the kept groups with the largest c, in
  *            descending order, the lower id on ties
  *   gates    scale * s_id, or with renorm scale * s_id / (sum of the k s)
- * The choice and its order are those of the scores and sums taken in 64 bits;
- * without a bias they are those of the logits (the scores rise with them).
+ * The choice and its order are those of the scores and sums taken in 64 bits
+ * (values closer than their rounding may go either way); without a bias they
+ * are those of the logits (the scores rise with them).
  * The k ids of a token are distinct and in [0, N) for any input: masked
  * experts come after all others and have gate 0, and a token with nothing
  * else has gates 0. A NaN logit (for the softmax also a +inf one) makes that
@@ -522,7 +523,8 @@ bmoe_status bmoe_router_backward(bmoe_dtype dt, int T, int d, int n_experts, int
  *          count >= 0 entries (2^40 in all at most), BMOE_F32 or BMOE_BF16.
  *          Read before the call returns. bf16 results are rounded once.
  *   out    host array of n tensors of the same types and counts, or NULL:
- *          in place. An out tensor may be its own grad; any other sharing of
+ *          in place (fastest where each is aligned as its gradient is, modulo
+ *          16 bytes). An out tensor may be its own grad; any other sharing of
  *          memory with a written tensor is refused (BMOE_E_VALUE).
  *   norm   device fp32: written by bmoe_grad_norm and bmoe_grad_clip, read by
  *          bmoe_grad_scale (where ranks hold parts of the gradients, each
