@@ -49,6 +49,30 @@ class RouteSpec(ctypes.Structure):
                          _GROUP_SCORES[group_score])
 
 
+class NormSpec(ctypes.Structure):
+    """bmoe_norm_spec: r' = res_scale * r + out_scale * z, eps of both norms."""
+    _fields_ = [("eps", ctypes.c_float), ("res_scale", ctypes.c_float),
+                ("out_scale", ctypes.c_float)]
+
+    def __init__(self, *, eps: float = 1e-6, res_scale: float = 1.0, out_scale: float = 1.0):
+        super().__init__(eps, res_scale, out_scale)
+
+
+class OrthoSpec(ctypes.Structure):
+    """bmoe_ortho_spec: Newton-Schulz steps with the coefficients (a, b, c)."""
+    _fields_ = [("steps", ctypes.c_int), ("a", ctypes.c_float), ("b", ctypes.c_float),
+                ("c", ctypes.c_float), ("eps", ctypes.c_float)]
+
+    def __init__(self, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), *, eps: float = 1e-7):
+        super().__init__(steps, *coeffs, eps)
+
+
+class OrthoUpdate(ctypes.Structure):
+    """bmoe_ortho_update: the scalars of one orthogonal_step()."""
+    _fields_ = [("lr", ctypes.c_float), ("beta", ctypes.c_float), ("nesterov", ctypes.c_int),
+                ("weight_decay", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
 class BmoeTensor(ctypes.Structure):
     """bmoe_tensor: one entry of a gradient list."""
     _fields_ = [("data", ctypes.c_void_p), ("count", ctypes.c_size_t), ("dtype", ctypes.c_int)]
@@ -163,6 +187,33 @@ def lib():
         L.bmoe_grad_scale.restype = c_int
         L.bmoe_grad_clip.argtypes = [c_int, vp, vp, c_f, vp, vp, c_sz, vp]
         L.bmoe_grad_clip.restype = c_int
+        L.bmoe_group_rows_workspace_bytes.argtypes = [c_int, c_int, c_int]
+        L.bmoe_group_rows_workspace_bytes.restype = c_sz
+        L.bmoe_group_rows.argtypes = [c_int, c_int, c_int, vp, vp, vp, vp, vp, c_sz, vp]
+        L.bmoe_group_rows.restype = c_int
+        L.bmoe_grouped_product.argtypes = [c_int, c_int, c_int, c_int, c_int, vp, c_int, vp, c_int,
+                                           vp, vp, vp, vp]
+        L.bmoe_grouped_product.restype = c_int
+        L.bmoe_grouped_product_backward_workspace_bytes.argtypes = [c_int] * 5
+        L.bmoe_grouped_product_backward_workspace_bytes.restype = c_sz
+        L.bmoe_grouped_product_backward.argtypes = [c_int, c_int, c_int, c_int, c_int, vp, c_int,
+                                                    vp, c_int, vp, vp, vp, vp, vp, vp, c_sz, vp]
+        L.bmoe_grouped_product_backward.restype = c_int
+        L.bmoe_residual_norm.argtypes = [c_int, c_int, c_int, c_int, vp, vp, c_int, vp, vp, vp, vp,
+                                         vp, vp, vp, vp]
+        L.bmoe_residual_norm.restype = c_int
+        L.bmoe_residual_norm_backward_workspace_bytes.argtypes = [c_int, c_int, c_int]
+        L.bmoe_residual_norm_backward_workspace_bytes.restype = c_sz
+        L.bmoe_residual_norm_backward.argtypes = ([c_int, c_int, c_int, c_int, vp, vp, c_int] +
+                                                  [vp] * 13 + [c_sz, vp])
+        L.bmoe_residual_norm_backward.restype = c_int
+        L.bmoe_orthogonalize_workspace_bytes.argtypes = [c_int, c_int, c_int]
+        L.bmoe_orthogonalize_workspace_bytes.restype = c_sz
+        L.bmoe_orthogonalize.argtypes = [c_int, c_int, c_int, c_int, vp, vp, vp, vp, c_sz, vp]
+        L.bmoe_orthogonalize.restype = c_int
+        L.bmoe_orthogonal_step.argtypes = [c_int, c_int, c_int, c_int, c_int, vp, vp, vp, vp, vp,
+                                           vp, c_sz, vp]
+        L.bmoe_orthogonal_step.restype = c_int
         L.bmoe_backward_timed.argtypes = L.bmoe_backward.argtypes + [vp]
         L.bmoe_backward_timed.restype = c_int
         L.bmoe_backward_kernel_count.argtypes = [c_int, c_int, c_int, c_int, c_int]
@@ -509,6 +560,72 @@ def bmoe_grad_scale(n: int, grads, out, norm, max_norm: float, stream=None) -> i
 def bmoe_grad_clip(n: int, grads, out, max_norm: float, norm, ws, stream=None) -> int:
     return lib().bmoe_grad_clip(n, grads, out, max_norm, _ptr(norm), _ptr(ws), _nbytes(ws),
                                 _stream(stream))
+
+
+def bmoe_group_rows_workspace_bytes(T: int, n_experts: int, k: int) -> int:
+    return lib().bmoe_group_rows_workspace_bytes(T, n_experts, k)
+
+
+def bmoe_group_rows(T: int, n_experts: int, k: int, ids, offsets, perm, inv, ws,
+                    stream=None) -> int:
+    return lib().bmoe_group_rows(T, n_experts, k, _ptr(ids), _ptr(offsets), _ptr(perm), _ptr(inv),
+                                 _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def bmoe_grouped_product(dt: int, M: int, K: int, O: int, n_groups: int, a, a_rows: int, perm,
+                         k: int, w, offsets, c, stream=None) -> int:
+    return lib().bmoe_grouped_product(dt, M, K, O, n_groups, _ptr(a), a_rows, _ptr(perm), k,
+                                      _ptr(w), _ptr(offsets), _ptr(c), _stream(stream))
+
+
+def bmoe_grouped_product_backward_workspace_bytes(dt: int, M: int, K: int, O: int,
+                                                  n_groups: int) -> int:
+    return lib().bmoe_grouped_product_backward_workspace_bytes(dt, M, K, O, n_groups)
+
+
+def bmoe_grouped_product_backward(dt: int, M: int, K: int, O: int, n_groups: int, a, a_rows: int,
+                                  perm, k: int, w, offsets, dc, da, dw, ws, stream=None) -> int:
+    return lib().bmoe_grouped_product_backward(dt, M, K, O, n_groups, _ptr(a), a_rows, _ptr(perm),
+                                               k, _ptr(w), _ptr(offsets), _ptr(dc), _ptr(da),
+                                               _ptr(dw), _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def bmoe_residual_norm(dt: int, T: int, d: int, k: int, spec, u, u_rows: int, inv, gates, r, w_post,
+                       w_pre, r_out, n, stream=None) -> int:
+    return lib().bmoe_residual_norm(dt, T, d, k, _ref(spec), _ptr(u), u_rows, _ptr(inv),
+                                    _ptr(gates), _ptr(r), _ptr(w_post), _ptr(w_pre), _ptr(r_out),
+                                    _ptr(n), _stream(stream))
+
+
+def bmoe_residual_norm_backward_workspace_bytes(dt: int, T: int, d: int) -> int:
+    return lib().bmoe_residual_norm_backward_workspace_bytes(dt, T, d)
+
+
+def bmoe_residual_norm_backward(dt: int, T: int, d: int, k: int, spec, u, u_rows: int, inv, gates,
+                                r_out, w_post, w_pre, dr_out, dn, du, dgates, dr, dw_post, dw_pre,
+                                ws, stream=None) -> int:
+    return lib().bmoe_residual_norm_backward(dt, T, d, k, _ref(spec), _ptr(u), u_rows, _ptr(inv),
+                                             _ptr(gates), _ptr(r_out), _ptr(w_post), _ptr(w_pre),
+                                             _ptr(dr_out), _ptr(dn), _ptr(du), _ptr(dgates),
+                                             _ptr(dr), _ptr(dw_post), _ptr(dw_pre), _ptr(ws),
+                                             _nbytes(ws), _stream(stream))
+
+
+def bmoe_orthogonalize_workspace_bytes(batch: int, rows: int, cols: int) -> int:
+    return lib().bmoe_orthogonalize_workspace_bytes(batch, rows, cols)
+
+
+def bmoe_orthogonalize(dt: int, batch: int, rows: int, cols: int, spec, u, o, ws,
+                       stream=None) -> int:
+    return lib().bmoe_orthogonalize(dt, batch, rows, cols, _ref(spec), _ptr(u), _ptr(o), _ptr(ws),
+                                    _nbytes(ws), _stream(stream))
+
+
+def bmoe_orthogonal_step(w_dt: int, grad_dt: int, batch: int, rows: int, cols: int, spec, update,
+                         grad, momentum, w, ws, stream=None) -> int:
+    return lib().bmoe_orthogonal_step(w_dt, grad_dt, batch, rows, cols, _ref(spec), _ref(update),
+                                      _ptr(grad), _ptr(momentum), _ptr(w), _ptr(ws), _nbytes(ws),
+                                      _stream(stream))
 
 
 # ---- conveniences over the entry points (allocation + error checks) -------
@@ -923,3 +1040,241 @@ def clip_grads(grads, max_norm: float, *, out=None, stream=None) -> torch.Tensor
         ws = torch.empty(bmoe_grad_workspace_bytes(len(arr)), dtype=torch.uint8, device=norm.device)
         _check(bmoe_grad_clip(len(arr), arr, oarr, max_norm, norm, ws, stream), "bmoe_grad_clip")
         return norm
+
+
+# ---- around a block: dense experts, norms, orthogonalised updates ---------------
+
+def _workspace(n: int, what: str, device) -> torch.Tensor:
+    if n == 0:
+        raise BmoeError(2, what)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def group_rows(ids: torch.Tensor, n_experts: int, *, stream=None):
+    """(offsets int32 [N+1], perm int32 [T*k], inv int32 [T*k]): the routed rows
+    r = t*k + j of ids int32 [T][k] grouped by expert, in order within one. An id
+    outside [0, N) is a padded pick: behind the last expert, inv = -1."""
+    T, k = _matrix("ids", ids).shape
+    dev = ids.device
+    _like("ids", ids, torch.int32, (T, k), dev)
+    with _at(ids, stream):
+        ws = _workspace(bmoe_group_rows_workspace_bytes(T, n_experts, k),
+                        "bmoe_group_rows_workspace_bytes", dev)
+        offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
+        perm = torch.empty(T * k, dtype=torch.int32, device=dev)
+        inv = torch.empty(T * k, dtype=torch.int32, device=dev)
+        _check(bmoe_group_rows(T, n_experts, k, ids, offsets, perm, inv, ws, stream),
+               "bmoe_group_rows")
+        return offsets, perm, inv
+
+
+def _grouped(a, w, offsets, perm, k):
+    """(dt, M, K, O, groups) of a grouped product's checked inputs."""
+    R, K = _matrix("a", a).shape
+    dt = dtype_code(a)
+    if w.dim() != 3:
+        raise ValueError(f"w must be [groups][O][K], got shape {tuple(w.shape)}")
+    G, O = w.shape[:2]
+    _like("w", w, a.dtype, (G, O, K), a.device)
+    _like("offsets", offsets, torch.int32, (G + 1,), a.device)
+    if perm is None:
+        return dt, R, K, O, G
+    _like("perm", perm, torch.int32, (perm.numel(),), a.device)
+    if k < 1:
+        raise ValueError("k must be at least 1")
+    return dt, perm.numel(), K, O, G
+
+
+def grouped_product(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, perm=None,
+                    k: int = 1, out=None, stream=None) -> torch.Tensor:
+    """c [M][O], c[q] = w[e] a[row(q)] for the rows q of group e = offsets[e] ..
+    offsets[e+1] (int32, on the GPU). a [R][K], w [groups][O][K] (one type, fp32
+    or bf16); row(q) = perm[q] // k with group_rows()'s perm, else q. Rows of no
+    group are left as they were."""
+    dt, M, K, O, G = _grouped(a, w, offsets, perm, k)
+    with _at(a, stream):
+        if out is None:
+            out = torch.empty(M, O, dtype=a.dtype, device=a.device)
+        else:
+            _like("out", out, a.dtype, (M, O), a.device)
+        _check(bmoe_grouped_product(dt, M, K, O, G, a, a.shape[0], perm, k, w, offsets, out,
+                                    stream), "bmoe_grouped_product")
+        return out
+
+
+def grouped_product_backward(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
+                             dc: torch.Tensor, *, perm=None, k: int = 1, da=None, dw=None,
+                             want_da: bool = True, want_dw: bool = True, stream=None) -> dict:
+    """Gradients of sum(dc * c) for grouped_product()'s c: dict of da [M][K] (one
+    row per row of the product, type of a) and dw fp32 [groups][O][K]. With
+    `perm`, residual_norm(da, k=k, inv=inv) sums a token's k rows."""
+    dt, M, K, O, G = _grouped(a, w, offsets, perm, k)
+    _like("dc", dc, a.dtype, (M, O), a.device)
+    with _at(a, stream):
+        if da is not None:
+            _like("da", da, a.dtype, (M, K), a.device)
+        elif want_da:
+            da = torch.empty(M, K, dtype=a.dtype, device=a.device)
+        if dw is not None:
+            _like("dw", dw, torch.float32, (G, O, K), a.device)
+        elif want_dw:
+            dw = torch.empty(G, O, K, dtype=torch.float32, device=a.device)
+        ws = _workspace(bmoe_grouped_product_backward_workspace_bytes(dt, M, K, O, G),
+                        "bmoe_grouped_product_backward_workspace_bytes", a.device)
+        _check(bmoe_grouped_product_backward(dt, M, K, O, G, a, a.shape[0], perm, k, w, offsets,
+                                             dc, da, dw, ws, stream),
+               "bmoe_grouped_product_backward")
+        return {"da": da, "dw": dw}
+
+
+def _norm_inputs(x, T, d, u, k, inv, gates, w_post, w_pre):
+    """Checks what both directions of residual_norm() read; the rows of u."""
+    dev = x.device
+    if u is not None:
+        if u.dim() != 2 or u.shape[1] != d:
+            raise ValueError(f"u must be [rows][{d}], got shape {tuple(u.shape)}")
+        _like("u", u, x.dtype, u.shape, dev)
+        if inv is not None:
+            _like("inv", inv, torch.int32, (T * k,), dev)
+        elif u.shape[0] != T * k:
+            raise ValueError(f"u must have {T * k} rows without inv, got {u.shape[0]}")
+        if gates is not None:
+            _like("gates", gates, torch.float32, (T, k), dev)
+    elif inv is not None or gates is not None or w_post is not None:
+        raise ValueError("inv, gates and w_post belong to u")
+    for name, w in (("w_post", w_post), ("w_pre", w_pre)):
+        if w is not None:
+            _like(name, w, torch.float32, (d,), dev)
+    return 0 if u is None else u.shape[0]
+
+
+def residual_norm(u, r, spec: Optional[NormSpec] = None, *, k: int = 1, inv=None, gates=None,
+                  w_post=None, w_pre=None, r_out=None, n=None, stream=None):
+    """(r', n): r' = res_scale * r + out_scale * z with z the (w_post: RMS-normed)
+    sum of a token's k gate-weighted rows of u, n the RMS norm of r' (None without
+    w_pre). u [rows][d]: grouped_product()'s c with inv (int32 [T*k] of
+    group_rows()) and gates fp32 [T][k], or a layer's y; None: n of r alone. r
+    [T][d] or None (0). r_out may be r."""
+    if u is None and r is None:
+        raise ValueError("u or r has to be given")
+    x = u if r is None else r
+    _matrix("r" if r is not None else "u", x)
+    if k < 1:
+        raise ValueError("k must be at least 1")
+    d = x.shape[1]
+    if r is not None:
+        T = r.shape[0]
+    elif inv is not None:
+        T = inv.numel() // k
+    else:
+        T = u.shape[0] // k
+    dt = dtype_code(x)
+    rows = _norm_inputs(x, T, d, u, k, inv, gates, w_post, w_pre)
+    if spec is None:
+        spec = NormSpec()
+    with _at(x, stream):
+        if r_out is not None:
+            _like("r_out", r_out, x.dtype, (T, d), x.device)
+        else:
+            r_out = torch.empty(T, d, dtype=x.dtype, device=x.device)
+        if n is not None and w_pre is None:
+            raise ValueError("n needs w_pre")
+        if n is not None:
+            _like("n", n, x.dtype, (T, d), x.device)
+        elif w_pre is not None:
+            n = torch.empty(T, d, dtype=x.dtype, device=x.device)
+        _check(bmoe_residual_norm(dt, T, d, k, spec, u, rows, inv, gates, r, w_post, w_pre, r_out,
+                                  n, stream), "bmoe_residual_norm")
+        return r_out, n
+
+
+def residual_norm_backward(u, r_out: torch.Tensor, spec: Optional[NormSpec] = None, *, k: int = 1,
+                           inv=None, gates=None, w_post=None, w_pre=None, dr_out=None, dn=None,
+                           du=None, dr=None, stream=None) -> dict:
+    """Gradients of sum(dr_out * r') + sum(dn * n) for residual_norm(): dict of
+    dr, du, dgates, dw_post and dw_pre (None where the input is). r_out: its r' as
+    stored. Rows of u that no pick names get no gradient: pass a zeroed `du`."""
+    T, d = _matrix("r_out", r_out).shape
+    dev = r_out.device
+    dt = dtype_code(r_out)
+    if k < 1:
+        raise ValueError("k must be at least 1")
+    rows = _norm_inputs(r_out, T, d, u, k, inv, gates, w_post, w_pre)
+    if (dn is None) != (w_pre is None):
+        raise ValueError("dn belongs to w_pre")
+    if dr_out is None and w_pre is None:
+        raise ValueError("dr_out is needed without w_pre")
+    if spec is None:
+        spec = NormSpec()
+    for name, t in (("dr_out", dr_out), ("dn", dn), ("dr", dr)):
+        if t is not None:
+            _like(name, t, r_out.dtype, (T, d), dev)
+    if du is not None:
+        if u is None:
+            raise ValueError("du belongs to u")
+        _like("du", du, u.dtype, u.shape, dev)
+    with _at(r_out, stream):
+        if du is None and u is not None:
+            du = torch.empty_like(u)
+        if dr is None:
+            dr = torch.empty_like(r_out)
+        dgates = None if gates is None else torch.empty_like(gates)
+        dw_post = None if w_post is None else torch.empty_like(w_post)
+        dw_pre = None if w_pre is None else torch.empty_like(w_pre)
+        ws = _workspace(bmoe_residual_norm_backward_workspace_bytes(dt, T, d),
+                        "bmoe_residual_norm_backward_workspace_bytes", dev)
+        _check(bmoe_residual_norm_backward(dt, T, d, k, spec, u, rows, inv, gates, r_out, w_post,
+                                           w_pre, dr_out, dn, du, dgates, dr, dw_post, dw_pre, ws,
+                                           stream), "bmoe_residual_norm_backward")
+        return {"dr": dr, "du": du, "dgates": dgates, "dw_post": dw_post, "dw_pre": dw_pre}
+
+
+def _matrices(name: str, t: torch.Tensor):
+    """(batch, rows, cols) of one matrix or a batch of them."""
+    if t.dim() not in (2, 3) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous matrix or a batch of matrices, got shape "
+                         f"{tuple(t.shape)}")
+    return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
+
+
+def orthogonalize(u: torch.Tensor, spec: Optional[OrthoSpec] = None, *, out=None,
+                  stream=None) -> torch.Tensor:
+    """The Newton-Schulz iterate of u / |u| for a matrix or a batch of matrices
+    (fp32 or bf16): u's singular vectors with singular values near 1. out may be
+    u."""
+    B, rows, cols = _matrices("u", u)
+    dt = dtype_code(u)
+    if spec is None:
+        spec = OrthoSpec()
+    with _at(u, stream):
+        if out is None:
+            out = torch.empty_like(u)
+        else:
+            _like("out", out, u.dtype, u.shape, u.device)
+        ws = _workspace(bmoe_orthogonalize_workspace_bytes(B, rows, cols),
+                        "bmoe_orthogonalize_workspace_bytes", u.device)
+        _check(bmoe_orthogonalize(dt, B, rows, cols, spec, u, out, ws, stream),
+               "bmoe_orthogonalize")
+        return out
+
+
+def orthogonal_step(w: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, lr: float,
+                    spec: Optional[OrthoSpec] = None, *, beta: float = 0.95, nesterov: bool = True,
+                    weight_decay: float = 0.0, scale: float = 1.0, stream=None) -> torch.Tensor:
+    """One step of the weights w (a matrix or a batch, fp32 or bf16) by the
+    orthogonalised momentum of grad (fp32 or bf16), in place: momentum (fp32) =
+    beta * momentum + grad; w = (1 - lr * weight_decay) * w - lr * scale *
+    orthogonalize(grad + beta * momentum, or momentum without nesterov)."""
+    B, rows, cols = _matrices("w", w)
+    w_dt, g_dt = dtype_code(w), dtype_code(grad)
+    _like("grad", grad, grad.dtype, w.shape, w.device)
+    _like("momentum", momentum, torch.float32, w.shape, w.device)
+    if spec is None:
+        spec = OrthoSpec()
+    update = OrthoUpdate(lr, beta, bool(nesterov), weight_decay, scale)
+    with _at(w, stream):
+        ws = _workspace(bmoe_orthogonalize_workspace_bytes(B, rows, cols),
+                        "bmoe_orthogonalize_workspace_bytes", w.device)
+        _check(bmoe_orthogonal_step(w_dt, g_dt, B, rows, cols, spec, update, grad, momentum, w, ws,
+                                    stream), "bmoe_orthogonal_step")
+        return w

@@ -1,0 +1,170 @@
+// Routed rows grouped by expert: a stable counting sort of the M = T k ids.
+//   offsets[e] .. offsets[e + 1]  the sorted slots of expert e
+//   perm[slot] = r                experts ascending, r ascending within one
+//   inv[r] = slot                 (-1 for an id outside [0, N): a padded pick)
+// Padded picks take the slots behind the last expert's, in order of r.
+//
+// Bound by latency: the ids are 4 M bytes. They are cut into at most 256
+// chunks. One launch counts each chunk's experts, a second gives every chunk
+// the counts before it (at most 256 x N words from L2) and ranks its own rows
+// (64 at a time, one ballot per bit of the expert). One chunk needs no counts
+// from elsewhere: a single launch.
+#include "common.h"
+#include "kernels.h"
+
+namespace bmoe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kMostChunks = 256;
+constexpr int kLeastChunk = 2048;
+
+struct GroupArgs {
+  const int32_t* ids;
+  int32_t *offsets, *perm, *inv;
+  int* count;  // [chunks][N + 1]
+  int M, N, chunk, chunks, nbits;
+};
+
+// Expert N is the padded picks'.
+__device__ __forceinline__ int key_of(const GroupArgs& p, int r) {
+  const int e = p.ids[r];
+  return (unsigned)e < (unsigned)p.N ? e : p.N;
+}
+
+__global__ __launch_bounds__(kThreads) void group_count_kernel(GroupArgs p) {
+  extern __shared__ int cnt[];
+  const int n = p.N + 1;
+  for (int e = threadIdx.x; e < n; e += kThreads) cnt[e] = 0;
+  __syncthreads();
+  const long long r0 = (long long)blockIdx.x * p.chunk;
+  const int len = (int)min((long long)p.chunk, p.M - r0);
+  for (int i = threadIdx.x; i < len; i += kThreads) atomicAdd(&cnt[key_of(p, (int)(r0 + i))], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e < n; e += kThreads) p.count[(size_t)blockIdx.x * n + e] = cnt[e];
+}
+
+__global__ __launch_bounds__(kThreads) void group_scatter_kernel(GroupArgs p) {
+  extern __shared__ int sh[];  // [kWaves][n] cursors, [n] bases
+  __shared__ int scratch[kWaves];
+  const int n = p.N + 1, tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  int* base = sh + kWaves * n;
+  const long long r0 = (long long)blockIdx.x * p.chunk;
+  const int len = (int)min((long long)p.chunk, p.M - r0);
+  for (int i = tid; i < kWaves * n; i += kThreads) sh[i] = 0;
+  __syncthreads();
+  // each wave owns a contiguous quarter of the chunk and counts it
+  const int quarter = (len + kWaves - 1) / kWaves;
+  const int wb = min(len, wave * quarter), we = min(len, wb + quarter);
+  int* cur = sh + wave * n;
+  for (int i = wb + lane; i < we; i += kWave) atomicAdd(&cur[key_of(p, (int)(r0 + i))], 1);
+  __syncthreads();
+  // per expert: the rows of all chunks, and of those before this one
+  for (int e = tid; e < n; e += kThreads) {
+    int total = 0, before = 0;
+    if (p.chunks == 1) {
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) total += sh[w * n + e];
+    } else {
+      for (int c = 0; c < p.chunks; ++c) {
+        const int v = p.count[(size_t)c * n + e];
+        total += v;
+        before += c < (int)blockIdx.x ? v : 0;
+      }
+    }
+    base[e] = total;
+    // the wave's own counts become cursors relative to the expert's base
+    int at = before;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const int v = sh[w * n + e];
+      sh[w * n + e] = at;
+      at += v;
+    }
+  }
+  __syncthreads();
+  // exclusive prefix sum of the totals: each thread owns a run of experts
+  const int per = (n + kThreads - 1) / kThreads;
+  const int lo = min(n, tid * per), hi = min(n, lo + per);
+  int seg = 0;
+  for (int e = lo; e < hi; ++e) seg += base[e];
+  const int incl = wave_incl_scan(seg);
+  if (lane == kWave - 1) scratch[wave] = incl;
+  __syncthreads();
+  int at = incl - seg;
+  for (int w = 0; w < wave; ++w) at += scratch[w];
+  for (int e = lo; e < hi; ++e) {
+    const int v = base[e];
+    base[e] = at;
+    if (blockIdx.x == 0) p.offsets[e] = at;  // e = N: where the padded picks begin
+    at += v;
+  }
+  __syncthreads();
+  // stable ranks: lanes with the same expert found by one ballot per bit
+  const uint64_t below = lane == 0 ? 0ull : ~0ull >> (kWave - lane);
+  for (int i0 = wb; i0 < we; i0 += kWave) {
+    const bool valid = i0 + lane < we;
+    const int r = (int)(r0 + i0 + lane);
+    const int e = valid ? key_of(p, r) : 0;
+    uint64_t same = __ballot(valid);
+    for (int b = 0; b < p.nbits; ++b) {
+      const bool bit = (e >> b) & 1;
+      const uint64_t has = __ballot(bit);
+      same &= bit ? has : ~has;
+    }
+    const int rank = __popcll(same & below), group = __popcll(same);
+    const int c = valid ? cur[e] : 0;
+    __builtin_amdgcn_wave_barrier();
+    if (valid) {
+      const int slot = base[e] + c + rank;
+      p.perm[slot] = r;
+      p.inv[r] = e < p.N ? slot : -1;
+      if (rank == group - 1) cur[e] = c + group;
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+int chunk_of(int M) {
+  const int c = (int)(((long long)M + kMostChunks - 1) / kMostChunks);
+  return c < kLeastChunk ? kLeastChunk : c;
+}
+
+}  // namespace
+
+size_t group_count_bytes(int M, int N) {
+  const size_t chunks = ((size_t)M + chunk_of(M) - 1) / chunk_of(M);
+  return chunks > 1 ? chunks * (N + 1) * sizeof(int) : 0;
+}
+
+hipError_t launch_group_rows(const int32_t* ids, int M, int N, int32_t* offsets, int32_t* perm,
+                             int32_t* inv, int* count, hipStream_t s) {
+  GroupArgs p;
+  p.ids = ids;
+  p.offsets = offsets;
+  p.perm = perm;
+  p.inv = inv;
+  p.count = count;
+  p.M = M;
+  p.N = N;
+  p.chunk = chunk_of(M);
+  p.chunks = M > 0 ? (int)(((long long)M + p.chunk - 1) / p.chunk) : 1;
+  p.nbits = 0;
+  while ((1 << p.nbits) < N + 1) ++p.nbits;
+  if (p.chunks > 1) {
+    const hipError_t e = launch_kernel(group_count_kernel, dim3(p.chunks), dim3(kThreads),
+                                       (uint32_t)(sizeof(int) * (N + 1)), s, KernelTiming{}, p);
+    if (e != hipSuccess) return e;
+  }
+  const size_t lds = sizeof(int) * (size_t)(kWaves + 1) * (N + 1);
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(group_scatter_kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  return launch_kernel(group_scatter_kernel, dim3(p.chunks), dim3(kThreads), (uint32_t)lds, s,
+                       KernelTiming{}, p);
+}
+
+}  // namespace bmoe

@@ -1,0 +1,329 @@
+// Matrix products grouped by expert, ragged groups:
+//   c[q]  = W_e a[row(q)]                  rows q of group e, e = 0 .. G - 1
+//   da[q] = W_e^T dc[q]
+//   dW_e  = sum over the rows q of e of dc[q] a[row(q)]^T      (fp32)
+// with group e the rows offsets[e] .. offsets[e + 1] and row(q) = perm[q] / k
+// (q itself without perm). The offsets live on the device: a workgroup finds
+// its tile of a group from them, so the host never waits for the router.
+#include "common.h"
+#include "kernels.h"
+#include "tile_product.h"
+
+namespace bmoe {
+namespace {
+
+using namespace tile;
+
+struct GroupTile {
+  int e, lo, hi;  // group and its rows
+  int i;          // tile within the group; e = -1: no such tile
+};
+
+// Rows of group e, whatever the offsets hold.
+__device__ __forceinline__ int2 group_rows_of(const int32_t* offsets, int e, int M) {
+  const int lo = min(max(offsets[e], 0), M), hi = min(max(offsets[e + 1], 0), M);
+  return make_int2(lo, max(lo, hi));
+}
+
+// Tile t of all groups' tiles of BM rows, groups ascending. Every wave looks
+// it up for itself: 64 groups at a time, a prefix sum over the lanes.
+template <int BM>
+__device__ __forceinline__ GroupTile find_tile(const int32_t* offsets, int G, int M, int t,
+                                               int lane) {
+  int before = 0;
+  for (int e0 = 0; e0 < G; e0 += kWave) {
+    int2 r = make_int2(0, 0);
+    if (e0 + lane < G) r = group_rows_of(offsets, e0 + lane, M);
+    const int n = (r.y - r.x + BM - 1) / BM;
+    const int incl = wave_incl_scan(n);
+    const uint64_t past = __ballot(before + incl > t);
+    if (past) {
+      const int src = __ffsll((unsigned long long)past) - 1;
+      GroupTile g;
+      g.e = e0 + src;
+      g.lo = __builtin_amdgcn_readlane(r.x, src);
+      g.hi = __builtin_amdgcn_readlane(r.y, src);
+      g.i = t - before - (__builtin_amdgcn_readlane(incl, src) - __builtin_amdgcn_readlane(n, src));
+      return g;
+    }
+    before += __builtin_amdgcn_readlane(incl, kWave - 1);
+  }
+  return {-1, 0, 0, 0};
+}
+
+struct ProductArgs {
+  const char* a;  // rows of the product's left operand, `red` values each
+  const char* w;  // [G][O][K]
+  char* c;        // [M][cols]
+  const int32_t* offsets;
+  const int32_t* perm;  // NULL: row q of a is row q of the product
+  int k, a_rows, M, G, red, cols, tiles_n;
+};
+
+// Row q's row of a.
+__device__ __forceinline__ int a_row(const ProductArgs& p, int q) {
+  if (!p.perm) return q;
+  const int t = p.perm[q] / p.k;
+  return min(max(t, 0), p.a_rows - 1);
+}
+
+// A wave's accumulator blocks to bf16 rows of c, 16 rows at a time through its
+// own LDS, so that stores are 16 bytes a lane over whole row segments.
+template <class C>
+__device__ __forceinline__ void store_bf16(const Acc<C>& acc, char* stg, char* c, size_t ld,
+                                           int rows, int cols, int lane) {
+  constexpr int PITCH = C::TN * 2, CHUNKS = C::TN / 8, RPQ = 64 / CHUNKS;
+  static_assert((CHUNKS & (CHUNKS - 1)) == 0 && CHUNKS <= 64, "chunk swizzle");
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int r = 8 * h; r < 8 * h + 8; ++r) {
+          const int row = acc_row(r, lane) - 16 * h, col = j * 32 + acc_col(lane);
+          const int off = row * PITCH + 16 * ((col >> 3) ^ (row & (CHUNKS - 1))) + 2 * (col & 7);
+          *reinterpret_cast<uint16_t*>(stg + off) = (uint16_t)f32_to_bf16_bits(acc[i][j][r]);
+        }
+#pragma unroll
+      for (int q = 0; q < 16 / RPQ; ++q) {
+        const int row = q * RPQ + lane / CHUNKS, ch = lane % CHUNKS;
+        const uint4 v =
+            *reinterpret_cast<const uint4*>(stg + row * PITCH + 16 * (ch ^ (row & (CHUNKS - 1))));
+        const int at = i * 32 + 16 * h + row;
+        if (at < rows && ch * 8 < cols)
+          *reinterpret_cast<uint4*>(c + (size_t)at * ld + ch * 16) = v;
+      }
+    }
+}
+
+// The same value by value: fp32, and bf16 rows of odd lengths.
+template <class C, typename T>
+__device__ __forceinline__ void store_plain(const Acc<C>& acc, char* c, size_t ld, int rows,
+                                            int cols, int lane) {
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+      const int col = j * 32 + acc_col(lane);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int row = i * 32 + acc_row(r, lane);
+        if (row < rows && col < cols) {
+          T* dst = reinterpret_cast<T*>(c + (size_t)row * ld) + col;
+          if constexpr (sizeof(T) == 2) *dst = (T)f32_to_bf16_bits(acc[i][j][r]);
+          else *dst = acc[i][j][r];
+        }
+      }
+    }
+}
+
+// c (BMODE kOutRows: W's rows are the output's columns) or da (kRedRows: they
+// are the reduction).
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void grouped_kernel(ProductArgs p, int run_items) {
+  __shared__ __attribute__((aligned(1024))) char st0[C::STAGE];
+  __shared__ __attribute__((aligned(1024))) char st1[C::STAGE];
+  __shared__ __attribute__((aligned(1024))) char st2[C::NSTAGE > 2 ? C::STAGE : 16];
+  __shared__ __attribute__((aligned(1024))) char st3[C::NSTAGE > 3 ? C::STAGE : 16];
+  char* all[4] = {st0, st1, st2, st3};
+  char* ring[C::NSTAGE];
+#pragma unroll
+  for (int s = 0; s < C::NSTAGE; ++s) ring[s] = all[s];
+
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int item = xcd_item(grid_block(), run_items);
+  const GroupTile t = find_tile<C::BM>(p.offsets, p.G, p.M, item / p.tiles_n, lane);
+  if (t.e < 0) return;  // the whole workgroup
+  const int row0 = t.lo + t.i * C::BM, rows = min(C::BM, t.hi - row0);
+  const int col0 = item % p.tiles_n * C::BN;
+
+  const size_t a_ld = (size_t)p.red * C::ES;
+  OutRowsSource<C, C::BM, C::A_LOADS> a;
+  a.init([&](int r) { return p.a + (size_t)a_row(p, row0 + min(r, rows - 1)) * a_ld; }, p.red, 0,
+         lane, wave);
+  const char* w = p.w + (size_t)t.e * p.red * p.cols * C::ES;
+  Acc<C> acc;
+  clear<C>(acc);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  Reader<C, kOutRows, C::BM, C::FM> ra;
+  ra.init(wm * C::TM, lane);
+  Reader<C, C::BMODE, C::BN, C::FN> rb;
+  rb.init(wn * C::TN, lane);
+  const int nsteps = (p.red + C::BK - 1) / C::BK;
+  if constexpr (C::BMODE == kOutRows) {
+    OutRowsSource<C, C::BN, C::B_LOADS> b;
+    b.init([&](int r) { return w + (size_t)min(col0 + r, p.cols - 1) * a_ld; }, p.red, 0, lane,
+           wave);
+    run<C>(acc, ring, a, b, ra, rb, nsteps, lane, wave);
+  } else {
+    RedRowsSource<C, C::BN, C::B_LOADS, SameRow> b;
+    b.init(w, (size_t)p.cols * C::ES, col0, p.cols, p.red, 0, SameRow{}, lane, wave);
+    run<C>(acc, ring, a, b, ra, rb, nsteps, lane, wave);
+  }
+
+  const size_t c_ld = (size_t)p.cols * C::ES;
+  char* c = p.c + (size_t)(row0 + wm * C::TM) * c_ld + (size_t)(col0 + wn * C::TN) * C::ES;
+  const int rl = rows - wm * C::TM, cl = p.cols - col0 - wn * C::TN;
+  if constexpr (C::E == kBf16 && C::ALIGNED) {
+    static_assert(C::WAVES * 16 * C::TN * 2 <= C::STAGE, "staging fits a stage");
+    lds_barrier();  // every wave is done with the ring
+    store_bf16<C>(acc, st0 + wave * 16 * C::TN * 2, c, c_ld, rl, cl, lane);
+  } else if constexpr (C::E == kBf16) {
+    store_plain<C, uint16_t>(acc, c, c_ld, rl, cl, lane);
+  } else {
+    store_plain<C, float>(acc, c, c_ld, rl, cl, lane);
+  }
+}
+
+// dW: one workgroup per expert and tile of its O x K entries. The rows of a
+// group are taken kListRows at a time, their rows of a listed in LDS first.
+constexpr int kListRows = 1024;
+
+struct DwArgs {
+  const char* a;   // [a_rows][K]
+  const char* dc;  // [M][O]
+  float* dw;       // [G][O][K]
+  const int32_t* offsets;
+  const int32_t* perm;
+  int k, a_rows, M, G, O, K, tiles_o, tiles_k;
+};
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void grouped_dw_kernel(DwArgs p, int run_items) {
+  __shared__ __attribute__((aligned(1024))) char st0[C::STAGE];
+  __shared__ __attribute__((aligned(1024))) char st1[C::STAGE];
+  __shared__ __attribute__((aligned(1024))) char st2[C::NSTAGE > 2 ? C::STAGE : 16];
+  __shared__ __attribute__((aligned(1024))) char st3[C::NSTAGE > 3 ? C::STAGE : 16];
+  __shared__ int32_t list[kListRows];
+  char* all[4] = {st0, st1, st2, st3};
+  char* ring[C::NSTAGE];
+#pragma unroll
+  for (int s = 0; s < C::NSTAGE; ++s) ring[s] = all[s];
+
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const unsigned item = xcd_item(grid_block(), run_items), tiles = p.tiles_o * p.tiles_k;
+  const int e = item / tiles;
+  if (e >= p.G) return;
+  const int t = item % tiles;
+  const int o0 = t / p.tiles_k * C::BM, k0 = t % p.tiles_k * C::BN;
+  const int2 rows = group_rows_of(p.offsets, e, p.M);
+
+  Acc<C> acc;
+  clear<C>(acc);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  Reader<C, kRedRows, C::BM, C::FM> ra;
+  ra.init(wm * C::TM, lane);
+  Reader<C, kRedRows, C::BN, C::FN> rb;
+  rb.init(wn * C::TN, lane);
+  for (int q0 = rows.x; q0 < rows.y; q0 += kListRows) {
+    const int n = min(kListRows, rows.y - q0);
+    __syncthreads();  // every wave is done with the list and the ring
+    for (int i = threadIdx.x; i < n; i += C::THREADS) {
+      const int q = q0 + i;
+      list[i] = p.perm ? min(max(p.perm[q] / p.k, 0), p.a_rows - 1) : q;
+    }
+    __syncthreads();
+    RedRowsSource<C, C::BM, C::A_LOADS, SameRow> a;
+    a.init(p.dc + (size_t)q0 * p.O * C::ES, (size_t)p.O * C::ES, o0, p.O, n, 0, SameRow{}, lane,
+           wave);
+    RedRowsSource<C, C::BN, C::B_LOADS, ListedRow> b;
+    b.init(p.a, (size_t)p.K * C::ES, k0, p.K, n, 0, ListedRow{list}, lane, wave);
+    tile::run<C>(acc, ring, a, b, ra, rb, (n + C::BK - 1) / C::BK, lane, wave);
+  }
+  const int ol = o0 + wm * C::TM, kl = k0 + wn * C::TN;
+  char* dst = reinterpret_cast<char*>(p.dw + ((size_t)e * p.O + ol) * p.K + kl);
+  store_plain<C, float>(acc, dst, (size_t)p.K * 4, p.O - ol, p.K - kl, lane);
+}
+
+template <class C>
+hipError_t launch_grouped_cfg(ProductArgs p, hipStream_t s) {
+  p.tiles_n = (p.cols + C::BN - 1) / C::BN;
+  // a group's last tile may be short: at most one more tile per group with rows
+  const size_t tiles_m = (size_t)p.M / C::BM + (p.G < p.M ? p.G : p.M);
+  const size_t items = tiles_m * p.tiles_n;
+  const int run_items = items >= 1024 ? 32 : 1;
+  const size_t super = 8 * run_items;
+  return launch_kernel(grouped_kernel<C>, grid_rows((items + super - 1) / super * super),
+                       dim3(C::THREADS), 0, s, KernelTiming{}, p, run_items);
+}
+
+template <class C>
+hipError_t launch_grouped_dw_cfg(DwArgs p, hipStream_t s) {
+  p.tiles_o = (p.O + C::BM - 1) / C::BM;
+  p.tiles_k = (p.K + C::BN - 1) / C::BN;
+  const size_t items = (size_t)p.G * p.tiles_o * p.tiles_k;
+  const int run_items = items >= 1024 ? 32 : 1;
+  const size_t super = 8 * run_items;
+  return launch_kernel(grouped_dw_kernel<C>, grid_rows((items + super - 1) / super * super),
+                       dim3(C::THREADS), 0, s, KernelTiming{}, p, run_items);
+}
+
+template <int E, int BMODE, bool ALIGNED>
+using Tile128 = Cfg<E, 1, 128, 128, 2, 2, 4, kOutRows, BMODE, ALIGNED>;
+template <int E, bool ALIGNED>
+using DwTile128 = Cfg<E, 1, 128, 128, 2, 2, 4, kRedRows, kRedRows, ALIGNED>;
+
+template <int E, int BMODE>
+hipError_t launch_grouped_type(const ProductArgs& p, hipStream_t s) {
+  constexpr int EPC = E == kF32 ? 4 : 8;
+  if (p.red % EPC == 0 && p.cols % EPC == 0)
+    return launch_grouped_cfg<Tile128<E, BMODE, true>>(p, s);
+  return launch_grouped_cfg<Tile128<E, BMODE, false>>(p, s);
+}
+
+template <int E>
+hipError_t launch_dw_type(const DwArgs& p, hipStream_t s) {
+  constexpr int EPC = E == kF32 ? 4 : 8;
+  if (p.O % EPC == 0 && p.K % EPC == 0) return launch_grouped_dw_cfg<DwTile128<E, true>>(p, s);
+  return launch_grouped_dw_cfg<DwTile128<E, false>>(p, s);
+}
+
+}  // namespace
+
+hipError_t launch_grouped(bmoe_dtype dt, bool back, int M, int red, int cols, int G, const void* a,
+                          const int32_t* perm, int k, int a_rows, const void* w,
+                          const int32_t* offsets, void* c, hipStream_t s) {
+  ProductArgs p;
+  p.a = static_cast<const char*>(a);
+  p.w = static_cast<const char*>(w);
+  p.c = static_cast<char*>(c);
+  p.offsets = offsets;
+  p.perm = perm;
+  p.k = k;
+  p.a_rows = a_rows;
+  p.M = M;
+  p.G = G;
+  p.red = red;
+  p.cols = cols;
+  p.tiles_n = 0;
+  if (dt == BMOE_BF16)
+    return back ? launch_grouped_type<kBf16, kRedRows>(p, s)
+                : launch_grouped_type<kBf16, kOutRows>(p, s);
+  return back ? launch_grouped_type<kF32, kRedRows>(p, s)
+              : launch_grouped_type<kF32, kOutRows>(p, s);
+}
+
+hipError_t launch_grouped_dw(bmoe_dtype dt, int M, int O, int K, int G, const void* a,
+                             const int32_t* perm, int k, int a_rows, const void* dc,
+                             const int32_t* offsets, float* dw, hipStream_t s) {
+  DwArgs p;
+  p.a = static_cast<const char*>(a);
+  p.dc = static_cast<const char*>(dc);
+  p.dw = dw;
+  p.offsets = offsets;
+  p.perm = perm;
+  p.k = k;
+  p.a_rows = a_rows;
+  p.M = M;
+  p.G = G;
+  p.O = O;
+  p.K = K;
+  p.tiles_o = p.tiles_k = 0;
+  return dt == BMOE_BF16 ? launch_dw_type<kBf16>(p, s) : launch_dw_type<kF32>(p, s);
+}
+
+}  // namespace bmoe

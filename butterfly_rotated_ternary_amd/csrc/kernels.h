@@ -317,4 +317,59 @@ hipError_t launch_grad_norm(const double* part, int n_part, float* norm, hipStre
 hipError_t launch_grad_scale(const GradTable& tab, const double* part, int n_part, float* norm,
                              float max_norm, int in_place, hipStream_t s);
 
+// ---- dense experts -----------------------------------------------------------------
+// Stable grouping of the M ids by expert: offsets [N + 1], perm [M], inv [M]
+// (-1 for an id outside [0, N), which go behind the last expert). count:
+// scratch of group_count_bytes(M, N).
+size_t group_count_bytes(int M, int N);
+hipError_t launch_group_rows(const int32_t* ids, int M, int N, int32_t* offsets, int32_t* perm,
+                             int32_t* inv, int* count, hipStream_t s);
+// Group e = rows offsets[e] .. offsets[e + 1] of M. back = false: c[q] [cols] =
+// w_e [cols][red] a[row(q)]; back = true: c[q] = w_e^T a[q] with w_e [red][cols].
+// row(q) = perm[q] / k within [0, a_rows), or q with perm NULL.
+hipError_t launch_grouped(bmoe_dtype dt, bool back, int M, int red, int cols, int G, const void* a,
+                          const int32_t* perm, int k, int a_rows, const void* w,
+                          const int32_t* offsets, void* c, hipStream_t s);
+// dw [G][O][K] = sums over the groups' rows of dc[q] a[row(q)]^T.
+hipError_t launch_grouped_dw(bmoe_dtype dt, int M, int O, int K, int G, const void* a,
+                             const int32_t* perm, int k, int a_rows, const void* dc,
+                             const int32_t* offsets, float* dw, hipStream_t s);
+
+// ---- orthogonalised updates ----------------------------------------------------------
+struct OrthoCall {
+  int batch, rows, cols, steps;
+  float a, b, c, eps;
+  const void* u;    // gradient
+  int u_bf16;
+  float* momentum;  // NULL: u is orthogonalised; else momentum = beta momentum + u is (with
+  float beta;       // nesterov u + beta momentum)
+  int nesterov;
+  void* o;          // result, or (update) o = keep o - rate * result
+  int o_bf16, update;
+  float keep, rate;
+};
+size_t ortho_workspace_bytes(int batch, int rows, int cols);
+hipError_t launch_ortho(const OrthoCall& call, void* ws, hipStream_t s);
+
+// ---- norms around a block ----------------------------------------------------------
+struct NormCall {
+  int T, d, k;
+  long long M;  // rows of u
+  float eps, res_scale, out_scale;
+  const void* u;       // [M][d] or NULL
+  const int32_t* inv;  // [T][k] or NULL
+  const float* gates;  // [T][k] or NULL
+  const float *w_post, *w_pre;
+  // forward
+  const void* r;  // [T][d] or NULL
+  void *r_out, *n;
+  // backward
+  const void *x, *dr_out, *dn;  // x: the forward's r_out
+  void *du, *dr;
+  float *dgates, *dw_post, *dw_pre;
+};
+hipError_t launch_norm(bmoe_dtype dt, const NormCall& c, hipStream_t s);
+size_t norm_part_bytes(int T, int d);
+hipError_t launch_norm_bwd(bmoe_dtype dt, const NormCall& c, float* part, hipStream_t s);
+
 }  // namespace bmoe

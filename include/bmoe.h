@@ -547,6 +547,162 @@ bmoe_status bmoe_grad_scale(int n, const bmoe_tensor* grads, const bmoe_tensor* 
 bmoe_status bmoe_grad_clip(int n, const bmoe_tensor* grads, const bmoe_tensor* out, float max_norm,
                            float* norm, void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * Dense experts: the routed rows grouped by expert, and the products of each
+ * group's rows with that expert's own weights (beside the butterfly experts,
+ * whose W_e is never formed).
+ *
+ * bmoe_group_rows: a stable grouping of the routed rows r = t*k + j of
+ * ids [T][k] by expert.
+ *   offsets  int32 [N+1]: expert e has the slots offsets[e] .. offsets[e+1].
+ *   perm     int32 [T*k]: slot -> r, ascending r within an expert. An id
+ *            outside [0, N) is a padded pick: these take the slots from
+ *            offsets[N] on, in order of r.
+ *   inv      int32 [T*k]: r -> slot, -1 for a padded pick.
+ * T = 0 sets offsets to 0. N and T*k as bmoe_route, k >= 1. ws: at least
+ * bmoe_group_rows_workspace_bytes().
+ */
+size_t bmoe_group_rows_workspace_bytes(int T, int n_experts, int k);
+bmoe_status bmoe_group_rows(int T, int n_experts, int k, const int32_t* ids, int32_t* offsets,
+                            int32_t* perm, int32_t* inv, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * c[q] = W_e a[row(q)] for the rows q in [offsets[e], offsets[e+1]) of each of
+ * n_groups groups e; row(q) = perm[q] / k, or q with perm NULL.
+ *   dt       element type of a, w and c (bf16: bf16 MFMA with fp32 sums, rounded
+ *            once; fp32: fp32 MFMA).
+ *   a        [a_rows][K] (perm NULL: [M][K], a_rows unused): with bmoe_group_rows'
+ *            perm and its k, the tokens themselves.
+ *   w        [n_groups][O][K], row o = output.
+ *   offsets  int32 [n_groups+1] on the device, ascending, within [0, M].
+ *   c        [M][O]. Rows that belong to no group (behind the last one, or
+ *            before the first) are left as they were.
+ * 1 <= K, O <= 65536, any lengths (rows that are whole multiples of 16 bytes
+ * are faster), 1 <= n_groups <= 4096. M = 0 is a no-op. Entries of offsets
+ * outside [0, M] and of perm outside [0, a_rows * k) are clamped for
+ * addressing; what such rows hold is unspecified.
+ */
+bmoe_status bmoe_grouped_product(bmoe_dtype dt, int M, int K, int O, int n_groups, const void* a,
+                                 int a_rows, const int32_t* perm, int k, const void* w,
+                                 const int32_t* offsets, void* c, void* stream);
+
+/*
+ * Gradients of bmoe_grouped_product for dc [M][O] = dL/dc:
+ *   da  [M][K], dtype dt, or NULL: da[q] = W_e^T dc[q], one row per row of the
+ *       product (a token's k rows are summed by bmoe_residual_norm, with inv and
+ *       without gates, or a w_post). Rows of no group are left as they were.
+ *   dw  fp32 [n_groups][O][K] or NULL: the sum over the group's rows of
+ *       dc[q] a[row(q)]^T, the same bits each run; 0 for a group without rows.
+ * The other arguments as there. w is read for da, a and perm for dw. M = 0
+ * sets dw to 0. ws: at least bmoe_grouped_product_backward_workspace_bytes().
+ */
+size_t bmoe_grouped_product_backward_workspace_bytes(bmoe_dtype dt, int M, int K, int O,
+                                                     int n_groups);
+bmoe_status bmoe_grouped_product_backward(bmoe_dtype dt, int M, int K, int O, int n_groups,
+                                          const void* a, int a_rows, const int32_t* perm, int k,
+                                          const void* w, const int32_t* offsets, const void* dc,
+                                          void* da, float* dw, void* ws, size_t ws_bytes,
+                                          void* stream);
+
+/*
+ * Norms around a block, fused with the sum of a token's expert rows, its gates
+ * and its scaled residual. For token t:
+ *   y  = sum over j < k of g_tj u[row(t, j)]       (ascending j)
+ *   z  = y / sqrt(mean(y^2) + eps) * w_post         (w_post NULL: z = y)
+ *   r' = res_scale * r + out_scale * z
+ *   n  = r' / sqrt(mean(r'^2) + eps) * w_pre
+ * all in fp32; r' and n are rounded once each (n is that of r' before rounding).
+ *   u      [u_rows][d], dtype dt: expert rows (of bmoe_grouped_product), or the
+ *          layer's output y of bmoe_forward (k = 1, no inv, no gates), or NULL: no
+ *          block before this norm, r' = res_scale * r.
+ *   inv    int32 [T][k] of bmoe_group_rows: row(t, j) = inv[t][j]; NULL: t*k + j
+ *          (u_rows >= T*k). A row outside [0, u_rows) contributes nothing.
+ *   gates  fp32 [T][k], NULL: 1.
+ *   r      [T][d] or NULL (0).
+ *   w_post, w_pre  fp32 [d]; NULL: no such norm (w_pre NULL: no n).
+ *   r_out  [T][d]: r'. May be r. May be NULL where u is.
+ *   n      [T][d].
+ * 1 <= d <= 8192, any length, 1 <= k <= 64. spec: eps >= 0, finite scales
+ * (BMOE_E_VALUE). Outputs share no memory with each other or with what is read,
+ * r aside (BMOE_E_VALUE). T = 0 is a no-op.
+ */
+typedef struct {
+  float eps, res_scale, out_scale;
+} bmoe_norm_spec;
+bmoe_status bmoe_residual_norm(bmoe_dtype dt, int T, int d, int k, const bmoe_norm_spec* spec,
+                               const void* u, int u_rows, const int32_t* inv, const float* gates,
+                               const void* r, const float* w_post, const float* w_pre, void* r_out,
+                               void* n, void* stream);
+
+/*
+ * Gradients of bmoe_residual_norm, from dr_out = dL/dr' [T][d] (NULL: 0; needed
+ * without w_pre) and dn = dL/dn (with w_pre only). r_out is the forward's r' as
+ * stored; the other inputs are the forward's.
+ *   du      [u_rows][d] or NULL: rows that no pick names are left as they were;
+ *           inv's rows have to be distinct (else such a row holds one of its
+ *           picks' gradients).
+ *   dgates  fp32 [T][k] or NULL (0 for a pick that contributes nothing).
+ *   dr      [T][d] or NULL; may be dr_out.
+ *   dw_post, dw_pre  fp32 [d] or NULL: sums over the tokens, the same bits each
+ *           run. T = 0 sets them to 0.
+ * Asking for a gradient of an input that is NULL is BMOE_E_NULL. ws: at least
+ * bmoe_residual_norm_backward_workspace_bytes().
+ */
+size_t bmoe_residual_norm_backward_workspace_bytes(bmoe_dtype dt, int T, int d);
+bmoe_status bmoe_residual_norm_backward(bmoe_dtype dt, int T, int d, int k,
+                                        const bmoe_norm_spec* spec, const void* u, int u_rows,
+                                        const int32_t* inv, const float* gates, const void* r_out,
+                                        const float* w_post, const float* w_pre,
+                                        const void* dr_out, const void* dn, void* du,
+                                        float* dgates, void* dr, float* dw_post, float* dw_pre,
+                                        void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Orthogonalisation of a gradient by Newton-Schulz products, for `batch`
+ * matrices [rows][cols] (a layer's dw, the router's, dense experts' [N][O][K]):
+ *   X = U / (|U|_F + eps); `steps` times: P = X X^T, X = (a I + b P + c P P) X
+ * (P = X^T X from the other side where rows > cols). It keeps U's singular
+ * vectors and moves the singular values towards 1; with a = 3.4445, b = -4.7750,
+ * c = 2.0315 and 5 steps into about [0.7, 1.2], but for very small ones.
+ * Products are taken with 22-bit operands and fp32 sums for either type; bf16
+ * results are rounded once. A zero matrix gives zeros (with eps = 0: NaN), one
+ * with a NaN or an infinity gives NaN throughout.
+ *   u, o  [batch][rows][cols], dtype dt; o may be u.
+ * 1 <= rows, cols <= 16384, 0 <= batch <= 65535 (0: a no-op). spec: 1 to 64
+ * steps, eps >= 0, and coefficients under which no singular value that starts
+ * within [0, 1] passes the range of the products (sigma^2 and |a + b sigma^2 + c
+ * sigma^4| at most 15 in every step; BMOE_E_VALUE). ws: at least
+ * bmoe_orthogonalize_workspace_bytes().
+ */
+typedef struct {
+  int steps;
+  float a, b, c, eps;
+} bmoe_ortho_spec;
+size_t bmoe_orthogonalize_workspace_bytes(int batch, int rows, int cols);
+bmoe_status bmoe_orthogonalize(bmoe_dtype dt, int batch, int rows, int cols,
+                               const bmoe_ortho_spec* spec, const void* u, void* o, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/*
+ * One step of weights by the orthogonalised momentum of their gradient:
+ *   momentum = beta * momentum + grad
+ *   U = grad + beta * momentum (nesterov) or momentum
+ *   w = (1 - lr * weight_decay) * w - lr * scale * X(U)
+ * with X of bmoe_orthogonalize, each matrix by itself. momentum fp32, w of type
+ * w_dt (bf16: rounded once), both [batch][rows][cols] and updated in place; grad
+ * of type grad_dt (bmoe_grad_clip's output). update: 0 <= beta < 1, the others
+ * finite (BMOE_E_VALUE). Shapes, spec and ws as bmoe_orthogonalize.
+ */
+typedef struct {
+  float lr, beta;
+  int nesterov;
+  float weight_decay, scale;
+} bmoe_ortho_update;
+bmoe_status bmoe_orthogonal_step(bmoe_dtype w_dt, bmoe_dtype grad_dt, int batch, int rows, int cols,
+                                 const bmoe_ortho_spec* spec, const bmoe_ortho_update* update,
+                                 const void* grad, float* momentum, void* w, void* ws,
+                                 size_t ws_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* bmoe_status_str(bmoe_status s);
 

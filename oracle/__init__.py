@@ -14,3 +14,5 @@ from .bmoe_pack3 import pack_ternary_b3, packed3_bytes, unpack_ternary_b3  # noq
 from .bmoe_outliers import crest_factor, quant_error, rotate_in  # noqa: F401
 from .bmoe_route import (clip_grads, grad_norm, route_balance, route_logits,  # noqa: F401
                          route_logits_backward, router_backward, scores)
+from .bmoe_block import (group_rows, grouped_product, grouped_product_backward,  # noqa: F401
+                         newton_schulz, residual_norm, residual_norm_backward)
