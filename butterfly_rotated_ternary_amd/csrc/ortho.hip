@@ -15,6 +15,9 @@
 //
 // P and Q are symmetric: only tiles on and below the diagonal are computed,
 // each written twice. Rows are padded to whole 16-byte chunks (zeros).
+#include <type_traits>
+#include <utility>
+
 #include "common.h"
 #include "kernels.h"
 #include "tile_product.h"
@@ -57,20 +60,58 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
   return s;
 }
 
-__global__ __launch_bounds__(kSumThreads) void ortho_sum_kernel(Source src, size_t count,
+// Eight consecutive entries of U from i on, the momentum's step included (STEP).
+template <bool STEP>
+__device__ __forceinline__ void load8(const Source& s, size_t i, float (&v)[8]) {
+  if (s.bf16) {
+    load16(static_cast<const uint16_t*>(s.u) + i, v);
+  } else {
+    load16(static_cast<const float*>(s.u) + i, v);
+    load16(static_cast<const float*>(s.u) + i + 4, v + 4);
+  }
+  if (!s.momentum) return;
+  float m[8];
+  load16(s.momentum + i, m);
+  load16(s.momentum + i + 4, m + 4);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (STEP) m[e] = fmaf(s.beta, m[e], v[e]);
+    v[e] = mixed(s, v[e], m[e]);
+  }
+  if (STEP) {
+    store16(m, s.momentum + i, 1.f);
+    store16(m + 4, s.momentum + i + 4, 1.f);
+  }
+}
+template <bool STEP>
+__device__ __forceinline__ float load1(const Source& s, size_t i) {
+  const float u = load_any(s.u, s.bf16, i);
+  if (!s.momentum) return u;
+  float m = s.momentum[i];
+  if (STEP) s.momentum[i] = m = fmaf(s.beta, m, u);
+  return mixed(s, u, m);
+}
+
+// whole: matrices of whole chunks of eight.
+__global__ __launch_bounds__(kSumThreads) void ortho_sum_kernel(Source src, size_t count, int whole,
                                                                 double* part) {
   __shared__ double lds[kSumThreads / 64];
-  const size_t first = (size_t)blockIdx.y * count;
+  const size_t first = (size_t)blockIdx.y * count, stride = (size_t)gridDim.x * kSumThreads;
+  const size_t i0 = (size_t)blockIdx.x * kSumThreads + threadIdx.x;
   double acc = 0.0;
-  for (size_t i = (size_t)blockIdx.x * kSumThreads + threadIdx.x; i < count;
-       i += (size_t)gridDim.x * kSumThreads) {
-    float u = load_any(src.u, src.bf16, first + i);
-    if (src.momentum) {
-      const float m = fmaf(src.beta, src.momentum[first + i], u);
-      src.momentum[first + i] = m;
-      u = mixed(src, u, m);
+  if (whole) {
+#pragma unroll 2
+    for (size_t i = i0; i < count / 8; i += stride) {
+      float v[8];
+      load8<true>(src, first + 8 * i, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc = fma((double)v[e], (double)v[e], acc);
     }
-    acc = fma((double)u, (double)u, acc);
+  } else {
+    for (size_t i = i0; i < count; i += stride) {
+      const float v = load1<true>(src, first + i);
+      acc = fma((double)v, (double)v, acc);
+    }
   }
   const double s = block_sum(acc, lds);
   if (threadIdx.x == 0) part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
@@ -93,19 +134,30 @@ __global__ __launch_bounds__(kSumThreads) void ortho_split_kernel(Source src, in
   for (int i = threadIdx.x; i < parts; i += kSumThreads) acc += mine[i];
   const float norm = (float)sqrt(block_sum(acc, lds)) + eps;
   const size_t in0 = (size_t)blockIdx.y * rows * cols, out0 = (size_t)blockIdx.y * rows * ld;
-  const size_t n = (size_t)rows * ld;
+  const int chunks = ld / 8;
+  const size_t n = (size_t)rows * chunks;
   for (size_t i = (size_t)blockIdx.x * kSumThreads + threadIdx.x; i < n;
        i += (size_t)gridDim.x * kSumThreads) {
-    const size_t row = i / ld;
-    const int col = (int)(i % ld);
-    float v = 0.f;
-    if (col < cols) {
-      const size_t at = in0 + row * cols + col;
-      v = load_any(src.u, src.bf16, at);
-      if (src.momentum) v = mixed(src, v, src.momentum[at]);
-      v = v / norm * kScale;
+    const size_t row = i / chunks;
+    const int col = (int)(i - row * chunks) * 8;
+    float v[8];
+    if (cols == ld) {
+      load8<false>(src, in0 + 8 * i, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        v[e] = col + e < cols ? load1<false>(src, in0 + row * cols + col + e) : 0.f;
     }
-    split(v, hi[out0 + i], lo[out0 + i]);
+    f16x8 h, l;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      _Float16 a, b;
+      split(v[e] / norm * kScale, a, b);
+      h[e] = a;
+      l[e] = b;
+    }
+    *reinterpret_cast<f16x8*>(hi + out0 + 8 * i) = h;
+    *reinterpret_cast<f16x8*>(lo + out0 + 8 * i) = l;
   }
 }
 
@@ -119,12 +171,134 @@ struct OrthoArgs {
   size_t out_part;        // elements
   int rows, cols, ld, m, ldm;  // of X; of P and Q
   int batch, tiles, tiles_n;  // tiles per matrix
+  int run_items;
   float a, b, c;          // kPoly
   // the last product's epilogue
   void* o;                // [batch][rows][cols]: X, or w = keep w - rate X
   int o_bf16, update;
   float keep, rate;
 };
+
+// A 32 x 32 block of accumulators through LDS, so that a lane gets sixteen
+// neighbours of a row, or of a column, and memory is read and written 16 bytes a
+// lane. One wave's own LDS; its operations are in order.
+struct Block {
+  static constexpr int PITCH = 36;  // floats: rows stay 16-byte aligned, banks spread
+  static constexpr int BYTES = 32 * PITCH * 4;
+  __device__ __forceinline__ static void order() {
+    __builtin_amdgcn_wave_barrier();
+    __asm__ volatile("" ::: "memory");
+  }
+  __device__ __forceinline__ void stage(float* s, const f32x16& acc, int lane) const {
+    order();  // the last block has been read
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[acc_row(r, lane) * PITCH + acc_col(lane)] = acc[r];
+    order();
+  }
+  __device__ __forceinline__ void row(const float* s, int lane, float (&v)[16]) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) load16(s + lane / 2 * PITCH + 16 * (lane & 1) + 4 * e, v + 4 * e);
+  }
+  __device__ __forceinline__ void put_row(float* s, int lane, const float (&v)[16]) const {
+    order();
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      store16(v + 4 * e, s + lane / 2 * PITCH + 16 * (lane & 1) + 4 * e, 1.f);
+    order();
+  }
+  __device__ __forceinline__ void column(const float* s, int lane, float (&v)[16]) const {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = s[(16 * (lane & 1) + e) * PITCH + lane / 2];
+  }
+};
+
+// v, sixteen entries of a row of P P times kScale, to those of Q.
+__device__ __forceinline__ void add_poly(const OrthoArgs& p, const char* q, int row, int col,
+                                         float (&v)[16]) {
+  const _Float16* hi = reinterpret_cast<const _Float16*>(q) + (size_t)row * p.ldm + col;
+  const _Float16* lo = reinterpret_cast<const _Float16*>(
+      reinterpret_cast<const char*>(hi) + p.q_part);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    f16x8 a = {}, b = {};
+    if (row < p.m && col + 8 * h < p.ldm) {
+      a = *reinterpret_cast<const f16x8*>(hi + 8 * h);
+      b = *reinterpret_cast<const f16x8*>(lo + 8 * h);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float pv = (float)a[e] + (float)b[e];
+      v[8 * h + e] = fmaf(p.c, v[8 * h + e], p.b * pv);
+      if (row == col + 8 * h + e) v[8 * h + e] += p.a * kScale;
+    }
+  }
+}
+
+// Sixteen entries of a row of an operand [rows][ld], cols of them values, the
+// rest zeros.
+__device__ __forceinline__ void store_parts(const OrthoArgs& p, int batch, int rows, int cols,
+                                            int ld, int row, int col, const float (&v)[16]) {
+  if (row >= rows) return;
+  _Float16* hi = p.out + ((size_t)batch * rows + row) * ld + col;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (col + 8 * h >= ld) continue;
+    f16x8 a, b;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      _Float16 x, y;
+      split(col + 8 * h + e < cols ? v[8 * h + e] : 0.f, x, y);
+      a[e] = x;
+      b[e] = y;
+    }
+    *reinterpret_cast<f16x8*>(hi + 8 * h) = a;
+    *reinterpret_cast<f16x8*>(hi + p.out_part + 8 * h) = b;
+  }
+}
+
+// Sixteen entries of the last iterate (times kScale) to the result or the weights.
+__device__ __forceinline__ void store_result(const OrthoArgs& p, int batch, int row, int col,
+                                             const float (&v)[16]) {
+  if (row >= p.rows) return;
+  const size_t at = ((size_t)batch * p.rows + row) * p.cols + col;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int n = p.cols - col - 8 * h;
+    if (n <= 0) continue;
+    float o[8];
+    if (p.cols % 8 == 0) {
+      if (p.update) {
+        if (p.o_bf16) {
+          load16(static_cast<const uint16_t*>(p.o) + at + 8 * h, o);
+        } else {
+          load16(static_cast<const float*>(p.o) + at + 8 * h, o);
+          load16(static_cast<const float*>(p.o) + at + 8 * h + 4, o + 4);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = v[8 * h + e] * (1.f / kScale);
+        o[e] = p.update ? fmaf(p.keep, o[e], -p.rate * x) : x;
+      }
+      if (p.o_bf16) {
+        store16(o, static_cast<uint16_t*>(p.o) + at + 8 * h, 1.f);
+      } else {
+        store16(o, static_cast<float*>(p.o) + at + 8 * h, 1.f);
+        store16(o + 4, static_cast<float*>(p.o) + at + 8 * h + 4, 1.f);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (e >= n) continue;
+        float x = v[8 * h + e] * (1.f / kScale);
+        const size_t i = at + 8 * h + e;
+        if (p.update) x = fmaf(p.keep, load_any(p.o, p.o_bf16, i), -p.rate * x);
+        if (p.o_bf16) static_cast<uint16_t*>(p.o)[i] = (uint16_t)f32_to_bf16_bits(x);
+        else static_cast<float*>(p.o)[i] = x;
+      }
+    }
+  }
+}
 
 __device__ __forceinline__ int2 triangle(int t) {
   int i = (int)((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);
@@ -137,16 +311,26 @@ template <class C, int PRODUCT, bool TALL>
 __global__ __launch_bounds__(C::THREADS) void ortho_product_kernel(OrthoArgs p) {
   __shared__ __attribute__((aligned(1024))) char st0[C::STAGE];
   __shared__ __attribute__((aligned(1024))) char st1[C::STAGE];
-  static_assert(C::NSTAGE == 2, "two stages");
-  char* ring[2] = {st0, st1};
+  __shared__ __attribute__((aligned(1024))) char st2[C::NSTAGE > 2 ? C::STAGE : 16];
+  static_assert(C::NSTAGE <= 3, "three stages");
+  char* all[3] = {st0, st1, st2};
+  char* ring[C::NSTAGE];
+#pragma unroll
+  for (int i = 0; i < C::NSTAGE; ++i) ring[i] = all[i];
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave / C::WN, wn = wave % C::WN;
-  const int batch = grid_block() / p.tiles, t = grid_block() % p.tiles;
+  const unsigned item = xcd_item(grid_block(), p.run_items);
+  const int batch = item / p.tiles, t = item % p.tiles;
   if (batch >= p.batch) return;
-  int2 tile;
-  if constexpr (PRODUCT == kApply) tile = make_int2(t / p.tiles_n, t % p.tiles_n);
-  else tile = triangle(t);
+  int2 tile;  // panels of four rows of tiles; of a symmetric matrix, rows of tiles
+  if constexpr (PRODUCT == kApply) {
+    const int panel = t / (4 * p.tiles_n), j = t - panel * 4 * p.tiles_n;
+    const int high = min(4, p.tiles / p.tiles_n - 4 * panel);
+    tile = make_int2(4 * panel + j % high, j / high);
+  } else {
+    tile = triangle(t);
+  }
   const int r0 = tile.x * C::BM, c0 = tile.y * C::BN;
   const char* x = reinterpret_cast<const char*>(p.x) + (size_t)batch * p.rows * p.ld * 2;
   const char* q = reinterpret_cast<const char*>(p.q) + (size_t)batch * p.m * p.ldm * 2;
@@ -158,124 +342,126 @@ __global__ __launch_bounds__(C::THREADS) void ortho_product_kernel(OrthoArgs p) 
   ra.init(wm * C::TM, lane);
   Reader<C, C::BMODE, C::BN, C::FN> rb;
   rb.init(wn * C::TN, lane);
-  // chunks of a row beyond its values are zeros in memory up to ld (ldm)
-  if constexpr (PRODUCT == kGram && TALL) {  // X^T X: down the rows of X
+  // Chunks of a row beyond its values are zeros in memory, up to ld (ldm). P and
+  // Q are symmetric: their rows, along the reduction, serve as rows and columns.
+  const int red = PRODUCT == kGram && !TALL ? p.ld : PRODUCT == kGram ? p.rows : p.m;
+  const int nsteps = (red + C::BK - 1) / C::BK;
+  if constexpr (PRODUCT == kGram && !TALL) {  // X X^T
+    OutRowsSource<C, C::BM, C::A_LOADS> a;
+    a.init(
+        x + r0 * x_ld, [&](int r) { return (uint32_t)(min(r, p.m - 1 - r0) * x_ld); }, red, p.x_part,
+        lane, wave);
+    OutRowsSource<C, C::BN, C::B_LOADS> b;
+    b.init(
+        x + c0 * x_ld, [&](int r) { return (uint32_t)(min(r, p.m - 1 - c0) * x_ld); }, red, p.x_part,
+        lane, wave);
+    run<C>(acc, ring, a, b, ra, rb, nsteps, lane, wave);
+  } else if constexpr (PRODUCT == kApply && TALL) {  // X Q
+    OutRowsSource<C, C::BM, C::A_LOADS> a;
+    a.init(
+        x + r0 * x_ld, [&](int r) { return (uint32_t)(min(r, p.rows - 1 - r0) * x_ld); }, red,
+        p.x_part, lane, wave);
+    RedRowsSource<C, C::BN, C::B_LOADS, SameRow> b;
+    b.init(q, q_ld, c0, p.ldm, red, p.q_part, SameRow{}, lane, wave);
+    run<C>(acc, ring, a, b, ra, rb, nsteps, lane, wave);
+  } else {  // X^T X, P P, Q X
+    const bool xa = PRODUCT == kGram, xb = PRODUCT != kPoly;
     RedRowsSource<C, C::BM, C::A_LOADS, SameRow> a;
-    a.init(x, x_ld, r0, p.ld, p.rows, p.x_part, SameRow{}, lane, wave);
+    a.init(xa ? x : q, xa ? x_ld : q_ld, r0, xa ? p.ld : p.ldm, red, xa ? p.x_part : p.q_part,
+           SameRow{}, lane, wave);
     RedRowsSource<C, C::BN, C::B_LOADS, SameRow> b;
-    b.init(x, x_ld, c0, p.ld, p.rows, p.x_part, SameRow{}, lane, wave);
-    run<C>(acc, ring, a, b, ra, rb, (p.rows + C::BK - 1) / C::BK, lane, wave);
-  } else if constexpr (PRODUCT == kGram || PRODUCT == kPoly) {  // X X^T, P P = P P^T
-    const char* src = PRODUCT == kGram ? x : q;
-    const size_t ld = PRODUCT == kGram ? x_ld : q_ld;
-    const int red = PRODUCT == kGram ? p.ld : p.ldm;
-    const size_t part = PRODUCT == kGram ? p.x_part : p.q_part;
-    OutRowsSource<C, C::BM, C::A_LOADS> a;
-    a.init([&](int r) { return src + (size_t)min(r0 + r, p.m - 1) * ld; }, red, part, lane, wave);
-    OutRowsSource<C, C::BN, C::B_LOADS> b;
-    b.init([&](int r) { return src + (size_t)min(c0 + r, p.m - 1) * ld; }, red, part, lane, wave);
-    run<C>(acc, ring, a, b, ra, rb, (red + C::BK - 1) / C::BK, lane, wave);
-  } else if constexpr (TALL) {  // X Q: Q symmetric, its rows serve as columns
-    OutRowsSource<C, C::BM, C::A_LOADS> a;
-    a.init([&](int r) { return x + (size_t)min(r0 + r, p.rows - 1) * x_ld; }, p.ldm, p.x_part, lane,
-           wave);
-    OutRowsSource<C, C::BN, C::B_LOADS> b;
-    b.init([&](int r) { return q + (size_t)min(c0 + r, p.m - 1) * q_ld; }, p.ldm, p.q_part, lane,
-           wave);
-    run<C>(acc, ring, a, b, ra, rb, (p.ldm + C::BK - 1) / C::BK, lane, wave);
-  } else {  // Q X
-    OutRowsSource<C, C::BM, C::A_LOADS> a;
-    a.init([&](int r) { return q + (size_t)min(r0 + r, p.m - 1) * q_ld; }, p.m, p.q_part, lane,
-           wave);
-    RedRowsSource<C, C::BN, C::B_LOADS, SameRow> b;
-    b.init(x, x_ld, c0, p.ld, p.m, p.x_part, SameRow{}, lane, wave);
-    run<C>(acc, ring, a, b, ra, rb, (p.m + C::BK - 1) / C::BK, lane, wave);
+    b.init(xb ? x : q, xb ? x_ld : q_ld, c0, xb ? p.ld : p.ldm, red, xb ? p.x_part : p.q_part,
+           SameRow{}, lane, wave);
+    run<C>(acc, ring, a, b, ra, rb, nsteps, lane, wave);
   }
 
-  const int out_rows = PRODUCT == kApply ? p.rows : p.m;
-  const int out_cols = PRODUCT == kApply ? p.cols : p.m;
-  const int out_ld = PRODUCT == kApply ? p.ld : p.ldm;
-  _Float16* hi = p.out + (size_t)batch * out_rows * out_ld;
-  _Float16* lo = hi + p.out_part;
-  const _Float16* ph = reinterpret_cast<const _Float16*>(q);
-  const _Float16* pl = reinterpret_cast<const _Float16*>(q + p.q_part);
+  lds_barrier();  // every wave is done with the ring
+  static_assert(C::WAVES * Block::BYTES <= C::STAGE, "staging fits a stage");
+  float* stg = reinterpret_cast<float*>(st0) + wave * (Block::BYTES / 4);
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) {
-      const int col = c0 + wn * C::TN + 32 * j + acc_col(lane);
+      Block b;
+      b.stage(stg, acc[i][j], lane);
+      const int row0 = r0 + wm * C::TM + 32 * i, col0 = c0 + wn * C::TN + 32 * j;
+      const int row = row0 + lane / 2, col = col0 + 16 * (lane & 1);
+      float v[16];
+      b.row(stg, lane, v);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int row = r0 + wm * C::TM + 32 * i + acc_row(4 * g, lane);  // and three more
-        float v[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = acc[i][j][4 * g + u] * (1.f / kScale);
-        if constexpr (PRODUCT == kPoly) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            float pv = 0.f;
-            if (row + u < p.m && col < p.m) {
-              const size_t at = (size_t)(row + u) * p.ldm + col;
-              pv = (float)ph[at] + (float)pl[at];
-            }
-            v[u] = fmaf(p.c, v[u], p.b * pv) + (row + u == col ? p.a * kScale : 0.f);
-          }
+      for (int e = 0; e < 16; ++e) v[e] *= 1.f / kScale;
+      if constexpr (PRODUCT == kPoly) add_poly(p, q, row, col, v);
+      if constexpr (PRODUCT == kApply) {
+        if (p.o) {
+          store_result(p, batch, row, col, v);
+        } else {
+          store_parts(p, batch, p.rows, p.cols, p.ld, row, col, v);
         }
-        if (PRODUCT == kApply && p.o) {
+      } else {
+        store_parts(p, batch, p.m, p.m, p.ldm, row, col, v);
+        if (tile.x != tile.y) {  // the mirrored block
+          if constexpr (PRODUCT == kPoly) b.put_row(stg, lane, v);
+          b.column(stg, lane, v);
+          if constexpr (PRODUCT == kGram) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            if (row + u >= out_rows || col >= out_cols) continue;
-            const size_t at = ((size_t)batch * out_rows + row + u) * out_cols + col;
-            float o = v[u] * (1.f / kScale);
-            if (p.update) o = fmaf(p.keep, load_any(p.o, p.o_bf16, at), -p.rate * o);
-            if (p.o_bf16) static_cast<uint16_t*>(p.o)[at] = (uint16_t)f32_to_bf16_bits(o);
-            else static_cast<float*>(p.o)[at] = o;
+            for (int e = 0; e < 16; ++e) v[e] *= 1.f / kScale;
           }
-          continue;
-        }
-        _Float16 h[4], l[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          split(col < out_cols ? v[u] : 0.f, h[u], l[u]);
-          if (row + u < out_rows && col < out_ld) {
-            const size_t at = (size_t)(row + u) * out_ld + col;
-            hi[at] = h[u];
-            lo[at] = l[u];
-          }
-        }
-        if constexpr (PRODUCT != kApply) {
-          // the mirrored tile: four consecutive columns of row `col`. (out_ld is
-          // a multiple of 4, so four from a multiple of 4 are in or out whole;
-          // their values past out_rows are the padding's zeros.)
-          if (tile.x != tile.y && col < out_cols && row < out_ld) {
-            typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-            f16x4 hv, lv;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              hv[u] = row + u < out_rows ? h[u] : (_Float16)0.f;
-              lv[u] = row + u < out_rows ? l[u] : (_Float16)0.f;
-            }
-            const size_t at = (size_t)col * out_ld + row;
-            *reinterpret_cast<f16x4*>(hi + at) = hv;
-            *reinterpret_cast<f16x4*>(lo + at) = lv;
-          }
+          store_parts(p, batch, p.m, p.m, p.ldm, col0 + lane / 2, row0 + 16 * (lane & 1), v);
         }
       }
     }
 }
 
-template <int AMODE, int BMODE>
-using Tile = Cfg<kF16, 2, 128, 128, 2, 2, 2, AMODE, BMODE, true>;
+// Tiles of 128 (four waves, two workgroups per CU), 192 (four waves of 96) and
+// 256 (eight waves of 128 x 64).
+template <int N, int AMODE, int BMODE>
+using Tile = std::conditional_t<
+    N == 256, Cfg<kF16, 2, 256, 256, 2, 4, 2, AMODE, BMODE, true>,
+    std::conditional_t<N == 192, Cfg<kF16, 2, 192, 192, 2, 2, 3, AMODE, BMODE, true>,
+                       Cfg<kF16, 2, 128, 128, 2, 2, 2, AMODE, BMODE, true>>>;
 
-template <int PRODUCT, bool TALL, int AMODE, int BMODE>
-hipError_t launch_product_cfg(OrthoArgs p, hipStream_t s) {
-  using C = Tile<AMODE, BMODE>;
-  const int tm = ((PRODUCT == kApply ? p.rows : p.m) + C::BM - 1) / C::BM;
-  p.tiles_n = ((PRODUCT == kApply ? p.cols : p.m) + C::BN - 1) / C::BN;
-  p.tiles = PRODUCT == kApply ? tm * p.tiles_n : tm * (tm + 1) / 2;
+template <int PRODUCT>
+int2 count_tiles(const OrthoArgs& p, int n) {  // of one matrix; per row of tiles
+  const int tm = ((PRODUCT == kApply ? p.rows : p.m) + n - 1) / n;
+  const int tn = ((PRODUCT == kApply ? p.cols : p.m) + n - 1) / n;
+  return make_int2(PRODUCT == kApply ? tm * tn : tm * (tm + 1) / 2, tn);
+}
+
+template <int PRODUCT, bool TALL, int N>
+hipError_t launch_tiles(OrthoArgs p, hipStream_t s) {
+  constexpr int AMODE = (PRODUCT == kGram && !TALL) || (PRODUCT == kApply && TALL) ? kOutRows
+                                                                                  : kRedRows;
+  constexpr int BMODE = PRODUCT == kGram && !TALL ? kOutRows : kRedRows;
+  using C = Tile<N, AMODE, BMODE>;
+  const int2 c = count_tiles<PRODUCT>(p, N);
+  p.tiles = c.x;
+  p.tiles_n = c.y;
+  const size_t items = (size_t)p.tiles * p.batch;
+  p.run_items = items >= 256 ? 32 : 1;
+  const size_t super = 8 * p.run_items;
   return launch_kernel(ortho_product_kernel<C, PRODUCT, TALL>,
-                       grid_rows((size_t)p.tiles * p.batch), dim3(C::THREADS), 0, s, KernelTiming{},
-                       p);
+                       grid_rows((items + super - 1) / super * super), dim3(C::THREADS), 0, s,
+                       KernelTiming{}, p);
+}
+
+// The tile by the time that the rounds of workgroups over 256 CUs take, in
+// units of a round of two workgroups per CU of 128 x 128 (one per CU: 0.55).
+// Measured at 4096 x 4096: whole products 351, 370 and 311 us, symmetric ones
+// 296, 210 and 256 us with tiles of 128, 192 and 256; 64 matrices 1024 x 512:
+// 150, 201, 136 and 111, 119, 110 us.
+template <int PRODUCT, bool TALL>
+hipError_t launch_product(const OrthoArgs& p, hipStream_t s) {
+  const auto rounds = [&](int n, long long slots) {
+    const long long t = (long long)count_tiles<PRODUCT>(p, n).x * p.batch;
+    return std::make_pair(t / slots, t % slots);
+  };
+  const auto r128 = rounds(128, 512), r192 = rounds(192, 256), r256 = rounds(256, 256);
+  const double t128 = r128.first + (r128.second > 256 ? 1.0 : r128.second > 0 ? 0.55 : 0.0);
+  const double t192 = 1.1 * (r192.first + (r192.second > 0));
+  const double t256 = 1.75 * (r256.first + (r256.second > 0));
+  if (t128 <= t192 && t128 <= t256) return launch_tiles<PRODUCT, TALL, 128>(p, s);
+  if (t192 <= t256) return launch_tiles<PRODUCT, TALL, 192>(p, s);
+  return launch_tiles<PRODUCT, TALL, 256>(p, s);
 }
 
 int padded(int n) { return (n + 7) / 8 * 8; }
@@ -320,16 +506,18 @@ hipError_t launch_ortho(const OrthoCall& call, void* ws, hipStream_t s) {
   src.nesterov = call.nesterov;
   src.bf16 = call.u_bf16;
   const size_t count = (size_t)rows * cols;
-  const size_t want = (count + 4 * kSumThreads - 1) / (4 * kSumThreads);
-  const int parts = (int)(want < kSumParts ? want : kSumParts);
+  // as many workgroups as fill the chip, at least a few rounds of entries each
+  const size_t most = batch >= 32 ? 32 : kSumParts;
+  const size_t want = (count + 16 * kSumThreads - 1) / (16 * kSumThreads);
+  const int parts = (int)(want < most ? want : most);
   hipError_t e = launch_kernel(ortho_sum_kernel, dim3(parts, batch), dim3(kSumThreads), 0, s,
-                               KernelTiming{}, src, count, part);
+                               KernelTiming{}, src, count, (int)(count % 8 == 0), part);
   if (e != hipSuccess) return e;
   _Float16* x[2] = {reinterpret_cast<_Float16*>(base + l.x0),
                     reinterpret_cast<_Float16*>(base + l.x1)};
-  const size_t padded_count = (size_t)rows * l.ld;
-  const size_t blocks = (padded_count + 4 * kSumThreads - 1) / (4 * kSumThreads);
-  e = launch_kernel(ortho_split_kernel, dim3((unsigned)(blocks < 2048 ? blocks : 2048), batch),
+  const size_t blocks = ((size_t)rows * l.ld / 8 + kSumThreads - 1) / kSumThreads;
+  const size_t enough = batch >= 32 ? 64 : 2048;
+  e = launch_kernel(ortho_split_kernel, dim3((unsigned)(blocks < enough ? blocks : enough), batch),
                     dim3(kSumThreads), 0, s, KernelTiming{}, src, rows, cols, l.ld, call.eps,
                     (const double*)part, parts, x[0], x[0] + l.x_part / 2);
   if (e != hipSuccess) return e;
@@ -360,19 +548,17 @@ hipError_t launch_ortho(const OrthoCall& call, void* ws, hipStream_t s) {
     p.q = nullptr;
     p.out = P;
     p.out_part = l.p_part / 2;
-    e = tall ? launch_product_cfg<kGram, true, kRedRows, kRedRows>(p, s)
-             : launch_product_cfg<kGram, false, kOutRows, kOutRows>(p, s);
+    e = tall ? launch_product<kGram, true>(p, s) : launch_product<kGram, false>(p, s);
     if (e != hipSuccess) return e;
     p.q = P;
     p.out = Q;
-    e = launch_product_cfg<kPoly, false, kOutRows, kOutRows>(p, s);
+    e = launch_product<kPoly, false>(p, s);
     if (e != hipSuccess) return e;
     p.q = Q;
     p.out = x[(i + 1) & 1];
     p.out_part = l.x_part / 2;
     if (i + 1 == call.steps) p.o = call.o;
-    e = tall ? launch_product_cfg<kApply, true, kOutRows, kOutRows>(p, s)
-             : launch_product_cfg<kApply, false, kOutRows, kRedRows>(p, s);
+    e = tall ? launch_product<kApply, true>(p, s) : launch_product<kApply, false>(p, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

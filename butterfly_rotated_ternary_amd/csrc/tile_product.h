@@ -33,18 +33,23 @@ enum Mode { kOutRows, kRedRows };
 // Sixteen zero bytes: the DMA source of what lies past the reduction's end.
 __device__ const uint4 kZeros = {0u, 0u, 0u, 0u};
 
+// KB: bytes of reduction per output row and K-step, 64 or 128.
 template <int E_, int PARTS_, int BM_, int BN_, int WM_, int WN_, int NSTAGE_, int AMODE_,
-          int BMODE_, bool ALIGNED_>
+          int BMODE_, bool ALIGNED_, int KB_ = 64>
 struct Cfg {
   static constexpr int E = E_, PARTS = PARTS_, BM = BM_, BN = BN_, WM = WM_, WN = WN_;
   static constexpr int NSTAGE = NSTAGE_, AHEAD = NSTAGE - 1, AMODE = AMODE_, BMODE = BMODE_;
   static constexpr bool ALIGNED = ALIGNED_;
   static constexpr int ES = E == kF32 ? 4 : 2;  // bytes per element
   static constexpr int EPC = 16 / ES;           // elements per chunk
-  static constexpr int BK = 64 / ES;            // reduction per K-step
+  static constexpr int KB = KB_, BK = KB / ES;  // reduction per K-step
+  static constexpr int SLICES = KB / 32;        // of two chunks each
   static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
   static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
-  static constexpr int A_PART = BM * 64, B_PART = BN * 64;
+  // a stage's A rows, rounded up so that every wave issues as many loads (the
+  // rows past BM repeat others)
+  static constexpr int GRAN = 1024 / KB * WAVES, AR = (BM + GRAN - 1) / GRAN * GRAN;
+  static constexpr int A_PART = AR * KB, B_PART = BN * KB;
   static constexpr int A_BYTES = PARTS * A_PART, B_BYTES = PARTS * B_PART;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int A_LOADS = A_PART / 1024 / WAVES, B_LOADS = B_PART / 1024 / WAVES;
@@ -81,64 +86,87 @@ __device__ __forceinline__ u32x4 partial_chunk(const char* p, int n) {
   return v;
 }
 
-// ---- kOutRows: LDS rows of 64 bytes -------------------------------------------
-// Four rows fill the 256 bytes of the banks once; sixteen lanes reading one
-// chunk of sixteen rows meet every bank group once with this swizzle.
-__device__ __forceinline__ int out_swz(int row, int ch) { return ch ^ ((row >> 2) & 3); }
+// ---- kOutRows: LDS rows of KB bytes -------------------------------------------
+// Four (two) rows fill the 256 bytes of the banks once; sixteen lanes reading
+// one chunk of sixteen rows meet every bank group once with this swizzle.
+template <int KB>
+__device__ __forceinline__ int out_swz(int row, int ch) {
+  return KB == 64 ? ch ^ ((row >> 2) & 3) : ch ^ ((row >> 1) & 7);
+}
 
-template <class C, int R, int LOADS>
+// Rows: SPREAD = false: row r lies r ld bytes (below 2^32 in all) behind a base
+// that is the same for the workgroup; true: anywhere.
+template <class C, int R, int LOADS, bool SPREAD = false>
 struct OutRowsSource {
-  const char* p[LOADS];  // this lane's chunk of step 0
-  int k0[LOADS];         // its first reduction index
+  const char* base;
+  uint32_t off[LOADS];                // this lane's chunk of step 0: base + off
+  const char* p[SPREAD ? LOADS : 1];  // or, for rows anywhere, its address
+  static constexpr int CH = C::KB / 16;
   int K;
-  size_t part;           // bytes between the parts
-  // row_of(r): address of the row of output row r (0 <= r < R; any valid row
-  // for those past the end, whose outputs are not stored).
+  size_t part;                        // bytes between the parts
+  // row_of(r): offset (SPREAD: address) of the row of output row r (0 <= r < R;
+  // any valid row for those past the end, whose outputs are not stored).
   template <typename F>
-  __device__ __forceinline__ void init(F row_of, int K_, size_t part_, int lane, int wave) {
+  __device__ __forceinline__ void init(const char* base_, F row_of, int K_, size_t part_, int lane,
+                                       int wave) {
+    base = base_;
     K = K_;
     part = part_;
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
       const int e = (wave * LOADS + j) * 64 + lane;
-      const int row = e >> 2, ch = out_swz(row, e & 3);
-      p[j] = row_of(row) + ch * 16;
-      k0[j] = ch * C::EPC;
+      const int row = e / CH, ch = out_swz<C::KB>(row, e % CH);
+      if constexpr (SPREAD) p[j] = row_of(row) + ch * 16;
+      else off[j] = row_of(row) + ch * 16;
     }
   }
+  // Number of steps that lie wholly before K.
+  __device__ __forceinline__ int whole_steps() const { return K / C::BK; }
+  // WHOLE: the step lies before K.
+  template <bool WHOLE>
   __device__ __forceinline__ void load(char* region, int step, int lane, int wave) const {
 #pragma unroll
-    for (int q = 0; q < C::PARTS; ++q)
+    for (int q = 0; q < C::PARTS; ++q) {
+      const char* b = base + (q * part + (size_t)step * C::KB);
 #pragma unroll
       for (int j = 0; j < LOADS; ++j) {
-        const int left = K - k0[j] - step * C::BK;
-        const char* g = p[j] + q * part + (size_t)step * 64;
-        char* dst = region + q * (R * 64) + (wave * LOADS + j) * 1024;
-        if constexpr (C::ALIGNED) {
-          dma16(left > 0 ? (const void*)g : (const void*)&kZeros, dst);
-        } else {
+        const char* g;
+        if constexpr (SPREAD) g = p[j] + (q * part + (size_t)step * C::KB);
+        else g = b + off[j];
+        char* dst = region + q * (R * C::KB) + (wave * LOADS + j) * 1024;
+        const int e = (wave * LOADS + j) * 64 + lane;
+        const int left = K - step * C::BK - out_swz<C::KB>(e / CH, e % CH) * C::EPC;
+        if constexpr (!C::ALIGNED) {
           *reinterpret_cast<u32x4*>(dst + lane * 16) = partial_chunk<C::ES>(g, left);
+        } else if constexpr (WHOLE) {
+          dma16(g, dst);
+        } else {
+          dma16(left > 0 ? (const void*)g : (const void*)&kZeros, dst);
         }
       }
+    }
   }
 };
 
 // ---- kRedRows: LDS rows of R elements -------------------------------------------
-// The four rows of a transposing read (fp32: the rows of the two lane halves)
-// land on different bank ranges.
+// The four rows of a transposing read land on different 64-byte bank ranges
+// (rows of whole 256 bytes all start on one bank, others alternate between two);
+// of fp32, the rows of the two lane halves on different 128-byte ranges.
 template <int ES, int R>
 __device__ __forceinline__ int red_swz(int r, int ch) {
   if constexpr (ES == 4) return ch ^ (((r >> 2) & 1) << 3);
-  else if constexpr (R >= 128) return ch ^ ((r & 3) << 2);
+  else if constexpr (R % 128 == 0) return ch ^ ((r & 3) << 2);
   else return ch ^ (((r >> 1) & 1) << 2);
 }
 
 // The memory row of reduction index k: k itself, or a row number that the
 // workgroup put in LDS.
 struct SameRow {
+  static constexpr bool SAME = true;
   __device__ __forceinline__ size_t operator()(int k) const { return (size_t)k; }
 };
 struct ListedRow {
+  static constexpr bool SAME = false;
   const int32_t* list;
   __device__ __forceinline__ size_t operator()(int k) const { return (size_t)list[k]; }
 };
@@ -147,62 +175,73 @@ template <class C, int R, int LOADS, class MAP>
 struct RedRowsSource {
   const char* base;
   size_t ld, part;      // bytes per row, between the parts
-  int r[LOADS];         // row within a step
-  uint32_t col[LOADS];  // byte offset of the chunk's column
-  int cols_left[LOADS]; // columns from it on (ALIGNED = false)
-  int K;
+  uint32_t off[LOADS];  // byte offset of this lane's chunk's column (SameRow: in its row)
+  int c0, cols, K;
   MAP map;
+  static constexpr bool SAME = MAP::SAME;
+  static constexpr int CH = R / C::EPC;  // chunks per row
   // Columns c0 .. of `cols`; ALIGNED needs cols to be whole chunks (chunks past
-  // the last repeat it: their outputs are not stored).
-  __device__ __forceinline__ void init(const char* base_, size_t ld_, int c0, int cols, int K_,
+  // the last repeat it: their outputs are not stored). A step's rows (SameRow)
+  // span less than 2^32 bytes.
+  __device__ __forceinline__ void init(const char* base_, size_t ld_, int c0_, int cols_, int K_,
                                        size_t part_, MAP map_, int lane, int wave) {
-    static_assert(R * C::ES / 16 >= 8, "swizzle range");
+    static_assert(R % 64 == 0, "swizzle range");
     base = base_;
     ld = ld_;
     part = part_;
+    c0 = c0_;
+    cols = cols_;
     K = K_;
     map = map_;
-    constexpr int CH = R / C::EPC;  // chunks per row
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
-      const int e = (wave * LOADS + j) * 64 + lane;
-      r[j] = e / CH;
-      const int c = c0 + red_swz<C::ES, R>(r[j], e % CH) * C::EPC;
-      cols_left[j] = cols - c;
-      col[j] = (uint32_t)((C::ALIGNED ? min(c, cols - C::EPC) : min(c, cols - 1)) * C::ES);
+      const int e = (wave * LOADS + j) * 64 + lane, r = e / CH;
+      const int c = c0 + red_swz<C::ES, R>(r, e % CH) * C::EPC;
+      off[j] = (uint32_t)((C::ALIGNED ? min(c, cols - C::EPC) : min(c, cols - 1)) * C::ES);
+      if constexpr (SAME) off[j] += (uint32_t)(r * ld);
     }
   }
+  __device__ __forceinline__ int whole_steps() const { return K / C::BK; }
+  template <bool WHOLE>
   __device__ __forceinline__ void load(char* region, int step, int lane, int wave) const {
 #pragma unroll
-    for (int q = 0; q < C::PARTS; ++q)
+    for (int q = 0; q < C::PARTS; ++q) {
+      const char* b = base + q * part;
+      if constexpr (SAME) b += (size_t)step * C::BK * ld;
 #pragma unroll
       for (int j = 0; j < LOADS; ++j) {
-        const int k = step * C::BK + r[j];
-        const bool in = k < K;
-        const char* g = base + q * part + map(in ? k : 0) * ld + col[j];
-        char* dst = region + q * (R * 64) + (wave * LOADS + j) * 1024;
-        if constexpr (C::ALIGNED) {
-          dma16(in ? (const void*)g : (const void*)&kZeros, dst);
-        } else {
+        const int e = (wave * LOADS + j) * 64 + lane, r = e / CH;
+        const int k = step * C::BK + r;
+        const bool in = WHOLE || k < K;
+        const char* g = b + off[j];
+        if constexpr (!SAME) g += map(in ? k : 0) * ld;
+        char* dst = region + q * (R * C::KB) + (wave * LOADS + j) * 1024;
+        if constexpr (!C::ALIGNED) {
           *reinterpret_cast<u32x4*>(dst + lane * 16) =
-              partial_chunk<C::ES>(g, in ? cols_left[j] : 0);
+              partial_chunk<C::ES>(g, in ? cols - c0 - red_swz<C::ES, R>(r, e % CH) * C::EPC : 0);
+        } else if constexpr (WHOLE) {
+          dma16(g, dst);
+        } else {
+          dma16(in ? (const void*)g : (const void*)&kZeros, dst);
         }
       }
+    }
   }
 };
 
 // ---- fragments --------------------------------------------------------------------
 // 16-bit types: lane l holds output row l % 32 of its block, reduction 8 (l /
 // 32) + 0..7 of a slice of 16 (one MFMA). fp32: reduction 4 (l / 32) + 0..3 of
-// a slice of 8 (four MFMAs of two each). A K-step is two slices.
+// a slice of 8 (four MFMAs of two each).
 template <class C, int MODE, int R, int F>
 struct Reader {
-  uint32_t off[MODE == kOutRows ? 2 : F];
+  uint32_t off[MODE == kOutRows ? C::SLICES : F];
   __device__ __forceinline__ void init(int row0, int lane) {
     if constexpr (MODE == kOutRows) {
       const int row = row0 + (lane & 31);
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) off[kk] = row * 64 + 16 * out_swz(row, 2 * kk + (lane >> 5));
+      for (int kk = 0; kk < C::SLICES; ++kk)
+        off[kk] = row * C::KB + 16 * out_swz<C::KB>(row, 2 * kk + (lane >> 5));
     } else if constexpr (C::ES == 2) {
       // In each 16-lane group, lane 4j + q points at row kb + j, columns 4q ..
       // 4q + 3 of the group's 16; the read hands lane i column i of these rows.
@@ -225,11 +264,11 @@ struct Reader {
   // The F fragments of slice KK, part q.
   template <int KK>
   __device__ __forceinline__ void read(u32x4 (&f)[F], const char* region, int q) const {
-    const char* s = region + q * (R * 64);
+    const char* s = region + q * (R * C::KB);
 #pragma unroll
     for (int i = 0; i < F; ++i) {
       if constexpr (MODE == kOutRows) {
-        f[i] = *reinterpret_cast<const u32x4*>(s + off[KK] + i * 32 * 64);
+        f[i] = *reinterpret_cast<const u32x4*>(s + off[KK] + i * 32 * C::KB);
       } else if constexpr (C::ES == 2) {
         typedef __attribute__((address_space(3))) v4s lds_v4s;
         const char* p = s + off[i] + KK * 16 * R * 2;
@@ -275,59 +314,127 @@ __device__ __forceinline__ void clear(Acc<C>& acc) {
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 }
 
+// The fragments of slice KK. Of pairs, the hi parts first, then the lo parts of
+// b and of a: in the order in which the products below leave registers free.
 template <class C, int KK, class RA, class RB>
 __device__ __forceinline__ void read_slice(u32x4 (&fa)[C::PARTS][C::FM],
                                            u32x4 (&fb)[C::PARTS][C::FN], const char* stg,
                                            const RA& ra, const RB& rb) {
-#pragma unroll
-  for (int q = 0; q < C::PARTS; ++q) {
-    ra.template read<KK>(fa[q], stg, q);
-    rb.template read<KK>(fb[q], stg + C::A_BYTES, q);
+  ra.template read<KK>(fa[0], stg, 0);
+  rb.template read<KK>(fb[0], stg + C::A_BYTES, 0);
+  if constexpr (C::PARTS == 2) {
+    rb.template read<KK>(fb[1], stg + C::A_BYTES, 1);
+    ra.template read<KK>(fa[1], stg, 1);
   }
 }
 
 template <class C>
-__device__ __forceinline__ void mma_slice(Acc<C>& acc, const u32x4 (&fa)[C::PARTS][C::FM],
-                                          const u32x4 (&fb)[C::PARTS][C::FN]) {
+__device__ __forceinline__ void mma_blocks(Acc<C>& acc, const u32x4 (&a)[C::FM],
+                                           const u32x4 (&b)[C::FN]) {
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j) {
-      if constexpr (C::PARTS == 2) {
-        mma<C::E>(acc[i][j], fa[0][i], fb[1][j]);
-        mma<C::E>(acc[i][j], fa[1][i], fb[0][j]);
-      }
-      mma<C::E>(acc[i][j], fa[0][i], fb[0][j]);
-    }
+    for (int j = 0; j < C::FN; ++j) mma<C::E>(acc[i][j], a[i], b[j]);
+}
+// Of pairs, the lo products first: b's lo part is done with after a third of
+// them, a's after two thirds, and the next slice's are read into their registers.
+template <class C>
+__device__ __forceinline__ void mma_slice(Acc<C>& acc, const u32x4 (&fa)[C::PARTS][C::FM],
+                                          const u32x4 (&fb)[C::PARTS][C::FN]) {
+  if constexpr (C::PARTS == 2) {
+    mma_blocks<C>(acc, fa[0], fb[1]);
+    mma_blocks<C>(acc, fa[1], fb[0]);
+  }
+  mma_blocks<C>(acc, fa[0], fb[0]);
 }
 
-template <class C, class SA, class SB>
+template <class C, bool WHOLE, class SA, class SB>
 __device__ __forceinline__ void issue(char* stg, const SA& a, const SB& b, int step, int lane,
                                       int wave) {
-  a.load(stg, step, lane, wave);
-  b.load(stg + C::A_BYTES, step, lane, wave);
-  __asm__ volatile("" ::: "memory");
+  a.template load<WHOLE>(stg, step, lane, wave);
+  b.template load<WHOLE>(stg + C::A_BYTES, step, lane, wave);
 }
+
+// How many LDS reads a slice of one part of an operand takes.
+template <class C, int MODE, int F>
+constexpr int reads_of() {
+  return F * (MODE == kOutRows ? 1 : C::ES == 2 ? 2 : 4);
+}
+
+// Order of one run of MFMAs: NDS LDS reads and NVM DMA issues spread between
+// them from the start.
+template <class C, int NDS, int NVM>
+__device__ __forceinline__ void interleave_blocks() {
+  constexpr int NMF = C::FM * C::FN * (C::E == kF32 ? 4 : 1);
+  constexpr int PER = (NDS + NMF - 1) / NMF, PERV = (NVM + NMF - 1) / NMF;
+#pragma unroll
+  for (int i = 0; i < NMF; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                           // MFMA
+    if (i * PER < NDS) __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);      // LDS read
+    if (i * PERV < NVM) __builtin_amdgcn_sched_group_barrier(0x020, PERV, 0);    // DMA
+    __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);                           // VALU
+  }
+}
+// Order of one slice's section: its MFMAs under which the next slice is read
+// and (DMA) a step's loads are issued.
+template <class C, bool DMA>
+__device__ __forceinline__ void interleave() {
+  constexpr int A = reads_of<C, C::AMODE, C::FM>(), B = reads_of<C, C::BMODE, C::FN>();
+  constexpr int NVM = DMA && C::ALIGNED ? C::V : 0;
+  interleave_blocks<C, A + B, NVM>();
+  if constexpr (C::PARTS == 2) {
+    interleave_blocks<C, B, 0>();
+    interleave_blocks<C, A, 0>();
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <class C>
+struct Frags {
+  u32x4 a[C::PARTS][C::FM], b[C::PARTS][C::FN];
+};
 
 // One K-step out of ring stage S (the stages are separate arrays and S is a
 // constant, so the compiler can tell the stage read from the stages being
-// filled and waits only for these reads).
-template <class C, int S, class SA, class SB, class RA, class RB>
-__device__ __forceinline__ void step(Acc<C>& acc, char* const (&ring)[C::NSTAGE], const SA& a,
-                                     const SB& b, const RA& ra, const RB& rb, int kt, int lane,
-                                     int wave) {
+// filled and waits only for these reads). On entry f holds slice 0 of step kt,
+// on return slice 0 of step kt + 1: each slice's reads run under the MFMAs of
+// the slice before.
+template <class C, int S, bool WHOLE, class SA, class SB, class RA, class RB>
+__device__ __forceinline__ void step(Acc<C>& acc, Frags<C>& f, char* const (&ring)[C::NSTAGE],
+                                     const SA& a, const SB& b, const RA& ra, const RB& rb, int kt,
+                                     int lane, int wave) {
+  // Every wave is done with step kt - 1 (the barrier in it), whose stage this
+  // DMA overwrites.
+  issue<C, WHOLE>(ring[(S + C::AHEAD) % C::NSTAGE], a, b, kt + C::AHEAD, lane, wave);
+  Frags<C> g;
+  read_slice<C, 1>(g.a, g.b, ring[S], ra, rb);
+  mma_slice<C>(acc, f.a, f.b);
+  interleave<C, true>();
+  if constexpr (C::SLICES == 4) {
+    read_slice<C, 2>(f.a, f.b, ring[S], ra, rb);
+    mma_slice<C>(acc, g.a, g.b);
+    interleave<C, false>();
+    read_slice<C, 3>(g.a, g.b, ring[S], ra, rb);
+    mma_slice<C>(acc, f.a, f.b);
+    interleave<C, false>();
+  }
   __asm__ volatile("" ::: "memory");
-  // this wave's part of step kt has landed once only the later steps' are out
+  // this wave's part of step kt + 1 has landed once only the later steps' are out
   wait_vm<(C::AHEAD - 1) * C::V>();
-  // every wave's has, and every wave is done with step kt - 1, whose stage the
-  // next DMA overwrites
   lds_barrier();
-  issue<C>(ring[(S + C::AHEAD) % C::NSTAGE], a, b, kt + C::AHEAD, lane, wave);
-  u32x4 fa[C::PARTS][C::FM], fb[C::PARTS][C::FN], ga[C::PARTS][C::FM], gb[C::PARTS][C::FN];
-  read_slice<C, 0>(fa, fb, ring[S], ra, rb);
-  read_slice<C, 1>(ga, gb, ring[S], ra, rb);
-  mma_slice<C>(acc, fa, fb);
-  mma_slice<C>(acc, ga, gb);
+  read_slice<C, 0>(f.a, f.b, ring[(S + 1) % C::NSTAGE], ra, rb);
+  mma_slice<C>(acc, g.a, g.b);
+  interleave<C, false>();
+}
+
+template <class C, bool WHOLE, class SA, class SB, class RA, class RB>
+__device__ __forceinline__ void round(Acc<C>& acc, Frags<C>& f, char* const (&ring)[C::NSTAGE],
+                                      const SA& a, const SB& b, const RA& ra, const RB& rb, int kt,
+                                      int lane, int wave) {
+  step<C, 0, WHOLE>(acc, f, ring, a, b, ra, rb, kt, lane, wave);
+  step<C, 1, WHOLE>(acc, f, ring, a, b, ra, rb, kt + 1, lane, wave);
+  if constexpr (C::NSTAGE > 2) step<C, 2, WHOLE>(acc, f, ring, a, b, ra, rb, kt + 2, lane, wave);
+  if constexpr (C::NSTAGE > 3) step<C, 3, WHOLE>(acc, f, ring, a, b, ra, rb, kt + 3, lane, wave);
 }
 
 // acc += the product over steps [0, nsteps), taken in whole rounds of the ring
@@ -340,13 +447,20 @@ __device__ __forceinline__ void run(Acc<C>& acc, char* const (&ring)[C::NSTAGE],
                                     const SB& b, const RA& ra, const RB& rb, int nsteps, int lane,
                                     int wave) {
 #pragma unroll
-  for (int s = 0; s < C::AHEAD; ++s) issue<C>(ring[s], a, b, s, lane, wave);
-  for (int kt = 0; kt < nsteps; kt += C::NSTAGE) {
-    step<C, 0>(acc, ring, a, b, ra, rb, kt, lane, wave);
-    step<C, 1>(acc, ring, a, b, ra, rb, kt + 1, lane, wave);
-    if constexpr (C::NSTAGE > 2) step<C, 2>(acc, ring, a, b, ra, rb, kt + 2, lane, wave);
-    if constexpr (C::NSTAGE > 3) step<C, 3>(acc, ring, a, b, ra, rb, kt + 3, lane, wave);
+  for (int s = 0; s < C::AHEAD; ++s) {
+    issue<C, false>(ring[s], a, b, s, lane, wave);
+    __asm__ volatile("" ::: "memory");
   }
+  wait_vm<(C::AHEAD - 1) * C::V>();
+  lds_barrier();
+  Frags<C> f;
+  read_slice<C, 0>(f.a, f.b, ring[0], ra, rb);
+  int kt = 0;
+  // rounds whose loads all lie before the reduction's end need no checks
+  for (const int whole = a.whole_steps() - C::AHEAD; kt + C::NSTAGE <= whole; kt += C::NSTAGE)
+    round<C, true>(acc, f, ring, a, b, ra, rb, kt, lane, wave);
+  for (; kt < nsteps; kt += C::NSTAGE)
+    round<C, false>(acc, f, ring, a, b, ra, rb, kt, lane, wave);
   wait_vm<0>();
 }
 
