@@ -152,7 +152,8 @@ bmoe_status bmoe_grouped_product(bmoe_dtype dt, int M, int K, int O, int n_group
 size_t bmoe_grouped_product_backward_workspace_bytes(bmoe_dtype dt, int M, int K, int O,
                                                      int n_groups) {
   if (!ok_type(dt) || !grouped_shape(M, K, O, n_groups, nullptr, 1, 1)) return 0;
-  return 256;
+  const int splits = grouped_dw_splits(dt, M, O, K, n_groups);
+  return (splits > 1 ? up256((size_t)splits * n_groups * O * K * sizeof(float)) : 0) + 256;
 }
 
 bmoe_status bmoe_grouped_product_backward(bmoe_dtype dt, int M, int K, int O, int n_groups,
@@ -179,7 +180,8 @@ bmoe_status bmoe_grouped_product_backward(bmoe_dtype dt, int M, int K, int O, in
   if (da && M > 0)
     h = launch_grouped(dt, true, M, O, K, n_groups, dc, nullptr, 1, M, w, offsets, da, s);
   if (h == hipSuccess && dw)
-    h = launch_grouped_dw(dt, M, O, K, n_groups, a, perm, k, perm ? a_rows : M, dc, offsets, dw, s);
+    h = launch_grouped_dw(dt, M, O, K, n_groups, a, perm, k, perm ? a_rows : M, dc, offsets, dw,
+                          static_cast<float*>(ws), s);
   return status_of(h);
 }
 

@@ -67,10 +67,17 @@ __global__ __launch_bounds__(kThreads) void group_scatter_kernel(GroupArgs p) {
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) total += sh[w * n + e];
     } else {
-      for (int c = 0; c < p.chunks; ++c) {
-        const int v = p.count[(size_t)c * n + e];
-        total += v;
-        before += c < (int)blockIdx.x ? v : 0;
+      // 16 loads in flight (131072 ids in 64 chunks: 33 us one by one)
+      for (int c0 = 0; c0 < p.chunks; c0 += 16) {
+        int v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          v[i] = c0 + i < p.chunks ? p.count[(size_t)(c0 + i) * n + e] : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          total += v[i];
+          before += c0 + i < (int)blockIdx.x ? v[i] : 0;
+        }
       }
     }
     base[e] = total;

@@ -5,6 +5,8 @@
 // with group e the rows offsets[e] .. offsets[e + 1] and row(q) = perm[q] / k
 // (q itself without perm). The offsets live on the device: a workgroup finds
 // its tile of a group from them, so the host never waits for the router.
+#include <algorithm>
+
 #include "common.h"
 #include "kernels.h"
 #include "tile_product.h"
@@ -14,53 +16,60 @@ namespace {
 
 using namespace tile;
 
-struct GroupTile {
-  int e, row0, rows;  // group, its tile's rows; e = -1: no such tile
-  int height;         // 64, 128, ... MOST: the tile's rows rounded up
-  int col_tile;
-};
-
 // Rows of group e, whatever the offsets hold.
 __device__ __forceinline__ int2 group_rows_of(const int32_t* offsets, int e, int M) {
   const int lo = min(max(offsets[e], 0), M), hi = min(max(offsets[e + 1], 0), M);
   return make_int2(lo, max(lo, hi));
 }
 
-// Work item t of all groups' tiles, groups ascending. A group has the fewest
-// rows of tiles of at most MOST rows that hold it, all equally high (in 64s): 532
-// rows are three of 192, not two of 256 and one almost empty. Its tiles come in
-// panels of four rows of tiles, so that the consecutive items that share an L2
-// are near square. Every wave looks its tile up for itself: 64 groups at a time,
-// a prefix sum over the lanes.
+struct GroupTile {
+  int e, lo, hi;     // group (-1: no such tile) and its rows
+  int tiles;         // rows of tiles in the group
+  int i, col_tile;   // this tile's
+};
+
+// Work item t of all groups' tiles, groups ascending; a group has rows / MOST
+// rows of tiles_n tiles, rounded up. They come in panels of four rows of tiles,
+// so that the consecutive items that share an L2 are near square. Every wave
+// looks its tile up for itself: 64 groups at a time, a prefix sum over the lanes;
+// the offsets of 256 groups are loaded at once.
 constexpr int kPanel = 4;
 template <int MOST>
 __device__ __forceinline__ GroupTile find_tile(const int32_t* offsets, int G, int M, int tiles_n,
                                                int t, int lane) {
   int before = 0;
-  for (int e0 = 0; e0 < G; e0 += kWave) {
-    int2 r = make_int2(0, 0);
-    if (e0 + lane < G) r = group_rows_of(offsets, e0 + lane, M);
-    const int n = (r.y - r.x + MOST - 1) / MOST * tiles_n;
-    const int incl = wave_incl_scan(n);
-    const uint64_t past = __ballot(before + incl > t);
-    if (past) {
-      const int src = __ffsll((unsigned long long)past) - 1;
-      const int lo = __builtin_amdgcn_readlane(r.x, src), hi = __builtin_amdgcn_readlane(r.y, src);
-      const int items = __builtin_amdgcn_readlane(n, src), tiles = items / tiles_n;
-      const int i = t - before - (__builtin_amdgcn_readlane(incl, src) - items);
-      const int panel = i / (kPanel * tiles_n), j = i - panel * kPanel * tiles_n;
-      const int rows_of_tiles = min(kPanel, tiles - panel * kPanel);
-      GroupTile g;
-      g.e = e0 + src;
-      g.height = ((hi - lo + tiles - 1) / tiles + 63) / 64 * 64;
-      g.row0 = lo + (panel * kPanel + j % rows_of_tiles) * g.height;
-      g.rows = min(g.height, hi - g.row0);  // none where rounding up left the last tiles empty
-      g.col_tile = j / rows_of_tiles;
-      return g;
+  for (int e1 = 0; e1 < G; e1 += 4 * kWave) {
+    int2 rows[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = e1 + u * kWave + lane;
+      rows[u] = e < G ? group_rows_of(offsets, e, M) : make_int2(0, 0);
     }
-    before += __builtin_amdgcn_readlane(incl, kWave - 1);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int2 r = rows[u];
+      const int n = (r.y - r.x + MOST - 1) / MOST * tiles_n;
+      const int incl = wave_incl_scan(n);
+      const uint64_t past = __ballot(before + incl > t);
+      if (past) {
+        const int src = __ffsll((unsigned long long)past) - 1;
+        const int items = __builtin_amdgcn_readlane(n, src);
+        const int at = t - before - (__builtin_amdgcn_readlane(incl, src) - items);
+        GroupTile g;
+        g.e = e1 + u * kWave + src;
+        g.lo = __builtin_amdgcn_readlane(r.x, src);
+        g.hi = __builtin_amdgcn_readlane(r.y, src);
+        g.tiles = items / tiles_n;
+        const int panel = at / (kPanel * tiles_n), j = at - panel * kPanel * tiles_n;
+        const int high = min(kPanel, g.tiles - panel * kPanel);
+        g.i = panel * kPanel + j % high;
+        g.col_tile = j / high;
+        return g;
+      }
+      before += __builtin_amdgcn_readlane(incl, kWave - 1);
+    }
   }
-  return {-1, 0, 0, 0, 0};
+  return {-1, 0, 0, 0, 0, 0};
 }
 
 struct ProductArgs {
@@ -110,8 +119,9 @@ __device__ __forceinline__ void store_bf16(const Acc<C>& acc, char* stg, char* c
     }
 }
 
-// The same value by value: fp32, and bf16 rows of odd lengths.
-template <class C, typename T>
+// The same value by value: fp32, and bf16 rows of odd lengths. STREAM: stores
+// that leave the caches to the operands.
+template <class C, typename T, bool STREAM = false>
 __device__ __forceinline__ void store_plain(const Acc<C>& acc, char* c, size_t ld, int rows,
                                             int cols, int lane) {
 #pragma unroll
@@ -125,6 +135,7 @@ __device__ __forceinline__ void store_plain(const Acc<C>& acc, char* c, size_t l
         if (row < rows && col < cols) {
           T* dst = reinterpret_cast<T*>(c + (size_t)row * ld) + col;
           if constexpr (sizeof(T) == 2) *dst = (T)f32_to_bf16_bits(acc[i][j][r]);
+          else if constexpr (STREAM) __builtin_nontemporal_store(acc[i][j][r], dst);
           else *dst = acc[i][j][r];
         }
       }
@@ -133,8 +144,11 @@ __device__ __forceinline__ void store_plain(const Acc<C>& acc, char* c, size_t l
 
 // One tile of c (BMODE kOutRows: W's rows are the output's columns) or of da
 // (kRedRows: they are the reduction).
+struct TileRows {
+  int e, row0, rows;
+};
 template <class C>
-__device__ __forceinline__ void grouped_tile(const ProductArgs& p, const GroupTile& t, int col0,
+__device__ __forceinline__ void grouped_tile(const ProductArgs& p, const TileRows& t, int col0,
                                              char* const (&ring)[C::NSTAGE], int lane, int wave) {
   const size_t a_ld = (size_t)p.red * C::ES;
   OutRowsSource<C, C::AR, C::A_LOADS, true> a;
@@ -165,19 +179,21 @@ __device__ __forceinline__ void grouped_tile(const ProductArgs& p, const GroupTi
   const size_t c_ld = (size_t)p.cols * C::ES;
   char* c = p.c + (size_t)(t.row0 + wm * C::TM) * c_ld + (size_t)(col0 + wn * C::TN) * C::ES;
   const int rl = t.rows - wm * C::TM, cl = p.cols - col0 - wn * C::TN;
-  if constexpr (C::E == kBf16 && C::ALIGNED) {
+  if constexpr (C::E == kF32) {
+    store_plain<C, float>(acc, c, c_ld, rl, cl, lane);
+  } else if (p.cols % 8 == 0) {
     static_assert(C::WAVES * 16 * C::TN * 2 <= C::STAGE, "staging fits a stage");
     lds_barrier();  // every wave is done with the ring
     store_bf16<C>(acc, ring[0] + wave * 16 * C::TN * 2, c, c_ld, rl, cl, lane);
-  } else if constexpr (C::E == kBf16) {
-    store_plain<C, uint16_t>(acc, c, c_ld, rl, cl, lane);
   } else {
-    store_plain<C, float>(acc, c, c_ld, rl, cl, lane);
+    store_plain<C, uint16_t>(acc, c, c_ld, rl, cl, lane);
   }
 }
 
 // Tiles of one width and heights of 64 to 64 FMAX rows (FMAX blocks of 32 for
-// each of two waves), chosen per tile: one copy of the product for each.
+// each of two waves). A group has the fewest rows of tiles that hold it, all
+// equally high: 532 rows are three of 192, not two of 256 and one almost empty.
+// One copy of the product for each height.
 template <int E_, int FMAX_, int BN_, int WN_, int NSTAGE_, int BMODE_, bool ALIGNED_>
 struct Family {
   static constexpr int NSTAGE = NSTAGE_;
@@ -201,30 +217,107 @@ __global__ __launch_bounds__(F::Most::THREADS) void grouped_kernel(ProductArgs p
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int item = xcd_item(grid_block(), run_items);
-  const GroupTile t = find_tile<F::Most::BM>(p.offsets, p.G, p.M, p.tiles_n, item, lane);
-  if (t.e < 0 || t.rows <= 0) return;  // the whole workgroup
-  const int col0 = t.col_tile * F::BN;
-  if (t.height == 64) {
+  const GroupTile g = find_tile<F::Most::BM>(p.offsets, p.G, p.M, p.tiles_n, item, lane);
+  if (g.e < 0) return;  // the whole workgroup
+  const int height = ((g.hi - g.lo + g.tiles - 1) / g.tiles + 63) / 64 * 64;
+  TileRows t;
+  t.e = g.e;
+  t.row0 = g.lo + g.i * height;
+  t.rows = min(height, g.hi - t.row0);
+  if (t.rows <= 0) return;  // rounding up left the last tiles empty
+  const int col0 = g.col_tile * F::BN;
+  if (height == 64) {
     grouped_tile<typename F::template Height<1>>(p, t, col0, ring, lane, wave);
-  } else if (F::FMAX <= 2 || t.height == 128) {
+  } else if (F::FMAX <= 2 || height == 128) {
     grouped_tile<typename F::template Height<2>>(p, t, col0, ring, lane, wave);
   } else if constexpr (F::FMAX > 2) {
-    if (t.height == 192) grouped_tile<typename F::template Height<3>>(p, t, col0, ring, lane, wave);
+    if (height == 192) grouped_tile<typename F::template Height<3>>(p, t, col0, ring, lane, wave);
     else grouped_tile<typename F::template Height<4>>(p, t, col0, ring, lane, wave);
   }
 }
 
-// dW: one workgroup per expert and tile of its O x K entries. The rows of a
-// group are taken kListRows at a time, their rows of a listed in LDS first.
+// ---- groups of few rows (bf16): bound by reading W ------------------------------
+// A workgroup computes 16 columns of c for up to 16 TB rows of a group: each of
+// its four waves takes a quarter of K straight from memory into
+// v_mfma_f32_16x16x32_bf16 (W's rows as the first operand, so a lane ends with
+// four neighbours of a row of c), eight loads of W in flight; the quarters are
+// added in order through LDS. Nothing is shared that LDS could keep: W is read
+// once, and the rows of a come from L2.
+typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
+constexpr int kFewCols = 16;
+constexpr int kFewWaves = 4;
+
+template <int TB>
+__global__ __launch_bounds__(64 * kFewWaves) void grouped_few_kernel(ProductArgs p) {
+  constexpr int U = TB == 1 ? 8 : 4;  // slices of 32 in flight
+  __shared__ f32x4 sums[kFewWaves][TB][64];
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const GroupTile g =
+      find_tile<16 * TB>(p.offsets, p.G, p.M, p.tiles_n, (int)grid_block(), lane);
+  if (g.e < 0) return;  // the whole workgroup
+  const int row0 = g.lo + g.i * 16 * TB, rows = min(16 * TB, g.hi - row0);
+  const int col0 = g.col_tile * kFewCols;
+  const int slices = (p.red + 31) / 32, per = (slices + kFewWaves - 1) / kFewWaves;
+  const int s0 = wave * per, s1 = min(slices, s0 + per);
+  const int k0 = 8 * (lane >> 4);  // this lane's chunk of a slice
+  const uint16_t* w = reinterpret_cast<const uint16_t*>(p.w) +
+                      ((size_t)g.e * p.cols + min(col0 + (lane & 15), p.cols - 1)) * p.red + k0;
+  const uint16_t* a[TB];
+#pragma unroll
+  for (int b = 0; b < TB; ++b) {
+    const int q = row0 + min(16 * b + (lane & 15), rows - 1);
+    a[b] = reinterpret_cast<const uint16_t*>(p.a) + (size_t)a_row(p, q) * p.red + k0;
+  }
+  f32x4 acc[TB];
+#pragma unroll
+  for (int b = 0; b < TB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  for (int s = s0; s < s1; s += U) {
+    uint4 wv[U], av[TB][U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool in = s + u < s1 && 32 * (s + u) + k0 < p.red;
+      wv[u] = in ? *reinterpret_cast<const uint4*>(w + 32 * (s + u)) : zero;
+#pragma unroll
+      for (int b = 0; b < TB; ++b)
+        av[b][u] = in ? *reinterpret_cast<const uint4*>(a[b] + 32 * (s + u)) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int b = 0; b < TB; ++b)
+        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8v, wv[u]),
+                                                         __builtin_bit_cast(bf16x8v, av[b][u]),
+                                                         acc[b], 0, 0, 0);
+  }
+#pragma unroll
+  for (int b = 0; b < TB; ++b) sums[wave][b][lane] = acc[b];
+  __syncthreads();
+  for (int b = wave; b < TB; b += kFewWaves) {
+    f32x4 c = sums[0][b][lane];
+#pragma unroll
+    for (int v = 1; v < kFewWaves; ++v) c += sums[v][b][lane];
+    const int row = 16 * b + (lane & 15), col = col0 + 4 * (lane >> 4);
+    if (row < rows && col < p.cols)  // (cols is a multiple of 8)
+      *reinterpret_cast<uint2*>(p.c + ((size_t)(row0 + row) * p.cols + col) * 2) =
+          make_uint2(pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3]));
+  }
+}
+
+// dW: one workgroup per expert, tile of its O x K entries and range of its rows
+// (`splits` equal ranges, whose sums are added in order by a second launch, so
+// that the result is the same each run). The rows are taken kListRows at a time,
+// their rows of a listed in LDS first.
 constexpr int kListRows = 1024;
 
 struct DwArgs {
   const char* a;   // [a_rows][K]
   const char* dc;  // [M][O]
-  float* dw;       // [G][O][K]
+  float* dw;       // [splits][G][O][K]
   const int32_t* offsets;
   const int32_t* perm;
-  int k, a_rows, M, G, O, K, tiles_o, tiles_k;
+  int k, a_rows, M, G, O, K, tiles_o, tiles_k, splits;
 };
 
 template <class C>
@@ -242,11 +335,15 @@ __global__ __launch_bounds__(C::THREADS) void grouped_dw_kernel(DwArgs p, int ru
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const unsigned item = xcd_item(grid_block(), run_items), tiles = p.tiles_o * p.tiles_k;
-  const int e = item / tiles;
+  const unsigned range = item / tiles;
+  const int e = range / p.splits, split = range % p.splits;
   if (e >= p.G) return;
   const int t = item % tiles;
   const int o0 = t / p.tiles_k * C::BM, k0 = t % p.tiles_k * C::BN;
-  const int2 rows = group_rows_of(p.offsets, e, p.M);
+  int2 rows = group_rows_of(p.offsets, e, p.M);
+  const int len = (rows.y - rows.x + p.splits - 1) / p.splits;
+  rows.x = min(rows.y, rows.x + split * len);
+  rows.y = min(rows.y, rows.x + len);
 
   Acc<C> acc;
   clear<C>(acc);
@@ -271,8 +368,38 @@ __global__ __launch_bounds__(C::THREADS) void grouped_dw_kernel(DwArgs p, int ru
     run<C>(acc, ring, a, b, ra, rb, (n + C::BK - 1) / C::BK, lane, wave);
   }
   const int ol = o0 + wm * C::TM, kl = k0 + wn * C::TN;
-  char* dst = reinterpret_cast<char*>(p.dw + ((size_t)e * p.O + ol) * p.K + kl);
-  store_plain<C, float>(acc, dst, (size_t)p.K * 4, p.O - ol, p.K - kl, lane);
+  char* dst = reinterpret_cast<char*>(p.dw + (((size_t)split * p.G + e) * p.O + ol) * p.K + kl);
+  // whole 128-byte lines stream past the caches (64 experts of 2048 x 2048: 490 -> 450
+  // us); others are put together in them
+  if (p.K % 32 == 0)
+    store_plain<C, float, true>(acc, dst, (size_t)p.K * 4, p.O - ol, p.K - kl, lane);
+  else
+    store_plain<C, float, false>(acc, dst, (size_t)p.K * 4, p.O - ol, p.K - kl, lane);
+}
+
+// dw = the sum of the ranges' parts, in order. n: entries of dw.
+__global__ __launch_bounds__(256) void grouped_dw_sum_kernel(const float* part, int splits, size_t n,
+                                                             float* dw) {
+  const size_t i = ((size_t)grid_block() * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  if (i + 4 <= n && n % 4 == 0) {
+    float4 s = *reinterpret_cast<const float4*>(part + i);
+#pragma unroll 8
+    for (int v = 1; v < splits; ++v) {
+      const float4 x = *reinterpret_cast<const float4*>(part + v * n + i);
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
+    }
+    *reinterpret_cast<float4*>(dw + i) = s;
+  } else {
+    for (size_t j = i; j < n && j < i + 4; ++j) {
+      float s = part[j];
+      for (int v = 1; v < splits; ++v) s += part[v * n + j];
+      dw[j] = s;
+    }
+  }
 }
 
 template <class F>
@@ -287,11 +414,19 @@ hipError_t launch_grouped_cfg(ProductArgs p, hipStream_t s) {
                        dim3(F::Most::THREADS), 0, s, KernelTiming{}, p, run_items);
 }
 
+template <int TB>
+hipError_t launch_few(ProductArgs p, hipStream_t s) {
+  p.tiles_n = (p.cols + kFewCols - 1) / kFewCols;
+  const size_t tiles_m = (size_t)p.M / (16 * TB) + (p.G < p.M ? p.G : p.M);
+  return launch_kernel(grouped_few_kernel<TB>, grid_rows(tiles_m * p.tiles_n),
+                       dim3(64 * kFewWaves), 0, s, KernelTiming{}, p);
+}
+
 template <class C>
 hipError_t launch_grouped_dw_cfg(DwArgs p, hipStream_t s) {
   p.tiles_o = (p.O + C::BM - 1) / C::BM;
   p.tiles_k = (p.K + C::BN - 1) / C::BN;
-  const size_t items = (size_t)p.G * p.tiles_o * p.tiles_k;
+  const size_t items = (size_t)p.G * p.splits * p.tiles_o * p.tiles_k;
   const int run_items = items >= 1024 ? 32 : 1;
   const size_t super = 8 * run_items;
   return launch_kernel(grouped_dw_kernel<C>, grid_rows((items + super - 1) / super * super),
@@ -302,25 +437,53 @@ template <int E, bool ALIGNED>
 using DwTile128 = Cfg<E, 1, 128, 128, 2, 2, 4, kRedRows, kRedRows, ALIGNED>;
 template <int E>
 using DwTile256 = Cfg<E, 1, 256, 256, 2, 4, 4, kRedRows, kRedRows, true>;
-
+// The tile's width by the time of its rounds over the CUs: one workgroup of 256
+// columns fits a CU, two of 128, three of 64; with fewer, a tile of 64 is done
+// first. Rows x reduction x columns, groups, 256, 128, 64 wide: 8192 x 512 x 1024,
+// 64: 21, 29, 29 us; 8192 x 1024 x 512, 64: 22, 30, -; 4096 x 1024 x 1024, 16: 26,
+// 21, 22.5; 256 x 1024 x 1024, 16: 13.7, 13.2, 11.7; 2000 x 512 x 512, 8: 14.5, 8.9,
+// 8.4.
 template <int E, int BMODE>
 hipError_t launch_grouped_type(const ProductArgs& p, hipStream_t s) {
   constexpr int EPC = E == kF32 ? 4 : 8;
-  if (p.red % EPC != 0 || p.cols % EPC != 0)
-    return launch_grouped_cfg<Family<E, 2, 128, 2, 2, BMODE, false>>(p, s);
-  if constexpr (E == kF32) return launch_grouped_cfg<Family<E, 2, 128, 2, 2, BMODE, true>>(p, s);
-  else return launch_grouped_cfg<Family<E, 4, 256, 4, 4, BMODE, true>>(p, s);
+  const long long used = p.G < p.M ? p.G : p.M;  // groups with rows, at most
+  const auto items = [&](int high, int wide) {
+    return (double)(used * (p.M / used / high + 1) * ((p.cols + wide - 1) / wide));
+  };
+  const double t256 = std::max(0.8, items(256, 256) * (0.8 / 256));
+  const double t128 = std::max(0.62, items(128, 128) * (1.0 / 512));
+  const double t64 = std::max(0.56, items(128, 64) * (1.0 / 1000));
+  if (p.red % EPC != 0 || (BMODE == kRedRows && p.cols % EPC != 0))
+    return t64 < t128 ? launch_grouped_cfg<Family<E, 2, 64, 2, 2, BMODE, false>>(p, s)
+                      : launch_grouped_cfg<Family<E, 2, 128, 2, 2, BMODE, false>>(p, s);
+  if constexpr (E == kBf16) {
+    // Few rows per group and few tiles even of 64 columns: one token of 8 experts
+    // of 256, 2048 x 1408, 12.3 us against 20 (memory 9.1); 72 rows of 13 experts,
+    // 640 x 2640 (546 tiles), 18 against 11.
+    if (BMODE == kOutRows && p.cols % 8 == 0 && p.M / used <= 16 && items(128, 64) < 256)
+      return launch_few<1>(p, s);
+    if (t256 < t128 && t256 < t64)
+      return launch_grouped_cfg<Family<E, 4, 256, 4, 4, BMODE, true>>(p, s);
+  }
+  return t64 < t128 ? launch_grouped_cfg<Family<E, 2, 64, 2, 2, BMODE, true>>(p, s)
+                    : launch_grouped_cfg<Family<E, 2, 128, 2, 2, BMODE, true>>(p, s);
+}
+
+// Tiles of 256 x 256 where three quarters of the CUs get one: 32768 rows, 64
+// experts of 2048 x 2048, 400 us against 540 with 128 x 128; 131072 rows, 256 of
+// 512 x 512, 106 against 115.
+bool dw_large(bmoe_dtype dt, int O, int K, int G) {
+  return dt == BMOE_BF16 && O % 8 == 0 && K % 8 == 0 && O >= 256 && K >= 256 &&
+         (long long)G * ((O + 255) / 256) * ((K + 255) / 256) >= 192;
 }
 
 template <int E>
 hipError_t launch_dw_type(const DwArgs& p, hipStream_t s) {
   constexpr int EPC = E == kF32 ? 4 : 8;
-  if (p.O % EPC == 0 && p.K % EPC == 0) {
-    if constexpr (E == kBf16)
-      if (p.O >= 256 && p.K >= 256) return launch_grouped_dw_cfg<DwTile256<E>>(p, s);
-    return launch_grouped_dw_cfg<DwTile128<E, true>>(p, s);
-  }
-  return launch_grouped_dw_cfg<DwTile128<E, false>>(p, s);
+  if (p.O % EPC != 0 || p.K % EPC != 0) return launch_grouped_dw_cfg<DwTile128<E, false>>(p, s);
+  if constexpr (E == kBf16)
+    if (dw_large(BMOE_BF16, p.O, p.K, p.G)) return launch_grouped_dw_cfg<DwTile256<E>>(p, s);
+  return launch_grouped_dw_cfg<DwTile128<E, true>>(p, s);
 }
 
 }  // namespace
@@ -348,13 +511,24 @@ hipError_t launch_grouped(bmoe_dtype dt, bool back, int M, int red, int cols, in
               : launch_grouped_type<kF32, kOutRows>(p, s);
 }
 
+// Ranges per group: enough that 128 x 128 tiles fill the CUs twice over, of at
+// least 128 rows on average (parts cost 8 bytes an entry).
+int grouped_dw_splits(bmoe_dtype dt, int M, int O, int K, int G) {
+  if (dw_large(dt, O, K, G)) return 1;
+  const long long tiles = (long long)G * ((O + 127) / 128) * ((K + 127) / 128);
+  const long long most = M / G / 128;
+  const long long want = 512 / tiles;
+  return (int)std::max(1LL, std::min(std::min(want, most), 64LL));
+}
+
 hipError_t launch_grouped_dw(bmoe_dtype dt, int M, int O, int K, int G, const void* a,
                              const int32_t* perm, int k, int a_rows, const void* dc,
-                             const int32_t* offsets, float* dw, hipStream_t s) {
+                             const int32_t* offsets, float* dw, float* part, hipStream_t s) {
   DwArgs p;
   p.a = static_cast<const char*>(a);
   p.dc = static_cast<const char*>(dc);
-  p.dw = dw;
+  p.splits = grouped_dw_splits(dt, M, O, K, G);
+  p.dw = p.splits > 1 ? part : dw;
   p.offsets = offsets;
   p.perm = perm;
   p.k = k;
@@ -364,7 +538,11 @@ hipError_t launch_grouped_dw(bmoe_dtype dt, int M, int O, int K, int G, const vo
   p.O = O;
   p.K = K;
   p.tiles_o = p.tiles_k = 0;
-  return dt == BMOE_BF16 ? launch_dw_type<kBf16>(p, s) : launch_dw_type<kF32>(p, s);
+  const hipError_t e = dt == BMOE_BF16 ? launch_dw_type<kBf16>(p, s) : launch_dw_type<kF32>(p, s);
+  if (e != hipSuccess || p.splits == 1) return e;
+  const size_t n = (size_t)G * O * K;
+  return launch_kernel(grouped_dw_sum_kernel, grid_rows((n + 1023) / 1024), dim3(256), 0, s,
+                       KernelTiming{}, (const float*)part, p.splits, n, dw);
 }
 
 }  // namespace bmoe

@@ -330,10 +330,12 @@ hipError_t launch_group_rows(const int32_t* ids, int M, int N, int32_t* offsets,
 hipError_t launch_grouped(bmoe_dtype dt, bool back, int M, int red, int cols, int G, const void* a,
                           const int32_t* perm, int k, int a_rows, const void* w,
                           const int32_t* offsets, void* c, hipStream_t s);
-// dw [G][O][K] = sums over the groups' rows of dc[q] a[row(q)]^T.
+// dw [G][O][K] = sums over the groups' rows of dc[q] a[row(q)]^T. part: scratch
+// [grouped_dw_splits][G][O][K] (unused where that is 1).
+int grouped_dw_splits(bmoe_dtype dt, int M, int O, int K, int G);
 hipError_t launch_grouped_dw(bmoe_dtype dt, int M, int O, int K, int G, const void* a,
                              const int32_t* perm, int k, int a_rows, const void* dc,
-                             const int32_t* offsets, float* dw, hipStream_t s);
+                             const int32_t* offsets, float* dw, float* part, hipStream_t s);
 
 // ---- orthogonalised updates ----------------------------------------------------------
 struct OrthoCall {

@@ -28,34 +28,54 @@ struct NormCfg {
   static constexpr bool ALIGNED = ALIGNED_;      // rows of whole 16-byte chunks
   static constexpr int EPC = 16 / sizeof(T);     // values per chunk
   static constexpr int VALS = EPC * NV;
+  static constexpr bool AHEAD = VALS <= 8;       // the gradient loads a token ahead
   static constexpr int THREADS = TPR > kThreads ? TPR : kThreads;
   static constexpr int ROWS = THREADS / TPR;     // per workgroup
 };
 
-__device__ __forceinline__ float get(const float* p) { return *p; }
-__device__ __forceinline__ float get(const uint16_t* p) { return bf16_lo(*p); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(uint16_t* p, float v) { *p = (uint16_t)f32_to_bf16_bits(v); }
+
+// The chunk of a row at column c: values c .. c + EPC - 1 of d, zeros past it.
+// Rows that are not aligned take 16-byte accesses all the same (the memory
+// system splits them; eight 2-byte loads each made 16384 rows of 1001 bf16 values
+// three times as slow), but for a row's last chunk.
+template <class C>
+__device__ __forceinline__ uint4 load_chunk(const typename C::T* p, int c, int d) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if constexpr (C::ALIGNED) {
+    if (c < d) v = *reinterpret_cast<const uint4*>(p + c);
+  } else if (c + C::EPC <= d) {
+    __builtin_memcpy(&v, p + c, 16);
+  } else {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < C::EPC; ++e)
+      if (c + e < d) {
+        if constexpr (C::EPC == 8)
+          w[e / 2] |= (uint32_t)p[c + e] << (16 * (e & 1));
+        else
+          w[e] = __float_as_uint(p[c + e]);
+      }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return v;
+}
+template <class C>
+__device__ __forceinline__ void widen(uint4 v, float* f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < C::EPC; ++e)
+    f[e] = C::EPC == 4 ? __uint_as_float(w[e]) : (e & 1) == 0 ? bf16_lo(w[e / 2]) : bf16_hi(w[e / 2]);
+}
 
 // This thread's values of a row of d: chunks lane, lane + TPR, ... (zeros past d).
 template <class C>
 __device__ __forceinline__ void load_row(const typename C::T* row, int d, int lane,
                                          float (&v)[C::VALS]) {
 #pragma unroll
-  for (int i = 0; i < C::NV; ++i) {
-    const int c = (i * C::TPR + lane) * C::EPC;
-    if constexpr (C::ALIGNED) {
-      if (c < d) {
-        load16(row + c, v + i * C::EPC);
-      } else {
-#pragma unroll
-        for (int e = 0; e < C::EPC; ++e) v[i * C::EPC + e] = 0.f;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < C::EPC; ++e) v[i * C::EPC + e] = c + e < d ? get(row + c + e) : 0.f;
-    }
-  }
+  for (int i = 0; i < C::NV; ++i)
+    widen<C>(load_chunk<C>(row, (i * C::TPR + lane) * C::EPC, d), v + i * C::EPC);
 }
 template <class C>
 __device__ __forceinline__ void store_row(typename C::T* row, int d, int lane,
@@ -65,6 +85,11 @@ __device__ __forceinline__ void store_row(typename C::T* row, int d, int lane,
     const int c = (i * C::TPR + lane) * C::EPC;
     if constexpr (C::ALIGNED) {
       if (c < d) store16(v + i * C::EPC, row + c, scale);
+    } else if (c + C::EPC <= d) {
+      typename C::T w[C::EPC];
+#pragma unroll
+      for (int e = 0; e < C::EPC; ++e) put(w + e, v[i * C::EPC + e] * scale);
+      __builtin_memcpy(row + c, w, 16);
     } else {
 #pragma unroll
       for (int e = 0; e < C::EPC; ++e)
@@ -92,14 +117,29 @@ __device__ __forceinline__ void load_weight(const float* w, int d, int lane, flo
   }
 }
 
+// The sum over a wave's lanes, in a fixed order: DPP shifts by 1, 2, 4 and 8
+// within rows of 16 lanes, then across the rows; the last lane has it all.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __int_as_float(
+                 __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, ROWS == 0xF));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = add_dpp<0x111, 0xF>(v);
+  v = add_dpp<0x112, 0xF>(v);
+  v = add_dpp<0x114, 0xF>(v);
+  v = add_dpp<0x118, 0xF>(v);
+  v = add_dpp<0x142, 0xA>(v);  // lane 15 (47) of the row before, into rows 1 and 3
+  v = add_dpp<0x143, 0xC>(v);  // lane 31, into rows 2 and 3
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), kWave - 1));
+}
+
 // Sums of N values over the TPR threads of a row, the same in all of them.
 // lds: N floats per wave.
 template <class C, int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float* lds) {
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v[i] += __shfl_xor(v[i], o, 64);
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
   if constexpr (C::TPR > kWave) {
     constexpr int W = C::TPR / kWave;
     const int wave = threadIdx.x / kWave;
@@ -119,27 +159,66 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* lds) {
   }
 }
 
-// Row of u that holds pick j of token t, or -1.
-__device__ __forceinline__ long long u_row(const NormCall& p, int t, int j) {
-  const long long at = (long long)t * p.k + j;
-  const long long row = p.inv ? p.inv[at] : at;
-  return row >= 0 && row < p.M ? row : -1;
-}
-
-// y of token t.
+// A thread's values of a row as they are in memory: chunk i * TPR + lane.
 template <class C>
-__device__ __forceinline__ void sum_picks(const NormCall& p, int t, int lane, float (&y)[C::VALS]) {
+struct RawRow {
+  uint4 v[C::NV];
+  __device__ __forceinline__ void load(const void* base, size_t row, int d, int lane) {
+    const typename C::T* p = static_cast<const typename C::T*>(base) + row * d;
 #pragma unroll
-  for (int e = 0; e < C::VALS; ++e) y[e] = 0.f;
-  const typename C::T* u = static_cast<const typename C::T*>(p.u);
-  for (int j = 0; j < p.k; ++j) {
-    const long long row = u_row(p, t, j);
-    if (row < 0) continue;  // a padded pick, the same in the whole row
-    const float g = p.gates ? p.gates[(long long)t * p.k + j] : 1.f;
-    float v[C::VALS];
-    load_row<C>(u + (size_t)row * p.d, p.d, lane, v);
+    for (int i = 0; i < C::NV; ++i) v[i] = load_chunk<C>(p, (i * C::TPR + lane) * C::EPC, d);
+  }
+  __device__ __forceinline__ void get(float (&f)[C::VALS]) const {
 #pragma unroll
-    for (int e = 0; e < C::VALS; ++e) y[e] = fmaf(g, v[e], y[e]);
+    for (int i = 0; i < C::NV; ++i) widen<C>(v[i], f + i * C::EPC);
+  }
+};
+
+// A token's picks, pick j in lane j of each wave (k <= 64): the row of u, -1 for
+// one outside it, and the gate. One load for all of them.
+struct Picks {
+  int32_t row;
+  float g;
+  __device__ __forceinline__ void load(const NormCall& p, long long t) {
+    const int j = threadIdx.x % kWave;
+    row = -1;
+    g = 1.f;
+    if (!p.u || j >= p.k || t >= p.T) return;
+    const int32_t at = (int32_t)(t * p.k + j);
+    row = p.inv ? p.inv[at] : at;
+    if (row >= p.M) row = -1;
+    if (p.gates) g = p.gates[at];
+  }
+  __device__ __forceinline__ int32_t row_of(int j) const {
+    return __builtin_amdgcn_readlane(row, j);
+  }
+  __device__ __forceinline__ float gate_of(int j) const {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), j));
+  }
+};
+
+// y += the picks j0 .. k - 1, ascending, four rows of u in flight.
+template <class C>
+__device__ __forceinline__ void add_picks(const NormCall& p, const Picks& picks, int j0, int lane,
+                                          float (&y)[C::VALS]) {
+  constexpr int U = C::NV == 1 ? 8 : 4;
+  for (int j = j0; j < p.k; j += U) {
+    RawRow<C> u[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (j + i >= p.k) continue;
+      const int32_t row = picks.row_of(j + i);
+      if (row >= 0) u[i].load(p.u, (size_t)row, p.d, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (j + i >= p.k || picks.row_of(j + i) < 0) continue;  // the same in the whole row
+      const float g = picks.gate_of(j + i);
+      float v[C::VALS];
+      u[i].get(v);
+#pragma unroll
+      for (int e = 0; e < C::VALS; ++e) y[e] = fmaf(g, v[e], y[e]);
+    }
   }
 }
 
@@ -156,6 +235,8 @@ __global__ __launch_bounds__(C::THREADS) void norm_kernel(NormCall p) {
   if (t64 >= p.T) return;  // a whole wave; whole workgroups where rows are theirs
   const int t = (int)t64;
   const size_t at = (size_t)t * p.d;
+  Picks picks;
+  picks.load(p, t);
   float r[C::VALS];
   if (p.r) {
     load_row<C>(static_cast<const T*>(p.r) + at, p.d, lane, r);
@@ -167,7 +248,9 @@ __global__ __launch_bounds__(C::THREADS) void norm_kernel(NormCall p) {
   }
   if (p.u) {
     float y[C::VALS];
-    sum_picks<C>(p, t, lane, y);
+#pragma unroll
+    for (int e = 0; e < C::VALS; ++e) y[e] = 0.f;
+    add_picks<C>(p, picks, 0, lane, y);
     if (p.w_post) {
       float w[C::VALS], s[1] = {0.f};
       load_weight<C>(p.w_post, p.d, lane, w);
@@ -195,32 +278,97 @@ __global__ __launch_bounds__(C::THREADS) void norm_kernel(NormCall p) {
   }
 }
 
+// What the gradient reads of a token, loaded a token ahead: its rows, and the
+// first K picks' rows of u (the picks two tokens ahead).
+template <class C, int K>
+struct TokenLoads {
+  RawRow<C> x, dn, dr, u[K];
+  Picks picks;
+  __device__ __forceinline__ void load(const NormCall& p, long long t, int lane) {
+    if (t >= p.T) return;
+    if (p.w_pre) {
+      x.load(p.x, (size_t)t, p.d, lane);
+      dn.load(p.dn, (size_t)t, p.d, lane);
+    }
+    if (p.dr_out) dr.load(p.dr_out, (size_t)t, p.d, lane);
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      const int32_t row = picks.row_of(j);
+      if (row >= 0) u[j].load(p.u, (size_t)row, p.d, lane);
+    }
+  }
+};
+
+// fp32 weights of this thread's columns: kept, or read again for each token
+// where a thread has many.
+template <class C>
+struct Weights {
+  static constexpr bool KEPT = C::VALS <= 8;
+  const float* p;
+  float v[KEPT ? C::VALS : 1];
+  __device__ __forceinline__ void init(const float* w, int d, int lane) {
+    p = w;
+    if constexpr (KEPT)
+      if (w) load_weight<C>(w, d, lane, v);
+  }
+  __device__ __forceinline__ void get(int d, int lane, float (&w)[C::VALS]) const {
+    if constexpr (KEPT) {
+#pragma unroll
+      for (int e = 0; e < C::VALS; ++e) w[e] = v[e];
+    } else {
+      load_weight<C>(p, d, lane, w);
+    }
+  }
+};
+
 // One workgroup takes ROWS tokens at a time, `gridDim.x` apart, and keeps the
 // weights' gradients of its columns in registers; they end as partial sums
-// part[side][workgroup][d], added in order by a second launch.
-template <class C>
+// part[side][workgroup][d], added in order by a second launch. A token is a
+// chain of loads, sums over its row and barriers, so the next token's loads are
+// issued before it. Its first K picks stay in registers for their dgates;
+// further ones are read again.
+template <class C, int K>
 __global__ __launch_bounds__(C::THREADS) void norm_bwd_kernel(NormCall p, float* part) {
-  __shared__ float lds[3 * (C::THREADS / kWave)];
+  __shared__ float lds[(K > 3 ? K : 3) * (C::THREADS / kWave)];
   __shared__ float fold[C::ROWS > 1 ? C::ROWS * C::TPR * C::VALS : 1];
   using T = typename C::T;
   const int lane = threadIdx.x % C::TPR, sub = threadIdx.x / C::TPR;
+  const long long stride = (long long)gridDim.x * C::ROWS;
   float dpre[C::VALS], dpost[C::VALS];
 #pragma unroll
   for (int e = 0; e < C::VALS; ++e) dpre[e] = dpost[e] = 0.f;
-  for (long long t0 = (long long)blockIdx.x * C::ROWS; t0 < p.T;
-       t0 += (long long)gridDim.x * C::ROWS) {
-    if (t0 + sub >= p.T) continue;  // whole waves (ROWS > 1 needs no barrier here)
-    const int t = (int)(t0 + sub);
-    const size_t at = (size_t)t * p.d;
+  const long long first = (long long)blockIdx.x * C::ROWS + sub;
+  TokenLoads<C, K> next;
+  next.picks.load(p, first);
+  if constexpr (C::AHEAD) next.load(p, first, lane);
+  Picks after;
+  after.load(p, first + stride);
+  Weights<C> w_pre, w_post;
+  w_pre.init(p.w_pre, p.d, lane);
+  w_post.init(p.w_post, p.d, lane);
+  // a wave of its own row stops with it; a workgroup's waves share theirs
+  for (long long t64 = first; t64 < p.T; t64 += stride) {
+    const size_t at = (size_t)t64 * p.d;
+    if constexpr (!C::AHEAD) next.load(p, t64, lane);
+    const TokenLoads<C, K> now = next;
+    next.picks = after;
+    after.load(p, t64 + 2 * stride);
+    if constexpr (C::AHEAD) next.load(p, t64 + stride, lane);
     float dr[C::VALS], y[C::VALS];
-    if (p.u) {
-      sum_picks<C>(p, t, lane, y);
-    } else {
 #pragma unroll
-      for (int e = 0; e < C::VALS; ++e) y[e] = 0.f;
+    for (int e = 0; e < C::VALS; ++e) y[e] = 0.f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      if (now.picks.row_of(j) < 0) continue;
+      const float g = now.picks.gate_of(j);
+      float v[C::VALS];
+      now.u[j].get(v);
+#pragma unroll
+      for (int e = 0; e < C::VALS; ++e) y[e] = fmaf(g, v[e], y[e]);
     }
+    if (p.u) add_picks<C>(p, now.picks, K, lane, y);
     if (p.dr_out) {
-      load_row<C>(static_cast<const T*>(p.dr_out) + at, p.d, lane, dr);
+      now.dr.get(dr);
     } else {
 #pragma unroll
       for (int e = 0; e < C::VALS; ++e) dr[e] = 0.f;
@@ -230,9 +378,9 @@ __global__ __launch_bounds__(C::THREADS) void norm_bwd_kernel(NormCall p, float*
     for (int e = 0; e < C::VALS; ++e) s[2] = fmaf(y[e], y[e], s[2]);
     if (p.w_pre) {
       float x[C::VALS], dn[C::VALS], w[C::VALS];
-      load_row<C>(static_cast<const T*>(p.x) + at, p.d, lane, x);
-      load_row<C>(static_cast<const T*>(p.dn) + at, p.d, lane, dn);
-      load_weight<C>(p.w_pre, p.d, lane, w);
+      now.x.get(x);
+      now.dn.get(dn);
+      w_pre.get(p.d, lane, w);
 #pragma unroll
       for (int e = 0; e < C::VALS; ++e) {
         s[0] = fmaf(x[e], x[e], s[0]);
@@ -255,7 +403,7 @@ __global__ __launch_bounds__(C::THREADS) void norm_bwd_kernel(NormCall p, float*
     for (int e = 0; e < C::VALS; ++e) dr[e] *= p.out_scale;
     if (p.w_post) {
       float w[C::VALS], b[1] = {0.f};
-      load_weight<C>(p.w_post, p.d, lane, w);
+      w_post.get(p.d, lane, w);
 #pragma unroll
       for (int e = 0; e < C::VALS; ++e) b[0] = fmaf(w[e] * dr[e], y[e], b[0]);
       row_sum<C, 1>(b, lds);
@@ -266,23 +414,54 @@ __global__ __launch_bounds__(C::THREADS) void norm_bwd_kernel(NormCall p, float*
         dr[e] = q * (w[e] * dr[e] - y[e] * m);
       }
     }
-    for (int j = 0; j < p.k; ++j) {
-      const long long row = u_row(p, t, j), pick = (long long)t * p.k + j;
-      float dg[1] = {0.f};
-      if (row >= 0) {
+    float dg[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      dg[j] = 0.f;
+      const int32_t row = now.picks.row_of(j);
+      if (row < 0) continue;
+      if (p.du)
+        store_row<C>(static_cast<T*>(p.du) + (size_t)row * p.d, p.d, lane, dr, now.picks.gate_of(j));
+      if (p.dgates) {
+        float v[C::VALS];
+        now.u[j].get(v);
+#pragma unroll
+        for (int e = 0; e < C::VALS; ++e) dg[j] = fmaf(dr[e], v[e], dg[j]);
+      }
+    }
+    if (p.dgates) {
+      row_sum<C, K>(dg, lds);
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (lane == 0 && j < p.k) p.dgates[t64 * p.k + j] = dg[j];
+    }
+    for (int j0 = K; j0 < p.k; j0 += 2) {
+      float d2[2] = {0.f, 0.f};
+      RawRow<C> u[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int32_t row = j0 + i < p.k ? now.picks.row_of(j0 + i) : -1;
+        if (row >= 0 && p.dgates) u[i].load(p.u, (size_t)row, p.d, lane);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int32_t row = j0 + i < p.k ? now.picks.row_of(j0 + i) : -1;
+        if (row < 0) continue;
         if (p.du)
           store_row<C>(static_cast<T*>(p.du) + (size_t)row * p.d, p.d, lane, dr,
-                       p.gates ? p.gates[pick] : 1.f);
+                       now.picks.gate_of(j0 + i));
         if (p.dgates) {
           float v[C::VALS];
-          load_row<C>(static_cast<const T*>(p.u) + (size_t)row * p.d, p.d, lane, v);
+          u[i].get(v);
 #pragma unroll
-          for (int e = 0; e < C::VALS; ++e) dg[0] = fmaf(dr[e], v[e], dg[0]);
+          for (int e = 0; e < C::VALS; ++e) d2[i] = fmaf(dr[e], v[e], d2[i]);
         }
       }
       if (p.dgates) {
-        row_sum<C, 1>(dg, lds);
-        if (lane == 0) p.dgates[pick] = dg[0];
+        row_sum<C, 2>(d2, lds);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (lane == 0 && j0 + i < p.k) p.dgates[t64 * p.k + j0 + i] = d2[i];
       }
     }
   }
@@ -319,29 +498,34 @@ __global__ __launch_bounds__(C::THREADS) void norm_bwd_kernel(NormCall p, float*
   }
 }
 
-// dw[c] = the partial sums of column c, in order: 64 columns a workgroup, four
-// waves taking a quarter of the parts each.
-__global__ __launch_bounds__(kThreads) void norm_weights_kernel(const float* part, int parts, int d,
-                                                                float* dw_pre, float* dw_post) {
-  __shared__ float lds[kThreads];
+// dw[c] = the partial sums of column c, in order and in 64 bits: 64 columns a
+// workgroup, sixteen waves taking a sixteenth of the parts each.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(64 * kSumWaves) void norm_weights_kernel(const float* part, int parts,
+                                                                      int d, float* dw_pre,
+                                                                      float* dw_post) {
+  __shared__ double lds[kSumWaves][64];
   float* dst = blockIdx.y ? dw_post : dw_pre;
   if (!dst) return;
-  const int col = blockIdx.x * 64 + threadIdx.x % 64, q = threadIdx.x / 64;
-  const int n = (parts + 3) / 4, lo = q * n, hi = min(parts, lo + n);
-  float s = 0.f;
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, col = blockIdx.x * 64 + lane;
+  const int n = (parts + kSumWaves - 1) / kSumWaves, lo = min(parts, wave * n),
+            hi = min(parts, lo + n);
+  double s = 0.0;
   if (col < d) {
     const float* src = part + (size_t)blockIdx.y * parts * d + col;
 #pragma unroll 8
-    for (int i = lo; i < hi; ++i) s += src[(size_t)i * d];
+    for (int i = lo; i < hi; ++i) s += (double)src[(size_t)i * d];
   }
-  lds[threadIdx.x] = s;
+  lds[wave][lane] = s;
   __syncthreads();
-  if (q == 0 && col < d)
-    dst[col] = ((s + lds[64 + threadIdx.x]) + lds[128 + threadIdx.x]) + lds[192 + threadIdx.x];
+  if (wave == 0 && col < d) {
+    for (int w = 1; w < kSumWaves; ++w) s += lds[w][lane];
+    dst[col] = (float)s;
+  }
 }
 
 // Workgroups of the gradient: enough rows each that their partial sums stay few.
-constexpr int kBwdGroups = 1024;
+constexpr int kBwdGroups = 768;
 
 template <class C>
 hipError_t launch_norm_cfg(const NormCall& c, hipStream_t s) {
@@ -353,30 +537,43 @@ template <class C>
 hipError_t launch_norm_bwd_cfg(const NormCall& c, float* part, hipStream_t s) {
   const size_t want = ((size_t)c.T + C::ROWS - 1) / C::ROWS;
   const int groups = (int)(want < kBwdGroups ? want : kBwdGroups);  // T = 0: no sums, dw = 0
-  const hipError_t e = groups ? launch_kernel(norm_bwd_kernel<C>, dim3(groups), dim3(C::THREADS), 0,
-                                              s, KernelTiming{}, c, part)
-                              : hipSuccess;
+  const auto launch = [&](auto kernel) {
+    return launch_kernel(kernel, dim3(groups), dim3(C::THREADS), 0, s, KernelTiming{}, c, part);
+  };
+  hipError_t e = hipSuccess;
+  if (groups) e = !c.u || c.k == 1 ? launch(norm_bwd_kernel<C, 1>) : launch(norm_bwd_kernel<C, 2>);
   if (e != hipSuccess || (!c.dw_pre && !c.dw_post)) return e;
-  return launch_kernel(norm_weights_kernel, dim3((c.d + 63) / 64, 2), dim3(kThreads), 0, s,
-                       KernelTiming{}, (const float*)part, groups, c.d, c.dw_pre, c.dw_post);
+  return launch_kernel(norm_weights_kernel, dim3((c.d + 63) / 64, 2),
+                       dim3(64 * kSumWaves), 0, s, KernelTiming{}, (const float*)part, groups, c.d, c.dw_pre, c.dw_post);
 }
 
-// f(config) for rows of d values: a wave per row up to 1024 values (fp32: 512),
-// 256 threads up to 4096 (2048), 1024 threads to 8192.
-template <typename T, bool ALIGNED, typename F>
+// f(config) for rows of d values (EPC per 16 bytes): a wave per row up to 128
+// chunks, then a workgroup. The gradient holds about ten values per column and
+// thread, so its long rows go to 512 threads (1024 would leave each 128
+// registers).
+template <bool BACK, typename T, bool ALIGNED, typename F>
 hipError_t with_width(int d, F f) {
   constexpr int EPC = 16 / sizeof(T);
   if (d <= 64 * EPC) return f(NormCfg<T, 64, 1, ALIGNED>{});
   if (d <= 128 * EPC) return f(NormCfg<T, 64, 2, ALIGNED>{});
   if (d <= 256 * EPC) return f(NormCfg<T, 256, 1, ALIGNED>{});
-  if (d <= 512 * EPC) return f(NormCfg<T, 256, 2, ALIGNED>{});
-  return f(NormCfg<T, 1024, sizeof(T) / 2, ALIGNED>{});
+  if constexpr (BACK) {
+    if (d <= 512 * EPC) return f(NormCfg<T, 512, 1, ALIGNED>{});
+    if (d <= 1024 * EPC) return f(NormCfg<T, 512, 2, ALIGNED>{});
+    if constexpr (EPC == 4) return f(NormCfg<T, 512, 4, ALIGNED>{});
+  } else {
+    if (d <= 512 * EPC) return f(NormCfg<T, 256, 2, ALIGNED>{});
+    if (d <= 1024 * EPC) return f(NormCfg<T, 1024, 1, ALIGNED>{});
+    if constexpr (EPC == 4) return f(NormCfg<T, 1024, 2, ALIGNED>{});
+  }
+  return hipErrorInvalidValue;
 }
-template <typename F>
+template <bool BACK, typename F>
 hipError_t with_cfg(bmoe_dtype dt, int d, F f) {
   if (dt == BMOE_BF16)
-    return d % 8 == 0 ? with_width<uint16_t, true>(d, f) : with_width<uint16_t, false>(d, f);
-  return d % 4 == 0 ? with_width<float, true>(d, f) : with_width<float, false>(d, f);
+    return d % 8 == 0 ? with_width<BACK, uint16_t, true>(d, f)
+                      : with_width<BACK, uint16_t, false>(d, f);
+  return d % 4 == 0 ? with_width<BACK, float, true>(d, f) : with_width<BACK, float, false>(d, f);
 }
 
 }  // namespace
@@ -387,11 +584,12 @@ size_t norm_part_bytes(int T, int d) {
 }
 
 hipError_t launch_norm(bmoe_dtype dt, const NormCall& c, hipStream_t s) {
-  return with_cfg(dt, c.d, [&](auto cfg) { return launch_norm_cfg<decltype(cfg)>(c, s); });
+  return with_cfg<false>(dt, c.d, [&](auto cfg) { return launch_norm_cfg<decltype(cfg)>(c, s); });
 }
 
 hipError_t launch_norm_bwd(bmoe_dtype dt, const NormCall& c, float* part, hipStream_t s) {
-  return with_cfg(dt, c.d, [&](auto cfg) { return launch_norm_bwd_cfg<decltype(cfg)>(c, part, s); });
+  return with_cfg<true>(
+      dt, c.d, [&](auto cfg) { return launch_norm_bwd_cfg<decltype(cfg)>(c, part, s); });
 }
 
 }  // namespace bmoe

@@ -69,11 +69,14 @@ __device__ __forceinline__ void dma16(const void* g, char* lds) {
                                    (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
 }
 
-// `n` elements at p (n <= 0: none) as one chunk, the rest zeros.
+// `n` elements at p (n <= 0: none) as one chunk, the rest zeros. Whole chunks
+// take one access, whatever their alignment.
 template <int ES>
 __device__ __forceinline__ u32x4 partial_chunk(const char* p, int n) {
   u32x4 v = {0u, 0u, 0u, 0u};
-  if constexpr (ES == 2) {
+  if (n >= 16 / ES) {
+    __builtin_memcpy(&v, p, 16);
+  } else if constexpr (ES == 2) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < n)
@@ -163,12 +166,10 @@ __device__ __forceinline__ int red_swz(int r, int ch) {
 // workgroup put in LDS.
 struct SameRow {
   static constexpr bool SAME = true;
-  __device__ __forceinline__ size_t operator()(int k) const { return (size_t)k; }
 };
 struct ListedRow {
   static constexpr bool SAME = false;
   const int32_t* list;
-  __device__ __forceinline__ size_t operator()(int k) const { return (size_t)list[k]; }
 };
 
 template <class C, int R, int LOADS, class MAP>
@@ -179,6 +180,9 @@ struct RedRowsSource {
   int c0, cols, K;
   MAP map;
   static constexpr bool SAME = MAP::SAME;
+  // ListedRow: the rows of the step that is loaded next (steps are loaded in
+  // order), read a step ahead so that no load waits for LDS.
+  int32_t row[SAME ? 1 : LOADS];
   static constexpr int CH = R / C::EPC;  // chunks per row
   // Columns c0 .. of `cols`; ALIGNED needs cols to be whole chunks (chunks past
   // the last repeat it: their outputs are not stored). A step's rows (SameRow)
@@ -199,11 +203,12 @@ struct RedRowsSource {
       const int c = c0 + red_swz<C::ES, R>(r, e % CH) * C::EPC;
       off[j] = (uint32_t)((C::ALIGNED ? min(c, cols - C::EPC) : min(c, cols - 1)) * C::ES);
       if constexpr (SAME) off[j] += (uint32_t)(r * ld);
+      else row[j] = map.list[min(r, K - 1)];
     }
   }
   __device__ __forceinline__ int whole_steps() const { return K / C::BK; }
   template <bool WHOLE>
-  __device__ __forceinline__ void load(char* region, int step, int lane, int wave) const {
+  __device__ __forceinline__ void load(char* region, int step, int lane, int wave) {
 #pragma unroll
     for (int q = 0; q < C::PARTS; ++q) {
       const char* b = base + q * part;
@@ -214,7 +219,10 @@ struct RedRowsSource {
         const int k = step * C::BK + r;
         const bool in = WHOLE || k < K;
         const char* g = b + off[j];
-        if constexpr (!SAME) g += map(in ? k : 0) * ld;
+        if constexpr (!SAME) {
+          g += (size_t)row[j] * ld;
+          row[j] = map.list[min(k + C::BK, K - 1)];
+        }
         char* dst = region + q * (R * C::KB) + (wave * LOADS + j) * 1024;
         if constexpr (!C::ALIGNED) {
           *reinterpret_cast<u32x4*>(dst + lane * 16) =
@@ -349,7 +357,7 @@ __device__ __forceinline__ void mma_slice(Acc<C>& acc, const u32x4 (&fa)[C::PART
 }
 
 template <class C, bool WHOLE, class SA, class SB>
-__device__ __forceinline__ void issue(char* stg, const SA& a, const SB& b, int step, int lane,
+__device__ __forceinline__ void issue(char* stg, SA& a, SB& b, int step, int lane,
                                       int wave) {
   a.template load<WHOLE>(stg, step, lane, wave);
   b.template load<WHOLE>(stg + C::A_BYTES, step, lane, wave);
@@ -401,7 +409,7 @@ struct Frags {
 // the slice before.
 template <class C, int S, bool WHOLE, class SA, class SB, class RA, class RB>
 __device__ __forceinline__ void step(Acc<C>& acc, Frags<C>& f, char* const (&ring)[C::NSTAGE],
-                                     const SA& a, const SB& b, const RA& ra, const RB& rb, int kt,
+                                     SA& a, SB& b, const RA& ra, const RB& rb, int kt,
                                      int lane, int wave) {
   // Every wave is done with step kt - 1 (the barrier in it), whose stage this
   // DMA overwrites.
@@ -429,7 +437,7 @@ __device__ __forceinline__ void step(Acc<C>& acc, Frags<C>& f, char* const (&rin
 
 template <class C, bool WHOLE, class SA, class SB, class RA, class RB>
 __device__ __forceinline__ void round(Acc<C>& acc, Frags<C>& f, char* const (&ring)[C::NSTAGE],
-                                      const SA& a, const SB& b, const RA& ra, const RB& rb, int kt,
+                                      SA& a, SB& b, const RA& ra, const RB& rb, int kt,
                                       int lane, int wave) {
   step<C, 0, WHOLE>(acc, f, ring, a, b, ra, rb, kt, lane, wave);
   step<C, 1, WHOLE>(acc, f, ring, a, b, ra, rb, kt + 1, lane, wave);
@@ -443,8 +451,8 @@ __device__ __forceinline__ void round(Acc<C>& acc, Frags<C>& f, char* const (&ri
 // same nsteps; on return no DMA is in flight, but other waves may still be
 // reading the ring.
 template <class C, class SA, class SB, class RA, class RB>
-__device__ __forceinline__ void run(Acc<C>& acc, char* const (&ring)[C::NSTAGE], const SA& a,
-                                    const SB& b, const RA& ra, const RB& rb, int nsteps, int lane,
+__device__ __forceinline__ void run(Acc<C>& acc, char* const (&ring)[C::NSTAGE], SA& a, SB& b,
+                                    const RA& ra, const RB& rb, int nsteps, int lane,
                                     int wave) {
 #pragma unroll
   for (int s = 0; s < C::AHEAD; ++s) {
