@@ -15,9 +15,6 @@
 //
 // P and Q are symmetric: only tiles on and below the diagonal are computed,
 // each written twice. Rows are padded to whole 16-byte chunks (zeros).
-#include <type_traits>
-#include <utility>
-
 #include "common.h"
 #include "kernels.h"
 #include "tile_product.h"
@@ -312,8 +309,8 @@ __global__ __launch_bounds__(C::THREADS) void ortho_product_kernel(OrthoArgs p) 
   __shared__ __attribute__((aligned(1024))) char st0[C::STAGE];
   __shared__ __attribute__((aligned(1024))) char st1[C::STAGE];
   __shared__ __attribute__((aligned(1024))) char st2[C::NSTAGE > 2 ? C::STAGE : 16];
-  static_assert(C::NSTAGE <= 3, "three stages");
-  char* all[3] = {st0, st1, st2};
+  __shared__ __attribute__((aligned(1024))) char st3[C::NSTAGE > 3 ? C::STAGE : 16];
+  char* all[4] = {st0, st1, st2, st3};
   char* ring[C::NSTAGE];
 #pragma unroll
   for (int i = 0; i < C::NSTAGE; ++i) ring[i] = all[i];
@@ -376,8 +373,10 @@ __global__ __launch_bounds__(C::THREADS) void ortho_product_kernel(OrthoArgs p) 
   }
 
   lds_barrier();  // every wave is done with the ring
-  static_assert(C::WAVES * Block::BYTES <= C::STAGE, "staging fits a stage");
-  float* stg = reinterpret_cast<float*>(st0) + wave * (Block::BYTES / 4);
+  constexpr int PER = C::STAGE / Block::BYTES;  // waves' staging a stage holds
+  static_assert(C::WAVES <= 2 * PER, "staging fits two stages");
+  float* stg =
+      reinterpret_cast<float*>((wave < PER ? st0 : st1) + (wave % PER) * Block::BYTES);
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
@@ -412,13 +411,33 @@ __global__ __launch_bounds__(C::THREADS) void ortho_product_kernel(OrthoArgs p) 
     }
 }
 
-// Tiles of 128 (four waves, two workgroups per CU), 192 (four waves of 96) and
-// 256 (eight waves of 128 x 64).
-template <int N, int AMODE, int BMODE>
-using Tile = std::conditional_t<
-    N == 256, Cfg<kF16, 2, 256, 256, 2, 4, 2, AMODE, BMODE, true>,
-    std::conditional_t<N == 192, Cfg<kF16, 2, 192, 192, 2, 2, 3, AMODE, BMODE, true>,
-                       Cfg<kF16, 2, 128, 128, 2, 2, 2, AMODE, BMODE, true>>>;
+// Tiles: of 128 x 128 (four waves, two workgroups per CU), 192 (four waves of 96)
+// and 256 (eight waves of 128 x 64). With no more of them than CUs, where a
+// launch lasts as long as its loads: 128 with eight waves and three steps ahead,
+// and 64 (four waves, 128 bytes of reduction a step, three steps ahead).
+enum TileKind { k64, k128Deep, k128, k192, k256 };
+template <int KIND, int A, int B>
+struct TileOf;
+template <int A, int B>
+struct TileOf<k64, A, B> {
+  using type = Cfg<kF16, 2, 64, 64, 2, 2, 4, A, B, true, 128>;
+};
+template <int A, int B>
+struct TileOf<k128Deep, A, B> {
+  using type = Cfg<kF16, 2, 128, 128, 2, 4, 4, A, B, true>;
+};
+template <int A, int B>
+struct TileOf<k128, A, B> {
+  using type = Cfg<kF16, 2, 128, 128, 2, 2, 2, A, B, true>;
+};
+template <int A, int B>
+struct TileOf<k192, A, B> {
+  using type = Cfg<kF16, 2, 192, 192, 2, 2, 3, A, B, true>;
+};
+template <int A, int B>
+struct TileOf<k256, A, B> {
+  using type = Cfg<kF16, 2, 256, 256, 2, 4, 2, A, B, true>;
+};
 
 template <int PRODUCT>
 int2 count_tiles(const OrthoArgs& p, int n) {  // of one matrix; per row of tiles
@@ -427,13 +446,13 @@ int2 count_tiles(const OrthoArgs& p, int n) {  // of one matrix; per row of tile
   return make_int2(PRODUCT == kApply ? tm * tn : tm * (tm + 1) / 2, tn);
 }
 
-template <int PRODUCT, bool TALL, int N>
+template <int PRODUCT, bool TALL, int KIND>
 hipError_t launch_tiles(OrthoArgs p, hipStream_t s) {
   constexpr int AMODE = (PRODUCT == kGram && !TALL) || (PRODUCT == kApply && TALL) ? kOutRows
                                                                                   : kRedRows;
   constexpr int BMODE = PRODUCT == kGram && !TALL ? kOutRows : kRedRows;
-  using C = Tile<N, AMODE, BMODE>;
-  const int2 c = count_tiles<PRODUCT>(p, N);
+  using C = typename TileOf<KIND, AMODE, BMODE>::type;
+  const int2 c = count_tiles<PRODUCT>(p, C::BM);
   p.tiles = c.x;
   p.tiles_n = c.y;
   const size_t items = (size_t)p.tiles * p.batch;
@@ -444,24 +463,343 @@ hipError_t launch_tiles(OrthoArgs p, hipStream_t s) {
                        KernelTiming{}, p);
 }
 
-// The tile by the time that the rounds of workgroups over 256 CUs take, in
-// units of a round of two workgroups per CU of 128 x 128 (one per CU: 0.55).
-// Measured at 4096 x 4096: whole products 351, 370 and 311 us, symmetric ones
-// 296, 210 and 256 us with tiles of 128, 192 and 256; 64 matrices 1024 x 512:
-// 150, 201, 136 and 111, 119, 110 us.
+// The tile: the deep ones as long as each CU gets one at most (two of 64) - 1000
+// x 1000 580 -> 230 us, 2048 x 2048 862 -> 687 us a call -, else by the time that
+// the rounds of workgroups over 256 CUs take, in units of a round of two
+// workgroups per CU of 128 x 128 (one per CU: 0.55). Measured at 4096 x 4096:
+// whole products 351, 370 and 311 us, symmetric ones 296, 210 and 256 us with
+// tiles of 128, 192 and 256; 64 matrices 1024 x 512: 150, 201, 136 and 111, 119,
+// 110 us.
 template <int PRODUCT, bool TALL>
 hipError_t launch_product(const OrthoArgs& p, hipStream_t s) {
-  const auto rounds = [&](int n, long long slots) {
-    const long long t = (long long)count_tiles<PRODUCT>(p, n).x * p.batch;
-    return std::make_pair(t / slots, t % slots);
+  const auto tiles = [&](int n) { return (long long)count_tiles<PRODUCT>(p, n).x * p.batch; };
+  if (tiles(64) <= 512) return launch_tiles<PRODUCT, TALL, k64>(p, s);
+  if (tiles(128) <= 256) return launch_tiles<PRODUCT, TALL, k128Deep>(p, s);
+  const long long n128 = tiles(128), rest = n128 % 512;
+  const double t128 = n128 / 512 + (rest > 256 ? 1.0 : rest > 0 ? 0.55 : 0.0);
+  const double t192 = 1.1 * ((tiles(192) + 255) / 256);
+  const double t256 = 1.75 * ((tiles(256) + 255) / 256);
+  if (t128 <= t192 && t128 <= t256) return launch_tiles<PRODUCT, TALL, k128>(p, s);
+  if (t192 <= t256) return launch_tiles<PRODUCT, TALL, k192>(p, s);
+  return launch_tiles<PRODUCT, TALL, k256>(p, s);
+}
+
+// ---- small matrices: the whole iteration in one workgroup --------------------------
+// min(rows, cols) <= 32 MB and max <= 256 NB: X [m][n] (transposed where rows >
+// cols) stays in registers, wave w holding the columns 32 NB w .. as MFMA
+// operands of two layouts:
+//   x1: lane = row m, eight columns n a slice     (P = X X^T)
+//   x2: lane = column n, eight rows m a slice     (Q X, X^T Q)
+// Accumulators of X^T Q (lane = column m, rows n) are x1's next values and those
+// of Q X (lane = column n, rows m) x2's, slice s of a block its registers 8 s ..
+// 8 s + 7: computing both costs MFMAs instead of transposing. This fixes the
+// order of the reduction inside a slice: element e of lane half h is index
+// 8 (e / 4) + 4 h + e % 4; all operands follow it. P is added over the waves, in
+// order, through LDS. One launch for 17: 64 x 512 fp32 141 -> 54 us, 64 of them
+// 57 us.
+constexpr int kSmallWaves = 8, kSmallThreads = 64 * kSmallWaves;
+constexpr int kPitch = 72;  // halves per row of P and Q in LDS
+
+struct SmallArgs {
+  Source src;
+  int rows, cols, steps, tall;
+  float a, b, c, eps;
+  void* o;
+  int o_bf16, update;
+  float keep, rate;
+};
+
+// The eight values of slice s in the order above, row `row` of P or Q.
+__device__ __forceinline__ u32x4 read_symmetric(const _Float16* q, int row, int s, int lane) {
+  const _Float16* p = q + row * kPitch + 16 * s + 4 * (lane >> 5);
+  const u32x2 x = *reinterpret_cast<const u32x2*>(p), y = *reinterpret_cast<const u32x2*>(p + 8);
+  return u32x4{x[0], x[1], y[0], y[1]};
+}
+// Operands are kept as dwords of two values: the loop over the steps would carry
+// single halves in a register each.
+__device__ __forceinline__ f32x16 mma3(const u32x4 (&a)[2], const u32x4 (&b)[2], f32x16 acc) {
+  mma<kF16>(acc, a[0], b[1]);
+  mma<kF16>(acc, a[1], b[0]);
+  mma<kF16>(acc, a[0], b[0]);
+  return acc;
+}
+__device__ __forceinline__ void split_slice(const f32x16& v, int s, float scale, u32x4 (&out)[2]) {
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const f32x2 x = {v[8 * s + 2 * e] * scale, v[8 * s + 2 * e + 1] * scale};
+    const f16x2 hi = __builtin_convertvector(x, f16x2);
+    const f32x2 back = __builtin_convertvector(hi, f32x2);
+    const f32x2 rest = {x[0] - back[0], x[1] - back[1]};
+    out[0][e] = __builtin_bit_cast(uint32_t, hi);
+    out[1][e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, f16x2));
+  }
+}
+
+// A block of the last iterate (lane = column ni, rows mi ..) to the result.
+template <typename T>
+__device__ __forceinline__ void store_small_as(const SmallArgs& p, T* out, const f32x16& x, int m,
+                                               int n, int mi, int ni, int lane) {
+  float w[16];
+  uint32_t at[16];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int row = mi + acc_row(r, lane);
+    at[r] = row >= m || ni >= n ? 0u : (uint32_t)(p.tall ? ni * p.cols + row : row * p.cols + ni);
+    w[r] = 0.f;
+  }
+  if (p.update) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      if constexpr (sizeof(T) == 2) w[r] = bf16_lo(out[at[r]]);
+      else w[r] = out[at[r]];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    float o = x[r] * (1.f / kScale) * (1.f / kScale);
+    if (p.update) o = fmaf(p.keep, w[r], -p.rate * o);
+    if (mi + acc_row(r, lane) < m && ni < n) {
+      if constexpr (sizeof(T) == 2) out[at[r]] = (T)f32_to_bf16_bits(o);
+      else out[at[r]] = o;
+    }
+  }
+}
+__device__ __forceinline__ void store_small(const SmallArgs& p, void* out, const f32x16& x, int m,
+                                            int n, int mi, int ni, int lane) {
+  if (p.o_bf16) store_small_as(p, static_cast<uint16_t*>(out), x, m, n, mi, ni, lane);
+  else store_small_as(p, static_cast<float*>(out), x, m, n, mi, ni, lane);
+}
+
+template <int MB, int NB>
+__global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(SmallArgs p) {
+  constexpr int BLOCKS = MB == 1 ? 1 : 3;  // of P on and above the diagonal
+  constexpr int RED = BLOCKS * 1024 > 1056 ? BLOCKS * 1024 : 1056;  // floats a wave
+  __shared__ float red[kSmallWaves][RED];
+  __shared__ __attribute__((aligned(16))) _Float16 P[2][32 * MB * kPitch], Q[2][32 * MB * kPitch];
+  __shared__ double dsum[kSmallWaves];
+  const int tid = threadIdx.x, lane = tid % kWave, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int m = p.tall ? p.cols : p.rows, n = p.tall ? p.rows : p.cols;
+  // this matrix; its entries' numbers take 16 bits
+  const size_t first = (size_t)blockIdx.x * p.rows * p.cols;
+  Source src = p.src;
+  src.u = static_cast<const char*>(src.u) + first * (src.bf16 ? 2 : 4);
+  if (src.momentum) src.momentum += first;
+  void* out = static_cast<char*>(p.o) + first * (p.o_bf16 ? 2 : 4);
+  const auto entry = [&](int mi, int ni) {
+    return p.tall ? (uint32_t)(ni * p.cols + mi) : (uint32_t)(mi * p.cols + ni);
   };
-  const auto r128 = rounds(128, 512), r192 = rounds(192, 256), r256 = rounds(256, 256);
-  const double t128 = r128.first + (r128.second > 256 ? 1.0 : r128.second > 0 ? 0.55 : 0.0);
-  const double t192 = 1.1 * (r192.first + (r192.second > 0));
-  const double t256 = 1.75 * (r256.first + (r256.second > 0));
-  if (t128 <= t192 && t128 <= t256) return launch_tiles<PRODUCT, TALL, 128>(p, s);
-  if (t192 <= t256) return launch_tiles<PRODUCT, TALL, 192>(p, s);
-  return launch_tiles<PRODUCT, TALL, 256>(p, s);
+  const int n0 = 32 * NB * wave + (lane & 31);  // this lane's column of block 0
+  const f32x16 zero = {};
+  const auto block_of = [](int i, int& r, int& c) {  // (0, 0), (0, 1), (1, 1)
+    r = i == 2;
+    c = i > 0;
+  };
+
+  // U, one entry a register as in an accumulator of Q X, and its norm. (Types are
+  // told apart outside of the loops, so that all loads are in flight together.)
+  f32x16 v[NB][MB];
+  const auto each = [&](auto f) {  // f(register, entry's number, whether it is one)
+    // (a value of its own, or the entries' numbers would be kept from one use to
+    // the next, in 32 MB NB registers)
+    int n1 = n0;
+    __asm__ volatile("" : "+v"(n1));
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int mi = 32 * mb + acc_row(r, lane), ni = n1 + 32 * nb;
+          const bool in = mi < m && ni < n;
+          float x = v[nb][mb][r];
+          f(x, in ? entry(mi, ni) : 0u, in);
+          v[nb][mb][r] = x;
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  if (src.bf16)
+    each([&](float& x, uint32_t i, bool in) {
+      const float u = bf16_lo(static_cast<const uint16_t*>(src.u)[i]);
+      x = in ? u : 0.f;
+    });
+  else
+    each([&](float& x, uint32_t i, bool in) {
+      const float u = static_cast<const float*>(src.u)[i];
+      x = in ? u : 0.f;
+    });
+  if (src.momentum)
+    each([&](float& x, uint32_t i, bool in) {
+      const float mo = fmaf(src.beta, src.momentum[i], x);
+      if (in) src.momentum[i] = mo;
+      x = in ? mixed(src, x, mo) : 0.f;
+    });
+  double acc2 = 0.0;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        acc2 = fma((double)v[nb][mb][r], (double)v[nb][mb][r], acc2);
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) acc2 += __shfl_xor(acc2, o, 64);
+  if (lane == 0) dsum[wave] = acc2;
+  __syncthreads();
+  double total = 0.0;
+#pragma unroll
+  for (int w = 0; w < kSmallWaves; ++w) total += dsum[w];
+  const float norm = (float)sqrt(total) + p.eps;
+
+  u32x4 x1[MB][2 * NB][2], x2[NB][2 * MB][2];  // [..][slice][part]
+  float* mine = red[wave];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      f32x16 x;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) x[r] = v[nb][mb][r] / norm * kScale;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) split_slice(x, s, 1.f, x2[nb][2 * mb + s]);
+      // the other layout once through LDS (33 floats a row: no bank twice)
+      Block::order();
+#pragma unroll
+      for (int r = 0; r < 16; ++r) mine[acc_row(r, lane) * 33 + (lane & 31)] = x[r];
+      Block::order();
+      f32x16 t;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) t[r] = mine[(lane & 31) * 33 + acc_row(r, lane)];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) split_slice(t, s, 1.f, x1[mb][2 * nb + s]);
+      __builtin_amdgcn_sched_barrier(0);  // (the next block's registers are this one's)
+    }
+
+  // Q of the current X, in LDS
+  const auto make_q = [&]() {
+    // P of this wave's columns
+    __syncthreads();  // red, P and Q have been read
+#pragma unroll
+    for (int i = 0; i < BLOCKS; ++i) {
+      int br, bc;
+      block_of(i, br, bc);
+      f32x16 acc = zero;
+#pragma unroll
+      for (int s = 0; s < 2 * NB; ++s) acc = mma3(x1[br][s], x1[bc][s], acc);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) mine[i * 1024 + r * 64 + lane] = acc[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < BLOCKS * 2; ++j) {
+      const int e = tid + j * kSmallThreads, i = e / 1024, r = e % 1024 / 64, l = e % 64;
+      float sum = red[0][e];
+#pragma unroll
+      for (int w = 1; w < kSmallWaves; ++w) sum += red[w][e];
+      int br, bc;
+      block_of(i, br, bc);
+      const int row = 32 * br + acc_row(r, l), col = 32 * bc + (l & 31);
+      _Float16 hi, lo;
+      split(sum * (1.f / kScale), hi, lo);
+      P[0][row * kPitch + col] = hi;
+      P[1][row * kPitch + col] = lo;
+      if (br != bc) {
+        P[0][col * kPitch + row] = hi;
+        P[1][col * kPitch + row] = lo;
+      }
+    }
+    __syncthreads();
+    // Q = a I + b P + c P P, a block a wave
+    if (wave < BLOCKS) {
+      int br, bc;
+      block_of(wave, br, bc);
+      f32x16 acc = zero;
+#pragma unroll
+      for (int s = 0; s < 2 * MB; ++s) {
+        u32x4 fa[2], fb[2];
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          fa[part] = read_symmetric(P[part], 32 * br + (lane & 31), s, lane);
+          fb[part] = read_symmetric(P[part], 32 * bc + (lane & 31), s, lane);
+        }
+        acc = mma3(fa, fb, acc);
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int row = 32 * br + acc_row(r, lane), col = 32 * bc + (lane & 31);
+        const float pv = (float)P[0][row * kPitch + col] + (float)P[1][row * kPitch + col];
+        float q = fmaf(p.c, acc[r] * (1.f / kScale), p.b * pv);
+        if (row == col) q += p.a * kScale;
+        _Float16 hi, lo;
+        split(q, hi, lo);
+        Q[0][row * kPitch + col] = hi;
+        Q[1][row * kPitch + col] = lo;
+        if (br != bc) {
+          Q[0][col * kPitch + row] = hi;
+          Q[1][col * kPitch + row] = lo;
+        }
+      }
+    }
+    __syncthreads();
+  };
+  const auto read_q = [&](int mb, u32x4 (&q)[2 * MB][2]) {
+#pragma unroll
+    for (int s = 0; s < 2 * MB; ++s)
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+        q[s][part] = read_symmetric(Q[part], 32 * mb + (lane & 31), s, lane);
+  };
+
+  for (int step = 1; step < p.steps; ++step) {
+    make_q();
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      f32x16 next[MB];
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        u32x4 q[2 * MB][2];
+        read_q(mb, q);
+        next[mb] = zero;  // Q X
+        f32x16 t = zero;  // X^T Q
+#pragma unroll
+        for (int s = 0; s < 2 * MB; ++s) {
+          next[mb] = mma3(q[s], x2[nb][s], next[mb]);
+          t = mma3(x2[nb][s], q[s], t);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) split_slice(t, s, 1.f / kScale, x1[mb][2 * nb + s]);
+        __builtin_amdgcn_sched_barrier(0);  // (two blocks at a time would spill)
+      }
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) split_slice(next[mb], s, 1.f / kScale, x2[nb][2 * mb + s]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  make_q();
+  int n1 = n0;  // (as above)
+  __asm__ volatile("" : "+v"(n1));
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      u32x4 q[2 * MB][2];
+      read_q(mb, q);
+      f32x16 x = zero;
+#pragma unroll
+      for (int s = 0; s < 2 * MB; ++s) x = mma3(q[s], x2[nb][s], x);
+      store_small(p, out, x, m, n, 32 * mb, n1 + 32 * nb, lane);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+template <int MB, int NB>
+hipError_t launch_small(const SmallArgs& p, int batch, hipStream_t s) {
+  return launch_kernel(ortho_small_kernel<MB, NB>, dim3(batch), dim3(kSmallThreads), 0, s,
+                       KernelTiming{}, p);
 }
 
 int padded(int n) { return (n + 7) / 8 * 8; }
@@ -496,6 +834,33 @@ size_t ortho_workspace_bytes(int batch, int rows, int cols) {
 
 hipError_t launch_ortho(const OrthoCall& call, void* ws, hipStream_t s) {
   const int batch = call.batch, rows = call.rows, cols = call.cols;
+  const int low = rows < cols ? rows : cols, high = rows < cols ? cols : rows;
+  if (low <= 64 && high <= (low <= 32 ? 1024 : 512)) {
+    SmallArgs p;
+    p.src.u = call.u;
+    p.src.momentum = call.momentum;
+    p.src.beta = call.beta;
+    p.src.nesterov = call.nesterov;
+    p.src.bf16 = call.u_bf16;
+    p.rows = rows;
+    p.cols = cols;
+    p.steps = call.steps;
+    p.tall = rows > cols;
+    p.a = call.a;
+    p.b = call.b;
+    p.c = call.c;
+    p.eps = call.eps;
+    p.o = call.o;
+    p.o_bf16 = call.o_bf16;
+    p.update = call.update;
+    p.keep = call.keep;
+    p.rate = call.rate;
+    if (low <= 32)
+      return high <= 256   ? launch_small<1, 1>(p, batch, s)
+             : high <= 512 ? launch_small<1, 2>(p, batch, s)
+                           : launch_small<1, 4>(p, batch, s);
+    return high <= 256 ? launch_small<2, 1>(p, batch, s) : launch_small<2, 2>(p, batch, s);
+  }
   const Layout l = layout(batch, rows, cols);
   char* base = static_cast<char*>(ws);
   double* part = reinterpret_cast<double*>(base + l.part);
