@@ -231,7 +231,7 @@ __global__ __launch_bounds__(C::THREADS) void norm_kernel(NormCall p) {
   __shared__ float lds[C::THREADS / kWave];
   using T = typename C::T;
   const int lane = threadIdx.x % C::TPR;
-  const long long t64 = (long long)blockIdx.x * C::ROWS + threadIdx.x / C::TPR;
+  const long long t64 = (long long)grid_block() * C::ROWS + threadIdx.x / C::TPR;
   if (t64 >= p.T) return;  // a whole wave; whole workgroups where rows are theirs
   const int t = (int)t64;
   const size_t at = (size_t)t * p.d;
@@ -530,8 +530,8 @@ constexpr int kBwdGroups = 768;
 template <class C>
 hipError_t launch_norm_cfg(const NormCall& c, hipStream_t s) {
   const size_t groups = ((size_t)c.T + C::ROWS - 1) / C::ROWS;
-  return launch_kernel(norm_kernel<C>, dim3((unsigned)groups), dim3(C::THREADS), 0, s,
-                       KernelTiming{}, c);
+  return launch_kernel(norm_kernel<C>, grid_rows(groups), dim3(C::THREADS), 0, s, KernelTiming{},
+                       c);
 }
 template <class C>
 hipError_t launch_norm_bwd_cfg(const NormCall& c, float* part, hipStream_t s) {
