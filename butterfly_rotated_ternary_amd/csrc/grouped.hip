@@ -48,7 +48,7 @@ __device__ __forceinline__ GroupTile find_tile(const int32_t* offsets, int G, in
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int2 r = rows[u];
-      const int n = (r.y - r.x + MOST - 1) / MOST * tiles_n;
+      const int n = (int)(((unsigned)(r.y - r.x) + MOST - 1) / MOST) * tiles_n;
       const int incl = wave_incl_scan(n);
       const uint64_t past = __ballot(before + incl > t);
       if (past) {
@@ -56,7 +56,8 @@ __device__ __forceinline__ GroupTile find_tile(const int32_t* offsets, int G, in
         const int items = __builtin_amdgcn_readlane(n, src);
         const int at = t - before - (__builtin_amdgcn_readlane(incl, src) - items);
         GroupTile g;
-        g.e = e1 + u * kWave + src;
+        // (offsets that do not ascend can overflow the sum: no tile then)
+        g.e = (unsigned)at < (unsigned)items ? e1 + u * kWave + src : -1;
         g.lo = __builtin_amdgcn_readlane(r.x, src);
         g.hi = __builtin_amdgcn_readlane(r.y, src);
         g.tiles = items / tiles_n;
@@ -219,7 +220,7 @@ __global__ __launch_bounds__(F::Most::THREADS) void grouped_kernel(ProductArgs p
   const int item = xcd_item(grid_block(), run_items);
   const GroupTile g = find_tile<F::Most::BM>(p.offsets, p.G, p.M, p.tiles_n, item, lane);
   if (g.e < 0) return;  // the whole workgroup
-  const int height = ((g.hi - g.lo + g.tiles - 1) / g.tiles + 63) / 64 * 64;
+  const int height = (((unsigned)(g.hi - g.lo) + g.tiles - 1) / g.tiles + 63) / 64 * 64;
   TileRows t;
   t.e = g.e;
   t.row0 = g.lo + g.i * height;
@@ -237,72 +238,57 @@ __global__ __launch_bounds__(F::Most::THREADS) void grouped_kernel(ProductArgs p
 }
 
 // ---- groups of few rows (bf16): bound by reading W ------------------------------
-// A workgroup computes 16 columns of c for up to 16 TB rows of a group: each of
-// its four waves takes a quarter of K straight from memory into
+// A workgroup computes 16 columns of c for up to 16 rows of a group: each of its
+// four waves takes a quarter of K straight from memory into
 // v_mfma_f32_16x16x32_bf16 (W's rows as the first operand, so a lane ends with
 // four neighbours of a row of c), eight loads of W in flight; the quarters are
 // added in order through LDS. Nothing is shared that LDS could keep: W is read
 // once, and the rows of a come from L2.
-typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
-constexpr int kFewCols = 16;
+constexpr int kFewRows = 16, kFewCols = 16;
 constexpr int kFewWaves = 4;
 
-template <int TB>
 __global__ __launch_bounds__(64 * kFewWaves) void grouped_few_kernel(ProductArgs p) {
-  constexpr int U = TB == 1 ? 8 : 4;  // slices of 32 in flight
-  __shared__ f32x4 sums[kFewWaves][TB][64];
+  constexpr int U = 8;  // slices of 32 in flight
+  __shared__ f32x4 sums[kFewWaves][64];
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const GroupTile g =
-      find_tile<16 * TB>(p.offsets, p.G, p.M, p.tiles_n, (int)grid_block(), lane);
+      find_tile<kFewRows>(p.offsets, p.G, p.M, p.tiles_n, (int)grid_block(), lane);
   if (g.e < 0) return;  // the whole workgroup
-  const int row0 = g.lo + g.i * 16 * TB, rows = min(16 * TB, g.hi - row0);
+  const int row0 = g.lo + g.i * kFewRows, rows = min(kFewRows, g.hi - row0);
   const int col0 = g.col_tile * kFewCols;
   const int slices = (p.red + 31) / 32, per = (slices + kFewWaves - 1) / kFewWaves;
   const int s0 = wave * per, s1 = min(slices, s0 + per);
   const int k0 = 8 * (lane >> 4);  // this lane's chunk of a slice
   const uint16_t* w = reinterpret_cast<const uint16_t*>(p.w) +
                       ((size_t)g.e * p.cols + min(col0 + (lane & 15), p.cols - 1)) * p.red + k0;
-  const uint16_t* a[TB];
-#pragma unroll
-  for (int b = 0; b < TB; ++b) {
-    const int q = row0 + min(16 * b + (lane & 15), rows - 1);
-    a[b] = reinterpret_cast<const uint16_t*>(p.a) + (size_t)a_row(p, q) * p.red + k0;
-  }
-  f32x4 acc[TB];
-#pragma unroll
-  for (int b = 0; b < TB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const uint16_t* a = reinterpret_cast<const uint16_t*>(p.a) +
+                      (size_t)a_row(p, row0 + min(lane & 15, rows - 1)) * p.red + k0;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   for (int s = s0; s < s1; s += U) {
-    uint4 wv[U], av[TB][U];
+    uint4 wv[U], av[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool in = s + u < s1 && 32 * (s + u) + k0 < p.red;
       wv[u] = in ? *reinterpret_cast<const uint4*>(w + 32 * (s + u)) : zero;
-#pragma unroll
-      for (int b = 0; b < TB; ++b)
-        av[b][u] = in ? *reinterpret_cast<const uint4*>(a[b] + 32 * (s + u)) : zero;
+      av[u] = in ? *reinterpret_cast<const uint4*>(a + 32 * (s + u)) : zero;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int b = 0; b < TB; ++b)
-        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8v, wv[u]),
-                                                         __builtin_bit_cast(bf16x8v, av[b][u]),
-                                                         acc[b], 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wv[u]),
+                                                    __builtin_bit_cast(bf16x8, av[u]), acc, 0, 0, 0);
   }
-#pragma unroll
-  for (int b = 0; b < TB; ++b) sums[wave][b][lane] = acc[b];
+  sums[wave][lane] = acc;
   __syncthreads();
-  for (int b = wave; b < TB; b += kFewWaves) {
-    f32x4 c = sums[0][b][lane];
+  if (wave) return;
+  f32x4 c = sums[0][lane];
 #pragma unroll
-    for (int v = 1; v < kFewWaves; ++v) c += sums[v][b][lane];
-    const int row = 16 * b + (lane & 15), col = col0 + 4 * (lane >> 4);
-    if (row < rows && col < p.cols)  // (cols is a multiple of 8)
-      *reinterpret_cast<uint2*>(p.c + ((size_t)(row0 + row) * p.cols + col) * 2) =
-          make_uint2(pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3]));
-  }
+  for (int v = 1; v < kFewWaves; ++v) c += sums[v][lane];
+  const int row = lane & 15, col = col0 + 4 * (lane >> 4);
+  if (row < rows && col < p.cols)  // (cols is a multiple of 8)
+    *reinterpret_cast<uint2*>(p.c + ((size_t)(row0 + row) * p.cols + col) * 2) =
+        make_uint2(pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3]));
 }
 
 // dW: one workgroup per expert, tile of its O x K entries and range of its rows
@@ -341,9 +327,9 @@ __global__ __launch_bounds__(C::THREADS) void grouped_dw_kernel(DwArgs p, int ru
   const int t = item % tiles;
   const int o0 = t / p.tiles_k * C::BM, k0 = t % p.tiles_k * C::BN;
   int2 rows = group_rows_of(p.offsets, e, p.M);
-  const int len = (rows.y - rows.x + p.splits - 1) / p.splits;
-  rows.x = min(rows.y, rows.x + split * len);
-  rows.y = min(rows.y, rows.x + len);
+  const unsigned all_rows = rows.y - rows.x, len = (all_rows + p.splits - 1) / p.splits;
+  rows.x += (int)min(all_rows, split * len);
+  const int count = (int)min((unsigned)(rows.y - rows.x), len);
 
   Acc<C> acc;
   clear<C>(acc);
@@ -352,8 +338,9 @@ __global__ __launch_bounds__(C::THREADS) void grouped_dw_kernel(DwArgs p, int ru
   ra.init(wm * C::TM, lane);
   Reader<C, kRedRows, C::BN, C::FN> rb;
   rb.init(wn * C::TN, lane);
-  for (int q0 = rows.x; q0 < rows.y; q0 += kListRows) {
-    const int n = min(kListRows, rows.y - q0);
+  for (int done = 0, n; done < count; done += n) {
+    const int q0 = rows.x + done;
+    n = min(kListRows, count - done);
     __syncthreads();  // every wave is done with the list and the ring
     for (int i = threadIdx.x; i < n; i += C::THREADS) {
       const int q = q0 + i;
@@ -414,11 +401,10 @@ hipError_t launch_grouped_cfg(ProductArgs p, hipStream_t s) {
                        dim3(F::Most::THREADS), 0, s, KernelTiming{}, p, run_items);
 }
 
-template <int TB>
 hipError_t launch_few(ProductArgs p, hipStream_t s) {
   p.tiles_n = (p.cols + kFewCols - 1) / kFewCols;
-  const size_t tiles_m = (size_t)p.M / (16 * TB) + (p.G < p.M ? p.G : p.M);
-  return launch_kernel(grouped_few_kernel<TB>, grid_rows(tiles_m * p.tiles_n),
+  const size_t tiles_m = (size_t)p.M / kFewRows + (p.G < p.M ? p.G : p.M);
+  return launch_kernel(grouped_few_kernel, grid_rows(tiles_m * p.tiles_n),
                        dim3(64 * kFewWaves), 0, s, KernelTiming{}, p);
 }
 
@@ -461,7 +447,7 @@ hipError_t launch_grouped_type(const ProductArgs& p, hipStream_t s) {
     // of 256, 2048 x 1408, 12.3 us against 20 (memory 9.1); 72 rows of 13 experts,
     // 640 x 2640 (546 tiles), 18 against 11.
     if (BMODE == kOutRows && p.cols % 8 == 0 && p.M / used <= 16 && items(128, 64) < 256)
-      return launch_few<1>(p, s);
+      return launch_few(p, s);
     if (t256 < t128 && t256 < t64)
       return launch_grouped_cfg<Family<E, 4, 256, 4, 4, BMODE, true>>(p, s);
   }

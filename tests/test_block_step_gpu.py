@@ -257,3 +257,31 @@ def test_matrices_past_32_bits():
         # (other tiles: sums in another order, then a rounding to bf16)
         diff = (o[i].double() - alone.double()).norm() / alone.double().norm()
         assert float(diff) <= 2.0 ** -8, i
+
+
+def test_most_rows():
+    """2^31 - 1 rows, the most there can be: their numbers' last sums do not wrap."""
+    M = 2 ** 31 - 1
+    off = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    a = torch.zeros(M, 1, dtype=BF, device="cuda")
+    dc = torch.zeros(M, 1, dtype=BF, device="cuda")
+    w = torch.full((1, 1, 1), 3.0, dtype=BF, device="cuda")
+    tail = torch.arange(1, 41, dtype=BF, device="cuda")[:, None]
+    a[-40:], dc[-40:] = tail, 2 * tail
+    a[5], dc[5] = 100.0, 1.0
+    c = bmoe.grouped_product(a, w, off)
+    assert torch.equal(c[-40:], 3 * tail) and float(c[5]) == 300.0
+    assert int(torch.count_nonzero(c)) == 41
+    del c
+    g = bmoe.grouped_product_backward(a, w, off, dc)
+    assert float(g["dw"]) == 100.0 + 2.0 * sum(i * i for i in range(1, 41))
+    assert torch.equal(g["da"][-40:], 6 * tail) and int(torch.count_nonzero(g["da"])) == 41
+    del a, dc, g
+    ids = torch.ones(M, 1, dtype=torch.int32, device="cuda")
+    ids[-3:] = 0
+    ids[7] = 9                                           # a padded pick
+    off, perm, inv = bmoe.group_rows(ids, 2)
+    assert off.tolist() == [0, 3, M - 1]
+    assert perm[:5].tolist() == [M - 3, M - 2, M - 1, 0, 1] and int(perm[-1]) == 7
+    assert inv[-4:].tolist() == [M - 2, 0, 1, 2] and int(inv[7]) == -1
+    assert torch.equal(perm[3 + 7:3 + 1000], torch.arange(8, 1001, dtype=torch.int32, device="cuda"))
