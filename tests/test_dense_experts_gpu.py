@@ -172,3 +172,23 @@ def test_large_tiles_many_rows(dt):
     mda, mdw = O.grouped_product_backward(abs(A), abs(W), o, rows, abs(D))
     close(r["da"], rda, mda, 520, dt)
     close(r["dw"], rdw, mdw, int(np.diff(o).max()), F32)
+
+
+# Tiles 256 columns wide at every height (64 to 256 rows, and groups of several),
+# of 128 columns, aligned and not; gradients of 256 x 256 and 128 x 128 entries
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,K,O_,N,k,skew", [(4110, 520, 1032, 60, 2, 0.3), (2050, 200, 1000, 16, 2, 0.2),
+                                             (2050, 201, 1000, 16, 2, 0.2),
+                                             (4110, 264, 259, 40, 2, 0.3)])
+def test_every_tile(T, K, O_, N, k, skew, dt):
+    ids, a, w, dc = draw(T, K, O_, N, k, dt, seed=K, skew=skew)
+    off, perm, inv = bmoe.group_rows(ids.cuda(), N)
+    c = bmoe.grouped_product(a.cuda(), w.cuda(), off, perm=perm, k=k)
+    r = bmoe.grouped_product_backward(a.cuda(), w.cuda(), off, dc.cuda(), perm=perm, k=k)
+    o, rows = off.cpu().numpy(), perm.cpu().numpy() // k
+    A, W, D = f64(a), f64(w), f64(dc)
+    close(c, O.grouped_product(A, W, o, rows), O.grouped_product(abs(A), abs(W), o, rows), K, dt)
+    rda, rdw = O.grouped_product_backward(A, W, o, rows, D)
+    mda, mdw = O.grouped_product_backward(abs(A), abs(W), o, rows, abs(D))
+    close(r["da"], rda, mda, O_, dt)
+    close(r["dw"], rdw, mdw, int(np.diff(o).max()), F32)

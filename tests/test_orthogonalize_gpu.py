@@ -121,3 +121,17 @@ def test_same_bits_each_run():
     first = bmoe.orthogonalize(u)
     for _ in range(3):
         assert torch.equal(first, bmoe.orthogonalize(u))
+
+
+# Batches and sizes whose launches take each of the tiles (64, 128 eight waves deep,
+# 128, 192 and 256), wide and tall, whole chunks and not
+@pytest.mark.parametrize("shape", [(1, 1500, 1510), (1, 2050, 2100), (42, 550, 561), (64, 500, 510),
+                                   (80, 500, 512)])
+@pytest.mark.parametrize("tall", [False, True])
+def test_every_tile(shape, tall):
+    B, m, n = shape
+    u = randn((B, n, m) if tall else shape, F32, B, 0.01)
+    steps = 1 if B == 1 else 5
+    o = bmoe.orthogonalize(u.cuda(), bmoe.OrthoSpec(steps))
+    for i in {0, B // 2, B - 1}:
+        assert rel(o[i], O.newton_schulz(f64(u[i]), steps)) <= tol(steps, F32), i
