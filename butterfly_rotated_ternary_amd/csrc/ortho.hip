@@ -484,10 +484,10 @@ hipError_t launch_product(const OrthoArgs& p, hipStream_t s) {
   return launch_tiles<PRODUCT, TALL, k256>(p, s);
 }
 
-// ---- small matrices: the whole iteration in one workgroup --------------------------
-// min(rows, cols) <= 32 MB and max <= 256 NB: X [m][n] (transposed where rows >
-// cols) stays in registers, wave w holding the columns 32 NB w .. as MFMA
-// operands of two layouts:
+// ---- small sides: the iteration with X in registers --------------------------------
+// X [m][n] (transposed where rows > cols) with m <= 32 MB. A workgroup holds 256 NB
+// columns of it in registers, wave w the columns 32 NB w .. as MFMA operands of
+// two layouts:
 //   x1: lane = row m, eight columns n a slice     (P = X X^T)
 //   x2: lane = column n, eight rows m a slice     (Q X, X^T Q)
 // Accumulators of X^T Q (lane = column m, rows n) are x1's next values and those
@@ -495,8 +495,7 @@ hipError_t launch_product(const OrthoArgs& p, hipStream_t s) {
 // 8 s + 7: computing both costs MFMAs instead of transposing. This fixes the
 // order of the reduction inside a slice: element e of lane half h is index
 // 8 (e / 4) + 4 h + e % 4; all operands follow it. P is added over the waves, in
-// order, through LDS. One launch for 17: 64 x 512 fp32 141 -> 54 us, 64 of them
-// 57 us.
+// order, through LDS.
 constexpr int kSmallWaves = 8, kSmallThreads = 64 * kSmallWaves;
 constexpr int kPitch = 72;  // halves per row of P and Q in LDS
 
@@ -507,6 +506,50 @@ struct SmallArgs {
   void* o;
   int o_bf16, update;
   float keep, rate;
+  // matrices in slabs
+  const double* part;  // [batch][parts]: sums of squares
+  int parts;
+  u32x4* x;            // [batch][slabs]: x2, as the lanes hold it
+  const float* p_in;   // [batch][slabs]: sums of P over the slabs' columns
+  float* p_out;
+};
+
+// Operands are kept as dwords of two values: the loop over the steps would carry
+// single halves in a register each.
+template <int MB, int NB>
+struct Operands {
+  u32x4 x1[MB][2 * NB][2], x2[NB][2 * MB][2];  // [..][slice][part]
+};
+template <int MB, int NB>
+using Entries = f32x16[NB][MB];  // as accumulators of Q X
+
+template <int MB>
+struct SmallLds {
+  static constexpr int BLOCKS = MB == 1 ? 1 : 3;  // of P on and above the diagonal
+  static constexpr int RED = BLOCKS * 1024 > 1056 ? BLOCKS * 1024 : 1056;  // floats a wave
+  __attribute__((aligned(16))) _Float16 P[2][32 * MB * kPitch], Q[2][32 * MB * kPitch];
+  double dsum[kSmallWaves];
+  float red[kSmallWaves][RED];
+  __device__ __forceinline__ static void block_of(int i, int& r, int& c) {  // (0, 0), (0, 1), (1, 1)
+    r = i == 2;
+    c = i > 0;
+  }
+};
+
+// This workgroup's matrix.
+struct SmallMatrix {
+  int m, n;
+  Source src;
+  void* out;
+  __device__ __forceinline__ SmallMatrix(const SmallArgs& p, int batch) {
+    m = p.tall ? p.cols : p.rows;
+    n = p.tall ? p.rows : p.cols;
+    const size_t first = (size_t)batch * p.rows * p.cols;
+    src = p.src;
+    src.u = static_cast<const char*>(src.u) + first * (src.bf16 ? 2 : 4);
+    if (src.momentum) src.momentum += first;
+    out = static_cast<char*>(p.o) + first * (p.o_bf16 ? 2 : 4);
+  }
 };
 
 // The eight values of slice s in the order above, row `row` of P or Q.
@@ -515,8 +558,6 @@ __device__ __forceinline__ u32x4 read_symmetric(const _Float16* q, int row, int 
   const u32x2 x = *reinterpret_cast<const u32x2*>(p), y = *reinterpret_cast<const u32x2*>(p + 8);
   return u32x4{x[0], x[1], y[0], y[1]};
 }
-// Operands are kept as dwords of two values: the loop over the steps would carry
-// single halves in a register each.
 __device__ __forceinline__ f32x16 mma3(const u32x4 (&a)[2], const u32x4 (&b)[2], f32x16 acc) {
   mma<kF16>(acc, a[0], b[1]);
   mma<kF16>(acc, a[1], b[0]);
@@ -533,6 +574,208 @@ __device__ __forceinline__ void split_slice(const f32x16& v, int s, float scale,
     const f32x2 rest = {x[0] - back[0], x[1] - back[1]};
     out[0][e] = __builtin_bit_cast(uint32_t, hi);
     out[1][e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, f16x2));
+  }
+}
+
+// f(register, entry's number, whether it is one) for the lane's entries from
+// column n0 on.
+template <int MB, int NB, class F>
+__device__ __forceinline__ void each_entry(const SmallArgs& p, const SmallMatrix& x, int n0, int lane,
+                                           Entries<MB, NB>& v, F f) {
+  // (a value of its own, or the entries' numbers would be kept from one use to
+  // the next, in 32 MB NB registers)
+  int n1 = n0;
+  __asm__ volatile("" : "+v"(n1));
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int mi = 32 * mb + acc_row(r, lane), ni = n1 + 32 * nb;
+        const bool in = mi < x.m && ni < x.n;
+        const uint32_t at = p.tall ? (uint32_t)(ni * p.cols + mi) : (uint32_t)(mi * p.cols + ni);
+        float e = v[nb][mb][r];
+        f(e, in ? at : 0u, in);
+        v[nb][mb][r] = e;
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// U's entries; STEP: the momentum's step with them. (Types are told apart outside
+// of the loops, so that all loads are in flight together.)
+template <int MB, int NB, bool STEP>
+__device__ __forceinline__ void load_entries(const SmallArgs& p, const SmallMatrix& x, int n0,
+                                             int lane, Entries<MB, NB>& v) {
+  const Source& src = x.src;
+  if (src.bf16)
+    each_entry<MB, NB>(p, x, n0, lane, v, [&](float& e, uint32_t i, bool in) {
+      const float u = bf16_lo(static_cast<const uint16_t*>(src.u)[i]);
+      e = in ? u : 0.f;
+    });
+  else
+    each_entry<MB, NB>(p, x, n0, lane, v, [&](float& e, uint32_t i, bool in) {
+      const float u = static_cast<const float*>(src.u)[i];
+      e = in ? u : 0.f;
+    });
+  if (src.momentum)
+    each_entry<MB, NB>(p, x, n0, lane, v, [&](float& e, uint32_t i, bool in) {
+      float mo = src.momentum[i];
+      if (STEP) {
+        mo = fmaf(src.beta, mo, e);
+        if (in) src.momentum[i] = mo;
+      }
+      e = in ? mixed(src, e, mo) : 0.f;
+    });
+}
+
+// The sum of v over the workgroup, in order.
+__device__ __forceinline__ double small_sum(double v, double* dsum, int lane, int wave) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  if (lane == 0) dsum[wave] = v;
+  __syncthreads();
+  double total = 0.0;
+#pragma unroll
+  for (int w = 0; w < kSmallWaves; ++w) total += dsum[w];
+  return total;
+}
+
+// X_0 in both layouts, the second through the wave's own LDS once (33 floats a
+// row: no bank twice).
+template <int MB, int NB>
+__device__ __forceinline__ void first_operands(const Entries<MB, NB>& v, float norm, float* mine,
+                                               int lane, Operands<MB, NB>& x) {
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      f32x16 y;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) y[r] = v[nb][mb][r] / norm * kScale;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) split_slice(y, s, 1.f, x.x2[nb][2 * mb + s]);
+      Block::order();
+#pragma unroll
+      for (int r = 0; r < 16; ++r) mine[acc_row(r, lane) * 33 + (lane & 31)] = y[r];
+      Block::order();
+      f32x16 t;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) t[r] = mine[(lane & 31) * 33 + acc_row(r, lane)];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) split_slice(t, s, 1.f, x.x1[mb][2 * nb + s]);
+      __builtin_amdgcn_sched_barrier(0);  // (the next block's registers are this one's)
+    }
+}
+
+// P of this wave's columns to its LDS, entry i * 1024 + 64 * register + lane of
+// block i.
+template <int MB, int NB>
+__device__ __forceinline__ void wave_gram(const Operands<MB, NB>& x, float* mine, int lane) {
+#pragma unroll
+  for (int i = 0; i < SmallLds<MB>::BLOCKS; ++i) {
+    int br, bc;
+    SmallLds<MB>::block_of(i, br, bc);
+    f32x16 acc = {};
+#pragma unroll
+    for (int s = 0; s < 2 * NB; ++s) acc = mma3(x.x1[br][s], x.x1[bc][s], acc);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) mine[i * 1024 + r * 64 + lane] = acc[r];
+  }
+}
+template <int MB>
+__device__ __forceinline__ float waves_sum(const SmallLds<MB>& lds, int e) {
+  float sum = lds.red[0][e];
+#pragma unroll
+  for (int w = 1; w < kSmallWaves; ++w) sum += lds.red[w][e];
+  return sum;
+}
+// P's entry e (as above) from its sum, which has the scale twice.
+template <int MB>
+__device__ __forceinline__ void put_p(SmallLds<MB>& lds, int e, float sum) {
+  const int i = e / 1024, r = e % 1024 / 64, l = e % 64;
+  int br, bc;
+  SmallLds<MB>::block_of(i, br, bc);
+  const int row = 32 * br + acc_row(r, l), col = 32 * bc + (l & 31);
+  _Float16 hi, lo;
+  split(sum * (1.f / kScale), hi, lo);
+  lds.P[0][row * kPitch + col] = hi;
+  lds.P[1][row * kPitch + col] = lo;
+  if (br != bc) {
+    lds.P[0][col * kPitch + row] = hi;
+    lds.P[1][col * kPitch + row] = lo;
+  }
+}
+// Q = a I + b P + c P P, a block a wave.
+template <int MB>
+__device__ __forceinline__ void small_poly(const SmallArgs& p, SmallLds<MB>& lds, int lane, int wave) {
+  if (wave >= SmallLds<MB>::BLOCKS) return;
+  int br, bc;
+  SmallLds<MB>::block_of(wave, br, bc);
+  f32x16 acc = {};
+#pragma unroll
+  for (int s = 0; s < 2 * MB; ++s) {
+    u32x4 fa[2], fb[2];
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      fa[part] = read_symmetric(lds.P[part], 32 * br + (lane & 31), s, lane);
+      fb[part] = read_symmetric(lds.P[part], 32 * bc + (lane & 31), s, lane);
+    }
+    acc = mma3(fa, fb, acc);
+  }
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int row = 32 * br + acc_row(r, lane), col = 32 * bc + (lane & 31);
+    const float pv = (float)lds.P[0][row * kPitch + col] + (float)lds.P[1][row * kPitch + col];
+    float q = fmaf(p.c, acc[r] * (1.f / kScale), p.b * pv);
+    if (row == col) q += p.a * kScale;
+    _Float16 hi, lo;
+    split(q, hi, lo);
+    lds.Q[0][row * kPitch + col] = hi;
+    lds.Q[1][row * kPitch + col] = lo;
+    if (br != bc) {
+      lds.Q[0][col * kPitch + row] = hi;
+      lds.Q[1][col * kPitch + row] = lo;
+    }
+  }
+}
+
+template <int MB>
+__device__ __forceinline__ void read_q(const SmallLds<MB>& lds, int mb, int lane,
+                                       u32x4 (&q)[2 * MB][2]) {
+#pragma unroll
+  for (int s = 0; s < 2 * MB; ++s)
+#pragma unroll
+    for (int part = 0; part < 2; ++part)
+      q[s][part] = read_symmetric(lds.Q[part], 32 * mb + (lane & 31), s, lane);
+}
+// X <- Q X, in both layouts.
+template <int MB, int NB>
+__device__ __forceinline__ void small_apply(const SmallLds<MB>& lds, int lane, Operands<MB, NB>& x) {
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    f32x16 next[MB];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      u32x4 q[2 * MB][2];
+      read_q<MB>(lds, mb, lane, q);
+      next[mb] = f32x16{};  // Q X
+      f32x16 t = {};        // X^T Q
+#pragma unroll
+      for (int s = 0; s < 2 * MB; ++s) {
+        next[mb] = mma3(q[s], x.x2[nb][s], next[mb]);
+        t = mma3(x.x2[nb][s], q[s], t);
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) split_slice(t, s, 1.f / kScale, x.x1[mb][2 * nb + s]);
+      __builtin_amdgcn_sched_barrier(0);  // (two blocks at a time would spill)
+    }
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) split_slice(next[mb], s, 1.f / kScale, x.x2[nb][2 * mb + s]);
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -565,235 +808,161 @@ __device__ __forceinline__ void store_small_as(const SmallArgs& p, T* out, const
     }
   }
 }
-__device__ __forceinline__ void store_small(const SmallArgs& p, void* out, const f32x16& x, int m,
-                                            int n, int mi, int ni, int lane) {
-  if (p.o_bf16) store_small_as(p, static_cast<uint16_t*>(out), x, m, n, mi, ni, lane);
-  else store_small_as(p, static_cast<float*>(out), x, m, n, mi, ni, lane);
-}
-
+// The last Q X, from column n0 on.
 template <int MB, int NB>
-__global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(SmallArgs p) {
-  constexpr int BLOCKS = MB == 1 ? 1 : 3;  // of P on and above the diagonal
-  constexpr int RED = BLOCKS * 1024 > 1056 ? BLOCKS * 1024 : 1056;  // floats a wave
-  __shared__ float red[kSmallWaves][RED];
-  __shared__ __attribute__((aligned(16))) _Float16 P[2][32 * MB * kPitch], Q[2][32 * MB * kPitch];
-  __shared__ double dsum[kSmallWaves];
-  const int tid = threadIdx.x, lane = tid % kWave, half = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int m = p.tall ? p.cols : p.rows, n = p.tall ? p.rows : p.cols;
-  // this matrix; its entries' numbers take 16 bits
-  const size_t first = (size_t)blockIdx.x * p.rows * p.cols;
-  Source src = p.src;
-  src.u = static_cast<const char*>(src.u) + first * (src.bf16 ? 2 : 4);
-  if (src.momentum) src.momentum += first;
-  void* out = static_cast<char*>(p.o) + first * (p.o_bf16 ? 2 : 4);
-  const auto entry = [&](int mi, int ni) {
-    return p.tall ? (uint32_t)(ni * p.cols + mi) : (uint32_t)(mi * p.cols + ni);
-  };
-  const int n0 = 32 * NB * wave + (lane & 31);  // this lane's column of block 0
-  const f32x16 zero = {};
-  const auto block_of = [](int i, int& r, int& c) {  // (0, 0), (0, 1), (1, 1)
-    r = i == 2;
-    c = i > 0;
-  };
-
-  // U, one entry a register as in an accumulator of Q X, and its norm. (Types are
-  // told apart outside of the loops, so that all loads are in flight together.)
-  f32x16 v[NB][MB];
-  const auto each = [&](auto f) {  // f(register, entry's number, whether it is one)
-    // (a value of its own, or the entries' numbers would be kept from one use to
-    // the next, in 32 MB NB registers)
-    int n1 = n0;
-    __asm__ volatile("" : "+v"(n1));
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int mi = 32 * mb + acc_row(r, lane), ni = n1 + 32 * nb;
-          const bool in = mi < m && ni < n;
-          float x = v[nb][mb][r];
-          f(x, in ? entry(mi, ni) : 0u, in);
-          v[nb][mb][r] = x;
-        }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  if (src.bf16)
-    each([&](float& x, uint32_t i, bool in) {
-      const float u = bf16_lo(static_cast<const uint16_t*>(src.u)[i]);
-      x = in ? u : 0.f;
-    });
-  else
-    each([&](float& x, uint32_t i, bool in) {
-      const float u = static_cast<const float*>(src.u)[i];
-      x = in ? u : 0.f;
-    });
-  if (src.momentum)
-    each([&](float& x, uint32_t i, bool in) {
-      const float mo = fmaf(src.beta, src.momentum[i], x);
-      if (in) src.momentum[i] = mo;
-      x = in ? mixed(src, x, mo) : 0.f;
-    });
-  double acc2 = 0.0;
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-      for (int r = 0; r < 16; ++r)
-        acc2 = fma((double)v[nb][mb][r], (double)v[nb][mb][r], acc2);
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) acc2 += __shfl_xor(acc2, o, 64);
-  if (lane == 0) dsum[wave] = acc2;
-  __syncthreads();
-  double total = 0.0;
-#pragma unroll
-  for (int w = 0; w < kSmallWaves; ++w) total += dsum[w];
-  const float norm = (float)sqrt(total) + p.eps;
-
-  u32x4 x1[MB][2 * NB][2], x2[NB][2 * MB][2];  // [..][slice][part]
-  float* mine = red[wave];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-      f32x16 x;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) x[r] = v[nb][mb][r] / norm * kScale;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) split_slice(x, s, 1.f, x2[nb][2 * mb + s]);
-      // the other layout once through LDS (33 floats a row: no bank twice)
-      Block::order();
-#pragma unroll
-      for (int r = 0; r < 16; ++r) mine[acc_row(r, lane) * 33 + (lane & 31)] = x[r];
-      Block::order();
-      f32x16 t;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) t[r] = mine[(lane & 31) * 33 + acc_row(r, lane)];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) split_slice(t, s, 1.f, x1[mb][2 * nb + s]);
-      __builtin_amdgcn_sched_barrier(0);  // (the next block's registers are this one's)
-    }
-
-  // Q of the current X, in LDS
-  const auto make_q = [&]() {
-    // P of this wave's columns
-    __syncthreads();  // red, P and Q have been read
-#pragma unroll
-    for (int i = 0; i < BLOCKS; ++i) {
-      int br, bc;
-      block_of(i, br, bc);
-      f32x16 acc = zero;
-#pragma unroll
-      for (int s = 0; s < 2 * NB; ++s) acc = mma3(x1[br][s], x1[bc][s], acc);
-#pragma unroll
-      for (int r = 0; r < 16; ++r) mine[i * 1024 + r * 64 + lane] = acc[r];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < BLOCKS * 2; ++j) {
-      const int e = tid + j * kSmallThreads, i = e / 1024, r = e % 1024 / 64, l = e % 64;
-      float sum = red[0][e];
-#pragma unroll
-      for (int w = 1; w < kSmallWaves; ++w) sum += red[w][e];
-      int br, bc;
-      block_of(i, br, bc);
-      const int row = 32 * br + acc_row(r, l), col = 32 * bc + (l & 31);
-      _Float16 hi, lo;
-      split(sum * (1.f / kScale), hi, lo);
-      P[0][row * kPitch + col] = hi;
-      P[1][row * kPitch + col] = lo;
-      if (br != bc) {
-        P[0][col * kPitch + row] = hi;
-        P[1][col * kPitch + row] = lo;
-      }
-    }
-    __syncthreads();
-    // Q = a I + b P + c P P, a block a wave
-    if (wave < BLOCKS) {
-      int br, bc;
-      block_of(wave, br, bc);
-      f32x16 acc = zero;
-#pragma unroll
-      for (int s = 0; s < 2 * MB; ++s) {
-        u32x4 fa[2], fb[2];
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          fa[part] = read_symmetric(P[part], 32 * br + (lane & 31), s, lane);
-          fb[part] = read_symmetric(P[part], 32 * bc + (lane & 31), s, lane);
-        }
-        acc = mma3(fa, fb, acc);
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int row = 32 * br + acc_row(r, lane), col = 32 * bc + (lane & 31);
-        const float pv = (float)P[0][row * kPitch + col] + (float)P[1][row * kPitch + col];
-        float q = fmaf(p.c, acc[r] * (1.f / kScale), p.b * pv);
-        if (row == col) q += p.a * kScale;
-        _Float16 hi, lo;
-        split(q, hi, lo);
-        Q[0][row * kPitch + col] = hi;
-        Q[1][row * kPitch + col] = lo;
-        if (br != bc) {
-          Q[0][col * kPitch + row] = hi;
-          Q[1][col * kPitch + row] = lo;
-        }
-      }
-    }
-    __syncthreads();
-  };
-  const auto read_q = [&](int mb, u32x4 (&q)[2 * MB][2]) {
-#pragma unroll
-    for (int s = 0; s < 2 * MB; ++s)
-#pragma unroll
-      for (int part = 0; part < 2; ++part)
-        q[s][part] = read_symmetric(Q[part], 32 * mb + (lane & 31), s, lane);
-  };
-
-  for (int step = 1; step < p.steps; ++step) {
-    make_q();
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      f32x16 next[MB];
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
-        u32x4 q[2 * MB][2];
-        read_q(mb, q);
-        next[mb] = zero;  // Q X
-        f32x16 t = zero;  // X^T Q
-#pragma unroll
-        for (int s = 0; s < 2 * MB; ++s) {
-          next[mb] = mma3(q[s], x2[nb][s], next[mb]);
-          t = mma3(x2[nb][s], q[s], t);
-        }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) split_slice(t, s, 1.f / kScale, x1[mb][2 * nb + s]);
-        __builtin_amdgcn_sched_barrier(0);  // (two blocks at a time would spill)
-      }
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) split_slice(next[mb], s, 1.f / kScale, x2[nb][2 * mb + s]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-  make_q();
-  int n1 = n0;  // (as above)
+__device__ __forceinline__ void small_result(const SmallArgs& p, const SmallMatrix& x,
+                                             const SmallLds<MB>& lds, int n0, int lane,
+                                             const Operands<MB, NB>& ops) {
+  int n1 = n0;  // (as in each_entry)
   __asm__ volatile("" : "+v"(n1));
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
       u32x4 q[2 * MB][2];
-      read_q(mb, q);
-      f32x16 x = zero;
+      read_q<MB>(lds, mb, lane, q);
+      f32x16 y = {};
 #pragma unroll
-      for (int s = 0; s < 2 * MB; ++s) x = mma3(q[s], x2[nb][s], x);
-      store_small(p, out, x, m, n, 32 * mb, n1 + 32 * nb, lane);
+      for (int s = 0; s < 2 * MB; ++s) y = mma3(q[s], ops.x2[nb][s], y);
+      const int ni = n1 + 32 * nb;
+      if (p.o_bf16)
+        store_small_as(p, static_cast<uint16_t*>(x.out), y, x.m, x.n, 32 * mb, ni, lane);
+      else
+        store_small_as(p, static_cast<float*>(x.out), y, x.m, x.n, 32 * mb, ni, lane);
       __builtin_amdgcn_sched_barrier(0);
     }
+}
+
+// n <= 256 NB: the whole iteration in one workgroup, one launch for 17: 64 x 512
+// fp32 141 -> 54 us, 64 of them 57 us.
+template <int MB, int NB>
+__global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(SmallArgs p) {
+  __shared__ SmallLds<MB> lds;
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const SmallMatrix x(p, blockIdx.x);
+  const int n0 = 32 * NB * wave + (lane & 31);  // this lane's column of block 0
+  Entries<MB, NB> v;
+  load_entries<MB, NB, true>(p, x, n0, lane, v);
+  double acc = 0.0;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc = fma((double)v[nb][mb][r], (double)v[nb][mb][r], acc);
+  const float norm = (float)sqrt(small_sum(acc, lds.dsum, lane, wave)) + p.eps;
+  Operands<MB, NB> ops;
+  first_operands<MB, NB>(v, norm, lds.red[wave], lane, ops);
+  const auto make_q = [&]() {
+    __syncthreads();  // red, P and Q have been read
+    wave_gram<MB, NB>(ops, lds.red[wave], lane);
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < SmallLds<MB>::BLOCKS * 2; ++j) {
+      const int e = tid + j * kSmallThreads;
+      put_p<MB>(lds, e, waves_sum<MB>(lds, e));
+    }
+    __syncthreads();
+    small_poly<MB>(p, lds, lane, wave);
+    __syncthreads();
+  };
+  for (int step = 1; step < p.steps; ++step) {
+    make_q();
+    small_apply<MB, NB>(lds, lane, ops);
+  }
+  make_q();
+  small_result<MB, NB>(p, x, lds, n0, lane, ops);
+}
+
+// Longer n: slabs of 256 NB columns, a workgroup each. Only P needs all of them, so
+// a launch takes a slab from one P to the next: it adds up the slabs' parts of P
+// (in order, out of L2), forms Q, applies it and leaves its part of the next P
+// and x2. The first launch has X_0 for X, the last one stores X: steps + 2 launches
+// (one for the norm) instead of 3 steps + 2 of the products above: 64 x 2048 141 ->
+// 57 us, 40 x 4096 195 -> 63 us, 64 matrices 64 x 2048 229 -> 170 us, 4096 of 8 x 2000
+// 6.1 -> 2.6 ms. (Where one workgroup holds a matrix it is as fast for one, 52 and 52
+// us at 64 x 512, and faster for many: 512 of them 135 and 269 us.)
+enum SlabPhase { kFirst, kStep, kLast };
+template <int MB, int NB, int PHASE>
+__global__ __launch_bounds__(kSmallThreads) void ortho_slab_kernel(SmallArgs p) {
+  __shared__ SmallLds<MB> lds;
+  constexpr int SUMS = SmallLds<MB>::BLOCKS * 1024;  // entries of a part of P
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const SmallMatrix x(p, blockIdx.y);
+  const int slabs = gridDim.x;
+  const size_t slab = (size_t)blockIdx.y * slabs + blockIdx.x;
+  const int n0 = 32 * NB * (blockIdx.x * kSmallWaves + wave) + (lane & 31);
+  u32x4* kept = p.x + slab * (NB * 2 * MB * 2) * kSmallThreads + tid;
+  Operands<MB, NB> ops;
+  if constexpr (PHASE == kFirst) {
+    Entries<MB, NB> v;
+    load_entries<MB, NB, false>(p, x, n0, lane, v);
+    double acc = 0.0;
+    for (int i = tid; i < p.parts; i += kSmallThreads) acc += p.part[(size_t)blockIdx.y * p.parts + i];
+    const float norm = (float)sqrt(small_sum(acc, lds.dsum, lane, wave)) + p.eps;
+    first_operands<MB, NB>(v, norm, lds.red[wave], lane, ops);
+  } else {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int s = 0; s < 2 * MB; ++s)
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+          ops.x2[nb][s][part] = kept[((nb * 2 * MB + s) * 2 + part) * kSmallThreads];
+    const float* sums = p.p_in + (size_t)blockIdx.y * slabs * SUMS;
+    constexpr int PAIRS = SUMS / 2 / kSmallThreads;  // of entries, a thread's
+    f32x2 sum[PAIRS];
+#pragma unroll
+    for (int j = 0; j < PAIRS; ++j) sum[j] = f32x2{0.f, 0.f};
+    for (int g0 = 0; g0 < slabs; g0 += 8) {
+      f32x2 part[8][PAIRS];
+#pragma unroll
+      for (int g = 0; g < 8; ++g)
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j)
+          part[g][j] = g0 + g < slabs
+                           ? *reinterpret_cast<const f32x2*>(sums + (size_t)(g0 + g) * SUMS +
+                                                             2 * (tid + j * kSmallThreads))
+                           : f32x2{0.f, 0.f};
+#pragma unroll
+      for (int g = 0; g < 8; ++g)
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j) {
+          sum[j][0] += part[g][j][0];
+          sum[j][1] += part[g][j][1];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < PAIRS; ++j) {
+      put_p<MB>(lds, 2 * (tid + j * kSmallThreads), sum[j][0]);
+      put_p<MB>(lds, 2 * (tid + j * kSmallThreads) + 1, sum[j][1]);
+    }
+    __syncthreads();
+    small_poly<MB>(p, lds, lane, wave);
+    __syncthreads();
+    if constexpr (PHASE == kLast) {
+      small_result<MB, NB>(p, x, lds, n0, lane, ops);
+      return;
+    } else {
+      small_apply<MB, NB>(lds, lane, ops);
+    }
+  }
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int s = 0; s < 2 * MB; ++s)
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+        kept[((nb * 2 * MB + s) * 2 + part) * kSmallThreads] = ops.x2[nb][s][part];
+  wave_gram<MB, NB>(ops, lds.red[wave], lane);
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < SUMS / kSmallThreads; ++j) {
+    const int e = tid + j * kSmallThreads;
+    p.p_out[slab * SUMS + e] = waves_sum<MB>(lds, e);
+  }
 }
 
 template <int MB, int NB>
@@ -801,9 +970,37 @@ hipError_t launch_small(const SmallArgs& p, int batch, hipStream_t s) {
   return launch_kernel(ortho_small_kernel<MB, NB>, dim3(batch), dim3(kSmallThreads), 0, s,
                        KernelTiming{}, p);
 }
+// p2: two buffers for the parts of P, taken in turn.
+template <int MB, int NB>
+hipError_t launch_slabs(SmallArgs p, int batch, int slabs, float* const (&p2)[2], hipStream_t s) {
+  const dim3 grid(slabs, batch);
+  for (int i = 0; i <= p.steps; ++i) {
+    p.p_in = p2[(i + 1) & 1];
+    p.p_out = p2[i & 1];
+    const auto kernel = i == 0         ? ortho_slab_kernel<MB, NB, kFirst>
+                        : i < p.steps ? ortho_slab_kernel<MB, NB, kStep>
+                                      : ortho_slab_kernel<MB, NB, kLast>;
+    const hipError_t e = launch_kernel(kernel, grid, dim3(kSmallThreads), 0, s, KernelTiming{}, p);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
 
 int padded(int n) { return (n + 7) / 8 * 8; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Whether a matrix's smaller side fits the kernels that keep X in registers, and
+// the blocks of 32 of each side that a wave of theirs holds.
+struct SmallShape {
+  int mb, nb, slabs;  // mb = 0: too large; slabs = 1: one workgroup
+};
+SmallShape small_shape(int rows, int cols) {
+  const int low = rows < cols ? rows : cols, high = rows < cols ? cols : rows;
+  if (low > 64) return {0, 0, 0};
+  const int mb = low <= 32 ? 1 : 2, most = mb == 1 ? 4 : 2;
+  if (high <= 256 * most) return {mb, high <= 256 ? 1 : high <= 512 ? 2 : 4, 1};
+  return {mb, 1, (high + 255) / 256};
+}
 
 struct Layout {
   size_t part, x0, x1, p, q, total;  // byte offsets
@@ -811,13 +1008,22 @@ struct Layout {
   int ld, m, ldm;
 };
 Layout layout(int batch, int rows, int cols) {
-  Layout l;
+  Layout l = {};
+  const SmallShape small = small_shape(rows, cols);
+  if (small.slabs == 1) return l;
+  if (small.mb) {  // x0: x2; p, q: the two buffers of the parts of P
+    const size_t n = (size_t)batch * small.slabs;
+    l.x0 = up256((size_t)batch * kSumParts * sizeof(double));
+    l.p = l.x0 + n * (small.nb * 2 * small.mb * 2) * kSmallThreads * sizeof(u32x4);
+    l.q = l.p + n * (small.mb == 1 ? 1 : 3) * 1024 * sizeof(float);
+    l.total = l.q + (l.q - l.p);
+    return l;
+  }
   l.ld = padded(cols);
   l.m = rows < cols ? rows : cols;
   l.ldm = padded(l.m);
   l.x_part = up256((size_t)batch * rows * l.ld * 2);
   l.p_part = up256((size_t)batch * l.m * l.ldm * 2);
-  l.part = 0;
   l.x0 = up256((size_t)batch * kSumParts * sizeof(double));
   l.x1 = l.x0 + 2 * l.x_part;
   l.p = l.x1 + 2 * l.x_part;
@@ -834,33 +1040,7 @@ size_t ortho_workspace_bytes(int batch, int rows, int cols) {
 
 hipError_t launch_ortho(const OrthoCall& call, void* ws, hipStream_t s) {
   const int batch = call.batch, rows = call.rows, cols = call.cols;
-  const int low = rows < cols ? rows : cols, high = rows < cols ? cols : rows;
-  if (low <= 64 && high <= (low <= 32 ? 1024 : 512)) {
-    SmallArgs p;
-    p.src.u = call.u;
-    p.src.momentum = call.momentum;
-    p.src.beta = call.beta;
-    p.src.nesterov = call.nesterov;
-    p.src.bf16 = call.u_bf16;
-    p.rows = rows;
-    p.cols = cols;
-    p.steps = call.steps;
-    p.tall = rows > cols;
-    p.a = call.a;
-    p.b = call.b;
-    p.c = call.c;
-    p.eps = call.eps;
-    p.o = call.o;
-    p.o_bf16 = call.o_bf16;
-    p.update = call.update;
-    p.keep = call.keep;
-    p.rate = call.rate;
-    if (low <= 32)
-      return high <= 256   ? launch_small<1, 1>(p, batch, s)
-             : high <= 512 ? launch_small<1, 2>(p, batch, s)
-                           : launch_small<1, 4>(p, batch, s);
-    return high <= 256 ? launch_small<2, 1>(p, batch, s) : launch_small<2, 2>(p, batch, s);
-  }
+  const SmallShape small = small_shape(rows, cols);
   const Layout l = layout(batch, rows, cols);
   char* base = static_cast<char*>(ws);
   double* part = reinterpret_cast<double*>(base + l.part);
@@ -870,6 +1050,28 @@ hipError_t launch_ortho(const OrthoCall& call, void* ws, hipStream_t s) {
   src.beta = call.beta;
   src.nesterov = call.nesterov;
   src.bf16 = call.u_bf16;
+  SmallArgs sp = {};
+  sp.src = src;
+  sp.rows = rows;
+  sp.cols = cols;
+  sp.steps = call.steps;
+  sp.tall = rows > cols;
+  sp.a = call.a;
+  sp.b = call.b;
+  sp.c = call.c;
+  sp.eps = call.eps;
+  sp.o = call.o;
+  sp.o_bf16 = call.o_bf16;
+  sp.update = call.update;
+  sp.keep = call.keep;
+  sp.rate = call.rate;
+  if (small.slabs == 1) {
+    if (small.mb == 1)
+      return small.nb == 1   ? launch_small<1, 1>(sp, batch, s)
+             : small.nb == 2 ? launch_small<1, 2>(sp, batch, s)
+                             : launch_small<1, 4>(sp, batch, s);
+    return small.nb == 1 ? launch_small<2, 1>(sp, batch, s) : launch_small<2, 2>(sp, batch, s);
+  }
   const size_t count = (size_t)rows * cols;
   // as many workgroups as fill the chip, at least a few rounds of entries each
   const size_t most = batch >= 32 ? 32 : kSumParts;
@@ -878,6 +1080,14 @@ hipError_t launch_ortho(const OrthoCall& call, void* ws, hipStream_t s) {
   hipError_t e = launch_kernel(ortho_sum_kernel, dim3(parts, batch), dim3(kSumThreads), 0, s,
                                KernelTiming{}, src, count, (int)(count % 8 == 0), part);
   if (e != hipSuccess) return e;
+  if (small.mb) {
+    sp.part = part;
+    sp.parts = parts;
+    sp.x = reinterpret_cast<u32x4*>(base + l.x0);
+    float* const p2[2] = {reinterpret_cast<float*>(base + l.p), reinterpret_cast<float*>(base + l.q)};
+    return small.mb == 1 ? launch_slabs<1, 1>(sp, batch, small.slabs, p2, s)
+                         : launch_slabs<2, 1>(sp, batch, small.slabs, p2, s);
+  }
   _Float16* x[2] = {reinterpret_cast<_Float16*>(base + l.x0),
                     reinterpret_cast<_Float16*>(base + l.x1)};
   const size_t blocks = ((size_t)rows * l.ld / 8 + kSumThreads - 1) / kSumThreads;

@@ -135,3 +135,33 @@ def test_every_tile(shape, tall):
     o = bmoe.orthogonalize(u.cuda(), bmoe.OrthoSpec(steps))
     for i in {0, B // 2, B - 1}:
         assert rel(o[i], O.newton_schulz(f64(u[i]), steps)) <= tol(steps, F32), i
+
+
+# Small sides: one workgroup, slabs of columns (up to 64 of them), batches, each
+# type, and the momentum's step; a slab of one column
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("shape", [(1, 64, 513), (1, 33, 1000), (3, 64, 2048), (1, 32, 1025),
+                                   (2, 17, 3001), (1, 1, 1300), (1, 50, 16384), (5, 8, 1281)])
+@pytest.mark.parametrize("tall", [False, True])
+def test_slabs(shape, tall, dt):
+    B, m, n = shape
+    shape = (B, n, m) if tall else shape
+    u = randn(shape, dt, n, 0.01)
+    for steps in (1, 2, 5):
+        o = bmoe.orthogonalize(u.cuda(), bmoe.OrthoSpec(steps))
+        for i in {0, B - 1}:
+            assert rel(o[i], O.newton_schulz(f64(u[i]), steps)) <= tol(steps, dt), (i, steps)
+    w, mo = randn(shape, dt, 1, 0.1), randn(shape, F32, 2, 0.01)
+    dw, dm = w.cuda(), mo.cuda()
+    bmoe.orthogonal_step(dw, u.cuda(), dm, 0.02, beta=0.5)
+    rm = 0.5 * f64(mo) + f64(u)
+    assert (np.abs(f64(dm) - rm) <= 2.0 ** -24 * np.abs(rm)).all()
+    half = 2.0 ** -8 if dt == BF else 2.0 ** -24
+    for i in {0, B - 1}:
+        o = O.newton_schulz(f64(u[i]) + 0.5 * rm[i])
+        err = np.abs(f64(dw[i]) - (f64(w[i]) - 0.02 * o)) - half * np.abs(f64(dw[i])) - \
+            2.0 ** -22 * np.abs(f64(w[i]))
+        assert np.linalg.norm(np.maximum(err, 0)) <= 0.02 * np.linalg.norm(o) * tol(5, F32)
+    bad = u.cuda()
+    bad[0, -1, -1] = float("nan")
+    assert bmoe.orthogonalize(bad)[0].isnan().all()
