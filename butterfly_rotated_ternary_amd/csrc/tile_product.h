@@ -10,8 +10,11 @@
 // read zeros, so every step issues the same number of DMA instructions and the
 // counted waits are exact.
 //
-// ALIGNED = false serves rows that are no multiple of 16 bytes: chunks are put
-// together from single elements in registers and written to the same places.
+// ALIGNED = false serves rows that are no multiple of 16 bytes: chunks go through
+// registers, loaded before a step's MFMAs and written to the same places behind
+// them. 8192 rows, 64 experts of 1000 x 500 bf16, c, da and dW: 23, 34 and 44 us
+// (38, 82 and 69 with the loads waited for at once), of 1000 x 504 by DMA 22, 24
+// and 40.
 //
 // PARTS = 2: operands are pairs (hi, lo) whose sum is the value; the product
 // is hi hi + hi lo + lo hi (three MFMAs per pair of fragments read, so LDS and
@@ -69,24 +72,34 @@ __device__ __forceinline__ void dma16(const void* g, char* lds) {
                                    (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
 }
 
-// `n` elements at p (n <= 0: none) as one chunk, the rest zeros. Whole chunks
-// take one access, whatever their alignment.
+// !ALIGNED: chunks are single accesses, whatever their alignment; the chunk at a
+// row's end takes the row's last 16 bytes, and end_chunk() moves its n elements
+// down once they are needed. Rows shorter than a chunk are read element by
+// element: n of them at p (n <= 0: none).
 template <int ES>
-__device__ __forceinline__ u32x4 partial_chunk(const char* p, int n) {
+__device__ __forceinline__ u32x4 short_chunk(const char* p, int n) {
   u32x4 v = {0u, 0u, 0u, 0u};
-  if (n >= 16 / ES) {
-    __builtin_memcpy(&v, p, 16);
-  } else if constexpr (ES == 2) {
+  if constexpr (ES == 2) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 7; ++i)
       if (i < n)
         v[i / 2] |= (uint32_t) * reinterpret_cast<const uint16_t*>(p + 2 * i) << (16 * (i & 1));
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 3; ++i)
       if (i < n) v[i] = *reinterpret_cast<const uint32_t*>(p + 4 * i);
   }
   return v;
+}
+template <int ES>
+__device__ __forceinline__ void end_chunk(u32x4& v, int n, int len) {
+  constexpr int EPC = 16 / ES;
+  if (n <= 0 || n >= EPC || len < EPC) return;
+  const int bytes = (EPC - n) * ES;
+  if (bytes & 8) v = u32x4{v[2], v[3], 0u, 0u};
+  if (bytes & 4) v = u32x4{v[1], v[2], v[3], 0u};
+  if (ES == 2 && (bytes & 2))
+    v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
 }
 
 // ---- kOutRows: LDS rows of KB bytes -------------------------------------------
@@ -107,6 +120,7 @@ struct OutRowsSource {
   static constexpr int CH = C::KB / 16;
   int K;
   size_t part;                        // bytes between the parts
+  u32x4 held[C::ALIGNED ? 1 : LOADS];  // !ALIGNED: the chunks of the step loaded last
   // row_of(r): offset (SPREAD: address) of the row of output row r (0 <= r < R;
   // any valid row for those past the end, whose outputs are not stored).
   template <typename F>
@@ -127,7 +141,7 @@ struct OutRowsSource {
   __device__ __forceinline__ int whole_steps() const { return K / C::BK; }
   // WHOLE: the step lies before K.
   template <bool WHOLE>
-  __device__ __forceinline__ void load(char* region, int step, int lane, int wave) const {
+  __device__ __forceinline__ void load(char* region, int step, int lane, int wave) {
 #pragma unroll
     for (int q = 0; q < C::PARTS; ++q) {
       const char* b = base + (q * part + (size_t)step * C::KB);
@@ -140,13 +154,30 @@ struct OutRowsSource {
         const int e = (wave * LOADS + j) * 64 + lane;
         const int left = K - step * C::BK - out_swz<C::KB>(e / CH, e % CH) * C::EPC;
         if constexpr (!C::ALIGNED) {
-          *reinterpret_cast<u32x4*>(dst + lane * 16) = partial_chunk<C::ES>(g, left);
+          if (K < C::EPC) {
+            held[j] = short_chunk<C::ES>(g, left);
+          } else {
+            if (!WHOLE && left < C::EPC)
+              g = left > 0 ? g - (C::EPC - left) * C::ES : reinterpret_cast<const char*>(&kZeros);
+            __builtin_memcpy(&held[j], g, 16);
+          }
         } else if constexpr (WHOLE) {
           dma16(g, dst);
         } else {
           dma16(left > 0 ? (const void*)g : (const void*)&kZeros, dst);
         }
       }
+    }
+  }
+  // !ALIGNED: the step's chunks to their places.
+  template <bool WHOLE>
+  __device__ __forceinline__ void put(char* region, int step, int lane, int wave) {
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      const int e = (wave * LOADS + j) * 64 + lane;
+      if constexpr (!WHOLE)
+        end_chunk<C::ES>(held[j], K - step * C::BK - out_swz<C::KB>(e / CH, e % CH) * C::EPC, K);
+      *reinterpret_cast<u32x4*>(region + (wave * LOADS + j) * 1024 + lane * 16) = held[j];
     }
   }
 };
@@ -183,10 +214,11 @@ struct RedRowsSource {
   // ListedRow: the rows of the step that is loaded next (steps are loaded in
   // order), read a step ahead so that no load waits for LDS.
   int32_t row[SAME ? 1 : LOADS];
+  u32x4 held[C::ALIGNED ? 1 : LOADS];  // (as above)
   static constexpr int CH = R / C::EPC;  // chunks per row
   // Columns c0 .. of `cols`; ALIGNED needs cols to be whole chunks (chunks past
-  // the last repeat it: their outputs are not stored). A step's rows (SameRow)
-  // span less than 2^32 bytes.
+  // the last read the row's last 16 bytes: their outputs are not stored). A step's
+  // rows (SameRow) span less than 2^32 bytes.
   __device__ __forceinline__ void init(const char* base_, size_t ld_, int c0_, int cols_, int K_,
                                        size_t part_, MAP map_, int lane, int wave) {
     static_assert(R % 64 == 0, "swizzle range");
@@ -201,7 +233,7 @@ struct RedRowsSource {
     for (int j = 0; j < LOADS; ++j) {
       const int e = (wave * LOADS + j) * 64 + lane, r = e / CH;
       const int c = c0 + red_swz<C::ES, R>(r, e % CH) * C::EPC;
-      off[j] = (uint32_t)((C::ALIGNED ? min(c, cols - C::EPC) : min(c, cols - 1)) * C::ES);
+      off[j] = (uint32_t)((C::ALIGNED || cols >= C::EPC ? min(c, cols - C::EPC) : c) * C::ES);
       if constexpr (SAME) off[j] += (uint32_t)(r * ld);
       else row[j] = map.list[min(r, K - 1)];
     }
@@ -225,14 +257,28 @@ struct RedRowsSource {
         }
         char* dst = region + q * (R * C::KB) + (wave * LOADS + j) * 1024;
         if constexpr (!C::ALIGNED) {
-          *reinterpret_cast<u32x4*>(dst + lane * 16) =
-              partial_chunk<C::ES>(g, in ? cols - c0 - red_swz<C::ES, R>(r, e % CH) * C::EPC : 0);
+          if (cols < C::EPC) {
+            held[j] = short_chunk<C::ES>(
+                g, in ? cols - c0 - red_swz<C::ES, R>(r, e % CH) * C::EPC : 0);
+          } else {
+            __builtin_memcpy(&held[j], in ? g : reinterpret_cast<const char*>(&kZeros), 16);
+          }
         } else if constexpr (WHOLE) {
           dma16(g, dst);
         } else {
           dma16(in ? (const void*)g : (const void*)&kZeros, dst);
         }
       }
+    }
+  }
+  template <bool WHOLE>
+  __device__ __forceinline__ void put(char* region, int step, int lane, int wave) {
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      const int e = (wave * LOADS + j) * 64 + lane, r = e / CH;
+      if (c0 + R > cols)  // the last columns' tile
+        end_chunk<C::ES>(held[j], cols - c0 - red_swz<C::ES, R>(r, e % CH) * C::EPC, cols);
+      *reinterpret_cast<u32x4*>(region + (wave * LOADS + j) * 1024 + lane * 16) = held[j];
     }
   }
 };
@@ -362,6 +408,15 @@ __device__ __forceinline__ void issue(char* stg, SA& a, SB& b, int step, int lan
   a.template load<WHOLE>(stg, step, lane, wave);
   b.template load<WHOLE>(stg + C::A_BYTES, step, lane, wave);
 }
+// What issue() loaded to its place, where no DMA puts it there.
+template <class C, bool WHOLE, class SA, class SB>
+__device__ __forceinline__ void settle(char* stg, SA& a, SB& b, int step, int lane, int wave) {
+  if constexpr (!C::ALIGNED) {
+    static_assert(C::PARTS == 1, "chunks held of one part");
+    a.template put<WHOLE>(stg, step, lane, wave);
+    b.template put<WHOLE>(stg + C::A_BYTES, step, lane, wave);
+  }
+}
 
 // How many LDS reads a slice of one part of an operand takes.
 template <class C, int MODE, int F>
@@ -426,6 +481,7 @@ __device__ __forceinline__ void step(Acc<C>& acc, Frags<C>& f, char* const (&rin
     mma_slice<C>(acc, f.a, f.b);
     interleave<C, false>();
   }
+  settle<C, WHOLE>(ring[(S + C::AHEAD) % C::NSTAGE], a, b, kt + C::AHEAD, lane, wave);
   __asm__ volatile("" ::: "memory");
   // this wave's part of step kt + 1 has landed once only the later steps' are out
   wait_vm<(C::AHEAD - 1) * C::V>();
@@ -457,6 +513,7 @@ __device__ __forceinline__ void run(Acc<C>& acc, char* const (&ring)[C::NSTAGE],
 #pragma unroll
   for (int s = 0; s < C::AHEAD; ++s) {
     issue<C, false>(ring[s], a, b, s, lane, wave);
+    settle<C, false>(ring[s], a, b, s, lane, wave);
     __asm__ volatile("" ::: "memory");
   }
   wait_vm<(C::AHEAD - 1) * C::V>();

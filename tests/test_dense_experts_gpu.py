@@ -192,3 +192,30 @@ def test_every_tile(T, K, O_, N, k, skew, dt):
     mda, mdw = O.grouped_product_backward(abs(A), abs(W), o, rows, abs(D))
     close(r["da"], rda, mda, O_, dt)
     close(r["dw"], rdw, mdw, int(np.diff(o).max()), F32)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("K", [1, 2, 3, 4, 5, 7, 8, 9, 15, 17, 65, 133])
+@pytest.mark.parametrize("O_", [1, 3, 5, 7, 9, 66, 131])
+def test_short_and_odd_rows(K, O_, dt):
+    """Rows shorter than 16 bytes and rows that end inside 16 bytes, each in an
+    array that ends with its last row, among NaN that no product may touch."""
+    N, M = 3, 150
+    ids, a, w, dc = draw(M, K, O_, N, 1, dt, seed=K * O_)
+    off, perm, inv = bmoe.group_rows(ids.cuda(), N)
+    o, rows = off.cpu().numpy(), perm.cpu().numpy()
+    A, W, D = f64(a), f64(w), f64(dc)
+
+    def between(t):  # the same rows between NaN, at 16 bytes
+        flat = torch.full((t.numel() + 128,), float("nan"), dtype=dt, device="cuda")
+        v = flat[64:64 + t.numel()].view(t.shape)
+        v.copy_(t)
+        return v
+    x, y, z = between(a), between(w), between(dc)
+    c = bmoe.grouped_product(x, y, off, perm=perm)
+    close(c, O.grouped_product(A, W, o, rows), O.grouped_product(abs(A), abs(W), o, rows), K, dt)
+    r = bmoe.grouped_product_backward(x, y, off, z, perm=perm)
+    rda, rdw = O.grouped_product_backward(A, W, o, rows, D)
+    mda, mdw = O.grouped_product_backward(abs(A), abs(W), o, rows, abs(D))
+    close(r["da"], rda, mda, O_, dt)
+    close(r["dw"], rdw, mdw, int(np.diff(o).max()), F32)
