@@ -201,7 +201,8 @@ struct Family {
   static constexpr int E = E_, FMAX = FMAX_, BN = BN_, WN = WN_, BMODE = BMODE_;
   static constexpr bool ALIGNED = ALIGNED_;
   template <int FM>
-  using Height = Cfg<E, 1, 64 * FM, BN, 2, WN, NSTAGE, kOutRows, BMODE, ALIGNED, NSTAGE == 2 ? 128 : 64>;
+  using Height =
+      Cfg<E, 1, 64 * FM, BN, 2, WN, NSTAGE, kOutRows, BMODE, ALIGNED, NSTAGE == 2 ? 128 : 64>;
   using Most = Height<FMAX>;
 };
 
@@ -421,7 +422,8 @@ hipError_t launch_grouped_dw_cfg(DwArgs p, hipStream_t s) {
 
 // (rows through registers: two stages of twice the reduction, 3 to 8 % faster)
 template <int E, bool ALIGNED>
-using DwTile128 = Cfg<E, 1, 128, 128, 2, 2, ALIGNED ? 4 : 2, kRedRows, kRedRows, ALIGNED, ALIGNED ? 64 : 128>;
+using DwTile128 =
+    Cfg<E, 1, 128, 128, 2, 2, ALIGNED ? 4 : 2, kRedRows, kRedRows, ALIGNED, ALIGNED ? 64 : 128>;
 template <int E>
 using DwTile256 = Cfg<E, 1, 256, 256, 2, 4, 4, kRedRows, kRedRows, true>;
 // The tile's width by the time of its rounds over the CUs: one workgroup of 256

@@ -11,7 +11,7 @@
 //
 // Bound by HBM: each array is read or written once (the gradient reads u a
 // second time, out of L2, because dy needs sums over the row). A row belongs to
-// TPR threads (a wave, or a whole workgroup), a thread to EPC * NV of its
+// TPR threads (sixteen, a wave, or a whole workgroup), a thread to EPC * NV of its
 // values, held in registers between the sums.
 #include "common.h"
 #include "kernels.h"
@@ -38,19 +38,25 @@ __device__ __forceinline__ void put(uint16_t* p, float v) { *p = (uint16_t)f32_t
 
 // The chunk of a row at column c: values c .. c + EPC - 1 of d, zeros past it.
 // Rows that are not aligned take 16-byte accesses all the same (the memory
-// system splits them; eight 2-byte loads each made 16384 rows of 1001 bf16 values
-// three times as slow), but for a row's last chunk.
+// system splits them); a row's last chunk takes the row's last 16 bytes and moves
+// them down. Rows shorter than that are read value by value.
 template <class C>
 __device__ __forceinline__ uint4 load_chunk(const typename C::T* p, int c, int d) {
   uint4 v = make_uint4(0u, 0u, 0u, 0u);
   if constexpr (C::ALIGNED) {
     if (c < d) v = *reinterpret_cast<const uint4*>(p + c);
-  } else if (c + C::EPC <= d) {
-    __builtin_memcpy(&v, p + c, 16);
+  } else if (d >= C::EPC) {
+    const int at = min(c, d - C::EPC), past = c - at;  // values to drop
+    __builtin_memcpy(&v, p + at, 16);
+    if (past & (C::EPC / 2)) v = make_uint4(v.z, v.w, 0u, 0u);
+    if (past & (C::EPC / 4)) v = make_uint4(v.y, v.z, v.w, 0u);
+    if (C::EPC == 8 && (past & 1))
+      v = make_uint4(v.x >> 16 | v.y << 16, v.y >> 16 | v.z << 16, v.z >> 16 | v.w << 16, v.w >> 16);
+    if (past >= C::EPC) v = make_uint4(0u, 0u, 0u, 0u);
   } else {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int e = 0; e < C::EPC; ++e)
+    for (int e = 0; e < C::EPC - 1; ++e)
       if (c + e < d) {
         if constexpr (C::EPC == 8)
           w[e / 2] |= (uint32_t)p[c + e] << (16 * (e & 1));
@@ -134,12 +140,21 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), kWave - 1));
 }
 
+// The sum over each sixteen lanes, the same bits in all of them: DPP swaps of
+// neighbours, of pairs, of fours and of eights.
+__device__ __forceinline__ float narrow_sum(float v) {
+  v = add_dpp<0xB1, 0xF>(v);   // lanes 1 0 3 2
+  v = add_dpp<0x4E, 0xF>(v);   // lanes 2 3 0 1
+  v = add_dpp<0x141, 0xF>(v);  // eight lanes mirrored
+  return add_dpp<0x140, 0xF>(v);  // sixteen lanes mirrored
+}
+
 // Sums of N values over the TPR threads of a row, the same in all of them.
 // lds: N floats per wave.
 template <class C, int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float* lds) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  for (int i = 0; i < N; ++i) v[i] = C::TPR < kWave ? narrow_sum(v[i]) : wave_sum(v[i]);
   if constexpr (C::TPR > kWave) {
     constexpr int W = C::TPR / kWave;
     const int wave = threadIdx.x / kWave;
@@ -174,32 +189,42 @@ struct RawRow {
   }
 };
 
-// A token's picks, pick j in lane j of each wave (k <= 64): the row of u, -1 for
-// one outside it, and the gate. One load for all of them.
+// A token's picks (k <= 64): the row of u, -1 for one outside it, and the gate, all
+// loaded at once. Pick j is in lane j of each wave; of rows of sixteen lanes, in
+// lane j % 16, register j / 16.
+template <class C>
 struct Picks {
-  int32_t row;
-  float g;
+  static constexpr int LANES = C::TPR < kWave ? C::TPR : kWave, REGS = kWave / LANES;
+  int32_t row[REGS], g[REGS];  // (the gate's bits)
   __device__ __forceinline__ void load(const NormCall& p, long long t) {
-    const int j = threadIdx.x % kWave;
-    row = -1;
-    g = 1.f;
-    if (!p.u || j >= p.k || t >= p.T) return;
-    const int32_t at = (int32_t)(t * p.k + j);
-    row = p.inv ? p.inv[at] : at;
-    if (row >= p.M) row = -1;
-    if (p.gates) g = p.gates[at];
+#pragma unroll
+    for (int i = 0; i < REGS; ++i) {
+      const int j = i * LANES + threadIdx.x % LANES;
+      row[i] = -1;
+      g[i] = __float_as_int(1.f);
+      if (!p.u || j >= p.k || t >= p.T) continue;
+      const int32_t at = (int32_t)(t * p.k + j);
+      row[i] = p.inv ? p.inv[at] : at;
+      if (row[i] >= p.M) row[i] = -1;
+      if (p.gates) g[i] = __float_as_int(p.gates[at]);
+    }
   }
-  __device__ __forceinline__ int32_t row_of(int j) const {
-    return __builtin_amdgcn_readlane(row, j);
+  __device__ __forceinline__ int pick(const int (&v)[REGS], int j) const {
+    if constexpr (REGS == 1) {
+      return __builtin_amdgcn_readlane(v[0], j);
+    } else {
+      static_assert(REGS == 4, "rows of sixteen lanes");
+      const int x = j < 16 ? v[0] : j < 32 ? v[1] : j < 48 ? v[2] : v[3];
+      return __shfl(x, j % LANES, LANES);
+    }
   }
-  __device__ __forceinline__ float gate_of(int j) const {
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), j));
-  }
+  __device__ __forceinline__ int32_t row_of(int j) const { return pick(row, j); }
+  __device__ __forceinline__ float gate_of(int j) const { return __int_as_float(pick(g, j)); }
 };
 
 // y += the picks j0 .. k - 1, ascending, four rows of u in flight.
 template <class C>
-__device__ __forceinline__ void add_picks(const NormCall& p, const Picks& picks, int j0, int lane,
+__device__ __forceinline__ void add_picks(const NormCall& p, const Picks<C>& picks, int j0, int lane,
                                           float (&y)[C::VALS]) {
   constexpr int U = C::NV == 1 ? 8 : 4;
   for (int j = j0; j < p.k; j += U) {
@@ -235,7 +260,7 @@ __global__ __launch_bounds__(C::THREADS) void norm_kernel(NormCall p) {
   if (t64 >= p.T) return;  // a whole wave; whole workgroups where rows are theirs
   const int t = (int)t64;
   const size_t at = (size_t)t * p.d;
-  Picks picks;
+  Picks<C> picks;
   picks.load(p, t);
   float r[C::VALS];
   if (p.r) {
@@ -283,7 +308,7 @@ __global__ __launch_bounds__(C::THREADS) void norm_kernel(NormCall p) {
 template <class C, int K>
 struct TokenLoads {
   RawRow<C> x, dn, dr, u[K];
-  Picks picks;
+  Picks<C> picks;
   __device__ __forceinline__ void load(const NormCall& p, long long t, int lane) {
     if (t >= p.T) return;
     if (p.w_pre) {
@@ -341,7 +366,7 @@ __global__ __launch_bounds__(C::THREADS) void norm_bwd_kernel(NormCall p, float*
   TokenLoads<C, K> next;
   next.picks.load(p, first);
   if constexpr (C::AHEAD) next.load(p, first, lane);
-  Picks after;
+  Picks<C> after;
   after.load(p, first + stride);
   Weights<C> w_pre, w_post;
   w_pre.init(p.w_pre, p.d, lane);
@@ -543,17 +568,19 @@ hipError_t launch_norm_bwd_cfg(const NormCall& c, float* part, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (groups) e = !c.u || c.k == 1 ? launch(norm_bwd_kernel<C, 1>) : launch(norm_bwd_kernel<C, 2>);
   if (e != hipSuccess || (!c.dw_pre && !c.dw_post)) return e;
-  return launch_kernel(norm_weights_kernel, dim3((c.d + 63) / 64, 2),
-                       dim3(64 * kSumWaves), 0, s, KernelTiming{}, (const float*)part, groups, c.d, c.dw_pre, c.dw_post);
+  return launch_kernel(norm_weights_kernel, dim3((c.d + 63) / 64, 2), dim3(64 * kSumWaves), 0, s,
+                       KernelTiming{}, (const float*)part, groups, c.d, c.dw_pre, c.dw_post);
 }
 
-// f(config) for rows of d values (EPC per 16 bytes): a wave per row up to 128
-// chunks, then a workgroup. The gradient holds about ten values per column and
+// f(config) for rows of d values (EPC per 16 bytes): sixteen lanes per row up to 16
+// chunks (32768 rows of 128 bf16 18 -> 12.5 us, their gradient 39 -> 25), a wave up to
+// 128, then a workgroup. The gradient holds about ten values per column and
 // thread, so its long rows go to 512 threads (1024 would leave each 128
 // registers).
 template <bool BACK, typename T, bool ALIGNED, typename F>
 hipError_t with_width(int d, F f) {
   constexpr int EPC = 16 / sizeof(T);
+  if (d <= 16 * EPC) return f(NormCfg<T, 16, 1, ALIGNED>{});
   if (d <= 64 * EPC) return f(NormCfg<T, 64, 1, ALIGNED>{});
   if (d <= 128 * EPC) return f(NormCfg<T, 64, 2, ALIGNED>{});
   if (d <= 256 * EPC) return f(NormCfg<T, 256, 1, ALIGNED>{});

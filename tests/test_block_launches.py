@@ -97,8 +97,8 @@ CASES = [
     (product_bwd(BF, TOP, 8, 8, 1), [TOP // 128, 1]),
     (product_bwd(BF, 100000, 4096, 1024, 4096), [1, 4096 * 64]),
     (product_bwd(F32, 1 << 24, 1000, 1000, 100), [(1 << 17) * 8, 6400]),
-    (norm(BF, TOP, 1, 1), [TOP // 4]),
-    (norm(F32, TOP // 64, 7, 64), [TOP // 256]),
+    (norm(BF, TOP, 1, 1), [TOP // 16]),
+    (norm(F32, TOP // 64, 7, 64), [TOP // 1024]),
     (norm(BF, 1 << 25, 2048, 1), [1 << 25]),
     (norm_bwd(BF, TOP, 1, 1), [512, 2]),
     (norm_bwd(F32, 1 << 23, 8192, 2), [512, 256]),
@@ -106,7 +106,8 @@ CASES = [
     (ortho(BF, 65535, 100, 1000), [65535, 65535, 65535]),
     (ortho(F32, 4, 16384, 16384), [1024, 4096, 8000]),
     (step(65535, 40, 300), [65535]),
-    (step(3, 16384, 1), [1, 1]),
+    (step(3, 16384, 1), [3, 192]),
+    (ortho(BF, 65535, 40, 16384), [65535, 65535 * 64, 65535 * 64]),
 ]
 
 

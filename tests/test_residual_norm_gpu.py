@@ -231,3 +231,14 @@ def test_zero_rows_and_infinities():
     assert not a[1].any() and not n[1].any() and a[4].isnan().all() and n[3, 7].isnan()
     good = [0, 1, 2, 5]
     assert torch.isfinite(a[good]).all() and torch.isfinite(n[good]).all()
+
+
+# Rows of sixteen lanes, several to a wave (picks in up to four registers), and rows
+# that end inside 16 bytes
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("d", [2, 3, 5, 8, 9, 15, 20, 61, 64, 66, 100, 127, 128, 129])
+@pytest.mark.parametrize("T,k", [(1, 1), (37, 2), (50, 17), (21, 64), (530, 3)])
+def test_narrow_rows(T, k, d, dt):
+    s = draw(T, d, k, dt, seed=d + k, routed=k > 1, gates=k > 1, pad=0.2 if k > 1 else 0.0,
+             extra=5 if k > 1 else 0)
+    check(s, dt)
