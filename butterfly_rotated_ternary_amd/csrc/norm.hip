@@ -10,7 +10,9 @@
 //   dy = D(y, w_post, dz);  du = g dy;  dg = <dy, u>
 //
 // Bound by HBM: each array is read or written once (the gradient reads u a
-// second time, out of L2, because dy needs sums over the row). A row belongs to
+// second time, out of L2, because dy needs sums over the row). 32768 tokens of
+// 4 rows of 4096 bf16, 1.88 GB: 349 us (5.4 TB/s); the gradient of 16384 tokens of 2
+// rows of 2048, 0.54 GB: 117 + 5 us (4.6 TB/s); one token of 8 rows 5.2 us. A row belongs to
 // TPR threads (sixteen, a wave, or a whole workgroup), a thread to EPC * NV of its
 // values, held in registers between the sums.
 #include "common.h"

@@ -1,6 +1,8 @@
 /*
  * bmoe.h — C ABI of libbmoe.so: the ButterflyMoE expert-layer forward and
- * its backward on AMD Instinct MI355X (gfx950).
+ * its backward on AMD Instinct MI355X (gfx950), the routing and training-step
+ * operators around it, and dense experts, the norms around a block and
+ * orthogonalised updates beside it.
  *
  * Method (ButterflyMoE: Sub-Linear Ternary Experts via Structured Butterfly
  * Orbits, gist.science technical summary):
@@ -52,7 +54,8 @@ typedef enum {
                             bmoe_pack_ternary and the size helpers) or in
                             [16, 8192] (every other entry point; the backward
                             also needs d <= 4096), N < 1 or N > 4096, k < 1 or
-                            k > N, T < 0, or T*k beyond 2^31 - 1 */
+                            k > N, T < 0, or T*k beyond 2^31 - 1; the calls with
+                            shapes of their own say so at their declaration */
   BMOE_E_DTYPE = 3,      /* unknown bmoe_dtype */
   BMOE_E_TERNARY = 4,    /* device: a W_base entry outside {-1, 0, +1} */
   BMOE_E_EXPERT = 5,     /* device: an expert id outside [0, N) */
@@ -666,7 +669,8 @@ bmoe_status bmoe_residual_norm_backward(bmoe_dtype dt, int T, int d, int k,
  * c = 2.0315 and 5 steps into about [0.7, 1.2], but for very small ones.
  * Products are taken with 22-bit operands and fp32 sums for either type; bf16
  * results are rounded once. A zero matrix gives zeros (with eps = 0: NaN), one
- * with a NaN or an infinity gives NaN throughout.
+ * with a NaN or an infinity gives NaN throughout. |U|_F has to be within fp32
+ * (beyond it the result is 0); its sum of squares is taken in 64 bits.
  *   u, o  [batch][rows][cols], dtype dt; o may be u.
  * 1 <= rows, cols <= 16384, 0 <= batch <= 65535 (0: a no-op). spec: 1 to 64
  * steps, eps >= 0, and coefficients under which no singular value that starts
