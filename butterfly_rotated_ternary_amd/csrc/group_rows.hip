@@ -8,18 +8,21 @@
 // chunks. One launch counts each chunk's experts, a second gives every chunk
 // the counts before it (at most 256 x N words from L2) and ranks its own rows
 // (64 at a time, one ballot per bit of the expert). One chunk needs no counts
-// from elsewhere: a single launch. 8 ids of 256 experts 3.2 us, 3009 of 60 2.0 + 7.3,
-// 131072 of 256 6.5 + 17.
+// from elsewhere: a single launch. 8 ids of 256 experts 3.5 us, 3009 of 60 5.2, 8192 of
+// 64 9.4, 131072 of 256 3.8 + 8.6.
 #include "common.h"
 #include "kernels.h"
 
 namespace bmoe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
+constexpr int kThreads = 256;  // of the count
 constexpr int kMostChunks = 256;
 constexpr int kLeastChunk = 2048;
+
+// Waves of the scatter, each with a cursor per expert in LDS: sixteen (131072 ids of
+// 256 experts 8.6 us, four 17), or four where sixteen would pass 64 KB.
+int waves_of(int N) { return 17 * (N + 1) * (int)sizeof(int) + 64 <= 65536 ? 16 : 4; }
 
 struct GroupArgs {
   const int32_t* ids;
@@ -46,27 +49,29 @@ __global__ __launch_bounds__(kThreads) void group_count_kernel(GroupArgs p) {
   for (int e = threadIdx.x; e < n; e += kThreads) p.count[(size_t)blockIdx.x * n + e] = cnt[e];
 }
 
-__global__ __launch_bounds__(kThreads) void group_scatter_kernel(GroupArgs p) {
-  extern __shared__ int sh[];  // [kWaves][n] cursors, [n] bases
-  __shared__ int scratch[kWaves];
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void group_scatter_kernel(GroupArgs p) {
+  constexpr int THREADS = 64 * WAVES;
+  extern __shared__ int sh[];  // [WAVES][n] cursors, [n] bases
+  __shared__ int scratch[WAVES];
   const int n = p.N + 1, tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  int* base = sh + kWaves * n;
+  int* base = sh + WAVES * n;
   const long long r0 = (long long)blockIdx.x * p.chunk;
   const int len = (int)min((long long)p.chunk, p.M - r0);
-  for (int i = tid; i < kWaves * n; i += kThreads) sh[i] = 0;
+  for (int i = tid; i < WAVES * n; i += THREADS) sh[i] = 0;
   __syncthreads();
-  // each wave owns a contiguous quarter of the chunk and counts it
-  const int quarter = (len + kWaves - 1) / kWaves;
-  const int wb = min(len, wave * quarter), we = min(len, wb + quarter);
+  // each wave owns a contiguous share of the chunk and counts it
+  const int share = (len + WAVES - 1) / WAVES;
+  const int wb = min(len, wave * share), we = min(len, wb + share);
   int* cur = sh + wave * n;
   for (int i = wb + lane; i < we; i += kWave) atomicAdd(&cur[key_of(p, (int)(r0 + i))], 1);
   __syncthreads();
   // per expert: the rows of all chunks, and of those before this one
-  for (int e = tid; e < n; e += kThreads) {
+  for (int e = tid; e < n; e += THREADS) {
     int total = 0, before = 0;
     if (p.chunks == 1) {
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) total += sh[w * n + e];
+      for (int w = 0; w < WAVES; ++w) total += sh[w * n + e];
     } else {
       // 16 loads in flight (131072 ids in 64 chunks: 33 us one by one)
       for (int c0 = 0; c0 < p.chunks; c0 += 16) {
@@ -85,7 +90,7 @@ __global__ __launch_bounds__(kThreads) void group_scatter_kernel(GroupArgs p) {
     // the wave's own counts become cursors relative to the expert's base
     int at = before;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
       const int v = sh[w * n + e];
       sh[w * n + e] = at;
       at += v;
@@ -93,7 +98,7 @@ __global__ __launch_bounds__(kThreads) void group_scatter_kernel(GroupArgs p) {
   }
   __syncthreads();
   // exclusive prefix sum of the totals: each thread owns a run of experts
-  const int per = (n + kThreads - 1) / kThreads;
+  const int per = (n + THREADS - 1) / THREADS;
   const int lo = min(n, tid * per), hi = min(n, lo + per);
   int seg = 0;
   for (int e = lo; e < hi; ++e) seg += base[e];
@@ -134,7 +139,10 @@ __global__ __launch_bounds__(kThreads) void group_scatter_kernel(GroupArgs p) {
   }
 }
 
-int chunk_of(int M) {
+// One chunk as long as a wave has at most eight times 64 rows (8200 ids of 64 experts
+// take 2.7 + 5.1 us in two launches).
+int chunk_of(int M, int N) {
+  if (M <= 512 * waves_of(N)) return 512 * waves_of(N);
   const int c = (int)(((long long)M + kMostChunks - 1) / kMostChunks);
   return c < kLeastChunk ? kLeastChunk : c;
 }
@@ -142,7 +150,7 @@ int chunk_of(int M) {
 }  // namespace
 
 size_t group_count_bytes(int M, int N) {
-  const size_t chunks = ((size_t)M + chunk_of(M) - 1) / chunk_of(M);
+  const size_t chunk = chunk_of(M, N), chunks = (M + chunk - 1) / chunk;
   return chunks > 1 ? chunks * (N + 1) * sizeof(int) : 0;
 }
 
@@ -156,7 +164,7 @@ hipError_t launch_group_rows(const int32_t* ids, int M, int N, int32_t* offsets,
   p.count = count;
   p.M = M;
   p.N = N;
-  p.chunk = chunk_of(M);
+  p.chunk = chunk_of(M, N);
   p.chunks = M > 0 ? (int)(((long long)M + p.chunk - 1) / p.chunk) : 1;
   p.nbits = 0;
   while ((1 << p.nbits) < N + 1) ++p.nbits;
@@ -165,13 +173,16 @@ hipError_t launch_group_rows(const int32_t* ids, int M, int N, int32_t* offsets,
                                        (uint32_t)(sizeof(int) * (N + 1)), s, KernelTiming{}, p);
     if (e != hipSuccess) return e;
   }
-  const size_t lds = sizeof(int) * (size_t)(kWaves + 1) * (N + 1);
+  if (waves_of(N) == 16)
+    return launch_kernel(group_scatter_kernel<16>, dim3(p.chunks), dim3(64 * 16),
+                         (uint32_t)(sizeof(int) * 17 * (N + 1)), s, KernelTiming{}, p);
+  const size_t lds = sizeof(int) * (size_t)5 * (N + 1);
   if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(group_scatter_kernel),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(group_scatter_kernel<4>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  return launch_kernel(group_scatter_kernel, dim3(p.chunks), dim3(kThreads), (uint32_t)lds, s,
+  return launch_kernel(group_scatter_kernel<4>, dim3(p.chunks), dim3(64 * 4), (uint32_t)lds, s,
                        KernelTiming{}, p);
 }
 

@@ -219,3 +219,14 @@ def test_short_and_odd_rows(K, O_, dt):
     mda, mdw = O.grouped_product_backward(abs(A), abs(W), o, rows, abs(D))
     close(r["da"], rda, mda, O_, dt)
     close(r["dw"], rdw, mdw, int(np.diff(o).max()), F32)
+
+
+@pytest.mark.parametrize("N", [959, 960, 961, 962, 963, 3273, 3274, 3275, 3276])
+@pytest.mark.parametrize("M", [2049, 8192, 8193, 20000])
+def test_group_rows_of_many_experts(M, N):
+    """Around the counts of experts and ids where the launches change."""
+    g = torch.Generator().manual_seed(N)
+    ids = torch.randint(-1, N + 1, (M, 1), generator=g, dtype=torch.int32)
+    got = bmoe.group_rows(ids.cuda(), N)
+    for name, x, y in zip(("offsets", "perm", "inv"), got, O.group_rows(ids.numpy(), N)):
+        assert np.array_equal(x.cpu().numpy(), y), name
