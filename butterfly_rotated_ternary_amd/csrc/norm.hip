@@ -563,7 +563,11 @@ hipError_t launch_norm_cfg(const NormCall& c, hipStream_t s) {
 template <class C>
 hipError_t launch_norm_bwd_cfg(const NormCall& c, float* part, hipStream_t s) {
   const size_t want = ((size_t)c.T + C::ROWS - 1) / C::ROWS;
-  const int groups = (int)(want < kBwdGroups ? want : kBwdGroups);  // T = 0: no sums, dw = 0
+  // T = 0: no sums, dw = 0. Two rounds at most: as many rows in each (1000 x 4096 fp32
+  // 36.5 -> 32 us; more rounds gain nothing by it)
+  const int groups = want > kBwdGroups && want <= 2 * kBwdGroups ? (int)((want + 1) / 2)
+                     : want < kBwdGroups                         ? (int)want
+                                                                 : kBwdGroups;
   const auto launch = [&](auto kernel) {
     return launch_kernel(kernel, dim3(groups), dim3(C::THREADS), 0, s, KernelTiming{}, c, part);
   };
