@@ -1044,6 +1044,12 @@ def clip_grads(grads, max_norm: float, *, out=None, stream=None) -> torch.Tensor
 
 # ---- around a block: dense experts, norms, orthogonalised updates ---------------
 
+def _fits(*counts: int):
+    """Refuses counts that the library's ints would wrap."""
+    if max(counts) > 0x7FFFFFFF:
+        raise ValueError(f"counts are at most 2^31 - 1, got {max(counts)}")
+
+
 def _workspace(n: int, what: str, device) -> torch.Tensor:
     if n == 0:
         raise BmoeError(2, what)
@@ -1057,6 +1063,7 @@ def group_rows(ids: torch.Tensor, n_experts: int, *, stream=None):
     T, k = _matrix("ids", ids).shape
     dev = ids.device
     _like("ids", ids, torch.int32, (T, k), dev)
+    _fits(T * k, n_experts)
     with _at(ids, stream):
         ws = _workspace(bmoe_group_rows_workspace_bytes(T, n_experts, k),
                         "bmoe_group_rows_workspace_bytes", dev)
@@ -1077,11 +1084,13 @@ def _grouped(a, w, offsets, perm, k):
     G, O = w.shape[:2]
     _like("w", w, a.dtype, (G, O, K), a.device)
     _like("offsets", offsets, torch.int32, (G + 1,), a.device)
+    _fits(R, K, O, k)
     if perm is None:
         return dt, R, K, O, G
     _like("perm", perm, torch.int32, (perm.numel(),), a.device)
     if k < 1:
         raise ValueError("k must be at least 1")
+    _fits(perm.numel())
     return dt, perm.numel(), K, O, G
 
 
@@ -1130,7 +1139,9 @@ def grouped_product_backward(a: torch.Tensor, w: torch.Tensor, offsets: torch.Te
 def _norm_inputs(x, T, d, u, k, inv, gates, w_post, w_pre):
     """Checks what both directions of residual_norm() read; the rows of u."""
     dev = x.device
+    _fits(T * k, d)
     if u is not None:
+        _fits(u.shape[0])
         if u.dim() != 2 or u.shape[1] != d:
             raise ValueError(f"u must be [rows][{d}], got shape {tuple(u.shape)}")
         _like("u", u, x.dtype, u.shape, dev)
@@ -1234,6 +1245,7 @@ def _matrices(name: str, t: torch.Tensor):
     if t.dim() not in (2, 3) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous matrix or a batch of matrices, got shape "
                          f"{tuple(t.shape)}")
+    _fits(*t.shape)
     return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
 
 

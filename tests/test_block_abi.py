@@ -192,3 +192,31 @@ def test_wrappers_refuse_before_the_library():
             bad()
     with pytest.raises(TypeError):
         bmoe.orthogonalize(x.half())
+
+
+def test_counts_past_an_int_are_refused():
+    """Not wrapped to small ones (tensors without storage: nothing runs)."""
+    lots = 2 ** 32 + 8
+
+    def meta(*shape, dt=torch.bfloat16):
+        return torch.empty(*shape, dtype=dt, device="meta")
+    i32, w = torch.int32, torch.float32
+    off = meta(3, dt=i32)
+    for call in [lambda: bmoe.group_rows(meta(lots, 1, dt=i32), 4),
+                 lambda: bmoe.group_rows(meta(2 ** 30, 4, dt=i32), 4),
+                 lambda: bmoe.group_rows(meta(4, 1, dt=i32), lots),
+                 lambda: bmoe.grouped_product(meta(lots, 8), meta(2, 8, 8), off),
+                 lambda: bmoe.grouped_product(meta(8, 8), meta(2, 8, 8), off, perm=meta(lots, dt=i32)),
+                 lambda: bmoe.grouped_product(meta(8, lots), meta(2, 8, lots), off),
+                 lambda: bmoe.grouped_product(meta(8, 8), meta(2, 8, 8), off, perm=meta(8, dt=i32),
+                                              k=lots),
+                 lambda: bmoe.grouped_product_backward(meta(lots, 8), meta(2, 8, 8), off,
+                                                       meta(lots, 8)),
+                 lambda: bmoe.residual_norm(None, meta(lots, 1), w_pre=meta(1, dt=w)),
+                 lambda: bmoe.residual_norm(meta(lots, 1), meta(4, 1), inv=meta(4, dt=i32)),
+                 lambda: bmoe.residual_norm_backward(None, meta(lots, 1), dr_out=meta(lots, 1)),
+                 lambda: bmoe.orthogonalize(meta(8, lots)),
+                 lambda: bmoe.orthogonalize(meta(lots, 8, 8)),
+                 lambda: bmoe.orthogonal_step(meta(8, lots), meta(8, lots), meta(8, lots, dt=w), 0.1)]:
+        with pytest.raises(ValueError, match="at most 2"):
+            call()
