@@ -71,34 +71,53 @@ bool norm_shape(int T, int d, int k, int M, const void* u, const void* inv) {
          (inv || M >= (long long)T * k);
 }
 
-// The singular values (all at most 1 at first) stay within what the products'
-// fp16 parts hold: 16 for the entries of X, P = X X^T and Q = a + b P + c P P,
-// bounded through sigma^2 and a + b sigma^2 + c sigma^4 on a fine grid.
-bool bounded(const bmoe_ortho_spec& s) {
-  double hi = 1.0;
+// The range of the iteration under given coefficients: the singular values (all at
+// most 1 at first) of X, whose squares are P's, and those of Q = a + b P + c P P,
+// bounded through sigma^2 and a + b sigma^2 + c sigma^4 on a fine grid. No entry of
+// a matrix passes its largest singular value.
+struct OrthoRange {
+  double x, q;
+  bool ok;  // within what the products' fp16 parts hold: 16 with a scale of 2^12
+};
+OrthoRange ortho_range(const bmoe_ortho_spec& s) {
+  double hi = 1.0, most_x = 1.0, most_q = 0.0;
   for (int i = 0; i < s.steps; ++i) {
     double next = 0.0;
+    if (hi > most_x) most_x = hi;
     for (int j = 0; j <= 1024; ++j) {
       const double v = hi * j / 1024, v2 = v * v;
-      const double q = s.a + (s.b + s.c * v2) * v2;
-      if (!(std::fabs(q) <= 15.0) || !(v2 <= 15.0)) return false;
-      if (std::fabs(q * v) > next) next = std::fabs(q * v);
+      const double q = std::fabs(s.a + (s.b + s.c * v2) * v2);
+      if (!(q <= 15.0) || !(v2 <= 15.0)) return {0.0, 0.0, false};
+      if (q > most_q) most_q = q;
+      if (q * v > next) next = q * v;
     }
     hi = next * 1.01;
   }
-  return hi <= 15.0;
+  return {most_x, most_q, hi <= 15.0};
+}
+// The largest power of two up to 2^15 that leaves values of up to `most` within
+// fp16 (65504, less what rounding and the grid may add).
+float fp16_scale(double most) {
+  int e = 15;
+  while (std::ldexp(most, e) > 61440.0) --e;
+  return (float)std::ldexp(1.0, e);
 }
 
 bmoe_status ortho_spec(const bmoe_ortho_spec* s, OrthoCall* c) {
   if (!s) return BMOE_E_NULL;
   if (s->steps < 1 || s->steps > 64 || !(s->eps >= 0.f) || !std::isfinite(s->eps) ||
-      !std::isfinite(s->a) || !std::isfinite(s->b) || !std::isfinite(s->c) || !bounded(*s))
+      !std::isfinite(s->a) || !std::isfinite(s->b) || !std::isfinite(s->c))
     return BMOE_E_VALUE;
+  const OrthoRange range = ortho_range(*s);
+  if (!range.ok) return BMOE_E_VALUE;
   c->steps = s->steps;
   c->a = s->a;
   c->b = s->b;
   c->c = s->c;
   c->eps = s->eps;
+  c->sx = fp16_scale(range.x);
+  c->sp = fp16_scale(range.x * range.x);
+  c->sq = fp16_scale(range.q);
   return BMOE_OK;
 }
 

@@ -5,13 +5,17 @@
 // columns, so P is always the smaller one). An odd polynomial of X moves its
 // singular values and leaves its singular vectors.
 //
-// Numbers. Operands are kept as pairs of fp16, hi + lo, of the value times
-// 2^12: 22 bits where a value is above 2^-14 of 1 after that scaling, an
-// absolute error of 2^-37 below. The singular values stay below 16 (checked on
-// the host for the given coefficients), so no scaled value passes 2^16. Three
-// fp16 MFMAs (hi hi + hi lo + lo hi, fp32 sums) make one product of about fp32's
-// accuracy at five times the rate that fp32 MFMAs have. The normalising sums are
-// in 64 bits.
+// Numbers. Operands are kept as pairs of fp16, hi + lo, of the value times a power
+// of two: the largest that leaves room for what X, P and Q can hold under the given
+// coefficients (the host bounds their singular values; for 3.4445, -4.7750, 2.0315
+// 2^15 for X and P, 2^14 for Q). That is 22 bits of a value above 2^-18, and an
+// absolute error of 2^-40 (2^-39) below. Three fp16 MFMAs (hi hi + hi lo + lo hi,
+// fp32 sums) make one product at five times the rate that fp32 MFMAs have. In the
+// norm the result is as near to the exact one as an iteration in fp32 (64 x 512
+// normal entries 1.5e-6 and 1.7e-6 off); a row or column far below the others meets
+// the absolute error: with rows from 1 down to 1e-6 the smallest is 2e-5 (64 x 512) to
+// 1e-4 (600 x 1500) off by itself, fp32 4e-6 to 2e-5. (One scale of 2^12 for all:
+// 1.6e-4 to 8e-4.) The normalising sums are in 64 bits.
 //
 // P and Q are symmetric: only tiles on and below the diagonal are computed,
 // each written twice. Rows are padded to whole 16-byte chunks (zeros).
@@ -29,8 +33,6 @@ namespace bmoe {
 namespace {
 
 using namespace tile;
-
-constexpr float kScale = 4096.f;  // of all fp16 operands
 
 // What U is: u itself, or the momentum of a step (grad added to it).
 struct Source {
@@ -120,7 +122,7 @@ __global__ __launch_bounds__(kSumThreads) void ortho_sum_kernel(Source src, size
   if (threadIdx.x == 0) part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
 }
 
-// A value times kScale as its two fp16 parts.
+// A scaled value as its two fp16 parts.
 __device__ __forceinline__ void split(float v, _Float16& hi, _Float16& lo) {
   hi = (_Float16)v;
   lo = (_Float16)(v - (float)hi);
@@ -128,7 +130,7 @@ __device__ __forceinline__ void split(float v, _Float16& hi, _Float16& lo) {
 
 // ---- X_0 -----------------------------------------------------------------------
 __global__ __launch_bounds__(kSumThreads) void ortho_split_kernel(Source src, int rows, int cols,
-                                                                  int ld, float eps,
+                                                                  int ld, float eps, float scale,
                                                                   const double* part, int parts,
                                                                   _Float16* hi, _Float16* lo) {
   __shared__ double lds[kSumThreads / 64];
@@ -155,7 +157,7 @@ __global__ __launch_bounds__(kSumThreads) void ortho_split_kernel(Source src, in
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       _Float16 a, b;
-      split(v[e] / norm * kScale, a, b);
+      split(v[e] / norm * scale, a, b);
       h[e] = a;
       l[e] = b;
     }
@@ -175,11 +177,12 @@ struct OrthoArgs {
   int rows, cols, ld, m, ldm;  // of X; of P and Q
   int batch, tiles, tiles_n;  // tiles per matrix
   int run_items;
-  float a, b, c;          // kPoly
+  float unit;             // of the accumulators: to the output's scale (kPoly: to P's)
+  float a, b, c;          // kPoly: to Q's scale
   // the last product's epilogue
   void* o;                // [batch][rows][cols]: X, or w = keep w - rate X
   int o_bf16, update;
-  float keep, rate;
+  float keep, rate, unscale;  // 1 / the scale of X
 };
 
 // A 32 x 32 block of accumulators through LDS, so that a lane gets sixteen
@@ -215,7 +218,7 @@ struct Block {
   }
 };
 
-// v, sixteen entries of a row of P P times kScale, to those of Q.
+// v, sixteen entries of a row of P P at P's scale, to those of Q.
 __device__ __forceinline__ void add_poly(const OrthoArgs& p, const char* q, int row, int col,
                                          float (&v)[16]) {
   const _Float16* hi = reinterpret_cast<const _Float16*>(q) + (size_t)row * p.ldm + col;
@@ -232,7 +235,7 @@ __device__ __forceinline__ void add_poly(const OrthoArgs& p, const char* q, int 
     for (int e = 0; e < 8; ++e) {
       const float pv = (float)a[e] + (float)b[e];
       v[8 * h + e] = fmaf(p.c, v[8 * h + e], p.b * pv);
-      if (row == col + 8 * h + e) v[8 * h + e] += p.a * kScale;
+      if (row == col + 8 * h + e) v[8 * h + e] += p.a;
     }
   }
 }
@@ -259,7 +262,7 @@ __device__ __forceinline__ void store_parts(const OrthoArgs& p, int batch, int r
   }
 }
 
-// Sixteen entries of the last iterate (times kScale) to the result or the weights.
+// Sixteen entries of the last iterate (at X's scale) to the result or the weights.
 __device__ __forceinline__ void store_result(const OrthoArgs& p, int batch, int row, int col,
                                              const float (&v)[16]) {
   if (row >= p.rows) return;
@@ -280,7 +283,7 @@ __device__ __forceinline__ void store_result(const OrthoArgs& p, int batch, int 
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float x = v[8 * h + e] * (1.f / kScale);
+        const float x = v[8 * h + e] * p.unscale;
         o[e] = p.update ? fmaf(p.keep, o[e], -p.rate * x) : x;
       }
       if (p.o_bf16) {
@@ -293,7 +296,7 @@ __device__ __forceinline__ void store_result(const OrthoArgs& p, int batch, int 
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         if (e >= n) continue;
-        float x = v[8 * h + e] * (1.f / kScale);
+        float x = v[8 * h + e] * p.unscale;
         const size_t i = at + 8 * h + e;
         if (p.update) x = fmaf(p.keep, load_any(p.o, p.o_bf16, i), -p.rate * x);
         if (p.o_bf16) static_cast<uint16_t*>(p.o)[i] = (uint16_t)f32_to_bf16_bits(x);
@@ -394,7 +397,7 @@ __global__ __launch_bounds__(C::THREADS) void ortho_product_kernel(OrthoArgs p) 
       float v[16];
       b.row(stg, lane, v);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] *= 1.f / kScale;
+      for (int e = 0; e < 16; ++e) v[e] *= p.unit;
       if constexpr (PRODUCT == kPoly) add_poly(p, q, row, col, v);
       if constexpr (PRODUCT == kApply) {
         if (p.o) {
@@ -409,7 +412,7 @@ __global__ __launch_bounds__(C::THREADS) void ortho_product_kernel(OrthoArgs p) 
           b.column(stg, lane, v);
           if constexpr (PRODUCT == kGram) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] *= 1.f / kScale;
+            for (int e = 0; e < 16; ++e) v[e] *= p.unit;
           }
           store_parts(p, batch, p.m, p.m, p.ldm, col0 + lane / 2, row0 + 16 * (lane & 1), v);
         }
@@ -508,10 +511,12 @@ constexpr int kPitch = 72;  // halves per row of P and Q in LDS
 struct SmallArgs {
   Source src;
   int rows, cols, steps, tall;
-  float a, b, c, eps;
+  float a, b, c, eps;           // a, b, c: to Q's scale
+  float sx;                     // the scale of X
+  float p_unit, pp_unit, x_unit;  // X X^T and P P to P's scale, Q X to X's
   void* o;
   int o_bf16, update;
-  float keep, rate;
+  float keep, rate, unscale;    // Q X to the result
   // matrices in slabs
   const double* part;  // [batch][parts]: sums of squares
   int parts;
@@ -651,15 +656,15 @@ __device__ __forceinline__ double small_sum(double v, double* dsum, int lane, in
 // X_0 in both layouts, the second through the wave's own LDS once (33 floats a
 // row: no bank twice).
 template <int MB, int NB>
-__device__ __forceinline__ void first_operands(const Entries<MB, NB>& v, float norm, float* mine,
-                                               int lane, Operands<MB, NB>& x) {
+__device__ __forceinline__ void first_operands(const Entries<MB, NB>& v, float norm, float scale,
+                                               float* mine, int lane, Operands<MB, NB>& x) {
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
       f32x16 y;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) y[r] = v[nb][mb][r] / norm * kScale;
+      for (int r = 0; r < 16; ++r) y[r] = v[nb][mb][r] / norm * scale;
 #pragma unroll
       for (int s = 0; s < 2; ++s) split_slice(y, s, 1.f, x.x2[nb][2 * mb + s]);
       Block::order();
@@ -697,15 +702,15 @@ __device__ __forceinline__ float waves_sum(const SmallLds<MB>& lds, int e) {
   for (int w = 1; w < kSmallWaves; ++w) sum += lds.red[w][e];
   return sum;
 }
-// P's entry e (as above) from its sum, which has the scale twice.
+// P's entry e (as above) from its sum at the square of X's scale.
 template <int MB>
-__device__ __forceinline__ void put_p(SmallLds<MB>& lds, int e, float sum) {
+__device__ __forceinline__ void put_p(const SmallArgs& p, SmallLds<MB>& lds, int e, float sum) {
   const int i = e / 1024, r = e % 1024 / 64, l = e % 64;
   int br, bc;
   SmallLds<MB>::block_of(i, br, bc);
   const int row = 32 * br + acc_row(r, l), col = 32 * bc + (l & 31);
   _Float16 hi, lo;
-  split(sum * (1.f / kScale), hi, lo);
+  split(sum * p.p_unit, hi, lo);
   lds.P[0][row * kPitch + col] = hi;
   lds.P[1][row * kPitch + col] = lo;
   if (br != bc) {
@@ -734,8 +739,8 @@ __device__ __forceinline__ void small_poly(const SmallArgs& p, SmallLds<MB>& lds
   for (int r = 0; r < 16; ++r) {
     const int row = 32 * br + acc_row(r, lane), col = 32 * bc + (lane & 31);
     const float pv = (float)lds.P[0][row * kPitch + col] + (float)lds.P[1][row * kPitch + col];
-    float q = fmaf(p.c, acc[r] * (1.f / kScale), p.b * pv);
-    if (row == col) q += p.a * kScale;
+    float q = fmaf(p.c, acc[r] * p.pp_unit, p.b * pv);
+    if (row == col) q += p.a;
     _Float16 hi, lo;
     split(q, hi, lo);
     lds.Q[0][row * kPitch + col] = hi;
@@ -758,7 +763,8 @@ __device__ __forceinline__ void read_q(const SmallLds<MB>& lds, int mb, int lane
 }
 // X <- Q X, in both layouts.
 template <int MB, int NB>
-__device__ __forceinline__ void small_apply(const SmallLds<MB>& lds, int lane, Operands<MB, NB>& x) {
+__device__ __forceinline__ void small_apply(const SmallArgs& p, const SmallLds<MB>& lds, int lane,
+                                            Operands<MB, NB>& x) {
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     f32x16 next[MB];
@@ -774,13 +780,13 @@ __device__ __forceinline__ void small_apply(const SmallLds<MB>& lds, int lane, O
         t = mma3(x.x2[nb][s], q[s], t);
       }
 #pragma unroll
-      for (int s = 0; s < 2; ++s) split_slice(t, s, 1.f / kScale, x.x1[mb][2 * nb + s]);
+      for (int s = 0; s < 2; ++s) split_slice(t, s, p.x_unit, x.x1[mb][2 * nb + s]);
       __builtin_amdgcn_sched_barrier(0);  // (two blocks at a time would spill)
     }
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) split_slice(next[mb], s, 1.f / kScale, x.x2[nb][2 * mb + s]);
+      for (int s = 0; s < 2; ++s) split_slice(next[mb], s, p.x_unit, x.x2[nb][2 * mb + s]);
     __builtin_amdgcn_sched_barrier(0);
   }
 }
@@ -806,7 +812,7 @@ __device__ __forceinline__ void store_small_as(const SmallArgs& p, T* out, const
   }
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
-    float o = x[r] * (1.f / kScale) * (1.f / kScale);
+    float o = x[r] * p.unscale;
     if (p.update) o = fmaf(p.keep, w[r], -p.rate * o);
     if (mi + acc_row(r, lane) < m && ni < n) {
       if constexpr (sizeof(T) == 2) out[at[r]] = (T)f32_to_bf16_bits(o);
@@ -859,7 +865,7 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(SmallArgs p)
       for (int r = 0; r < 16; ++r) acc = fma((double)v[nb][mb][r], (double)v[nb][mb][r], acc);
   const float norm = (float)sqrt(small_sum(acc, lds.dsum, lane, wave)) + p.eps;
   Operands<MB, NB> ops;
-  first_operands<MB, NB>(v, norm, lds.red[wave], lane, ops);
+  first_operands<MB, NB>(v, norm, p.sx, lds.red[wave], lane, ops);
   const auto make_q = [&]() {
     __syncthreads();  // red, P and Q have been read
     wave_gram<MB, NB>(ops, lds.red[wave], lane);
@@ -867,7 +873,7 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(SmallArgs p)
 #pragma unroll
     for (int j = 0; j < SmallLds<MB>::BLOCKS * 2; ++j) {
       const int e = tid + j * kSmallThreads;
-      put_p<MB>(lds, e, waves_sum<MB>(lds, e));
+      put_p<MB>(p, lds, e, waves_sum<MB>(lds, e));
     }
     __syncthreads();
     small_poly<MB>(p, lds, lane, wave);
@@ -875,7 +881,7 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(SmallArgs p)
   };
   for (int step = 1; step < p.steps; ++step) {
     make_q();
-    small_apply<MB, NB>(lds, lane, ops);
+    small_apply<MB, NB>(p, lds, lane, ops);
   }
   make_q();
   small_result<MB, NB>(p, x, lds, n0, lane, ops);
@@ -908,7 +914,7 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_slab_kernel(SmallArgs p) 
     double acc = 0.0;
     for (int i = tid; i < p.parts; i += kSmallThreads) acc += p.part[(size_t)blockIdx.y * p.parts + i];
     const float norm = (float)sqrt(small_sum(acc, lds.dsum, lane, wave)) + p.eps;
-    first_operands<MB, NB>(v, norm, lds.red[wave], lane, ops);
+    first_operands<MB, NB>(v, norm, p.sx, lds.red[wave], lane, ops);
   } else {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -942,8 +948,8 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_slab_kernel(SmallArgs p) 
     }
 #pragma unroll
     for (int j = 0; j < PAIRS; ++j) {
-      put_p<MB>(lds, 2 * (tid + j * kSmallThreads), sum[j][0]);
-      put_p<MB>(lds, 2 * (tid + j * kSmallThreads) + 1, sum[j][1]);
+      put_p<MB>(p, lds, 2 * (tid + j * kSmallThreads), sum[j][0]);
+      put_p<MB>(p, lds, 2 * (tid + j * kSmallThreads) + 1, sum[j][1]);
     }
     __syncthreads();
     small_poly<MB>(p, lds, lane, wave);
@@ -952,7 +958,7 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_slab_kernel(SmallArgs p) 
       small_result<MB, NB>(p, x, lds, n0, lane, ops);
       return;
     } else {
-      small_apply<MB, NB>(lds, lane, ops);
+      small_apply<MB, NB>(p, lds, lane, ops);
     }
   }
 #pragma unroll
@@ -1062,9 +1068,15 @@ hipError_t launch_ortho(const OrthoCall& call, void* ws, hipStream_t s) {
   sp.cols = cols;
   sp.steps = call.steps;
   sp.tall = rows > cols;
-  sp.a = call.a;
-  sp.b = call.b;
-  sp.c = call.c;
+  // (powers of two: exact)
+  sp.a = call.a * call.sq;
+  sp.b = call.b * (call.sq / call.sp);
+  sp.c = call.c * (call.sq / call.sp);
+  sp.sx = call.sx;
+  sp.p_unit = call.sp / (call.sx * call.sx);
+  sp.pp_unit = 1.f / call.sp;
+  sp.x_unit = 1.f / call.sq;
+  sp.unscale = 1.f / (call.sq * call.sx);
   sp.eps = call.eps;
   sp.o = call.o;
   sp.o_bf16 = call.o_bf16;
@@ -1099,7 +1111,7 @@ hipError_t launch_ortho(const OrthoCall& call, void* ws, hipStream_t s) {
   const size_t blocks = ((size_t)rows * l.ld / 8 + kSumThreads - 1) / kSumThreads;
   const size_t enough = batch >= 32 ? 64 : 2048;
   e = launch_kernel(ortho_split_kernel, dim3((unsigned)(blocks < enough ? blocks : enough), batch),
-                    dim3(kSumThreads), 0, s, KernelTiming{}, src, rows, cols, l.ld, call.eps,
+                    dim3(kSumThreads), 0, s, KernelTiming{}, src, rows, cols, l.ld, call.eps, call.sx,
                     (const double*)part, parts, x[0], x[0] + l.x_part / 2);
   if (e != hipSuccess) return e;
 
@@ -1114,9 +1126,10 @@ hipError_t launch_ortho(const OrthoCall& call, void* ws, hipStream_t s) {
   p.ldm = l.ldm;
   p.x_part = l.x_part;
   p.q_part = l.p_part;
-  p.a = call.a;
-  p.b = call.b;
-  p.c = call.c;
+  p.a = sp.a;
+  p.b = sp.b;
+  p.c = sp.c;
+  p.unscale = 1.f / call.sx;
   p.o_bf16 = call.o_bf16;
   p.update = call.update;
   p.keep = call.keep;
@@ -1129,14 +1142,17 @@ hipError_t launch_ortho(const OrthoCall& call, void* ws, hipStream_t s) {
     p.q = nullptr;
     p.out = P;
     p.out_part = l.p_part / 2;
+    p.unit = sp.p_unit;
     e = tall ? launch_product<kGram, true>(p, s) : launch_product<kGram, false>(p, s);
     if (e != hipSuccess) return e;
     p.q = P;
     p.out = Q;
+    p.unit = sp.pp_unit;
     e = launch_product<kPoly, false>(p, s);
     if (e != hipSuccess) return e;
     p.q = Q;
     p.out = x[(i + 1) & 1];
+    p.unit = sp.x_unit;
     p.out_part = l.x_part / 2;
     if (i + 1 == call.steps) p.o = call.o;
     e = tall ? launch_product<kApply, true>(p, s) : launch_product<kApply, false>(p, s);

@@ -667,8 +667,11 @@ bmoe_status bmoe_residual_norm_backward(bmoe_dtype dt, int T, int d, int k,
  * (P = X^T X from the other side where rows > cols). It keeps U's singular
  * vectors and moves the singular values towards 1; with a = 3.4445, b = -4.7750,
  * c = 2.0315 and 5 steps into about [0.7, 1.2], but for very small ones.
- * Products are taken with 22-bit operands and fp32 sums for either type; bf16
- * results are rounded once. A zero matrix gives zeros (with eps = 0: NaN), one
+ * Products are taken with operands of two fp16 parts and fp32 sums for either type:
+ * 22 bits of a value above 2^-17 and an absolute error of 2^-39 below, with |U|_F = 1
+ * and these coefficients (2^-15 and 2^-37 with any that are taken). In the norm the result is as
+ * near as an iteration in fp32; a row or column that is 1e-6 of the others may be 1e-4
+ * of itself off. bf16 results are rounded once. A zero matrix gives zeros (with eps = 0: NaN), one
  * with a NaN or an infinity gives NaN throughout. |U|_F has to be within fp32
  * (beyond it the result is 0); its sum of squares is taken in 64 bits.
  *   u, o  [batch][rows][cols], dtype dt; o may be u.

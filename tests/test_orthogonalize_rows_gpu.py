@@ -1,0 +1,59 @@
+"""Newton-Schulz steps of matrices whose rows or columns differ in size, each row
+and column judged by itself.
+
+Tolerance. X's entries are pairs of fp16 of 2^15 times the value (for the default
+coefficients): below 2^-18 what is lost is uniform within half of the last
+subnormal place, 2^-40, so 2^-40 / sqrt(3) in the mean square. One step takes a row
+that is small to about a = 3.4445 times itself, and with it that error: for n
+entries 3.4445 sqrt(n) 2^-40 / sqrt(3) = 2 sqrt(n) 2^-40 in the 2-norm. P's and Q's
+own entries add a term of a few 2^-40 without sqrt(n). Two and a half times the mean
+square's is allowed (a sum over hundreds of independent roundings is within a few
+hundredths of it), and 2^-19 of the row's own norm for the 22 bits and the fp32 sums."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from butterfly_rotated_ternary_amd import bmoe
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def f64(t):
+    return t.detach().cpu().to(torch.float64).numpy()
+
+
+def randn(shape, seed):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed))
+
+
+# one workgroup, slabs, tiles of 64 and of 128
+@pytest.mark.parametrize("m,n", [(32, 900), (64, 512), (24, 3000), (130, 520), (600, 1500)])
+@pytest.mark.parametrize("tall", [False, True])
+@pytest.mark.parametrize("side", ["short", "long"])
+def test_small_rows_and_columns(m, n, tall, side):
+    u = randn((m, n), m + n)
+    if side == "short":
+        u *= torch.logspace(0, -6, m)[:, None]
+    else:
+        u *= torch.logspace(0, -6, n)[None]
+    if tall:
+        u = u.t().contiguous()
+    o = f64(bmoe.orthogonalize(u.cuda(), bmoe.OrthoSpec(1)))
+    ref = O.newton_schulz(f64(u), 1)
+    if (side == "short") == tall:
+        o, ref = o.T, ref.T
+    err, size = np.linalg.norm(o - ref, axis=1), np.linalg.norm(ref, axis=1)
+    tol = 5 * np.sqrt(ref.shape[1]) * 2.0 ** -40 + 2.0 ** -19 * size
+    assert (err <= tol).all(), float((err / tol).max())
+
+
+@pytest.mark.parametrize("m,n", [(64, 512), (24, 3000), (200, 520)])
+def test_one_row_far_above_the_others(m, n):
+    u = randn((m, n), 3)
+    u[5] *= 1e5
+    o = f64(bmoe.orthogonalize(u.cuda(), bmoe.OrthoSpec(1)))
+    ref = O.newton_schulz(f64(u), 1)
+    err, size = np.linalg.norm(o - ref, axis=1), np.linalg.norm(ref, axis=1)
+    assert (err <= 5 * np.sqrt(n) * 2.0 ** -40 + 2.0 ** -19 * size).all()
