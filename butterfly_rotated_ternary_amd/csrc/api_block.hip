@@ -91,9 +91,9 @@ OrthoRange ortho_range(const bmoe_ortho_spec& s) {
       if (q > most_q) most_q = q;
       if (q * v > next) next = q * v;
     }
-    hi = next * 1.01;
+    hi = next * 1.01;  // (the last iterate is the result: no operand, so no bound)
   }
-  return {most_x, most_q, hi <= 15.0};
+  return {most_x, most_q, true};
 }
 // The largest power of two up to 2^15 that leaves values of up to `most` within
 // fp16 (65504, less what rounding and the grid may add).

@@ -669,11 +669,12 @@ bmoe_status bmoe_residual_norm_backward(bmoe_dtype dt, int T, int d, int k,
  * c = 2.0315 and 5 steps into about [0.7, 1.2], but for very small ones.
  * Products are taken with operands of two fp16 parts and fp32 sums for either type:
  * 22 bits of a value above 2^-17 and an absolute error of 2^-39 below, with |U|_F = 1
- * and these coefficients (2^-15 and 2^-37 with any that are taken). In the norm the result is as
- * near as an iteration in fp32; a row or column that is 1e-6 of the others may be 1e-4
- * of itself off. bf16 results are rounded once. A zero matrix gives zeros (with eps = 0: NaN), one
- * with a NaN or an infinity gives NaN throughout. |U|_F has to be within fp32
- * (beyond it the result is 0); its sum of squares is taken in 64 bits.
+ * and these coefficients (2^-15 and 2^-37 with any that are taken). In the norm the
+ * result is as near as an iteration in fp32; a row or column that is 1e-6 of the
+ * others may be 1e-4 of itself off. bf16 results are rounded once. A zero matrix
+ * gives zeros (with eps = 0: NaN), one with a NaN or an infinity gives NaN
+ * throughout. |U|_F has to be within fp32 (beyond it the result is 0); its sum of
+ * squares is taken in 64 bits.
  *   u, o  [batch][rows][cols], dtype dt; o may be u.
  * 1 <= rows, cols <= 16384, 0 <= batch <= 65535 (0: a no-op). spec: 1 to 64
  * steps, eps >= 0, and coefficients under which no singular value that starts

@@ -57,3 +57,22 @@ def test_one_row_far_above_the_others(m, n):
     ref = O.newton_schulz(f64(u), 1)
     err, size = np.linalg.norm(o - ref, axis=1), np.linalg.norm(ref, axis=1)
     assert (err <= 5 * np.sqrt(n) * 2.0 ** -40 + 2.0 ** -19 * size).all()
+
+
+# Coefficients up to the range's ends: whatever scales they leave, no operand passes
+# fp16. A polynomial of these entries is at most 15 in Q and 3.87 in X: the errors are
+# those of the scales 2^12 and up, relative to the whole matrix.
+@pytest.mark.parametrize("steps,coeffs", [(1, (14.9, 0.0, 0.0)), (2, (3.8, 0.0, 0.0)),
+                                          (1, (0.0, 0.0, 14.9)), (3, (1.9, 0.0, -0.4)),
+                                          (2, (0.02, 0.01, 0.0)), (1, (-14.0, 28.0, -14.0))])
+@pytest.mark.parametrize("shape", [(40, 72), (16, 1500), (130, 200), (200, 130)])
+def test_coefficients_at_the_range(shape, steps, coeffs):
+    # one singular value is nearly all of the matrix: as near to 1 as it can be
+    u = randn((shape[0], 1), 4) @ randn((1, shape[1]), 5) + 1e-2 * randn(shape, 6)
+    spec = bmoe.OrthoSpec(steps, coeffs)
+    o = f64(bmoe.orthogonalize(u.cuda(), spec))
+    ref = O.newton_schulz(f64(u), steps, coeffs)
+    assert np.isfinite(o).all()
+    # each step: operands of 2^-22 with terms of up to |a| + |b| + |c| times the iterate
+    grow = np.prod([max(1.0, sum(abs(c) for c in coeffs))] * steps)
+    assert np.linalg.norm(o - ref) <= 2.0 ** -19 * steps * grow * max(1.0, np.linalg.norm(ref))
