@@ -76,3 +76,33 @@ def test_coefficients_at_the_range(shape, steps, coeffs):
     # each step: operands of 2^-22 with terms of up to |a| + |b| + |c| times the iterate
     grow = np.prod([max(1.0, sum(abs(c) for c in coeffs))] * steps)
     assert np.linalg.norm(o - ref) <= 2.0 ** -19 * steps * grow * max(1.0, np.linalg.norm(ref))
+
+
+def amplified(u, steps, a=3.4445, b=-4.7750, c=2.0315):
+    """How much of one step's relative error the whole iteration can make: an odd
+    polynomial of a matrix moves a small change by its divided differences between the
+    singular values and their negatives."""
+    s = np.linalg.svd(u, compute_uv=False)
+    s = s / np.sqrt(np.sum(s * s))
+    total = 0.0
+    for _ in range(steps):
+        p = a * s + b * s ** 3 + c * s ** 5
+        x, y = np.concatenate([s, -s]), np.concatenate([p, -p])
+        dx, dy = x[:, None] - x[None], y[:, None] - y[None]
+        slope = a + 3 * b * x ** 2 + 5 * c * x ** 4
+        near = np.abs(dx) < 1e-9
+        grow = np.abs(np.where(near, slope[:, None], dy / np.where(near, 1.0, dx))).max()
+        total = (total * grow * np.linalg.norm(s) + np.linalg.norm(p)) / np.linalg.norm(p)
+        s = p
+    return total
+
+
+# A step's own error is below 2^-19 of the result (three products of 22-bit operands,
+# coefficients of up to 4.8, fp32 sums); later steps amplify it as far as these
+# singular values let them, 30 to 100 times in all.
+@pytest.mark.parametrize("shape", [(64, 512), (512, 64), (32, 900), (24, 3000), (130, 520),
+                                   (520, 130), (300, 260)])
+def test_five_steps_in_the_norm(shape):
+    u = randn(shape, sum(shape))
+    o, ref = f64(bmoe.orthogonalize(u.cuda())), O.newton_schulz(f64(u))
+    assert np.linalg.norm(o - ref) <= 2.0 ** -19 * amplified(f64(u), 5) * np.linalg.norm(ref)
