@@ -194,11 +194,15 @@ def lib():
         L.bmoe_grouped_product.argtypes = [c_int, c_int, c_int, c_int, c_int, vp, c_int, vp, c_int,
                                            vp, vp, vp, vp]
         L.bmoe_grouped_product.restype = c_int
+        L.bmoe_grouped_product_filled.argtypes = L.bmoe_grouped_product.argtypes
+        L.bmoe_grouped_product_filled.restype = c_int
         L.bmoe_grouped_product_backward_workspace_bytes.argtypes = [c_int] * 5
         L.bmoe_grouped_product_backward_workspace_bytes.restype = c_sz
         L.bmoe_grouped_product_backward.argtypes = [c_int, c_int, c_int, c_int, c_int, vp, c_int,
                                                     vp, c_int, vp, vp, vp, vp, vp, vp, c_sz, vp]
         L.bmoe_grouped_product_backward.restype = c_int
+        L.bmoe_grouped_product_backward_filled.argtypes = L.bmoe_grouped_product_backward.argtypes
+        L.bmoe_grouped_product_backward_filled.restype = c_int
         L.bmoe_residual_norm.argtypes = [c_int, c_int, c_int, c_int, vp, vp, c_int, vp, vp, vp, vp,
                                          vp, vp, vp, vp]
         L.bmoe_residual_norm.restype = c_int
@@ -207,6 +211,10 @@ def lib():
         L.bmoe_residual_norm_backward.argtypes = ([c_int, c_int, c_int, c_int, vp, vp, c_int] +
                                                   [vp] * 13 + [c_sz, vp])
         L.bmoe_residual_norm_backward.restype = c_int
+        L.bmoe_residual_norm_backward_filled_workspace_bytes.argtypes = [c_int] * 4
+        L.bmoe_residual_norm_backward_filled_workspace_bytes.restype = c_sz
+        L.bmoe_residual_norm_backward_filled.argtypes = L.bmoe_residual_norm_backward.argtypes
+        L.bmoe_residual_norm_backward_filled.restype = c_int
         L.bmoe_orthogonalize_workspace_bytes.argtypes = [c_int, c_int, c_int]
         L.bmoe_orthogonalize_workspace_bytes.restype = c_sz
         L.bmoe_orthogonalize.argtypes = [c_int, c_int, c_int, c_int, vp, vp, vp, vp, c_sz, vp]
@@ -578,6 +586,12 @@ def bmoe_grouped_product(dt: int, M: int, K: int, O: int, n_groups: int, a, a_ro
                                       _ptr(w), _ptr(offsets), _ptr(c), _stream(stream))
 
 
+def bmoe_grouped_product_filled(dt: int, M: int, K: int, O: int, n_groups: int, a, a_rows: int,
+                                perm, k: int, w, offsets, c, stream=None) -> int:
+    return lib().bmoe_grouped_product_filled(dt, M, K, O, n_groups, _ptr(a), a_rows, _ptr(perm), k,
+                                             _ptr(w), _ptr(offsets), _ptr(c), _stream(stream))
+
+
 def bmoe_grouped_product_backward_workspace_bytes(dt: int, M: int, K: int, O: int,
                                                   n_groups: int) -> int:
     return lib().bmoe_grouped_product_backward_workspace_bytes(dt, M, K, O, n_groups)
@@ -588,6 +602,14 @@ def bmoe_grouped_product_backward(dt: int, M: int, K: int, O: int, n_groups: int
     return lib().bmoe_grouped_product_backward(dt, M, K, O, n_groups, _ptr(a), a_rows, _ptr(perm),
                                                k, _ptr(w), _ptr(offsets), _ptr(dc), _ptr(da),
                                                _ptr(dw), _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def bmoe_grouped_product_backward_filled(dt: int, M: int, K: int, O: int, n_groups: int, a,
+                                         a_rows: int, perm, k: int, w, offsets, dc, da, dw, ws,
+                                         stream=None) -> int:
+    return lib().bmoe_grouped_product_backward_filled(
+        dt, M, K, O, n_groups, _ptr(a), a_rows, _ptr(perm), k, _ptr(w), _ptr(offsets), _ptr(dc),
+        _ptr(da), _ptr(dw), _ptr(ws), _nbytes(ws), _stream(stream))
 
 
 def bmoe_residual_norm(dt: int, T: int, d: int, k: int, spec, u, u_rows: int, inv, gates, r, w_post,
@@ -609,6 +631,19 @@ def bmoe_residual_norm_backward(dt: int, T: int, d: int, k: int, spec, u, u_rows
                                              _ptr(dr_out), _ptr(dn), _ptr(du), _ptr(dgates),
                                              _ptr(dr), _ptr(dw_post), _ptr(dw_pre), _ptr(ws),
                                              _nbytes(ws), _stream(stream))
+
+
+def bmoe_residual_norm_backward_filled_workspace_bytes(dt: int, T: int, d: int, u_rows: int) -> int:
+    return lib().bmoe_residual_norm_backward_filled_workspace_bytes(dt, T, d, u_rows)
+
+
+def bmoe_residual_norm_backward_filled(dt: int, T: int, d: int, k: int, spec, u, u_rows: int, inv,
+                                       gates, r_out, w_post, w_pre, dr_out, dn, du, dgates, dr,
+                                       dw_post, dw_pre, ws, stream=None) -> int:
+    return lib().bmoe_residual_norm_backward_filled(
+        dt, T, d, k, _ref(spec), _ptr(u), u_rows, _ptr(inv), _ptr(gates), _ptr(r_out), _ptr(w_post),
+        _ptr(w_pre), _ptr(dr_out), _ptr(dn), _ptr(du), _ptr(dgates), _ptr(dr), _ptr(dw_post),
+        _ptr(dw_pre), _ptr(ws), _nbytes(ws), _stream(stream))
 
 
 def bmoe_orthogonalize_workspace_bytes(batch: int, rows: int, cols: int) -> int:
@@ -1099,15 +1134,16 @@ def grouped_product(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, 
     """c [M][O], c[q] = w[e] a[row(q)] for the rows q of group e = offsets[e] ..
     offsets[e+1] (int32, on the GPU). a [R][K], w [groups][O][K] (one type, fp32
     or bf16); row(q) = perm[q] // k with group_rows()'s perm, else q. Rows of no
-    group are left as they were."""
+    group (padded picks) are 0; those of a given `out` are left as they were."""
     dt, M, K, O, G = _grouped(a, w, offsets, perm, k)
     with _at(a, stream):
         if out is None:
-            out = torch.empty(M, O, dtype=a.dtype, device=a.device)
+            call, out = bmoe_grouped_product_filled, torch.empty(M, O, dtype=a.dtype, device=a.device)
         else:
+            call = bmoe_grouped_product
             _like("out", out, a.dtype, (M, O), a.device)
-        _check(bmoe_grouped_product(dt, M, K, O, G, a, a.shape[0], perm, k, w, offsets, out,
-                                    stream), "bmoe_grouped_product")
+        _check(call(dt, M, K, O, G, a, a.shape[0], perm, k, w, offsets, out, stream),
+               "bmoe_grouped_product")
         return out
 
 
@@ -1116,13 +1152,16 @@ def grouped_product_backward(a: torch.Tensor, w: torch.Tensor, offsets: torch.Te
                              want_da: bool = True, want_dw: bool = True, stream=None) -> dict:
     """Gradients of sum(dc * c) for grouped_product()'s c: dict of da [M][K] (one
     row per row of the product, type of a) and dw fp32 [groups][O][K]. With
-    `perm`, residual_norm(da, k=k, inv=inv) sums a token's k rows."""
+    `perm`, residual_norm(da, k=k, inv=inv) sums a token's k rows. Rows of no group
+    are 0 in da; those of a given `da` are left as they were."""
     dt, M, K, O, G = _grouped(a, w, offsets, perm, k)
     _like("dc", dc, a.dtype, (M, O), a.device)
     with _at(a, stream):
+        call = bmoe_grouped_product_backward
         if da is not None:
             _like("da", da, a.dtype, (M, K), a.device)
         elif want_da:
+            call = bmoe_grouped_product_backward_filled
             da = torch.empty(M, K, dtype=a.dtype, device=a.device)
         if dw is not None:
             _like("dw", dw, torch.float32, (G, O, K), a.device)
@@ -1130,8 +1169,7 @@ def grouped_product_backward(a: torch.Tensor, w: torch.Tensor, offsets: torch.Te
             dw = torch.empty(G, O, K, dtype=torch.float32, device=a.device)
         ws = _workspace(bmoe_grouped_product_backward_workspace_bytes(dt, M, K, O, G),
                         "bmoe_grouped_product_backward_workspace_bytes", a.device)
-        _check(bmoe_grouped_product_backward(dt, M, K, O, G, a, a.shape[0], perm, k, w, offsets,
-                                             dc, da, dw, ws, stream),
+        _check(call(dt, M, K, O, G, a, a.shape[0], perm, k, w, offsets, dc, da, dw, ws, stream),
                "bmoe_grouped_product_backward")
         return {"da": da, "dw": dw}
 
@@ -1204,7 +1242,8 @@ def residual_norm_backward(u, r_out: torch.Tensor, spec: Optional[NormSpec] = No
                            du=None, dr=None, stream=None) -> dict:
     """Gradients of sum(dr_out * r') + sum(dn * n) for residual_norm(): dict of
     dr, du, dgates, dw_post and dw_pre (None where the input is). r_out: its r' as
-    stored. Rows of u that no pick names get no gradient: pass a zeroed `du`."""
+    stored. Rows of u that no pick names (padded picks') are 0 in du; those of a
+    given `du` are left as they were."""
     T, d = _matrix("r_out", r_out).shape
     dev = r_out.device
     dt = dtype_code(r_out)
@@ -1225,6 +1264,8 @@ def residual_norm_backward(u, r_out: torch.Tensor, spec: Optional[NormSpec] = No
             raise ValueError("du belongs to u")
         _like("du", du, u.dtype, u.shape, dev)
     with _at(r_out, stream):
+        # without inv every row of u is a pick's
+        fill = du is None and inv is not None
         if du is None and u is not None:
             du = torch.empty_like(u)
         if dr is None:
@@ -1232,11 +1273,12 @@ def residual_norm_backward(u, r_out: torch.Tensor, spec: Optional[NormSpec] = No
         dgates = None if gates is None else torch.empty_like(gates)
         dw_post = None if w_post is None else torch.empty_like(w_post)
         dw_pre = None if w_pre is None else torch.empty_like(w_pre)
-        ws = _workspace(bmoe_residual_norm_backward_workspace_bytes(dt, T, d),
+        ws = _workspace(bmoe_residual_norm_backward_filled_workspace_bytes(dt, T, d, rows) if fill
+                        else bmoe_residual_norm_backward_workspace_bytes(dt, T, d),
                         "bmoe_residual_norm_backward_workspace_bytes", dev)
-        _check(bmoe_residual_norm_backward(dt, T, d, k, spec, u, rows, inv, gates, r_out, w_post,
-                                           w_pre, dr_out, dn, du, dgates, dr, dw_post, dw_pre, ws,
-                                           stream), "bmoe_residual_norm_backward")
+        call = bmoe_residual_norm_backward_filled if fill else bmoe_residual_norm_backward
+        _check(call(dt, T, d, k, spec, u, rows, inv, gates, r_out, w_post, w_pre, dr_out, dn, du,
+                    dgates, dr, dw_post, dw_pre, ws, stream), "bmoe_residual_norm_backward")
         return {"dr": dr, "du": du, "dgates": dgates, "dw_post": dw_post, "dw_pre": dw_pre}
 
 

@@ -121,6 +121,115 @@ bmoe_status ortho_spec(const bmoe_ortho_spec* s, OrthoCall* c) {
   return BMOE_OK;
 }
 
+// The calls that leave rows without a group or a pick as they were, or (fill) set
+// them to 0.
+bmoe_status grouped_product(bmoe_dtype dt, int M, int K, int O, int n_groups, const void* a,
+                            int a_rows, const int32_t* perm, int k, const void* w,
+                            const int32_t* offsets, void* c, bool fill, void* stream) {
+  if (!ok_type(dt)) return BMOE_E_DTYPE;
+  if (!grouped_shape(M, K, O, n_groups, perm, k, a_rows)) return BMOE_E_SHAPE;
+  if (M == 0) return BMOE_OK;
+  if (!a || !w || !offsets || !c) return BMOE_E_NULL;
+  if (!all16({a, perm, w, offsets, c})) return BMOE_E_ALIGN;
+  const size_t e = elem(dt);
+  if (!apart({{c, (size_t)M * O * e}},
+             {{a, (size_t)(perm ? a_rows : M) * K * e},
+              {perm, (size_t)M * sizeof(int32_t)},
+              {w, (size_t)n_groups * O * K * e},
+              {offsets, (n_groups + 1) * sizeof(int32_t)}}))
+    return BMOE_E_VALUE;
+  return status_of(launch_grouped(dt, false, M, K, O, n_groups, a, perm, k, a_rows, w, offsets, c,
+                                  fill, static_cast<hipStream_t>(stream)));
+}
+
+bmoe_status grouped_product_backward(bmoe_dtype dt, int M, int K, int O, int n_groups,
+                                     const void* a, int a_rows, const int32_t* perm, int k,
+                                     const void* w, const int32_t* offsets, const void* dc, void* da,
+                                     float* dw, bool fill, void* ws, size_t ws_bytes, void* stream) {
+  if (!ok_type(dt)) return BMOE_E_DTYPE;
+  if (!grouped_shape(M, K, O, n_groups, perm, k, a_rows)) return BMOE_E_SHAPE;
+  if (!offsets || (M > 0 && (!dc || (da && !w) || (dw && !a)))) return BMOE_E_NULL;
+  const size_t need = bmoe_grouped_product_backward_workspace_bytes(dt, M, K, O, n_groups);
+  if (!ws || ws_bytes < need) return BMOE_E_WORKSPACE;
+  if (!all16({a, perm, w, offsets, dc, da, dw, ws})) return BMOE_E_ALIGN;
+  const size_t e = elem(dt), w_entries = (size_t)n_groups * O * K;
+  if (!apart({{da, (size_t)M * K * e}, {dw, w_entries * sizeof(float)}, {ws, need}},
+             {{a, (size_t)(perm ? a_rows : M) * K * e},
+              {perm, (size_t)M * sizeof(int32_t)},
+              {w, w_entries * e},
+              {offsets, (n_groups + 1) * sizeof(int32_t)},
+              {dc, (size_t)M * O * e}}))
+    return BMOE_E_VALUE;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t h = hipSuccess;
+  if (da && M > 0)
+    h = launch_grouped(dt, true, M, O, K, n_groups, dc, nullptr, 1, M, w, offsets, da, fill, s);
+  if (h == hipSuccess && dw)
+    h = launch_grouped_dw(dt, M, O, K, n_groups, a, perm, k, perm ? a_rows : M, dc, offsets, dw,
+                          static_cast<float*>(ws), s);
+  return status_of(h);
+}
+
+bmoe_status norm_backward(bmoe_dtype dt, int T, int d, int k, const bmoe_norm_spec* spec,
+                          const void* u, int u_rows, const int32_t* inv, const float* gates,
+                          const void* r_out, const float* w_post, const float* w_pre,
+                          const void* dr_out, const void* dn, void* du, float* dgates, void* dr,
+                          float* dw_post, float* dw_pre, bool fill, void* ws, size_t ws_bytes,
+                          void* stream) {
+  if (!ok_type(dt)) return BMOE_E_DTYPE;
+  if (!norm_shape(T, d, k, u_rows, u, inv)) return BMOE_E_SHAPE;
+  NormCall c = {};
+  const bmoe_status st = norm_spec(spec, &c);
+  if (st != BMOE_OK) return st;
+  // every gradient has what it is the gradient of, and dn what it came through
+  // (arrays of no tokens may be NULL)
+  if ((dw_post && !w_post) || (dw_pre && !w_pre) ||
+      (T > 0 && ((!u && (du || dgates || w_post)) || (dgates && !gates) ||
+                 (w_pre && (!r_out || !dn)) || (!w_pre && (dn || !dr_out)))))
+    return BMOE_E_NULL;
+  const size_t need = fill ? bmoe_residual_norm_backward_filled_workspace_bytes(dt, T, d, u_rows)
+                           : bmoe_residual_norm_backward_workspace_bytes(dt, T, d);
+  if (!need) return BMOE_E_SHAPE;  // (u_rows < 0 without u)
+  if (!ws || ws_bytes < need) return BMOE_E_WORKSPACE;
+  if (!all16({u, inv, gates, r_out, w_post, w_pre, dr_out, dn, du, dgates, dr, dw_post, dw_pre, ws}))
+    return BMOE_E_ALIGN;
+  const size_t rows = (size_t)T * d * elem(dt), picks = u ? (size_t)T * k * 4 : 0;
+  const size_t u_bytes = (size_t)u_rows * d * elem(dt), w_bytes = d * sizeof(float);
+  if (!apart({{du, u_bytes}, {dgates, picks}, {dr, rows}, {dw_post, w_bytes}, {dw_pre, w_bytes},
+              {ws, need}},
+             {{u, u_bytes},
+              {inv, picks},
+              {gates, picks},
+              {r_out, rows},
+              {w_post, w_bytes},
+              {w_pre, w_bytes},
+              {dr_out == dr ? nullptr : dr_out, rows},  // read row by row before it is written
+              {dn, rows}}))
+    return BMOE_E_VALUE;
+  c.T = T;
+  c.d = d;
+  c.k = k;
+  c.M = u_rows;
+  c.u = u;
+  c.inv = inv;
+  c.gates = gates;
+  c.w_post = w_post;
+  c.w_pre = w_pre;
+  c.x = r_out;
+  c.dr_out = dr_out;
+  c.dn = dn;
+  c.du = du;
+  c.dr = dr;
+  c.dgates = dgates;
+  c.dw_post = dw_post;
+  c.dw_pre = dw_pre;
+  if (fill && du) {
+    c.fill = 1;
+    c.marks = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + up256(norm_part_bytes(T, d)));
+  }
+  return status_of(launch_norm_bwd(dt, c, static_cast<float*>(ws), static_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 }  // namespace bmoe
 
@@ -152,20 +261,14 @@ bmoe_status bmoe_group_rows(int T, int n_experts, int k, const int32_t* ids, int
 bmoe_status bmoe_grouped_product(bmoe_dtype dt, int M, int K, int O, int n_groups, const void* a,
                                  int a_rows, const int32_t* perm, int k, const void* w,
                                  const int32_t* offsets, void* c, void* stream) {
-  if (!ok_type(dt)) return BMOE_E_DTYPE;
-  if (!grouped_shape(M, K, O, n_groups, perm, k, a_rows)) return BMOE_E_SHAPE;
-  if (M == 0) return BMOE_OK;
-  if (!a || !w || !offsets || !c) return BMOE_E_NULL;
-  if (!all16({a, perm, w, offsets, c})) return BMOE_E_ALIGN;
-  const size_t e = elem(dt);
-  if (!apart({{c, (size_t)M * O * e}},
-             {{a, (size_t)(perm ? a_rows : M) * K * e},
-              {perm, (size_t)M * sizeof(int32_t)},
-              {w, (size_t)n_groups * O * K * e},
-              {offsets, (n_groups + 1) * sizeof(int32_t)}}))
-    return BMOE_E_VALUE;
-  return status_of(launch_grouped(dt, false, M, K, O, n_groups, a, perm, k, a_rows, w, offsets, c,
-                                  static_cast<hipStream_t>(stream)));
+  return grouped_product(dt, M, K, O, n_groups, a, a_rows, perm, k, w, offsets, c, false, stream);
+}
+
+bmoe_status bmoe_grouped_product_filled(bmoe_dtype dt, int M, int K, int O, int n_groups,
+                                        const void* a, int a_rows, const int32_t* perm, int k,
+                                        const void* w, const int32_t* offsets, void* c,
+                                        void* stream) {
+  return grouped_product(dt, M, K, O, n_groups, a, a_rows, perm, k, w, offsets, c, true, stream);
 }
 
 size_t bmoe_grouped_product_backward_workspace_bytes(bmoe_dtype dt, int M, int K, int O,
@@ -180,28 +283,17 @@ bmoe_status bmoe_grouped_product_backward(bmoe_dtype dt, int M, int K, int O, in
                                           const void* w, const int32_t* offsets, const void* dc,
                                           void* da, float* dw, void* ws, size_t ws_bytes,
                                           void* stream) {
-  if (!ok_type(dt)) return BMOE_E_DTYPE;
-  if (!grouped_shape(M, K, O, n_groups, perm, k, a_rows)) return BMOE_E_SHAPE;
-  if (!offsets || (M > 0 && (!dc || (da && !w) || (dw && !a)))) return BMOE_E_NULL;
-  const size_t need = bmoe_grouped_product_backward_workspace_bytes(dt, M, K, O, n_groups);
-  if (!ws || ws_bytes < need) return BMOE_E_WORKSPACE;
-  if (!all16({a, perm, w, offsets, dc, da, dw, ws})) return BMOE_E_ALIGN;
-  const size_t e = elem(dt), w_entries = (size_t)n_groups * O * K;
-  if (!apart({{da, (size_t)M * K * e}, {dw, w_entries * sizeof(float)}, {ws, need}},
-             {{a, (size_t)(perm ? a_rows : M) * K * e},
-              {perm, (size_t)M * sizeof(int32_t)},
-              {w, w_entries * e},
-              {offsets, (n_groups + 1) * sizeof(int32_t)},
-              {dc, (size_t)M * O * e}}))
-    return BMOE_E_VALUE;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t h = hipSuccess;
-  if (da && M > 0)
-    h = launch_grouped(dt, true, M, O, K, n_groups, dc, nullptr, 1, M, w, offsets, da, s);
-  if (h == hipSuccess && dw)
-    h = launch_grouped_dw(dt, M, O, K, n_groups, a, perm, k, perm ? a_rows : M, dc, offsets, dw,
-                          static_cast<float*>(ws), s);
-  return status_of(h);
+  return grouped_product_backward(dt, M, K, O, n_groups, a, a_rows, perm, k, w, offsets, dc, da, dw,
+                                  false, ws, ws_bytes, stream);
+}
+
+bmoe_status bmoe_grouped_product_backward_filled(bmoe_dtype dt, int M, int K, int O, int n_groups,
+                                                 const void* a, int a_rows, const int32_t* perm,
+                                                 int k, const void* w, const int32_t* offsets,
+                                                 const void* dc, void* da, float* dw, void* ws,
+                                                 size_t ws_bytes, void* stream) {
+  return grouped_product_backward(dt, M, K, O, n_groups, a, a_rows, perm, k, w, offsets, dc, da, dw,
+                                  true, ws, ws_bytes, stream);
 }
 
 bmoe_status bmoe_residual_norm(bmoe_dtype dt, int T, int d, int k, const bmoe_norm_spec* spec,
@@ -246,6 +338,11 @@ size_t bmoe_residual_norm_backward_workspace_bytes(bmoe_dtype dt, int T, int d) 
   return up256(norm_part_bytes(T, d)) + 256;
 }
 
+size_t bmoe_residual_norm_backward_filled_workspace_bytes(bmoe_dtype dt, int T, int d, int u_rows) {
+  const size_t n = bmoe_residual_norm_backward_workspace_bytes(dt, T, d);
+  return n && u_rows >= 0 ? n + up256((size_t)u_rows * sizeof(int32_t)) : 0;
+}
+
 bmoe_status bmoe_residual_norm_backward(bmoe_dtype dt, int T, int d, int k,
                                         const bmoe_norm_spec* spec, const void* u, int u_rows,
                                         const int32_t* inv, const float* gates, const void* r_out,
@@ -253,52 +350,17 @@ bmoe_status bmoe_residual_norm_backward(bmoe_dtype dt, int T, int d, int k,
                                         const void* dr_out, const void* dn, void* du,
                                         float* dgates, void* dr, float* dw_post, float* dw_pre,
                                         void* ws, size_t ws_bytes, void* stream) {
-  if (!ok_type(dt)) return BMOE_E_DTYPE;
-  if (!norm_shape(T, d, k, u_rows, u, inv)) return BMOE_E_SHAPE;
-  NormCall c = {};
-  const bmoe_status st = norm_spec(spec, &c);
-  if (st != BMOE_OK) return st;
-  // every gradient has what it is the gradient of, and dn what it came through
-  // (arrays of no tokens may be NULL)
-  if ((dw_post && !w_post) || (dw_pre && !w_pre) ||
-      (T > 0 && ((!u && (du || dgates || w_post)) || (dgates && !gates) ||
-                 (w_pre && (!r_out || !dn)) || (!w_pre && (dn || !dr_out)))))
-    return BMOE_E_NULL;
-  const size_t need = bmoe_residual_norm_backward_workspace_bytes(dt, T, d);
-  if (!ws || ws_bytes < need) return BMOE_E_WORKSPACE;
-  if (!all16({u, inv, gates, r_out, w_post, w_pre, dr_out, dn, du, dgates, dr, dw_post, dw_pre, ws}))
-    return BMOE_E_ALIGN;
-  const size_t rows = (size_t)T * d * elem(dt), picks = u ? (size_t)T * k * 4 : 0;
-  const size_t u_bytes = (size_t)u_rows * d * elem(dt), w_bytes = d * sizeof(float);
-  if (!apart({{du, u_bytes}, {dgates, picks}, {dr, rows}, {dw_post, w_bytes}, {dw_pre, w_bytes},
-              {ws, need}},
-             {{u, u_bytes},
-              {inv, picks},
-              {gates, picks},
-              {r_out, rows},
-              {w_post, w_bytes},
-              {w_pre, w_bytes},
-              {dr_out == dr ? nullptr : dr_out, rows},  // read row by row before it is written
-              {dn, rows}}))
-    return BMOE_E_VALUE;
-  c.T = T;
-  c.d = d;
-  c.k = k;
-  c.M = u_rows;
-  c.u = u;
-  c.inv = inv;
-  c.gates = gates;
-  c.w_post = w_post;
-  c.w_pre = w_pre;
-  c.x = r_out;
-  c.dr_out = dr_out;
-  c.dn = dn;
-  c.du = du;
-  c.dr = dr;
-  c.dgates = dgates;
-  c.dw_post = dw_post;
-  c.dw_pre = dw_pre;
-  return status_of(launch_norm_bwd(dt, c, static_cast<float*>(ws), static_cast<hipStream_t>(stream)));
+  return norm_backward(dt, T, d, k, spec, u, u_rows, inv, gates, r_out, w_post, w_pre, dr_out, dn,
+                       du, dgates, dr, dw_post, dw_pre, false, ws, ws_bytes, stream);
+}
+
+bmoe_status bmoe_residual_norm_backward_filled(
+    bmoe_dtype dt, int T, int d, int k, const bmoe_norm_spec* spec, const void* u, int u_rows,
+    const int32_t* inv, const float* gates, const void* r_out, const float* w_post,
+    const float* w_pre, const void* dr_out, const void* dn, void* du, float* dgates, void* dr,
+    float* dw_post, float* dw_pre, void* ws, size_t ws_bytes, void* stream) {
+  return norm_backward(dt, T, d, k, spec, u, u_rows, inv, gates, r_out, w_post, w_pre, dr_out, dn,
+                       du, dgates, dr, dw_post, dw_pre, true, ws, ws_bytes, stream);
 }
 
 size_t bmoe_orthogonalize_workspace_bytes(int batch, int rows, int cols) {

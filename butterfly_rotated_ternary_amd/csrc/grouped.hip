@@ -24,9 +24,11 @@ namespace {
 
 using namespace tile;
 
-// Rows of group e, whatever the offsets hold.
-__device__ __forceinline__ int2 group_rows_of(const int32_t* offsets, int e, int M) {
-  const int lo = min(max(offsets[e], 0), M), hi = min(max(offsets[e + 1], 0), M);
+// Rows of group e, whatever the offsets hold; e = G: those behind the last group,
+// e = G + 1: those before the first.
+__device__ __forceinline__ int2 group_rows_of(const int32_t* offsets, int e, int G, int M) {
+  const int lo = e > G ? 0 : min(max(offsets[e], 0), M);
+  const int hi = e == G ? M : min(max(offsets[e > G ? 0 : e + 1], 0), M);
   return make_int2(lo, max(lo, hi));
 }
 
@@ -36,22 +38,22 @@ struct GroupTile {
   int i, col_tile;   // this tile's
 };
 
-// Work item t of all groups' tiles, groups ascending; a group has rows / MOST
-// rows of tiles_n tiles, rounded up. They come in panels of four rows of tiles,
-// so that the consecutive items that share an L2 are near square. Every wave
-// looks its tile up for itself: 64 groups at a time, a prefix sum over the lanes;
-// the offsets of 256 groups are loaded at once.
+// Work item t of all groups' tiles, groups ascending (`groups` of them: G, or G + 2
+// with the rows of no group); a group has rows / MOST rows of tiles_n tiles, rounded
+// up. They come in panels of four rows of tiles, so that the consecutive items that
+// share an L2 are near square. Every wave looks its tile up for itself: 64 groups at a
+// time, a prefix sum over the lanes; the offsets of 256 groups are loaded at once.
 constexpr int kPanel = 4;
 template <int MOST>
-__device__ __forceinline__ GroupTile find_tile(const int32_t* offsets, int G, int M, int tiles_n,
-                                               int t, int lane) {
+__device__ __forceinline__ GroupTile find_tile(const int32_t* offsets, int G, int groups, int M,
+                                               int tiles_n, int t, int lane) {
   int before = 0;
-  for (int e1 = 0; e1 < G; e1 += 4 * kWave) {
+  for (int e1 = 0; e1 < groups; e1 += 4 * kWave) {
     int2 rows[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int e = e1 + u * kWave + lane;
-      rows[u] = e < G ? group_rows_of(offsets, e, M) : make_int2(0, 0);
+      rows[u] = e < groups ? group_rows_of(offsets, e, G, M) : make_int2(0, 0);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -88,6 +90,7 @@ struct ProductArgs {
   const int32_t* offsets;
   const int32_t* perm;  // NULL: row q of a is row q of the product
   int k, a_rows, M, G, red, cols, tiles_n;
+  int fill;  // whether rows of no group become 0
 };
 
 // Row q's row of a.
@@ -155,6 +158,7 @@ __device__ __forceinline__ void store_plain(const Acc<C>& acc, char* c, size_t l
 // (kRedRows: they are the reduction).
 struct TileRows {
   int e, row0, rows;
+  int red;  // 0 for rows of no group: nothing is read, the sums are 0
 };
 template <class C>
 __device__ __forceinline__ void grouped_tile(const ProductArgs& p, const TileRows& t, int col0,
@@ -163,7 +167,7 @@ __device__ __forceinline__ void grouped_tile(const ProductArgs& p, const TileRow
   OutRowsSource<C, C::AR, C::A_LOADS, true> a;
   a.init(
       nullptr, [&](int r) { return p.a + (size_t)a_row(p, t.row0 + min(r, t.rows - 1)) * a_ld; },
-      p.red, 0, lane, wave);
+      t.red, 0, lane, wave);
   const char* w = p.w + (size_t)t.e * p.red * p.cols * C::ES;
   Acc<C> acc;
   clear<C>(acc);
@@ -172,16 +176,16 @@ __device__ __forceinline__ void grouped_tile(const ProductArgs& p, const TileRow
   ra.init(wm * C::TM, lane);
   Reader<C, C::BMODE, C::BN, C::FN> rb;
   rb.init(wn * C::TN, lane);
-  const int nsteps = (p.red + C::BK - 1) / C::BK;
+  const int nsteps = (t.red + C::BK - 1) / C::BK;
   if constexpr (C::BMODE == kOutRows) {
     OutRowsSource<C, C::BN, C::B_LOADS> b;
     b.init(
         w + (size_t)col0 * a_ld,
-        [&](int r) { return (uint32_t)(min(r, p.cols - 1 - col0) * a_ld); }, p.red, 0, lane, wave);
+        [&](int r) { return (uint32_t)(min(r, p.cols - 1 - col0) * a_ld); }, t.red, 0, lane, wave);
     run<C>(acc, ring, a, b, ra, rb, nsteps, lane, wave);
   } else {
     RedRowsSource<C, C::BN, C::B_LOADS, SameRow> b;
-    b.init(w, (size_t)p.cols * C::ES, col0, p.cols, p.red, 0, SameRow{}, lane, wave);
+    b.init(w, (size_t)p.cols * C::ES, col0, p.cols, t.red, 0, SameRow{}, lane, wave);
     run<C>(acc, ring, a, b, ra, rb, nsteps, lane, wave);
   }
 
@@ -227,11 +231,13 @@ __global__ __launch_bounds__(F::Most::THREADS) void grouped_kernel(ProductArgs p
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int item = xcd_item(grid_block(), run_items);
-  const GroupTile g = find_tile<F::Most::BM>(p.offsets, p.G, p.M, p.tiles_n, item, lane);
+  const GroupTile g =
+      find_tile<F::Most::BM>(p.offsets, p.G, p.G + 2 * p.fill, p.M, p.tiles_n, item, lane);
   if (g.e < 0) return;  // the whole workgroup
   const int height = (((unsigned)(g.hi - g.lo) + g.tiles - 1) / g.tiles + 63) / 64 * 64;
   TileRows t;
-  t.e = g.e;
+  t.e = g.e < p.G ? g.e : 0;
+  t.red = g.e < p.G ? p.red : 0;
   t.row0 = g.lo + g.i * height;
   t.rows = min(height, g.hi - t.row0);
   if (t.rows <= 0) return;  // rounding up left the last tiles empty
@@ -261,16 +267,17 @@ __global__ __launch_bounds__(64 * kFewWaves) void grouped_few_kernel(ProductArgs
   __shared__ f32x4 sums[kFewWaves][64];
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const GroupTile g =
-      find_tile<kFewRows>(p.offsets, p.G, p.M, p.tiles_n, (int)grid_block(), lane);
+  const GroupTile g = find_tile<kFewRows>(p.offsets, p.G, p.G + 2 * p.fill, p.M, p.tiles_n,
+                                          (int)grid_block(), lane);
   if (g.e < 0) return;  // the whole workgroup
   const int row0 = g.lo + g.i * kFewRows, rows = min(kFewRows, g.hi - row0);
   const int col0 = g.col_tile * kFewCols;
-  const int slices = (p.red + 31) / 32, per = (slices + kFewWaves - 1) / kFewWaves;
+  const int e = g.e < p.G ? g.e : 0, red = g.e < p.G ? p.red : 0;  // (no group: sums of 0)
+  const int slices = (red + 31) / 32, per = (slices + kFewWaves - 1) / kFewWaves;
   const int s0 = wave * per, s1 = min(slices, s0 + per);
   const int k0 = 8 * (lane >> 4);  // this lane's chunk of a slice
   const uint16_t* w = reinterpret_cast<const uint16_t*>(p.w) +
-                      ((size_t)g.e * p.cols + min(col0 + (lane & 15), p.cols - 1)) * p.red + k0;
+                      ((size_t)e * p.cols + min(col0 + (lane & 15), p.cols - 1)) * p.red + k0;
   const uint16_t* a = reinterpret_cast<const uint16_t*>(p.a) +
                       (size_t)a_row(p, row0 + min(lane & 15, rows - 1)) * p.red + k0;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -279,7 +286,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void grouped_few_kernel(ProductArgs
     uint4 wv[U], av[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool in = s + u < s1 && 32 * (s + u) + k0 < p.red;
+      const bool in = s + u < s1 && 32 * (s + u) + k0 < red;
       wv[u] = in ? *reinterpret_cast<const uint4*>(w + 32 * (s + u)) : zero;
       av[u] = in ? *reinterpret_cast<const uint4*>(a + 32 * (s + u)) : zero;
     }
@@ -335,7 +342,7 @@ __global__ __launch_bounds__(C::THREADS) void grouped_dw_kernel(DwArgs p, int ru
   if (e >= p.G) return;
   const int t = item % tiles;
   const int o0 = t / p.tiles_k * C::BM, k0 = t % p.tiles_k * C::BN;
-  int2 rows = group_rows_of(p.offsets, e, p.M);
+  int2 rows = group_rows_of(p.offsets, e, p.G, p.M);
   const unsigned all_rows = rows.y - rows.x, len = (all_rows + p.splits - 1) / p.splits;
   rows.x += (int)min(all_rows, split * len);
   const int count = (int)min((unsigned)(rows.y - rows.x), len);
@@ -398,11 +405,16 @@ __global__ __launch_bounds__(256) void grouped_dw_sum_kernel(const float* part, 
   }
 }
 
+// Rows of tiles of up to `high` rows: a group's last may be short, so at most one more
+// per group with rows, and per end with rows of no group.
+size_t rows_of_tiles(const ProductArgs& p, int high) {
+  return (size_t)p.M / high + (p.G < p.M ? p.G : p.M) + 2 * p.fill;
+}
+
 template <class F>
 hipError_t launch_grouped_cfg(ProductArgs p, hipStream_t s) {
   p.tiles_n = (p.cols + F::BN - 1) / F::BN;
-  // a group's last tile may be short: at most one more tile per group with rows
-  const size_t tiles_m = (size_t)p.M / F::Most::BM + (p.G < p.M ? p.G : p.M);
+  const size_t tiles_m = rows_of_tiles(p, F::Most::BM);
   const size_t items = tiles_m * p.tiles_n;
   const int run_items = items >= 1024 ? 32 : 1;
   const size_t super = 8 * run_items;
@@ -412,8 +424,7 @@ hipError_t launch_grouped_cfg(ProductArgs p, hipStream_t s) {
 
 hipError_t launch_few(ProductArgs p, hipStream_t s) {
   p.tiles_n = (p.cols + kFewCols - 1) / kFewCols;
-  const size_t tiles_m = (size_t)p.M / kFewRows + (p.G < p.M ? p.G : p.M);
-  return launch_kernel(grouped_few_kernel, grid_rows(tiles_m * p.tiles_n),
+  return launch_kernel(grouped_few_kernel, grid_rows(rows_of_tiles(p, kFewRows) * p.tiles_n),
                        dim3(64 * kFewWaves), 0, s, KernelTiming{}, p);
 }
 
@@ -487,7 +498,7 @@ hipError_t launch_dw_type(const DwArgs& p, hipStream_t s) {
 
 hipError_t launch_grouped(bmoe_dtype dt, bool back, int M, int red, int cols, int G, const void* a,
                           const int32_t* perm, int k, int a_rows, const void* w,
-                          const int32_t* offsets, void* c, hipStream_t s) {
+                          const int32_t* offsets, void* c, bool fill, hipStream_t s) {
   ProductArgs p;
   p.a = static_cast<const char*>(a);
   p.w = static_cast<const char*>(w);
@@ -501,6 +512,7 @@ hipError_t launch_grouped(bmoe_dtype dt, bool back, int M, int red, int cols, in
   p.red = red;
   p.cols = cols;
   p.tiles_n = 0;
+  p.fill = fill;
   if (dt == BMOE_BF16)
     return back ? launch_grouped_type<kBf16, kRedRows>(p, s)
                 : launch_grouped_type<kBf16, kOutRows>(p, s);

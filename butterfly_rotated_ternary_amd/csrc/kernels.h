@@ -326,10 +326,11 @@ hipError_t launch_group_rows(const int32_t* ids, int M, int N, int32_t* offsets,
                              int32_t* inv, int* count, hipStream_t s);
 // Group e = rows offsets[e] .. offsets[e + 1] of M. back = false: c[q] [cols] =
 // w_e [cols][red] a[row(q)]; back = true: c[q] = w_e^T a[q] with w_e [red][cols].
-// row(q) = perm[q] / k within [0, a_rows), or q with perm NULL.
+// row(q) = perm[q] / k within [0, a_rows), or q with perm NULL. fill: rows of no
+// group become 0.
 hipError_t launch_grouped(bmoe_dtype dt, bool back, int M, int red, int cols, int G, const void* a,
                           const int32_t* perm, int k, int a_rows, const void* w,
-                          const int32_t* offsets, void* c, hipStream_t s);
+                          const int32_t* offsets, void* c, bool fill, hipStream_t s);
 // dw [G][O][K] = sums over the groups' rows of dc[q] a[row(q)]^T. part: scratch
 // [grouped_dw_splits][G][O][K] (unused where that is 1).
 int grouped_dw_splits(bmoe_dtype dt, int M, int O, int K, int G);
@@ -370,6 +371,8 @@ struct NormCall {
   const void *x, *dr_out, *dn;  // x: the forward's r_out
   void *du, *dr;
   float *dgates, *dw_post, *dw_pre;
+  int fill;        // rows of du that no pick names become 0
+  int32_t* marks;  // [M], with fill: the last pick that named a row (others: anything)
 };
 hipError_t launch_norm(bmoe_dtype dt, const NormCall& c, hipStream_t s);
 size_t norm_part_bytes(int T, int d);

@@ -523,17 +523,59 @@ __global__ __launch_bounds__(C::THREADS) void norm_bwd_kernel(NormCall p, float*
       }
     }
   }
+  // for fill_rows: a row's pick (here, where no token's values are live: in the loop
+  // it took registers, and of some widths a wave per SIMD)
+  if (p.marks && p.inv) {
+    const long long picks = (long long)p.T * p.k, all = (long long)gridDim.x * C::THREADS;
+    for (long long i = (long long)blockIdx.x * C::THREADS + threadIdx.x; i < picks; i += all) {
+      const int32_t row = p.inv[i];
+      if (row >= 0 && row < p.M) p.marks[row] = (int32_t)i;
+    }
+  }
+}
+
+// The rows of du that no pick names become 0, 64 rows a wave at a time. A row that a
+// pick names holds a pick that names it in marks; of the others, where marks holds
+// whatever the workspace did, no pick can name them.
+constexpr int kSumWaves = 16;
+struct FillArgs {
+  const int32_t *inv, *marks;
+  long long rows, picks;
+  size_t row_bytes;
+  char* du;
+};
+__device__ __forceinline__ void fill_rows(const FillArgs& f, int lane, int wave) {
+  const long long step = (long long)gridDim.x * kSumWaves * kWave;
+  for (long long r0 = ((long long)blockIdx.x * kSumWaves + wave) * kWave; r0 < f.rows; r0 += step) {
+    const long long r = r0 + lane;
+    bool named = r >= f.rows || (!f.inv && r < f.picks);
+    if (!named && f.inv) {
+      const int32_t m = f.marks[r];
+      named = m >= 0 && m < f.picks && f.inv[m] == r;
+    }
+    for (uint64_t left = __ballot(!named); left; left &= left - 1) {
+      char* row = f.du + (size_t)(r0 + __ffsll((unsigned long long)left) - 1) * f.row_bytes;
+      if (f.row_bytes % 16 == 0) {
+        for (size_t i = 16 * lane; i < f.row_bytes; i += 16 * kWave)
+          *reinterpret_cast<uint4*>(row + i) = make_uint4(0u, 0u, 0u, 0u);
+      } else {
+        for (size_t i = 2 * lane; i < f.row_bytes; i += 2 * kWave)
+          *reinterpret_cast<uint16_t*>(row + i) = 0;
+      }
+    }
+  }
 }
 
 // dw[c] = the partial sums of column c, in order and in 64 bits: 64 columns a
-// workgroup, sixteen waves taking a sixteenth of the parts each.
-constexpr int kSumWaves = 16;
+// workgroup, sixteen waves taking a sixteenth of the parts each. blockIdx.y = 2:
+// fill_rows.
 __global__ __launch_bounds__(64 * kSumWaves) void norm_weights_kernel(const float* part, int parts,
                                                                       int d, float* dw_pre,
-                                                                      float* dw_post) {
+                                                                      float* dw_post, FillArgs fill) {
   __shared__ double lds[kSumWaves][64];
+  if (blockIdx.y == 2) return fill_rows(fill, threadIdx.x % 64, threadIdx.x / 64);
   float* dst = blockIdx.y ? dw_post : dw_pre;
-  if (!dst) return;
+  if (!dst || blockIdx.x * 64 >= (unsigned)d) return;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, col = blockIdx.x * 64 + lane;
   const int n = (parts + kSumWaves - 1) / kSumWaves, lo = min(parts, wave * n),
             hi = min(parts, lo + n);
@@ -553,6 +595,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void norm_weights_kernel(const floa
 
 // Workgroups of the gradient: enough rows each that their partial sums stay few.
 constexpr int kBwdGroups = 768;
+constexpr unsigned kFillGroups = 256;  // of fill_rows, at most
 
 template <class C>
 hipError_t launch_norm_cfg(const NormCall& c, hipStream_t s) {
@@ -573,9 +616,21 @@ hipError_t launch_norm_bwd_cfg(const NormCall& c, float* part, hipStream_t s) {
   };
   hipError_t e = hipSuccess;
   if (groups) e = !c.u || c.k == 1 ? launch(norm_bwd_kernel<C, 1>) : launch(norm_bwd_kernel<C, 2>);
-  if (e != hipSuccess || (!c.dw_pre && !c.dw_post)) return e;
-  return launch_kernel(norm_weights_kernel, dim3((c.d + 63) / 64, 2), dim3(64 * kSumWaves), 0, s,
-                       KernelTiming{}, (const float*)part, groups, c.d, c.dw_pre, c.dw_post);
+  if (e != hipSuccess || (!c.dw_pre && !c.dw_post && !c.fill)) return e;
+  FillArgs fill = {};
+  unsigned wide = (c.d + 63) / 64;
+  if (c.fill) {
+    fill.inv = c.inv;
+    fill.marks = c.marks;
+    fill.rows = c.M;
+    fill.picks = (long long)c.T * c.k;
+    fill.row_bytes = (size_t)c.d * sizeof(typename C::T);
+    fill.du = static_cast<char*>(c.du);
+    const long long most = (c.M + kSumWaves * kWave - 1) / (kSumWaves * kWave);
+    if (most > wide) wide = most < kFillGroups ? (unsigned)most : kFillGroups;
+  }
+  return launch_kernel(norm_weights_kernel, dim3(wide, c.fill ? 3 : 2), dim3(64 * kSumWaves), 0, s,
+                       KernelTiming{}, (const float*)part, groups, c.d, c.dw_pre, c.dw_post, fill);
 }
 
 // f(config) for rows of d values (EPC per 16 bytes): sixteen lanes per row up to 16

@@ -579,7 +579,8 @@ bmoe_status bmoe_group_rows(int T, int n_experts, int k, const int32_t* ids, int
  *   w        [n_groups][O][K], row o = output.
  *   offsets  int32 [n_groups+1] on the device, ascending, within [0, M].
  *   c        [M][O]. Rows that belong to no group (behind the last one, or
- *            before the first) are left as they were.
+ *            before the first) are left as they were; the _filled call sets
+ *            them to 0.
  * 1 <= K, O <= 65536, any lengths (rows that are whole multiples of 16 bytes
  * are faster), 1 <= n_groups <= 4096. M = 0 is a no-op. Entries of offsets
  * outside [0, M] and of perm outside [0, a_rows * k) are clamped for
@@ -588,12 +589,17 @@ bmoe_status bmoe_group_rows(int T, int n_experts, int k, const int32_t* ids, int
 bmoe_status bmoe_grouped_product(bmoe_dtype dt, int M, int K, int O, int n_groups, const void* a,
                                  int a_rows, const int32_t* perm, int k, const void* w,
                                  const int32_t* offsets, void* c, void* stream);
+bmoe_status bmoe_grouped_product_filled(bmoe_dtype dt, int M, int K, int O, int n_groups,
+                                        const void* a, int a_rows, const int32_t* perm, int k,
+                                        const void* w, const int32_t* offsets, void* c,
+                                        void* stream);
 
 /*
  * Gradients of bmoe_grouped_product for dc [M][O] = dL/dc:
  *   da  [M][K], dtype dt, or NULL: da[q] = W_e^T dc[q], one row per row of the
  *       product (a token's k rows are summed by bmoe_residual_norm, with inv and
- *       without gates, or a w_post). Rows of no group are left as they were.
+ *       without gates, or a w_post). Rows of no group are left as they were; the
+ *       _filled call sets them to 0.
  *   dw  fp32 [n_groups][O][K] or NULL: the sum over the group's rows of
  *       dc[q] a[row(q)]^T, the same bits each run; 0 for a group without rows.
  * The other arguments as there. w is read for da, a and perm for dw. M = 0
@@ -606,6 +612,11 @@ bmoe_status bmoe_grouped_product_backward(bmoe_dtype dt, int M, int K, int O, in
                                           const void* w, const int32_t* offsets, const void* dc,
                                           void* da, float* dw, void* ws, size_t ws_bytes,
                                           void* stream);
+bmoe_status bmoe_grouped_product_backward_filled(bmoe_dtype dt, int M, int K, int O, int n_groups,
+                                                 const void* a, int a_rows, const int32_t* perm,
+                                                 int k, const void* w, const int32_t* offsets,
+                                                 const void* dc, void* da, float* dw, void* ws,
+                                                 size_t ws_bytes, void* stream);
 
 /*
  * Norms around a block, fused with the sum of a token's expert rows, its gates
@@ -641,15 +652,16 @@ bmoe_status bmoe_residual_norm(bmoe_dtype dt, int T, int d, int k, const bmoe_no
  * Gradients of bmoe_residual_norm, from dr_out = dL/dr' [T][d] (NULL: 0; needed
  * without w_pre) and dn = dL/dn (with w_pre only). r_out is the forward's r' as
  * stored; the other inputs are the forward's.
- *   du      [u_rows][d] or NULL: rows that no pick names are left as they were;
- *           inv's rows have to be distinct (else such a row holds one of its
- *           picks' gradients).
+ *   du      [u_rows][d] or NULL: rows that no pick names are left as they were,
+ *           and set to 0 by the _filled call; inv's rows have to be distinct
+ *           (else such a row holds one of its picks' gradients).
  *   dgates  fp32 [T][k] or NULL (0 for a pick that contributes nothing).
  *   dr      [T][d] or NULL; may be dr_out.
  *   dw_post, dw_pre  fp32 [d] or NULL: sums over the tokens, the same bits each
  *           run. T = 0 sets them to 0.
  * Asking for a gradient of an input that is NULL is BMOE_E_NULL. ws: at least
- * bmoe_residual_norm_backward_workspace_bytes().
+ * bmoe_residual_norm_backward_workspace_bytes(), or for the _filled call
+ * bmoe_residual_norm_backward_filled_workspace_bytes() (4 u_rows more).
  */
 size_t bmoe_residual_norm_backward_workspace_bytes(bmoe_dtype dt, int T, int d);
 bmoe_status bmoe_residual_norm_backward(bmoe_dtype dt, int T, int d, int k,
@@ -659,6 +671,12 @@ bmoe_status bmoe_residual_norm_backward(bmoe_dtype dt, int T, int d, int k,
                                         const void* dr_out, const void* dn, void* du,
                                         float* dgates, void* dr, float* dw_post, float* dw_pre,
                                         void* ws, size_t ws_bytes, void* stream);
+size_t bmoe_residual_norm_backward_filled_workspace_bytes(bmoe_dtype dt, int T, int d, int u_rows);
+bmoe_status bmoe_residual_norm_backward_filled(
+    bmoe_dtype dt, int T, int d, int k, const bmoe_norm_spec* spec, const void* u, int u_rows,
+    const int32_t* inv, const float* gates, const void* r_out, const float* w_post,
+    const float* w_pre, const void* dr_out, const void* dn, void* du, float* dgates, void* dr,
+    float* dw_post, float* dw_pre, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Orthogonalisation of a gradient by Newton-Schulz products, for `batch`
