@@ -24,11 +24,9 @@ namespace {
 
 using namespace tile;
 
-// Rows of group e, whatever the offsets hold; e = G: those behind the last group,
-// e = G + 1: those before the first.
-__device__ __forceinline__ int2 group_rows_of(const int32_t* offsets, int e, int G, int M) {
-  const int lo = e > G ? 0 : min(max(offsets[e], 0), M);
-  const int hi = e == G ? M : min(max(offsets[e > G ? 0 : e + 1], 0), M);
+// Rows of group e, whatever the offsets hold.
+__device__ __forceinline__ int2 group_rows_of(const int32_t* offsets, int e, int M) {
+  const int lo = min(max(offsets[e], 0), M), hi = min(max(offsets[e + 1], 0), M);
   return make_int2(lo, max(lo, hi));
 }
 
@@ -38,22 +36,39 @@ struct GroupTile {
   int i, col_tile;   // this tile's
 };
 
-// Work item t of all groups' tiles, groups ascending (`groups` of them: G, or G + 2
-// with the rows of no group); a group has rows / MOST rows of tiles_n tiles, rounded
-// up. They come in panels of four rows of tiles, so that the consecutive items that
-// share an L2 are near square. Every wave looks its tile up for itself: 64 groups at a
-// time, a prefix sum over the lanes; the offsets of 256 groups are loaded at once.
+// Work item t of all groups' tiles, groups ascending; a group has rows / MOST
+// rows of tiles_n tiles, rounded up. They come in panels of four rows of tiles,
+// so that the consecutive items that share an L2 are near square. Every wave
+// looks its tile up for itself: 64 groups at a time, a prefix sum over the lanes;
+// the offsets of 256 groups are loaded at once. fill: the rows behind the last group
+// are one more, G, those before the first another, G + 1 (behind the loop: as lanes
+// of it they cost one token of 8 experts 0.7 of 11.4 us).
 constexpr int kPanel = 4;
+// Tile `at` of the `items` of group e.
+__device__ __forceinline__ GroupTile tile_of(int e, int lo, int hi, int items, int tiles_n, int at) {
+  // (offsets that do not ascend can overflow the sum: no tile then)
+  if ((unsigned)at >= (unsigned)items) return {-1, 0, 0, 0, 0, 0};
+  GroupTile g;
+  g.e = e;
+  g.lo = lo;
+  g.hi = hi;
+  g.tiles = items / tiles_n;
+  const int panel = at / (kPanel * tiles_n), j = at - panel * kPanel * tiles_n;
+  const int high = min(kPanel, g.tiles - panel * kPanel);
+  g.i = panel * kPanel + j % high;
+  g.col_tile = j / high;
+  return g;
+}
 template <int MOST>
-__device__ __forceinline__ GroupTile find_tile(const int32_t* offsets, int G, int groups, int M,
-                                               int tiles_n, int t, int lane) {
+__device__ __forceinline__ GroupTile find_tile(const int32_t* offsets, int G, int M, int tiles_n,
+                                               int fill, int t, int lane) {
   int before = 0;
-  for (int e1 = 0; e1 < groups; e1 += 4 * kWave) {
+  for (int e1 = 0; e1 < G; e1 += 4 * kWave) {
     int2 rows[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int e = e1 + u * kWave + lane;
-      rows[u] = e < groups ? group_rows_of(offsets, e, G, M) : make_int2(0, 0);
+      rows[u] = e < G ? group_rows_of(offsets, e, M) : make_int2(0, 0);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -64,33 +79,37 @@ __device__ __forceinline__ GroupTile find_tile(const int32_t* offsets, int G, in
       if (past) {
         const int src = __ffsll((unsigned long long)past) - 1;
         const int items = __builtin_amdgcn_readlane(n, src);
-        const int at = t - before - (__builtin_amdgcn_readlane(incl, src) - items);
-        GroupTile g;
-        // (offsets that do not ascend can overflow the sum: no tile then)
-        g.e = (unsigned)at < (unsigned)items ? e1 + u * kWave + src : -1;
-        g.lo = __builtin_amdgcn_readlane(r.x, src);
-        g.hi = __builtin_amdgcn_readlane(r.y, src);
-        g.tiles = items / tiles_n;
-        const int panel = at / (kPanel * tiles_n), j = at - panel * kPanel * tiles_n;
-        const int high = min(kPanel, g.tiles - panel * kPanel);
-        g.i = panel * kPanel + j % high;
-        g.col_tile = j / high;
-        return g;
+        return tile_of(e1 + u * kWave + src, __builtin_amdgcn_readlane(r.x, src),
+                       __builtin_amdgcn_readlane(r.y, src), items, tiles_n,
+                       t - before - (__builtin_amdgcn_readlane(incl, src) - items));
       }
       before += __builtin_amdgcn_readlane(incl, kWave - 1);
     }
   }
+  if (fill) {
+    const int end = min(max(offsets[G], 0), M), begin = min(max(offsets[0], 0), M);
+    const int behind = (int)(((unsigned)(M - end) + MOST - 1) / MOST) * tiles_n;
+    const int ahead = (int)(((unsigned)begin + MOST - 1) / MOST) * tiles_n;
+    if (t - before < behind) return tile_of(G, end, M, behind, tiles_n, t - before);
+    if (t - before - behind < ahead)
+      return tile_of(G + 1, 0, begin, ahead, tiles_n, t - before - behind);
+  }
   return {-1, 0, 0, 0, 0, 0};
 }
 
+// In the order in which a workgroup needs them: the first 16 dwords are in registers
+// at its start, the others a load away (with `fill` among those one token of 8 experts
+// took 12.8 us instead of 11.4).
 struct ProductArgs {
-  const char* a;  // rows of the product's left operand, `red` values each
-  const char* w;  // [G][O][K]
-  char* c;        // [M][cols]
   const int32_t* offsets;
+  int M, G, tiles_n;
+  int fill;             // whether rows of no group become 0
+  int red, cols;
+  const char* a;        // rows of the product's left operand, `red` values each
+  const char* w;        // [G][O][K]
+  char* c;              // [M][cols]
   const int32_t* perm;  // NULL: row q of a is row q of the product
-  int k, a_rows, M, G, red, cols, tiles_n;
-  int fill;  // whether rows of no group become 0
+  int k, a_rows;
 };
 
 // Row q's row of a.
@@ -232,7 +251,7 @@ __global__ __launch_bounds__(F::Most::THREADS) void grouped_kernel(ProductArgs p
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int item = xcd_item(grid_block(), run_items);
   const GroupTile g =
-      find_tile<F::Most::BM>(p.offsets, p.G, p.G + 2 * p.fill, p.M, p.tiles_n, item, lane);
+      find_tile<F::Most::BM>(p.offsets, p.G, p.M, p.tiles_n, p.fill, item, lane);
   if (g.e < 0) return;  // the whole workgroup
   const int height = (((unsigned)(g.hi - g.lo) + g.tiles - 1) / g.tiles + 63) / 64 * 64;
   TileRows t;
@@ -267,8 +286,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void grouped_few_kernel(ProductArgs
   __shared__ f32x4 sums[kFewWaves][64];
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const GroupTile g = find_tile<kFewRows>(p.offsets, p.G, p.G + 2 * p.fill, p.M, p.tiles_n,
-                                          (int)grid_block(), lane);
+  const GroupTile g =
+      find_tile<kFewRows>(p.offsets, p.G, p.M, p.tiles_n, p.fill, (int)grid_block(), lane);
   if (g.e < 0) return;  // the whole workgroup
   const int row0 = g.lo + g.i * kFewRows, rows = min(kFewRows, g.hi - row0);
   const int col0 = g.col_tile * kFewCols;
@@ -342,7 +361,7 @@ __global__ __launch_bounds__(C::THREADS) void grouped_dw_kernel(DwArgs p, int ru
   if (e >= p.G) return;
   const int t = item % tiles;
   const int o0 = t / p.tiles_k * C::BM, k0 = t % p.tiles_k * C::BN;
-  int2 rows = group_rows_of(p.offsets, e, p.G, p.M);
+  int2 rows = group_rows_of(p.offsets, e, p.M);
   const unsigned all_rows = rows.y - rows.x, len = (all_rows + p.splits - 1) / p.splits;
   rows.x += (int)min(all_rows, split * len);
   const int count = (int)min((unsigned)(rows.y - rows.x), len);
@@ -406,9 +425,9 @@ __global__ __launch_bounds__(256) void grouped_dw_sum_kernel(const float* part, 
 }
 
 // Rows of tiles of up to `high` rows: a group's last may be short, so at most one more
-// per group with rows, and per end with rows of no group.
+// per group with rows, and per end with rows of no group; each holds a row.
 size_t rows_of_tiles(const ProductArgs& p, int high) {
-  return (size_t)p.M / high + (p.G < p.M ? p.G : p.M) + 2 * p.fill;
+  return std::min((size_t)p.M / high + std::min(p.G, p.M) + 2 * p.fill, (size_t)p.M);
 }
 
 template <class F>
