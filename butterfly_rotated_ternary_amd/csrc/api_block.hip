@@ -115,9 +115,8 @@ bmoe_status ortho_spec(const bmoe_ortho_spec* s, OrthoCall* c) {
   c->b = s->b;
   c->c = s->c;
   c->eps = s->eps;
-  c->sx = fp16_scale(range.x);
-  c->sp = fp16_scale(range.x * range.x);
-  c->sq = fp16_scale(range.q);
+  c->x_scale = fp16_scale(range.x * range.x);  // (range.x >= 1)
+  c->q_scale = fp16_scale(range.q);
   return BMOE_OK;
 }
 

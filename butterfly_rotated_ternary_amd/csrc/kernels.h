@@ -342,7 +342,7 @@ hipError_t launch_grouped_dw(bmoe_dtype dt, int M, int O, int K, int G, const vo
 struct OrthoCall {
   int batch, rows, cols, steps;
   float a, b, c, eps;
-  float sx, sp, sq;  // scales (powers of two) of X, P and Q as fp16 operands
+  float x_scale, q_scale;  // of X and P, and of Q, as fp16 operands: powers of two
   const void* u;    // gradient
   int u_bf16;
   float* momentum;  // NULL: u is orthogonalised; else momentum = beta momentum + u is (with

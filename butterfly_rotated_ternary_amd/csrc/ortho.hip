@@ -7,8 +7,8 @@
 //
 // Numbers. Operands are kept as pairs of fp16, hi + lo, of the value times a power
 // of two: the largest that leaves room for what X, P and Q can hold under the given
-// coefficients (the host bounds their singular values; for 3.4445, -4.7750, 2.0315
-// 2^15 for X and P, 2^14 for Q). That is 22 bits of a value above 2^-18, and an
+// coefficients (the host bounds their singular values; X and P share one; for 3.4445,
+// -4.7750, 2.0315 2^15, and 2^14 for Q). That is 22 bits of a value above 2^-18, and an
 // absolute error of 2^-40 (2^-39) below. Three fp16 MFMAs (hi hi + hi lo + lo hi,
 // fp32 sums) make one product at five times the rate that fp32 MFMAs have. In the
 // norm the result is as near to the exact one as an iteration in fp32 (64 x 512
@@ -177,7 +177,7 @@ struct OrthoArgs {
   int rows, cols, ld, m, ldm;  // of X; of P and Q
   int batch, tiles, tiles_n;  // tiles per matrix
   int run_items;
-  float unit;             // of the accumulators: to the output's scale (kPoly: to P's)
+  float unit;             // of the accumulators: to X's and P's scale
   float a, b, c;          // kPoly: to Q's scale
   // the last product's epilogue
   void* o;                // [batch][rows][cols]: X, or w = keep w - rate X
@@ -512,8 +512,8 @@ struct SmallArgs {
   Source src;
   int rows, cols, steps, tall;
   float a, b, c, eps;           // a, b, c: to Q's scale
-  float sx;                     // the scale of X
-  float p_unit, pp_unit, x_unit;  // X X^T and P P to P's scale, Q X to X's
+  float scale;                  // of X and P
+  float p_unit, x_unit;         // X X^T and P P, Q X: to that scale
   void* o;
   int o_bf16, update;
   float keep, rate, unscale;    // Q X to the result
@@ -702,7 +702,7 @@ __device__ __forceinline__ float waves_sum(const SmallLds<MB>& lds, int e) {
   for (int w = 1; w < kSmallWaves; ++w) sum += lds.red[w][e];
   return sum;
 }
-// P's entry e (as above) from its sum at the square of X's scale.
+// P's entry e (as above) from its sum, which has the scale twice.
 template <int MB>
 __device__ __forceinline__ void put_p(const SmallArgs& p, SmallLds<MB>& lds, int e, float sum) {
   const int i = e / 1024, r = e % 1024 / 64, l = e % 64;
@@ -739,7 +739,7 @@ __device__ __forceinline__ void small_poly(const SmallArgs& p, SmallLds<MB>& lds
   for (int r = 0; r < 16; ++r) {
     const int row = 32 * br + acc_row(r, lane), col = 32 * bc + (lane & 31);
     const float pv = (float)lds.P[0][row * kPitch + col] + (float)lds.P[1][row * kPitch + col];
-    float q = fmaf(p.c, acc[r] * p.pp_unit, p.b * pv);
+    float q = fmaf(p.c, acc[r] * p.p_unit, p.b * pv);
     if (row == col) q += p.a;
     _Float16 hi, lo;
     split(q, hi, lo);
@@ -865,7 +865,7 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(SmallArgs p)
       for (int r = 0; r < 16; ++r) acc = fma((double)v[nb][mb][r], (double)v[nb][mb][r], acc);
   const float norm = (float)sqrt(small_sum(acc, lds.dsum, lane, wave)) + p.eps;
   Operands<MB, NB> ops;
-  first_operands<MB, NB>(v, norm, p.sx, lds.red[wave], lane, ops);
+  first_operands<MB, NB>(v, norm, p.scale, lds.red[wave], lane, ops);
   const auto make_q = [&]() {
     __syncthreads();  // red, P and Q have been read
     wave_gram<MB, NB>(ops, lds.red[wave], lane);
@@ -914,7 +914,7 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_slab_kernel(SmallArgs p) 
     double acc = 0.0;
     for (int i = tid; i < p.parts; i += kSmallThreads) acc += p.part[(size_t)blockIdx.y * p.parts + i];
     const float norm = (float)sqrt(small_sum(acc, lds.dsum, lane, wave)) + p.eps;
-    first_operands<MB, NB>(v, norm, p.sx, lds.red[wave], lane, ops);
+    first_operands<MB, NB>(v, norm, p.scale, lds.red[wave], lane, ops);
   } else {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -1069,14 +1069,13 @@ hipError_t launch_ortho(const OrthoCall& call, void* ws, hipStream_t s) {
   sp.steps = call.steps;
   sp.tall = rows > cols;
   // (powers of two: exact)
-  sp.a = call.a * call.sq;
-  sp.b = call.b * (call.sq / call.sp);
-  sp.c = call.c * (call.sq / call.sp);
-  sp.sx = call.sx;
-  sp.p_unit = call.sp / (call.sx * call.sx);
-  sp.pp_unit = 1.f / call.sp;
-  sp.x_unit = 1.f / call.sq;
-  sp.unscale = 1.f / (call.sq * call.sx);
+  sp.a = call.a * call.q_scale;
+  sp.b = call.b * (call.q_scale / call.x_scale);
+  sp.c = call.c * (call.q_scale / call.x_scale);
+  sp.scale = call.x_scale;
+  sp.p_unit = 1.f / call.x_scale;
+  sp.x_unit = 1.f / call.q_scale;
+  sp.unscale = sp.p_unit * sp.x_unit;
   sp.eps = call.eps;
   sp.o = call.o;
   sp.o_bf16 = call.o_bf16;
@@ -1111,7 +1110,7 @@ hipError_t launch_ortho(const OrthoCall& call, void* ws, hipStream_t s) {
   const size_t blocks = ((size_t)rows * l.ld / 8 + kSumThreads - 1) / kSumThreads;
   const size_t enough = batch >= 32 ? 64 : 2048;
   e = launch_kernel(ortho_split_kernel, dim3((unsigned)(blocks < enough ? blocks : enough), batch),
-                    dim3(kSumThreads), 0, s, KernelTiming{}, src, rows, cols, l.ld, call.eps, call.sx,
+                    dim3(kSumThreads), 0, s, KernelTiming{}, src, rows, cols, l.ld, call.eps, call.x_scale,
                     (const double*)part, parts, x[0], x[0] + l.x_part / 2);
   if (e != hipSuccess) return e;
 
@@ -1129,7 +1128,7 @@ hipError_t launch_ortho(const OrthoCall& call, void* ws, hipStream_t s) {
   p.a = sp.a;
   p.b = sp.b;
   p.c = sp.c;
-  p.unscale = 1.f / call.sx;
+  p.unscale = sp.p_unit;
   p.o_bf16 = call.o_bf16;
   p.update = call.update;
   p.keep = call.keep;
@@ -1147,7 +1146,6 @@ hipError_t launch_ortho(const OrthoCall& call, void* ws, hipStream_t s) {
     if (e != hipSuccess) return e;
     p.q = P;
     p.out = Q;
-    p.unit = sp.pp_unit;
     e = launch_product<kPoly, false>(p, s);
     if (e != hipSuccess) return e;
     p.q = Q;
