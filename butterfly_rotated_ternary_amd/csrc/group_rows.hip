@@ -8,8 +8,9 @@
 // chunks. One launch counts each chunk's experts, a second gives every chunk
 // the counts before it (at most 256 x N words from L2) and ranks its own rows
 // (64 at a time, one ballot per bit of the expert). One chunk needs no counts
-// from elsewhere: a single launch. 8 ids of 256 experts 3.5 us, 3009 of 60 5.2, 8192 of
-// 64 9.4, 131072 of 256 3.8 + 8.6.
+// from elsewhere: a single launch. In the trace 8 ids of 256 experts take 3.3 to 3.8 us,
+// 3009 of 60 5.2, 8192 of 64 8.9 to 9.4, 131072 of 256 3.3 + 8.9 call after call and
+// 6.2 + 10.6 where other work has been in between.
 #include "common.h"
 #include "kernels.h"
 
@@ -139,8 +140,11 @@ __global__ __launch_bounds__(64 * WAVES) void group_scatter_kernel(GroupArgs p) 
   }
 }
 
-// One chunk as long as a wave has at most eight times 64 rows (8200 ids of 64 experts
-// take 2.7 + 5.1 us in two launches).
+// One chunk as long as a wave has at most eight times 64 rows. On the device one launch
+// is the shorter way up to about 5000 ids (64 experts, in a captured graph: 4096 6.2
+// against 7.2 us, 6144 7.9 against 7.6, 8192 9.5 against 7.7), but the host pays 2.5 us
+// for the second one (any of these, call after call: 11.8 against 14.3 us; alone, with
+// the GPU waited for, 8192 28.1 against 26.1).
 int chunk_of(int M, int N) {
   if (M <= 512 * waves_of(N)) return 512 * waves_of(N);
   const int c = (int)(((long long)M + kMostChunks - 1) / kMostChunks);

@@ -12,7 +12,8 @@
 // of which four experts read); 32768 rows of 64 experts 2048 -> 2048: c and da 340 us,
 // dW 400 to 470 (1.07 GB of fp32 results). One group of 4096 x 4096 x 4096: 113, 110
 // and 117 us (1180 to 1250 TFLOP/s), fp32 1.0 to 1.1 ms (123 to 138). Few rows are
-// bound by reading the weights: one token of 8 experts of 256, 46 MB, 12.7 us.
+// bound by reading the weights: one token of 8 experts of 256, 46 MB, 11.4 us in a
+// captured graph, 12 to 14 in the trace.
 #include <algorithm>
 
 #include "common.h"
@@ -40,9 +41,10 @@ struct GroupTile {
 // rows of tiles_n tiles, rounded up. They come in panels of four rows of tiles,
 // so that the consecutive items that share an L2 are near square. Every wave
 // looks its tile up for itself: 64 groups at a time, a prefix sum over the lanes;
-// the offsets of 256 groups are loaded at once. fill: the rows behind the last group
-// are one more, G, those before the first another, G + 1 (behind the loop: as lanes
-// of it they cost one token of 8 experts 0.7 of 11.4 us).
+// the loads of four times 64 groups' offsets come before the first sum, but the
+// compiler waits for each. fill: the rows behind the last group are one more, G, those
+// before the first another, G + 1 (behind the loop: as lanes of it they made one
+// token of 8 experts 12.0 us instead of 11.4).
 constexpr int kPanel = 4;
 // Tile `at` of the `items` of group e.
 __device__ __forceinline__ GroupTile tile_of(int e, int lo, int hi, int items, int tiles_n, int at) {
@@ -97,19 +99,14 @@ __device__ __forceinline__ GroupTile find_tile(const int32_t* offsets, int G, in
   return {-1, 0, 0, 0, 0, 0};
 }
 
-// In the order in which a workgroup needs them: the first 16 dwords are in registers
-// at its start, the others a load away (with `fill` among those one token of 8 experts
-// took 12.8 us instead of 11.4).
 struct ProductArgs {
+  const char* a;  // rows of the product's left operand, `red` values each
+  const char* w;  // [G][O][K]
+  char* c;        // [M][cols]
   const int32_t* offsets;
-  int M, G, tiles_n;
-  int fill;             // whether rows of no group become 0
-  int red, cols;
-  const char* a;        // rows of the product's left operand, `red` values each
-  const char* w;        // [G][O][K]
-  char* c;              // [M][cols]
   const int32_t* perm;  // NULL: row q of a is row q of the product
-  int k, a_rows;
+  int k, a_rows, M, G, red, cols, tiles_n;
+  int fill;  // whether rows of no group become 0
 };
 
 // Row q's row of a.
@@ -275,9 +272,13 @@ __global__ __launch_bounds__(F::Most::THREADS) void grouped_kernel(ProductArgs p
 // A workgroup computes 16 columns of c for up to 16 rows of a group: each of its
 // four waves takes a quarter of K straight from memory into
 // v_mfma_f32_16x16x32_bf16 (W's rows as the first operand, so a lane ends with
-// four neighbours of a row of c), eight loads of W in flight; the quarters are
-// added in order through LDS. Nothing is shared that LDS could keep: W is read
-// once, and the rows of a come from L2.
+// four neighbours of a row of c); the quarters are added in order through LDS.
+// Nothing is shared that LDS could keep: W is read once, and the rows of a come from
+// L2. The source asks for eight loads of W at a time; the compiler turns the zeros of
+// what is out of range into an address on the stack, so the loads are flat ones: six
+// pairs are in flight together, the seventh and the eighth wait one by one, and none
+// of the next eight is ahead. At K = 2048 that is six trips to memory in a row: one
+// token of 8 experts 2048 -> 1408 takes 11.4 us, its bytes 9.1.
 constexpr int kFewRows = 16, kFewCols = 16;
 constexpr int kFewWaves = 4;
 
@@ -485,7 +486,7 @@ hipError_t launch_grouped_type(const ProductArgs& p, hipStream_t s) {
                       : launch_grouped_cfg<Family<E, 2, 128, 2, 2, BMODE, false>>(p, s);
   if constexpr (E == kBf16) {
     // Few rows per group and few tiles even of 64 columns: one token of 8 experts
-    // of 256, 2048 x 1408, 12.3 us against 20 (memory 9.1); 72 rows of 13 experts,
+    // of 256, 2048 x 1408, 11.4 us against 20 (memory 9.1); 72 rows of 13 experts,
     // 640 x 2640 (546 tiles), 18 against 11.
     if (BMODE == kOutRows && p.cols % 8 == 0 && p.M / used <= 16 && items(128, 64) < 256)
       return launch_few(p, s);

@@ -14,7 +14,10 @@
 // 4 rows of 4096 bf16, 1.88 GB: 349 us (5.4 TB/s); the gradient of 16384 tokens of 2
 // rows of 2048, 0.54 GB: 117 + 5 us (4.6 TB/s); one token of 8 rows 5.2 us. A row belongs to
 // TPR threads (sixteen, a wave, or a whole workgroup), a thread to EPC * NV of its
-// values, held in registers between the sums.
+// values, held in registers between the sums - but in the gradient of fp32 rows above
+// 4096, whose sixteen values a thread leave 42 to 63 registers in scratch memory (8192
+// tokens of 2 rows of 8192: 491 us, 4.4 TB/s). With eps = 0 a row of zeros, a token
+// without picks too, has 0 / 0 for its norm: NaN; squares have to be within fp32.
 #include "common.h"
 #include "kernels.h"
 
@@ -224,7 +227,8 @@ struct Picks {
   __device__ __forceinline__ float gate_of(int j) const { return __int_as_float(pick(g, j)); }
 };
 
-// y += the picks j0 .. k - 1, ascending, four rows of u in flight.
+// y += the picks j0 .. k - 1, ascending, eight rows of u in flight where a thread has
+// one chunk of a row, else four.
 template <class C>
 __device__ __forceinline__ void add_picks(const NormCall& p, const Picks<C>& picks, int j0, int lane,
                                           float (&y)[C::VALS]) {
@@ -259,7 +263,9 @@ __global__ __launch_bounds__(C::THREADS) void norm_kernel(NormCall p) {
   using T = typename C::T;
   const int lane = threadIdx.x % C::TPR;
   const long long t64 = (long long)grid_block() * C::ROWS + threadIdx.x / C::TPR;
-  if (t64 >= p.T) return;  // a whole wave; whole workgroups where rows are theirs
+  // all TPR threads of a row: its sums and picks use no lane outside of them (sixteen
+  // lanes within a wave, whole waves, or the workgroup whose barriers they share)
+  if (t64 >= p.T) return;
   const int t = (int)t64;
   const size_t at = (size_t)t * p.d;
   Picks<C> picks;
@@ -373,7 +379,7 @@ __global__ __launch_bounds__(C::THREADS) void norm_bwd_kernel(NormCall p, float*
   Weights<C> w_pre, w_post;
   w_pre.init(p.w_pre, p.d, lane);
   w_post.init(p.w_post, p.d, lane);
-  // a wave of its own row stops with it; a workgroup's waves share theirs
+  // (the threads of a row leave it together, as in norm_kernel)
   for (long long t64 = first; t64 < p.T; t64 += stride) {
     const size_t at = (size_t)t64 * p.d;
     if constexpr (!C::AHEAD) next.load(p, t64, lane);
@@ -637,7 +643,7 @@ hipError_t launch_norm_bwd_cfg(const NormCall& c, float* part, hipStream_t s) {
 // chunks (32768 rows of 128 bf16 18 -> 12.5 us, their gradient 39 -> 25), a wave up to
 // 128, then a workgroup. The gradient holds about ten values per column and
 // thread, so its long rows go to 512 threads (1024 would leave each 128
-// registers).
+// registers; fp32 above 4096, four chunks a thread, does not fit 256 either).
 template <bool BACK, typename T, bool ALIGNED, typename F>
 hipError_t with_width(int d, F f) {
   constexpr int EPC = 16 / sizeof(T);
