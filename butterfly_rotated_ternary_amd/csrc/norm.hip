@@ -12,12 +12,13 @@
 // Bound by HBM: each array is read or written once (the gradient reads u a
 // second time, out of L2, because dy needs sums over the row). 32768 tokens of
 // 4 rows of 4096 bf16, 1.88 GB: 349 us (5.4 TB/s); the gradient of 16384 tokens of 2
-// rows of 2048, 0.54 GB: 117 + 5 us (4.6 TB/s); one token of 8 rows 5.2 us. A row belongs to
-// TPR threads (sixteen, a wave, or a whole workgroup), a thread to EPC * NV of its
-// values, held in registers between the sums - but in the gradient of fp32 rows above
-// 4096, whose sixteen values a thread leave 42 to 63 registers in scratch memory (8192
-// tokens of 2 rows of 8192: 491 us, 4.4 TB/s). With eps = 0 a row of zeros, a token
-// without picks too, has 0 / 0 for its norm: NaN; squares have to be within fp32.
+// rows of 2048, 0.54 GB: 118 + 5 us (4.5 TB/s); one token of 8 rows 5.5 us. A row
+// belongs to TPR threads (sixteen, a wave, or a whole workgroup), a thread to EPC * NV
+// of its values, held in registers between the sums - but in the gradient of rows above
+// 4096, whose sixteen values a thread of each array leave 42 to 63 registers in scratch
+// memory in fp32 (8192 tokens of 2 rows of 8192: 491 us, 4.4 TB/s) and two in bf16 with
+// several picks (234 us, 4.6 TB/s). With eps = 0 a row of zeros, a token without picks
+// too, has 0 / 0 for its norm: NaN; squares have to be within fp32.
 #include "common.h"
 #include "kernels.h"
 

@@ -20,11 +20,11 @@
 // P and Q are symmetric: only tiles on and below the diagonal are computed,
 // each written twice. Rows are padded to whole 16-byte chunks (zeros).
 //
-// Bound by the matrix units where a side is long: 4096 x 4096, five steps, 3.6 ms
-// (P 210, Q 200, X 315 us a step; 70, 70 and 81 % of the MFMA cycles). 64 matrices
-// 1024 x 512, 1.39 ms: reductions of 512 and 1024 are 16 to 32 steps, so each round
-// of tiles spends as long filling its ring and storing as multiplying (P 101, Q 68,
-// X 119 us; 51, 36 and 49 %).
+// Bound by the matrix units where a side is long: 4096 x 4096, five steps, 3.6 to 3.8
+// ms by the card (P 210, Q 200, X 320 us a step; 70, 70 and 81 % of the MFMA cycles).
+// 64 matrices 1024 x 512, 1.31 to 1.43 ms: reductions of 512 and 1024 are 16 to 32
+// steps, so each round of tiles spends as long filling its ring and storing as
+// multiplying (P 97 to 101, Q 66 to 68, X 116 to 119 us; 51, 36 and 49 %).
 #include "common.h"
 #include "kernels.h"
 #include "tile_product.h"

@@ -625,7 +625,9 @@ bmoe_status bmoe_grouped_product_backward_filled(bmoe_dtype dt, int M, int K, in
  *   z  = y / sqrt(mean(y^2) + eps) * w_post         (w_post NULL: z = y)
  *   r' = res_scale * r + out_scale * z
  *   n  = r' / sqrt(mean(r'^2) + eps) * w_pre
- * all in fp32; r' and n are rounded once each (n is that of r' before rounding).
+ * all in fp32 (squares too: y and r' have to stay below 1.8e19); r' and n are rounded
+ * once each (n is that of r' before rounding). With eps = 0 the norm of a row of zeros,
+ * as of a token without picks, is NaN.
  *   u      [u_rows][d], dtype dt: expert rows (of bmoe_grouped_product), or the
  *          layer's output y of bmoe_forward (k = 1, no inv, no gates), or NULL: no
  *          block before this norm, r' = res_scale * r.
