@@ -157,3 +157,15 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         for x, y in zip(out, step()):
             assert torch.equal(x, y), i
+
+
+def test_rows_behind_the_picks_without_inv():
+    T, k, d, rows = 30, 2, 100, 67
+    u, r = torch.randn(rows, d, device="cuda"), torch.randn(T, d, device="cuda")
+    du, dr = torch.full_like(u, float("nan")), torch.empty_like(r)
+    n = bmoe.bmoe_residual_norm_backward_filled_workspace_bytes(bmoe.BMOE_F32, T, d, rows)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    assert bmoe.bmoe_residual_norm_backward_filled(
+        bmoe.BMOE_F32, T, d, k, bmoe.NormSpec(), u, rows, None, None, r, None, None, r, None, du,
+        None, dr, None, None, ws) == 0
+    assert torch.equal(du[:T * k], r.repeat_interleave(k, 0)) and not du[T * k:].any()
